@@ -13,6 +13,10 @@ call raises.
 q, k [B,T,H,dk] and v [B,T,H,dv] in bf16 or fp32, g and beta [B,T,H] fp32,
 initial_state [N,H,dk,dv] fp32, cu_seqlens int32 [N+1] (then B = 1), all on
 the same CUDA device.
+
+The operators of the layer around the recurrence (layer norm, the short causal
+convolution, the selective scan, single-token steps) are in layer_ops and
+re-exported here.
 """
 from __future__ import annotations
 
@@ -23,6 +27,8 @@ from typing import Optional
 import torch
 
 from . import build as _build
+from . import layer_ops
+from .layer_ops import *  # noqa: F401,F403
 
 __all__ = [
     "GdnOptions", "GdnPlanInfo", "GdnPlanCosts", "GdnWorkspaceLayout", "WORK_ITEM_DTYPE",
@@ -39,7 +45,7 @@ __all__ = [
     "gdn_status_string", "gdn_version", "gdn_last_error_detail", "chunk_fwd", "chunk_fwd_host", "workspace_for", "GdnError",
     "CP_AUTO", "CP_OFF", "CP_FORCE", "KERNEL_AUTO", "KERNEL_TC", "KERNEL_SIMT", "BF16", "F32",
     "STAGE_PREP", "STAGE_INVERSE", "STAGE_CORRECTION", "STAGE_FUSED",
-]
+] + layer_ops.__all__
 
 BF16, F32 = 0, 1
 CP_AUTO, CP_OFF, CP_FORCE = 0, 1, 2
@@ -168,6 +174,7 @@ def load_library(build_if_missing: bool = False):
     lib.gdn_version.restype = ctypes.c_char_p
     lib.gdn_last_error_detail.argtypes = []
     lib.gdn_last_error_detail.restype = ctypes.c_char_p
+    layer_ops.bind(lib)
     _lib = lib
     _apply_measured_costs(lib)
     return lib

@@ -1,0 +1,591 @@
+// Short causal depthwise convolution along the tokens of a sequence, the step
+// between a linear-attention layer's projections and its recurrence:
+//
+//     u_t = bias + sum_{i < W} w_i x_{t - (W-1) + i},   y_t = act(u_t),
+//
+// per channel, W = 2, 3 or 4, act the identity or SiLU.  Rows before a
+// sequence's first token are those of its state (the last W - 1 inputs of what
+// came before, oldest first) or zero.  With du_t = dy_t act'(u_t),
+//
+//     dx_q = sum_i w_i du_{q + (W-1) - i},  dw_i = sum_t du_t x_{t - (W-1) + i},
+//     dbias = sum_t du_t,
+//
+// where the state's rows count as x_{-(W-1)} .. x_{-1}.
+//
+// All three forms are streams bound by HBM: a thread owns four neighbouring
+// channels (one without alignment), a warp a run of tokens that it walks with
+// the window of the last W - 1 inputs in registers, so that a row is read once
+// from memory (W - 1 rows of halo per run come from L2); the next kSub rows are
+// loaded while the current ones are computed.  A sequence boundary inside a run
+// only replaces the window.  In the backward pass the walk also carries the
+// W partial sums of the dx that are not complete yet, so dy and x are read
+// once; dw and dbias stay in registers over the run, are added over the block's
+// warps and leave as one partial row per block that a second kernel adds in
+// order.
+#include <algorithm>
+
+#include "elem.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kConvWarps = 4;   // token runs per block
+constexpr int kSub = 8;         // rows loaded ahead (forward)
+constexpr int kSubB = 4;        // rows of x and dy loaded ahead (backward)
+
+struct ConvArgs {
+    const void *x, *dy, *w, *bias, *init, *d_final;
+    void *out, *last;           // y and final state; or dx and d_init
+    float *partial;             // [groups][W + 1][D]
+    const int32_t *cu, *slots;
+    int32_t *status;
+    long long x_batch, x_token, dy_batch, dy_token;
+    int B, T, D, n_seqs, w_f32, silu, run, groups, chan_blocks, pool;
+};
+
+__device__ __forceinline__ float conv_param(const void *p, long long i, int f32) {
+    return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+template <int W, int VEC>
+__device__ __forceinline__ void load_weights(const ConvArgs &a, int c, int live, float (*w)[VEC], float *b) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][e] = live ? conv_param(a.w, (long long)(c + e) * W + i, a.w_f32) : 0.f;
+        b[e] = live && a.bias ? conv_param(a.bias, c + e, a.w_f32) : 0.f;
+    }
+}
+
+// Rows of a sequence's state as the window before its first token.
+template <typename T, int W, int VEC>
+__device__ __forceinline__ void state_window(const ConvArgs &a, int n, int c, bool live, float (*win)[VEC]) {
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) {
+        if (live && a.init)
+            unpack<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.init) + ((long long)n * (W - 1) + r) * a.D + c), win[r]);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[r][e] = 0.f;
+    }
+}
+
+// Where a run of tokens [t0, t1) of batch row b lies.
+struct Run {
+    int b, t0, t1, n, begin, end;   // begin, end: of the sequence that holds t0
+};
+
+__device__ __forceinline__ void enter_seq(const ConvArgs &a, Run &r, int t) {
+    if (a.cu) {
+        r.begin = min(max(__ldg(a.cu + r.n), 0), t);
+        r.end = min(max(__ldg(a.cu + r.n + 1), t + 1), a.T);
+    }
+}
+
+// The window before token t0: rows of the run's sequence, or of its state.
+template <typename T, int W, int VEC>
+__device__ __forceinline__ void first_window(const ConvArgs &a, const Run &r, int c, bool live, float (*win)[VEC]) {
+    const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        const int t = r.t0 - (W - 1) + i;
+        const int s = (W - 1) + t - r.begin;   // the state's row when t < begin
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[i][e] = 0.f;
+        if (live && t >= r.begin) unpack<T, VEC>(load_raw<T, VEC>(x + t * a.x_token), win[i]);
+        else if (live && a.init)
+            unpack<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.init) + ((long long)r.n * (W - 1) + s) * a.D + c), win[i]);
+    }
+}
+
+template <typename T, int W, int VEC>
+__global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
+    if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
+    const int tile = (blockIdx.x / a.chan_blocks) * kConvWarps + warp;   // over all batch rows
+    const bool live = c < a.D;
+    const int per_row = a.groups / a.B * kConvWarps;
+    Run r;
+    r.b = tile / per_row;
+    r.t0 = (tile % per_row) * a.run;
+    r.t1 = min(a.T, r.t0 + a.run);
+    // states of empty sequences, dealt over the runs
+    if (a.cu && a.last && live) {
+        for (int n = tile; n < a.n_seqs; n += a.groups * kConvWarps) {
+            if (__ldg(a.cu + n) < __ldg(a.cu + n + 1)) continue;
+            float win[W - 1][VEC];
+            state_window<T, W, VEC>(a, n, c, true, win);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+                store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)n * (W - 1) + i) * a.D + c, pack<T, VEC>(win[i]));
+        }
+    }
+    if (r.t0 >= r.t1) {
+        // batched rows without a token keep their state
+        if (!a.cu && a.T == 0 && a.last && live && r.t0 == 0) {
+            float win[W - 1][VEC];
+            state_window<T, W, VEC>(a, r.b, c, true, win);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+                store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)r.b * (W - 1) + i) * a.D + c, pack<T, VEC>(win[i]));
+        }
+        return;
+    }
+    const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
+    T *y = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
+    Raw<T, VEC> next[kSub];
+    auto load_rows = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+            next[i] = live && t + i < r.t1 ? load_raw<T, VEC>(x + (t + i) * a.x_token) : zero_raw<T, VEC>();
+    };
+    load_rows(r.t0);
+    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+    load_weights<W, VEC>(a, c, live, w, bias);
+    r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
+    r.begin = 0, r.end = a.T;
+    enter_seq(a, r, r.t0);
+    first_window<T, W, VEC>(a, r, c, live, win);
+    for (int t = r.t0; t < r.t1; t += kSub) {
+        Raw<T, VEC> cur[kSub];
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) cur[i] = next[i];
+        load_rows(t + kSub);
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) {
+            if (t + i >= r.t1) break;
+            if (t + i == r.end) {   // the next sequence that has a token
+                while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= t + i) ++r.n;
+                enter_seq(a, r, t + i);
+                state_window<T, W, VEC>(a, r.n, c, live, win);
+            }
+            float xv[VEC], u[VEC];
+            unpack<T, VEC>(cur[i], xv);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                u[e] = fmaf(w[W - 1][e], xv[e], bias[e]);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) u[e] = fmaf(w[k][e], win[k][e], u[e]);
+                if (a.silu) u[e] *= sigmoid_f32(u[e]);
+#pragma unroll
+                for (int k = 0; k < W - 2; ++k) win[k][e] = win[k + 1][e];
+                win[W - 2][e] = xv[e];
+            }
+            if (live) {
+                store_raw<T, VEC>(y + (long long)(t + i) * a.D, pack<T, VEC>(u));
+                if (a.last && t + i + 1 == r.end) {
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k)
+                        store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)r.n * (W - 1) + k) * a.D + c,
+                                          pack<T, VEC>(win[k]));
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int W, int VEC>
+__global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
+    __shared__ float sum[kConvWarps][W + 1][32 * VEC];
+    if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
+    const int group = blockIdx.x / a.chan_blocks;
+    const int tile = group * kConvWarps + warp;
+    const bool live = c < a.D;
+    const int per_row = a.groups / a.B * kConvWarps;
+    Run r;
+    r.b = tile / per_row;
+    r.t0 = (tile % per_row) * a.run;
+    r.t1 = min(a.T, r.t0 + a.run);
+    T *dinit = static_cast<T *>(a.last);
+    const T *dfin = static_cast<const T *>(a.d_final);
+    // a sequence without a token hands the gradient of its final state on
+    auto pass_on = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const long long at = ((long long)n * (W - 1) + i) * a.D + c;
+            store_raw<T, VEC>(dinit + at, dfin ? load_raw<T, VEC>(dfin + at) : zero_raw<T, VEC>());
+        }
+    };
+    if (dinit && live) {
+        if (a.cu) {
+            for (int n = tile; n < a.n_seqs; n += a.groups * kConvWarps)
+                if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) pass_on(n);
+        } else if (a.T == 0 && r.t0 == 0) {
+            pass_on(r.b);
+        }
+    }
+    float dw[W][VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
+    }
+    if (r.t0 < r.t1) {
+        const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
+        const T *dy = static_cast<const T *>(a.dy) + r.b * a.dy_batch + c;
+        T *dx = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
+        const int stop = min(a.T, r.t1 + W - 1);
+        Raw<T, VEC> nx[kSubB], ng[kSubB];
+        auto load_rows = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < kSubB; ++i) {
+                const bool in = live && t + i < stop;
+                nx[i] = in ? load_raw<T, VEC>(x + (t + i) * a.x_token) : zero_raw<T, VEC>();
+                ng[i] = in ? load_raw<T, VEC>(dy + (t + i) * a.dy_token) : zero_raw<T, VEC>();
+            }
+        };
+        load_rows(r.t0);
+        float w[W][VEC], bias[VEC], win[W - 1][VEC], acc[W][VEC];
+        load_weights<W, VEC>(a, c, live, w, bias);
+        r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
+        r.begin = 0, r.end = a.T;
+        enter_seq(a, r, r.t0);
+        first_window<T, W, VEC>(a, r, c, live, win);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
+        // the complete sum of position q, to whom it belongs
+        auto emit = [&](int q, const float *v) {
+            if (!live) return;
+            if (q >= r.begin) {
+                if (q >= r.t0 && q < r.t1) store_raw<T, VEC>(dx + (long long)q * a.D, pack<T, VEC>(v));
+            } else if (dinit && r.begin >= r.t0 && r.begin < r.t1) {
+                store_raw<T, VEC>(dinit + ((long long)r.n * (W - 1) + (W - 1) + q - r.begin) * a.D + c, pack<T, VEC>(v));
+            }
+        };
+        // the last W - 1 positions before a sequence's end (at t): no token follows
+        auto flush = [&](int t) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                if (dfin && live) {
+                    float f[VEC];
+                    unpack<T, VEC>(load_raw<T, VEC>(dfin + ((long long)r.n * (W - 1) + k) * a.D + c), f);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[k][e] += f[e];
+                }
+                emit(t - (W - 1) + k, acc[k]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
+            }
+        };
+        bool done = false;
+        for (int t = r.t0; t < stop && !done; t += kSubB) {
+            Raw<T, VEC> cx[kSubB], cg[kSubB];
+#pragma unroll
+            for (int i = 0; i < kSubB; ++i) cx[i] = nx[i], cg[i] = ng[i];
+            load_rows(t + kSubB);
+#pragma unroll
+            for (int i = 0; i < kSubB; ++i) {
+                const int q = t + i;
+                if (q >= stop || done) break;
+                if (q == r.end) {
+                    flush(q);
+                    if (q >= r.t1) {
+                        done = true;
+                        break;
+                    }
+                    while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= q) ++r.n;
+                    enter_seq(a, r, q);
+                    state_window<T, W, VEC>(a, r.n, c, live, win);
+                }
+                float xv[VEC], gv[VEC];
+                unpack<T, VEC>(cx[i], xv);
+                unpack<T, VEC>(cg[i], gv);
+                const float mine = q < r.t1 ? 1.f : 0.f;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    float du = gv[e];
+                    if (a.silu) {
+                        float u = fmaf(w[W - 1][e], xv[e], bias[e]);
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) u = fmaf(w[k][e], win[k][e], u);
+                        const float sg = sigmoid_f32(u);
+                        du *= sg * fmaf(u, 1.f - sg, 1.f);
+                    }
+#pragma unroll
+                    for (int k = 0; k < W; ++k) acc[k][e] = fmaf(w[k][e], du, acc[k][e]);
+                    const float own = du * mine;   // tokens past the run belong to the next one's sums
+                    db[e] += own;
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(own, win[k][e], dw[k][e]);
+                    dw[W - 1][e] = fmaf(own, xv[e], dw[W - 1][e]);
+#pragma unroll
+                    for (int k = 0; k < W - 2; ++k) win[k][e] = win[k + 1][e];
+                    win[W - 2][e] = xv[e];
+                }
+                emit(q - (W - 1), acc[0]);
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[k][e] = k + 1 < W ? acc[k + 1 < W ? k + 1 : k][e] : 0.f;
+            }
+        }
+        if (!done && stop == r.end) flush(stop);
+    }
+    if (!a.partial) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) sum[warp][k][lane * VEC + e] = dw[k][e];
+        sum[warp][W][lane * VEC + e] = db[e];
+    }
+    __syncthreads();
+    const int c0 = (blockIdx.x % a.chan_blocks) * 32 * VEC;
+    for (int i = threadIdx.x; i < (W + 1) * 32 * VEC; i += blockDim.x) {
+        const int k = i / (32 * VEC), j = i % (32 * VEC);
+        if (c0 + j >= a.D) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < kConvWarps; ++v) s += sum[v][k][j];
+        a.partial[((long long)group * (W + 1) + k) * a.D + c0 + j] = s;
+    }
+}
+
+// dw [D][W] and dbias [D] from the blocks' partial rows, in the blocks' order.
+__global__ void __launch_bounds__(256) conv_reduce_kernel(const float *partial, int groups, int W, int D, float *dw,
+                                                          float *dbias) {
+    __shared__ float sum[8][32];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
+    float s = 0.f;
+    if (c < D) {
+#pragma unroll 4
+        for (int g = grp; g < groups; g += 8) s += partial[((long long)g * (W + 1) + k) * D + c];
+    }
+    sum[grp][lane] = s;
+    __syncthreads();
+    if (grp == 0 && c < D) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sum[i][lane];
+        if (k < W && dw) dw[(long long)c * W + k] = s;
+        if (k == W && dbias) dbias[c] = s;
+    }
+}
+
+// One token of each sequence: the window is the cached state, which moves on
+// by one row in place.
+template <typename T, int W, int VEC>
+__global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
+    const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
+    const int n = blockIdx.y;
+    if (c >= a.D) return;
+    T *y = static_cast<T *>(a.out) + (long long)n * a.D + c;
+    const int slot = a.slots ? __ldg(a.slots + n) : n;
+    if (slot < 0 || slot >= a.pool) {   // a padded row
+        store_raw<T, VEC>(y, zero_raw<T, VEC>());
+        return;
+    }
+    T *state = static_cast<T *>(a.last) + (long long)slot * (W - 1) * a.D + c;
+    Raw<T, VEC> row[W];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) row[k] = load_raw<T, VEC>(state + (long long)k * a.D);
+    row[W - 1] = load_raw<T, VEC>(static_cast<const T *>(a.x) + n * a.x_batch + c);
+    float w[W][VEC], u[VEC];
+    load_weights<W, VEC>(a, c, 1, w, u);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        float v[VEC];
+        unpack<T, VEC>(row[k], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) u[e] = fmaf(w[k][e], v[e], u[e]);
+    }
+    if (a.silu) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) u[e] *= sigmoid_f32(u[e]);
+    }
+    store_raw<T, VEC>(y, pack<T, VEC>(u));
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_raw<T, VEC>(state + (long long)k * a.D, row[k + 1]);
+}
+
+enum class Conv { kFwd, kBwd, kStep };
+
+template <Conv OP, typename T, int W, int VEC>
+void launch_conv_one(const ConvArgs &a, cudaStream_t s) {
+    if constexpr (OP == Conv::kStep) {
+        conv_step_kernel<T, W, VEC><<<dim3((a.D + 128 * VEC - 1) / (128 * VEC), a.B), 128, 0, s>>>(a);
+    } else {
+        const unsigned grid = (unsigned)((long long)a.groups * a.chan_blocks);
+        if constexpr (OP == Conv::kFwd) conv_fwd_kernel<T, W, VEC><<<grid, 32 * kConvWarps, 0, s>>>(a);
+        else conv_bwd_kernel<T, W, VEC><<<grid, 32 * kConvWarps, 0, s>>>(a);
+    }
+}
+
+template <Conv OP, typename T>
+cudaError_t launch_conv(ConvArgs a, int W, bool vec, cudaStream_t s) {
+    const int per_block = 32 * (vec ? 4 : 1);
+    a.chan_blocks = (a.D + per_block - 1) / per_block;
+#define GDN_CONV(WW) (vec ? launch_conv_one<OP, T, WW, 4>(a, s) : launch_conv_one<OP, T, WW, 1>(a, s))
+    if (W == 2) GDN_CONV(2);
+    else if (W == 3) GDN_CONV(3);
+    else GDN_CONV(4);
+#undef GDN_CONV
+    return cudaGetLastError();
+}
+
+// Tokens per warp: 64 amortise the halo of W - 1 rows (5% more reads from L2)
+// and the weights; fewer where the problem would not give every SM about 16
+// warps.
+int conv_run(int B, int T, int D, int vec) {
+    const long long warps_wanted = 16ll * device_sm_count();
+    const int chan = (D + 32 * vec - 1) / (32 * vec);
+    int run = 64;
+    while (run > kSub && (long long)B * ((T + run - 1) / run) * chan < warps_wanted) run >>= 1;
+    return run;
+}
+
+// Groups of kConvWarps runs over all batch rows (at least one per row).
+int conv_groups(int B, int T, int run) { return B * std::max(1, (T + run * kConvWarps - 1) / (run * kConvWarps)); }
+
+struct ConvShape {
+    const int32_t *cu;
+    int n_seqs, B, T, D, W, dtype, w_dtype;
+};
+
+gdn_status conv_shape_ok(const ConvShape &p, int64_t batch_stride, int64_t token_stride) {
+    if (p.B < 0 || p.T < 0 || p.D < 1) return GDN_ERR_INVALID_ARG;
+    if (p.W < 2 || p.W > 4) return GDN_ERR_UNSUPPORTED;
+    if ((p.dtype != GDN_BF16 && p.dtype != GDN_F32) || (p.w_dtype != GDN_F32 && p.w_dtype != p.dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (p.cu && (p.B != 1 || p.n_seqs < 1)) return GDN_ERR_INVALID_ARG;
+    if (token_stride < p.D || batch_stride < 0) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+bool conv_vec(const ConvShape &p, const void *const *ptrs, int n, int64_t s0, int64_t s1) {
+    const uintptr_t mask = (p.dtype == GDN_F32 ? 16 : 8) - 1;
+    bool ok = p.D % 4 == 0 && s0 % 4 == 0 && s1 % 4 == 0;
+    for (int i = 0; i < n; ++i) ok = ok && (reinterpret_cast<uintptr_t>(ptrs[i]) & mask) == 0;
+    return ok;
+}
+
+bool conv_elems(const void *const *ptrs, int n, int dtype) {
+    for (int i = 0; i < n; ++i)
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) & (dtype == GDN_F32 ? 3u : 1u)) return false;
+    return true;
+}
+
+}  // namespace
+
+}  // namespace gdn
+
+extern "C" gdn_status gdn_causal_conv_fwd(const void *x, int64_t x_batch_stride, int64_t x_token_stride,
+                                          const void *weight, const void *bias, gdn_dtype w_dtype,
+                                          const void *initial_state, const int32_t *cu_seqlens, int n_seqs, int B,
+                                          int T, int D, int W, int silu, gdn_dtype dtype, void *y, void *final_state,
+                                          int32_t *device_status, gdn_stream_t stream) {
+    using namespace gdn;
+    const ConvShape p = {cu_seqlens, n_seqs, B, T, D, W, dtype, w_dtype};
+    const gdn_status st = conv_shape_ok(p, x_batch_stride, x_token_stride);
+    if (st != GDN_OK) return st;
+    if (B == 0) return GDN_OK;
+    if (!weight || (T > 0 && (!x || !y))) return GDN_ERR_INVALID_ARG;
+    const void *act[] = {x, y, initial_state, final_state}, *par[] = {weight, bias};
+    if (!conv_elems(act, 4, dtype) || !conv_elems(par, 2, w_dtype)) return GDN_ERR_INVALID_ARG;
+    const bool vec = conv_vec(p, act, 4, x_batch_stride, x_token_stride);
+    ConvArgs a = {};
+    a.x = x, a.w = weight, a.bias = bias, a.init = initial_state, a.out = y, a.last = final_state;
+    a.cu = cu_seqlens, a.status = device_status, a.x_batch = x_batch_stride, a.x_token = x_token_stride;
+    a.B = B, a.T = T, a.D = D, a.n_seqs = cu_seqlens ? n_seqs : B, a.w_f32 = w_dtype == GDN_F32, a.silu = silu != 0;
+    a.run = conv_run(B, T, D, vec ? 4 : 1);
+    a.groups = conv_groups(B, T, a.run);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == GDN_BF16 ? launch_conv<Conv::kFwd, __nv_bfloat16>(a, W, vec, s)
+                                            : launch_conv<Conv::kFwd, float>(a, W, vec, s);
+    if (e != cudaSuccess) {
+        set_error_detail("launch causal_conv_fwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+extern "C" size_t gdn_causal_conv_bwd_workspace_size(int B, int T, int D, int W) {
+    if (B < 0 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
+    // the narrower of the two layouts needs more groups: room for either
+    const int g4 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 4)), g1 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 1));
+    return std::max<size_t>(16, (size_t)std::max(g4, g1) * (W + 1) * (size_t)D * sizeof(float));
+}
+
+extern "C" gdn_status gdn_causal_conv_bwd(const void *dy, int64_t dy_batch_stride, int64_t dy_token_stride,
+                                          const void *x, int64_t x_batch_stride, int64_t x_token_stride,
+                                          const void *weight, const void *bias, gdn_dtype w_dtype,
+                                          const void *initial_state, const void *d_final_state,
+                                          const int32_t *cu_seqlens, int n_seqs, int B, int T, int D, int W, int silu,
+                                          gdn_dtype dtype, void *dx, float *dweight, float *dbias,
+                                          void *d_initial_state, int32_t *device_status, void *workspace,
+                                          size_t workspace_bytes, gdn_stream_t stream) {
+    using namespace gdn;
+    const ConvShape p = {cu_seqlens, n_seqs, B, T, D, W, dtype, w_dtype};
+    gdn_status st = conv_shape_ok(p, x_batch_stride, x_token_stride);
+    if (st == GDN_OK) st = conv_shape_ok(p, dy_batch_stride, dy_token_stride);
+    if (st != GDN_OK) return st;
+    if (!weight || (B > 0 && T > 0 && (!x || !dy || !dx))) return GDN_ERR_INVALID_ARG;
+    const void *act[] = {x, dy, dx, initial_state, d_final_state, d_initial_state}, *par[] = {weight, bias};
+    const void *f32[] = {dweight, dbias};
+    if (!conv_elems(act, 6, dtype) || !conv_elems(par, 2, w_dtype) || !conv_elems(f32, 2, GDN_F32))
+        return GDN_ERR_INVALID_ARG;
+    const bool vec = conv_vec(p, act, 6, x_batch_stride | dy_batch_stride, x_token_stride | dy_token_stride);
+    const bool params = dweight || dbias;
+    if (params && B > 0) {
+        if (!workspace || !aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+        if (workspace_bytes < gdn_causal_conv_bwd_workspace_size(B, T, D, W)) return GDN_ERR_WORKSPACE;
+    }
+    ConvArgs a = {};
+    a.x = x, a.dy = dy, a.w = weight, a.bias = bias, a.init = initial_state, a.d_final = d_final_state;
+    a.out = dx, a.last = d_initial_state, a.partial = params ? static_cast<float *>(workspace) : nullptr;
+    a.cu = cu_seqlens, a.status = device_status;
+    a.x_batch = x_batch_stride, a.x_token = x_token_stride, a.dy_batch = dy_batch_stride, a.dy_token = dy_token_stride;
+    a.B = B, a.T = T, a.D = D, a.n_seqs = cu_seqlens ? n_seqs : B, a.w_f32 = w_dtype == GDN_F32, a.silu = silu != 0;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (B > 0) {
+        a.run = conv_run(B, T, D, vec ? 4 : 1);
+        a.groups = conv_groups(B, T, a.run);
+        e = dtype == GDN_BF16 ? launch_conv<Conv::kBwd, __nv_bfloat16>(a, W, vec, s)
+                              : launch_conv<Conv::kBwd, float>(a, W, vec, s);
+    }
+    if (e == cudaSuccess && params) {
+        conv_reduce_kernel<<<dim3((D + 31) / 32, W + 1), 256, 0, s>>>(static_cast<const float *>(workspace),
+                                                                     B > 0 ? a.groups : 0, W, D, dweight, dbias);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+        set_error_detail("launch causal_conv_bwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+extern "C" gdn_status gdn_causal_conv_step(const void *x, int64_t x_stride, void *state, const int32_t *state_indices,
+                                           int n_states, const void *weight, const void *bias, gdn_dtype w_dtype,
+                                           int N, int D, int W, int silu, gdn_dtype dtype, void *y,
+                                           gdn_stream_t stream) {
+    using namespace gdn;
+    const ConvShape p = {nullptr, 0, N, 1, D, W, dtype, w_dtype};
+    const gdn_status st = conv_shape_ok(p, 0, x_stride);
+    if (st != GDN_OK) return st;
+    if (N > 65535 || n_states < 0 || (!state_indices && n_states < N)) return GDN_ERR_INVALID_ARG;
+    if (N == 0) return GDN_OK;
+    if (!x || !state || !weight || !y) return GDN_ERR_INVALID_ARG;
+    const void *act[] = {x, state, y}, *par[] = {weight, bias};
+    if (!conv_elems(act, 3, dtype) || !conv_elems(par, 2, w_dtype)) return GDN_ERR_INVALID_ARG;
+    const bool vec = conv_vec(p, act, 3, x_stride, x_stride);
+    ConvArgs a = {};
+    a.x = x, a.w = weight, a.bias = bias, a.out = y, a.last = state, a.slots = state_indices, a.pool = n_states;
+    a.x_batch = x_stride, a.B = N, a.T = 1, a.D = D, a.w_f32 = w_dtype == GDN_F32, a.silu = silu != 0;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == GDN_BF16 ? launch_conv<Conv::kStep, __nv_bfloat16>(a, W, vec, s)
+                                            : launch_conv<Conv::kStep, float>(a, W, vec, s);
+    if (e != cudaSuccess) {
+        set_error_detail("launch causal_conv_step", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}

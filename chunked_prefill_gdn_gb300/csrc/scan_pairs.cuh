@@ -1,0 +1,134 @@
+// What the selective scan's kernels share: pairs of fp32 values in one 64-bit
+// register (mul / fma act on both), the exponential and softplus, the
+// arguments, and where a tile of tokens lies among the sequences.
+#pragma once
+
+#include "elem.cuh"
+
+namespace gdn {
+
+using F2 = unsigned long long;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 32;   // tokens per tile
+
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo(F2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 2^x, at most 2^-22 off relatively; results below 2^-126 are zero.
+__device__ __forceinline__ float exp2_f32(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ F2 exp2_pair(F2 x) { return pair(exp2_f32(lo(x)), exp2_f32(hi(x))); }
+
+// log(1 + exp(x)); above 20 it is x to fp32.
+__device__ __forceinline__ float softplus_f32(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+
+struct ScanArgs {
+    const void *x, *dt, *z, *Bm, *Cm, *dy;
+    const float *A, *skip, *bias, *init, *d_final;
+    const int32_t *cu, *slots;
+    int32_t *status;
+    void *out;                       // y; or dx
+    float *final_state;
+    void *ddt, *dz;
+    float *dinit;
+    // workspace: per segment (forward) or per tile (backward) and channel
+    float *hloc, *gloc, *sums;       // [maps][D][NP], [maps][D][NP], [maps][D]
+    int32_t *flags;                  // [maps]: bit 0 a sequence starts at its first token, bit 1 at a later one
+    float *part_a, *part_v, *part_bc;   // [segments][D][NP], [segments][2][D], [chan_blocks][tokens][2][NP]
+    long long x_batch, x_token, dt_batch, dt_token, z_batch, z_token, b_batch, b_token, c_batch, c_token, dy_batch,
+        dy_token;
+    int B, T, D, N, n_seqs, softplus, vec, bc_vec, chan_blocks, segs, seg_tokens, row_tiles, pool, has_carry;
+};
+
+// Tokens [t0, t1) of row b, and the sequence that holds the current one.
+struct Span {
+    int b, t0, t1, n, begin, end;
+};
+
+// The bounds of sequence r.n, made to contain token t whatever cu_seqlens holds.
+__device__ __forceinline__ void span_bounds(const ScanArgs &a, Span &r, int t) {
+    if (a.cu) {
+        r.begin = min(max(__ldg(a.cu + r.n), 0), t);
+        r.end = min(max(__ldg(a.cu + r.n + 1), t + 1), a.T);
+    } else {
+        r.begin = 0;
+        r.end = a.T;
+    }
+}
+__device__ __forceinline__ void span_find(const ScanArgs &a, Span &r) {
+    r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
+    span_bounds(a, r, r.t0);
+}
+// The sequence that starts at token t, where the last one ended.
+__device__ __forceinline__ void span_next(const ScanArgs &a, Span &r, int t) {
+    if (!a.cu) return;
+    while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= t) ++r.n;
+    span_bounds(a, r, t);
+}
+
+// Eight neighbouring elements of which `live` exist.
+template <typename T>
+__device__ __forceinline__ Raw<T, 8> load8(const T *p, int live, bool vec) {
+    if (live <= 0) return zero_raw<T, 8>();
+    if (vec && live >= 8) return load_raw<T, 8>(p);
+    return load_some<T, 8>(p, live);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float *v, int live, bool vec) {
+    if (live <= 0) return;
+    if (vec && live >= 8) store_raw<T, 8>(p, pack<T, 8>(v));
+    else store_some<T, 8>(p, v, live);
+}
+
+// M pairs of consecutive n from n0 of a row of N values (null: zero).
+template <int M>
+__device__ __forceinline__ void load_pairs(const float *row, int n0, int N, bool live, F2 (&h)[M]) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const int n = n0 + 2 * i;
+        h[i] = pair(row && live && n < N ? row[n] : 0.f, row && live && n + 1 < N ? row[n + 1] : 0.f);
+    }
+}
+template <int M>
+__device__ __forceinline__ void store_pairs(float *row, int n0, int N, const F2 (&h)[M]) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const int n = n0 + 2 * i;
+        if (n < N) row[n] = lo(h[i]);
+        if (n + 1 < N) row[n + 1] = hi(h[i]);
+    }
+}
+
+cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_bwd(ScanArgs a, int dtype, void *dB, void *dC, float *dA, float *dskip, float *dbias,
+                            cudaStream_t s);
+cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s);
+
+// Threads over n of the scanning kernels: eight n each.
+inline int scan_parts(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
+
+}  // namespace gdn

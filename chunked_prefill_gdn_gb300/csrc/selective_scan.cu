@@ -1,0 +1,515 @@
+// Selective state space scan with a diagonal transition: per channel d and
+// state index n of a sequence,
+//
+//     h_t = a_t h_{t-1} + s_t x_t B_t[n],  a_t = exp(s_t A[d][n]),
+//     y_t = sum_n C_t[n] h_t + D x_t,      out_t = y_t silu(z_t),
+//
+// with the step s_t = dt_t + dt_bias (through softplus when asked).  This file
+// holds the forward pass, the single-token form and the entry points.
+//
+// What bounds the forward pass is arithmetic, not memory: one exponential and
+// four multiply-adds per (token, channel, n) against about 8 bytes per (token,
+// channel).  ex2 runs at 32 lanes per clock and SM, FP32 FMA at 128 (measured
+// on a GB300), so both pipes are full at the same rate, 32 (token, channel, n)
+// per clock and SM; the arithmetic is written on pairs (two-wide FP32), which
+// leaves issue slots for the rest.  A thread keeps eight n of one channel in
+// registers, LP threads share a channel.  B and C of a tile of tokens are read
+// from shared memory by every channel of the block, and what is per (token,
+// channel) only (softplus, the gate) is computed once, by the threads that load
+// the tile, not by the LP threads that scan it.  The next tile is loaded into
+// registers during the scan of the current one.
+//
+// When the (sequence, channel) pairs do not fill the GPU, the token axis is cut
+// into segments: a first pass gives every segment's end state from a zero
+// start, a short pass combines them (the map of a segment is h -> exp(A sum s)
+// h + end), and the full pass starts every segment from its exact state.  Each
+// exponential is then taken twice.
+#include <algorithm>
+
+#include "scan_pairs.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kScanThreads = 64;
+
+// STATE_ONLY: the end state from a zero start and the sum of the steps of every
+// segment; else the full pass.
+template <typename T, int LP, bool STATE_ONLY>
+__global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
+    constexpr int CH = kScanThreads / LP;          // channels of the block
+    constexpr int NP = 8 * LP;                     // n, padded
+    constexpr int VPR = CH / 8;                    // loads of eight channels per row
+    constexpr int RPP = kScanThreads / VPR;        // rows per pass of the loading threads
+    constexpr int PASSES = RPP >= kTile ? 1 : kTile / RPP;
+    __shared__ __align__(16) float2 sd[kTile][CH]; // step, step * x
+    __shared__ __align__(16) float bc[kTile][2][NP];
+    __shared__ __align__(16) float ys[STATE_ONLY ? 1 : kTile][CH];
+
+    if (!STATE_ONLY && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
+    const int tid = threadIdx.x;
+    const int chan0 = (blockIdx.x % a.chan_blocks) * CH;
+    // the last segment of a row needs no map
+    const int spr = STATE_ONLY ? a.segs - 1 : a.segs;
+    Span r;
+    r.b = blockIdx.x / a.chan_blocks / spr;
+    const int seg = r.b * a.segs + blockIdx.x / a.chan_blocks % spr;
+    r.t0 = (seg - r.b * a.segs) * a.seg_tokens;
+    r.t1 = min(a.T, r.t0 + a.seg_tokens);
+
+    const int part = tid % LP, n0 = part * 8, chl = tid / LP, ch = chan0 + chl;
+    const bool live = ch < a.D;
+    if (!STATE_ONLY && a.final_state && live) {    // a sequence without a token keeps its state
+        auto keep = [&](int n) {
+            const long long at = ((long long)n * a.D + ch) * a.N;
+            F2 v[4];
+            load_pairs(a.init ? a.init + at : nullptr, n0, a.N, true, v);
+            store_pairs(a.final_state + at, n0, a.N, v);
+        };
+        if (!a.cu && a.T == 0) keep(r.b);
+        for (int n = seg; a.cu && n < a.n_seqs; n += a.segs)
+            if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) keep(n);
+    }
+    if (r.t0 >= r.t1) return;
+
+    F2 A2[4], h[4];
+    load_pairs(a.A + (long long)ch * a.N, n0, a.N, live, A2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A2[i] = mul2(A2[i], pair(kLog2e, kLog2e));
+    span_find(a, r);
+    const bool starts = r.begin == r.t0;
+    bool inside = false;
+    auto initial = [&](int n) {
+        load_pairs(a.init ? a.init + ((long long)n * a.D + ch) * a.N : nullptr, n0, a.N, live, h);
+    };
+    if (starts) initial(r.n);
+    else load_pairs(!STATE_ONLY && a.has_carry ? a.hloc + ((long long)seg * a.D + ch) * NP : nullptr, n0, NP, live, h);
+    float step_sum = 0.f;
+
+    // loading: thread -> (row of the pass, eight channels)
+    const int lv = tid % VPR, lrow = tid / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
+    const bool loads = lrow < kTile;
+    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + lc;
+    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + lc;
+    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + lc;
+    const bool gated = !STATE_ONLY && a.z != nullptr;
+    float bias[8], skip[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bias[i] = a.bias && i < lrest ? a.bias[lc + i] : 0.f;
+        skip[i] = !STATE_ONLY && a.skip && i < lrest ? a.skip[lc + i] : 0.f;
+    }
+    Raw<T, 8> rx[PASSES], rd[PASSES], rz[PASSES], rbc[LP];
+    auto load_tile = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int q = t + i * RPP + lrow;
+            const int n = loads && q < r.t1 ? lrest : 0;
+            rx[i] = load8<T>(px + q * a.x_token, n, a.vec);
+            rd[i] = load8<T>(pd + q * a.dt_token, n, a.vec);
+            rz[i] = load8<T>(pz + q * a.z_token, gated ? n : 0, a.vec);
+        }
+#pragma unroll
+        for (int i = 0; i < LP; ++i) {             // rows of B and C, eight n each
+            const int j = i * kScanThreads + tid, v = j % LP, c = j / LP % 2, q = t + j / (2 * LP);
+            const T *src = c ? static_cast<const T *>(a.Cm) + r.b * a.c_batch + q * a.c_token
+                             : static_cast<const T *>(a.Bm) + r.b * a.b_batch + q * a.b_token;
+            rbc[i] = load8<T>(src + v * 8, q < r.t1 ? a.N - v * 8 : 0, a.bc_vec);
+        }
+    };
+    load_tile(r.t0);
+    for (int t = r.t0; t < r.t1; t += kTile) {
+        Raw<T, 8> cx[PASSES], cz[PASSES];
+        // (the threads' last reads of sd and bc lie before the barrier after the scan)
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            cx[i] = rx[i];
+            cz[i] = rz[i];
+            const int q = i * RPP + lrow;
+            float x[8], d[8];
+            unpack<T, 8>(rx[i], x);
+            unpack<T, 8>(rd[i], d);
+            if (loads) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float p0 = d[e] + bias[e], p1 = d[e + 1] + bias[e + 1];
+                    const float s0 = a.softplus ? softplus_f32(p0) : p0, s1 = a.softplus ? softplus_f32(p1) : p1;
+                    *reinterpret_cast<float4 *>(&sd[q][lv * 8 + e]) = make_float4(s0, s0 * x[e], s1, s1 * x[e + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < LP; ++i) {
+            const int j = i * kScanThreads + tid, v = j % LP, c = j / LP % 2, q = j / (2 * LP);
+            float f[8];
+            unpack<T, 8>(rbc[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4 *>(&bc[q][c][v * 8 + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+        load_tile(t + kTile);
+        __syncthreads();
+        const int stop = min(r.t1, t + kTile);
+        for (int q = t; q < stop;) {
+            const int run_end = min(stop, r.end);
+#pragma unroll 4
+            for (int k = q - t; k < run_end - t; ++k) {
+                const float2 s = sd[k][chl];
+                const F2 ss = pair(s.x, s.x), sx = pair(s.y, s.y);
+                const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(&bc[k][0][n0]);
+                const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(&bc[k][1][n0]);
+                F2 y = pair(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const ulonglong2 b = Bk[i];
+                    h[2 * i] = fma2(exp2_pair(mul2(ss, A2[2 * i])), h[2 * i], mul2(sx, b.x));
+                    h[2 * i + 1] = fma2(exp2_pair(mul2(ss, A2[2 * i + 1])), h[2 * i + 1], mul2(sx, b.y));
+                    if (!STATE_ONLY) {
+                        const ulonglong2 c = Ck[i];
+                        y = fma2(c.x, h[2 * i], y);
+                        y = fma2(c.y, h[2 * i + 1], y);
+                    }
+                }
+                if (STATE_ONLY) {
+                    step_sum += s.x;
+                } else {
+                    float v = lo(y) + hi(y);
+#pragma unroll
+                    for (int off = 1; off < LP; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                    if (part == 0) ys[k][chl] = v;
+                }
+            }
+            q = run_end;
+            if (q == r.end) {   // the sequence is complete
+                if (!STATE_ONLY && a.final_state && live)
+                    store_pairs(a.final_state + ((long long)r.n * a.D + ch) * a.N, n0, a.N, h);
+                if (q < r.t1) {
+                    span_next(a, r, q);
+                    initial(r.n);
+                    inside = true;
+                }
+            }
+        }
+        __syncthreads();
+        if (!STATE_ONLY) {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int q = i * RPP + lrow;
+                if (!loads || t + q >= r.t1) continue;
+                float x[8], z[8], o[8];
+                unpack<T, 8>(cx[i], x);
+                unpack<T, 8>(cz[i], z);
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&ys[q][lv * 8 + e]);
+                    o[e] = v.x, o[e + 1] = v.y, o[e + 2] = v.z, o[e + 3] = v.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    o[e] = fmaf(skip[e], x[e], o[e]);
+                    if (gated) o[e] *= z[e] * sigmoid_f32(z[e]);
+                }
+                store8<T>(static_cast<T *>(a.out) + ((long long)r.b * a.T + t + q) * a.D + lc, o, lrest, a.vec);
+            }
+        }
+    }
+    if (STATE_ONLY) {
+        if (live) {
+            store_pairs(a.hloc + ((long long)seg * a.D + ch) * NP, n0, NP, h);
+            if (part == 0) a.sums[(long long)seg * a.D + ch] = step_sum;
+        }
+        if (chan0 == 0 && tid == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
+    }
+}
+
+// Replaces every map's end state by the state before it, and (GRAD) every
+// map's start gradient by the gradient at its end.  A thread per (row, channel,
+// n); eight maps are loaded ahead.
+template <bool GRAD>
+__global__ void __launch_bounds__(128) scan_combine_kernel(ScanArgs a, int maps, int NP) {
+    constexpr int AHEAD = 8;
+    const long long at = (long long)blockIdx.x * 128 + threadIdx.x, size = (long long)a.D * NP;
+    if (at >= size) return;
+    const int ch = (int)(at / NP), n = (int)(at % NP);
+    const float A2 = n < a.N ? a.A[(long long)ch * a.N + n] * kLog2e : 0.f;
+    const bool back = GRAD && blockIdx.z == 1;
+    float *maps_at = (back ? a.gloc : a.hloc) + (long long)blockIdx.y * maps * size + at;
+    const float *sums = a.sums + (long long)blockIdx.y * maps * a.D + ch;
+    const int32_t *flags = a.flags + (long long)blockIdx.y * maps;
+    float carry = 0.f;
+    for (int m0 = 0; m0 < maps; m0 += AHEAD) {
+        float v[AHEAD], s[AHEAD];
+        int f[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int m = back ? maps - 1 - m0 - i : m0 + i;
+            const bool in = m0 + i < maps && (GRAD || m + 1 < maps);   // forward only: the last map is not there
+            v[i] = in ? maps_at[m * size] : 0.f;
+            s[i] = in ? sums[(long long)m * a.D] : 0.f;
+            f[i] = in ? flags[m] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (m0 + i >= maps) break;
+            const int m = back ? maps - 1 - m0 - i : m0 + i;
+            maps_at[m * size] = carry;
+            const float through = exp2_f32(A2 * s[i]);
+            if (back) carry = f[i] & 1 ? 0.f : f[i] & 2 ? v[i] : fmaf(through, carry, v[i]);
+            else carry = f[i] ? v[i] : fmaf(through, carry, v[i]);
+        }
+    }
+}
+
+// One token of each sequence: 4 n per thread, LANES threads per channel.
+template <typename T, int LANES>
+__global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
+    const int part = threadIdx.x % LANES, ch = (int)((blockIdx.x * 128ll + threadIdx.x) / LANES);
+    const int b = blockIdx.y, n0 = part * 4;
+    const bool live = ch < a.D;
+    const int slot = a.slots ? __ldg(a.slots + b) : b;
+    if (slot < 0 || slot >= a.pool) {   // a padded row
+        if (live && part == 0) static_cast<T *>(a.out)[(long long)b * a.D + ch] = from_f32<T>(0.f);
+        return;
+    }
+    float y = 0.f, x = 0.f;
+    if (live) {
+        float *state = a.final_state + ((long long)slot * a.D + ch) * a.N + n0;
+        const float *A = a.A + (long long)ch * a.N + n0;
+        float h[4], av[4], Bv[4], Cv[4];
+        const T *B = static_cast<const T *>(a.Bm) + b * a.b_batch + n0, *C = static_cast<const T *>(a.Cm) + b * a.c_batch + n0;
+        if (vec && n0 < a.N) {
+            const float4 hv = *reinterpret_cast<const float4 *>(state), aw = *reinterpret_cast<const float4 *>(A);
+            h[0] = hv.x, h[1] = hv.y, h[2] = hv.z, h[3] = hv.w;
+            av[0] = aw.x, av[1] = aw.y, av[2] = aw.z, av[3] = aw.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = n0 + i < a.N ? state[i] : 0.f, av[i] = n0 + i < a.N ? A[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Bv[i] = n0 + i < a.N ? to_f32(B[i]) : 0.f, Cv[i] = n0 + i < a.N ? to_f32(C[i]) : 0.f;
+        x = to_f32(static_cast<const T *>(a.x)[b * a.x_batch + ch]);
+        float s = to_f32(static_cast<const T *>(a.dt)[b * a.dt_batch + ch]) + (a.bias ? a.bias[ch] : 0.f);
+        if (a.softplus) s = softplus_f32(s);
+        const float sx = s * x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = fmaf(exp2_f32(s * kLog2e * av[i]), h[i], sx * Bv[i]);
+            y = fmaf(Cv[i], h[i], y);
+        }
+        if (vec && n0 < a.N) {
+            *reinterpret_cast<float4 *>(state) = make_float4(h[0], h[1], h[2], h[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n0 + i < a.N) state[i] = h[i];
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < LANES; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    if (live && part == 0) {
+        y = fmaf(a.skip ? a.skip[ch] : 0.f, x, y);
+        if (a.z) {
+            const float z = to_f32(static_cast<const T *>(a.z)[b * a.z_batch + ch]);
+            y *= z * sigmoid_f32(z);
+        }
+        static_cast<T *>(a.out)[(long long)b * a.D + ch] = from_f32<T>(y);
+    }
+}
+
+template <typename T, int LP>
+cudaError_t launch_scan_parts(ScanArgs a, cudaStream_t s) {
+    constexpr int CH = kScanThreads / LP;
+    a.chan_blocks = (a.D + CH - 1) / CH;
+    a.has_carry = a.segs > 1;
+    if (a.segs > 1) {
+        scan_kernel<T, LP, true><<<(unsigned)((long long)a.chan_blocks * a.B * (a.segs - 1)), kScanThreads, 0, s>>>(a);
+        const cudaError_t e = launch_scan_combine(a, a.segs, false, s);
+        if (e != cudaSuccess) return e;
+    }
+    scan_kernel<T, LP, false><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), kScanThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_scan_typed(const ScanArgs &a, cudaStream_t s) {
+    switch (scan_parts(a.N)) {
+        case 1: return launch_scan_parts<T, 1>(a, s);
+        case 2: return launch_scan_parts<T, 2>(a, s);
+        case 4: return launch_scan_parts<T, 4>(a, s);
+        default: return launch_scan_parts<T, 8>(a, s);
+    }
+}
+
+template <typename T>
+cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
+    const int lanes = a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16;
+    const dim3 grid((unsigned)(((long long)a.D * lanes + 127) / 128), a.B);
+    if (lanes == 2) scan_step_kernel<T, 2><<<grid, 128, 0, s>>>(a, vec);
+    else if (lanes == 4) scan_step_kernel<T, 4><<<grid, 128, 0, s>>>(a, vec);
+    else if (lanes == 8) scan_step_kernel<T, 8><<<grid, 128, 0, s>>>(a, vec);
+    else scan_step_kernel<T, 16><<<grid, 128, 0, s>>>(a, vec);
+    return cudaGetLastError();
+}
+
+// Segments per row in the forward pass.  One segment takes each exponential
+// once; several take it twice but put that many times the blocks to work.  An
+// SM is busy with about eight blocks of two warps (one warp of every two
+// schedulers hides the other's latency); segments are cut when whole rows
+// leave it with less than half of that.
+int scan_segments(int B, int T, int D, int N) {
+    const int ch = kScanThreads / scan_parts(N), tiles = (T + kTile - 1) / kTile;
+    const long long blocks = (long long)B * ((D + ch - 1) / ch), wanted = 8ll * device_sm_count();
+    if (tiles <= 1 || 2 * blocks >= wanted) return 1;
+    const int segs = (int)std::min<long long>((wanted + blocks - 1) / blocks, tiles);
+    const int len = (tiles + segs - 1) / segs;
+    return (tiles + len - 1) / len;
+}
+int scan_segment_tokens(int T, int segs) {
+    const int tiles = (T + kTile - 1) / kTile;
+    return std::max(1, (tiles + segs - 1) / segs) * kTile;
+}
+
+}  // namespace
+
+cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s) {
+    const int NP = 8 * scan_parts(a.N);
+    const dim3 grid((unsigned)(((long long)a.D * NP + 127) / 128), a.B, grad ? 2 : 1);
+    if (grad) scan_combine_kernel<true><<<grid, 128, 0, s>>>(a, maps, NP);
+    else scan_combine_kernel<false><<<grid, 128, 0, s>>>(a, maps, NP);
+    return cudaGetLastError();
+}
+
+namespace {
+
+gdn_status scan_desc_ok(const gdn_scan_desc *p) {
+    if (!p || p->B < 0 || p->T < 0 || p->D < 1 || p->N < 1) return GDN_ERR_INVALID_ARG;
+    if (p->dtype != GDN_BF16 && p->dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (p->N > 64 || p->B > 65535) return GDN_ERR_UNSUPPORTED;
+    if (p->cu_seqlens && (p->B != 1 || p->n_seqs < 1)) return GDN_ERR_INVALID_ARG;
+    if (p->B > 0 && (!p->A || (p->T > 0 && (!p->x || !p->dt || !p->B_ || !p->C_)))) return GDN_ERR_INVALID_ARG;
+    const int64_t chan[] = {p->x_token_stride, p->dt_token_stride, p->z ? p->z_token_stride : p->D};
+    for (int64_t st : chan)
+        if (st < p->D) return GDN_ERR_INVALID_ARG;
+    if (p->b_token_stride < p->N || p->c_token_stride < p->N) return GDN_ERR_INVALID_ARG;
+    const int64_t batch[] = {p->x_batch_stride, p->dt_batch_stride, p->z_batch_stride, p->b_batch_stride,
+                             p->c_batch_stride};
+    for (int64_t st : batch)
+        if (st < 0) return GDN_ERR_INVALID_ARG;
+    const uintptr_t em = p->dtype == GDN_F32 ? 3 : 1;
+    const void *elems[] = {p->x, p->dt, p->z, p->B_, p->C_};
+    for (const void *q : elems)
+        if (reinterpret_cast<uintptr_t>(q) & em) return GDN_ERR_INVALID_ARG;
+    const void *f32[] = {p->A, p->D_skip, p->dt_bias, p->initial_state, p->cu_seqlens};
+    for (const void *q : f32)
+        if (reinterpret_cast<uintptr_t>(q) & 3) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+bool all_aligned(const void *const *ptrs, int n, const int64_t *strides, int m, int elems) {
+    bool ok = true;
+    for (int i = 0; i < n; ++i) ok = ok && aligned16(ptrs[i]);
+    for (int i = 0; i < m; ++i) ok = ok && strides[i] % elems == 0;
+    return ok;
+}
+
+ScanArgs scan_args(const gdn_scan_desc &p) {
+    ScanArgs a = {};
+    a.x = p.x, a.dt = p.dt, a.z = p.z, a.Bm = p.B_, a.Cm = p.C_;
+    a.A = p.A, a.skip = p.D_skip, a.bias = p.dt_bias, a.init = p.initial_state, a.cu = p.cu_seqlens;
+    a.x_batch = p.x_batch_stride, a.x_token = p.x_token_stride, a.dt_batch = p.dt_batch_stride;
+    a.dt_token = p.dt_token_stride, a.z_batch = p.z_batch_stride, a.z_token = p.z_token_stride;
+    a.b_batch = p.b_batch_stride, a.b_token = p.b_token_stride, a.c_batch = p.c_batch_stride;
+    a.c_token = p.c_token_stride;
+    a.B = p.B, a.T = p.T, a.D = p.D, a.N = p.N, a.n_seqs = p.cu_seqlens ? p.n_seqs : p.B;
+    a.softplus = p.dt_softplus != 0;
+    const int per = p.dtype == GDN_F32 ? 4 : 8;   // elements of 16 bytes
+    const void *wide[] = {p.x, p.dt, p.z};
+    const int64_t ws[] = {p.x_batch_stride, p.x_token_stride, p.dt_batch_stride, p.dt_token_stride,
+                          p.z ? p.z_batch_stride : 0, p.z ? p.z_token_stride : 0, p.D};
+    a.vec = all_aligned(wide, 3, ws, 7, per);
+    const void *bc[] = {p.B_, p.C_};
+    const int64_t bs[] = {p.b_batch_stride, p.b_token_stride, p.c_batch_stride, p.c_token_stride};
+    a.bc_vec = all_aligned(bc, 2, bs, 4, per);
+    return a;
+}
+
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// Workspace of the maps: end states (and start gradients), step sums, flags.
+size_t maps_bytes(long long maps, int D, int N, int arrays) {
+    const size_t np = 8 * (size_t)scan_parts(N);
+    return arrays * round16(maps * D * np * 4) + round16(maps * (size_t)D * 4) + round16(maps * 4);
+}
+char *place_maps(ScanArgs &a, char *p, long long maps, int arrays) {
+    const size_t np = 8 * (size_t)scan_parts(a.N);
+    a.hloc = reinterpret_cast<float *>(p), p += round16(maps * a.D * np * 4);
+    if (arrays == 2) a.gloc = reinterpret_cast<float *>(p), p += round16(maps * a.D * np * 4);
+    a.sums = reinterpret_cast<float *>(p), p += round16(maps * (size_t)a.D * 4);
+    a.flags = reinterpret_cast<int32_t *>(p), p += round16(maps * 4);
+    return p;
+}
+
+}  // namespace
+
+}  // namespace gdn
+
+extern "C" size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int N) {
+    if (B < 0 || T < 0 || D < 1 || N < 1 || N > 64) return 0;
+    const int segs = gdn::scan_segments(B, T, D, N);
+    return segs > 1 ? gdn::maps_bytes((long long)B * segs, D, N, 1) : 16;
+}
+
+extern "C" gdn_status gdn_selective_scan_fwd(const gdn_scan_desc *desc, void *y, float *final_state,
+                                             int32_t *device_status, void *workspace, size_t workspace_bytes,
+                                             gdn_stream_t stream) {
+    using namespace gdn;
+    const gdn_status st = scan_desc_ok(desc);
+    if (st != GDN_OK) return st;
+    const gdn_scan_desc &p = *desc;
+    if (p.B == 0) return GDN_OK;
+    const uintptr_t em = p.dtype == GDN_F32 ? 3 : 1;
+    if ((p.T > 0 && !y) || (reinterpret_cast<uintptr_t>(y) & em) || (reinterpret_cast<uintptr_t>(final_state) & 3))
+        return GDN_ERR_INVALID_ARG;
+    ScanArgs a = scan_args(p);
+    a.vec = a.vec && aligned16(y);
+    a.out = y, a.final_state = final_state, a.status = device_status;
+    a.segs = scan_segments(p.B, p.T, p.D, p.N);
+    a.seg_tokens = scan_segment_tokens(p.T, a.segs);
+    if (a.segs > 1) {
+        if (!workspace || !aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+        if (workspace_bytes < gdn_selective_scan_fwd_workspace_size(p.B, p.T, p.D, p.N)) return GDN_ERR_WORKSPACE;
+        place_maps(a, static_cast<char *>(workspace), (long long)p.B * a.segs, 1);
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = p.dtype == GDN_BF16 ? launch_scan_typed<__nv_bfloat16>(a, s) : launch_scan_typed<float>(a, s);
+    if (e != cudaSuccess) {
+        set_error_detail("launch selective_scan_fwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+extern "C" gdn_status gdn_selective_scan_step(const gdn_scan_desc *desc, float *state, const int32_t *state_indices,
+                                              int n_states, void *y, gdn_stream_t stream) {
+    using namespace gdn;
+    const gdn_status st = scan_desc_ok(desc);
+    if (st != GDN_OK) return st;
+    const gdn_scan_desc &p = *desc;
+    if (p.T != 1 || p.cu_seqlens || n_states < 0 || (!state_indices && n_states < p.B)) return GDN_ERR_INVALID_ARG;
+    if (p.B == 0) return GDN_OK;
+    const uintptr_t em = p.dtype == GDN_F32 ? 3 : 1;
+    if (!y || !state || (reinterpret_cast<uintptr_t>(y) & em) || (reinterpret_cast<uintptr_t>(state) & 3))
+        return GDN_ERR_INVALID_ARG;
+    ScanArgs a = scan_args(p);
+    a.out = y, a.final_state = state, a.slots = state_indices, a.pool = n_states;
+    const int vec = p.N % 4 == 0 && aligned16(state) && aligned16(p.A);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = p.dtype == GDN_BF16 ? launch_step_typed<__nv_bfloat16>(a, vec, s)
+                                              : launch_step_typed<float>(a, vec, s);
+    if (e != cudaSuccess) {
+        set_error_detail("launch selective_scan_step", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}

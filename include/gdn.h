@@ -1,6 +1,8 @@
 /*
  * gdn.h — C ABI of the GB300 (sm_103a) Gated Delta Network chunked-prefill
- * forward pass (and its backward, gdn_chunk_bwd).
+ * forward pass (and its backward, gdn_chunk_bwd), and of the layer operators
+ * around it: layer norm, the short causal convolution, the selective state
+ * space scan and the single-token delta step.
  *
  * The operation (FlashQLA talk "Qwen系列模型线性注意力高性能优化实践", the
  * recurrent-form and GDN paragraphs): for every sequence n and head h, with the
@@ -531,6 +533,147 @@ gdn_kernel gdn_get_backward_kernel(void);
 /* Synchronises `stream` and reads the error word of a gdn_chunk_bwd
  * workspace: GDN_OK, GDN_ERR_DEVICE_CHECK (bad cu_seqlens) or GDN_ERR_TIMEOUT. */
 gdn_status gdn_chunk_bwd_check(const void *workspace, gdn_stream_t stream);
+
+/*
+ * Layer operators: what a linear-attention layer computes around the
+ * recurrence.  All of them run on `stream` without synchronising, keep nothing
+ * between calls, and take buffers that the caller owns; data pointers need the
+ * alignment of their element type only (16-byte aligned rows take the faster
+ * path).  Activations are bf16 or fp32 (`dtype`), arithmetic and sums are
+ * fp32, results are rounded once.  Strides count elements; the last axis is
+ * contiguous.
+ *
+ * Operators on packed batches (cu_seqlens, int32 [n_seqs + 1] in device
+ * memory, B = 1) take `device_status`: NULL, or a device int32 into which the
+ * call writes 0, or GDN_ERR_DEVICE_CHECK for entries that do not start at 0,
+ * decrease, or do not end at T.  The outputs are then unspecified; no access
+ * leaves the given buffers.  Sequences may be empty.
+ *
+ * Single-token forms update a cached state in place.  With state_indices
+ * (int32 [N] in device memory) row r uses state state_indices[r] of the
+ * n_states there are; a row whose index is outside [0, n_states) is padding:
+ * its output is zero and no state changes.  Without it row r uses state r.
+ * Two rows of one call must not name the same state.
+ */
+
+/*
+ * Layer norm over rows of D elements:
+ *
+ *     y = (x - mean) rstd w + b,  rstd = (var + eps)^-1/2,
+ *
+ * var the mean squared deviation.  x: `rows` rows, x_stride elements apart;
+ * y: [rows, D]; weight, bias: [D] in w_dtype, either may be NULL (one, zero);
+ * mean, rstd: fp32 [rows] outputs, either may be NULL.  eps >= 0.  Any D.
+ */
+gdn_status gdn_layer_norm_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias,
+                              gdn_dtype w_dtype, float eps, int64_t rows, int D, gdn_dtype dtype, void *y,
+                              float *mean, float *rstd, gdn_stream_t stream);
+
+/*
+ * Its backward pass from the forward's mean and rstd: with xh = (x - mean) rstd
+ * and g = dy w,
+ *
+ *     dx = rstd (g - mean_d(g) - xh mean_d(g xh)),  dw = sum dy xh,  db = sum dy.
+ *
+ * dx [rows, D] in dtype; dweight, dbias fp32 [D], either may be NULL.  The
+ * workspace (16-byte aligned, gdn_layer_norm_bwd_workspace_size() bytes, no
+ * initialisation) is needed for dweight or dbias only.  The sums are added in
+ * a fixed order: the same inputs give the same bits.
+ */
+size_t gdn_layer_norm_bwd_workspace_size(int64_t rows, int D);
+gdn_status gdn_layer_norm_bwd(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const float *mean,
+                              const float *rstd, const void *weight, gdn_dtype w_dtype, int64_t rows, int D,
+                              gdn_dtype dtype, void *dx, float *dweight, float *dbias, void *workspace,
+                              size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Short causal depthwise convolution along each sequence,
+ *
+ *     u_t = bias + sum_{i < W} w_i x_{t - (W-1) + i},  y = silu ? u sigmoid(u) : u,
+ *
+ * W in {2, 3, 4}.  x: [B, T, D] with the given batch and token strides;
+ * weight: [D, W], bias: [D] or NULL, in w_dtype (fp32 or dtype); y: [B, T, D].
+ * The inputs before a sequence's first token are the rows of initial_state
+ * [n, W - 1, D] (dtype, oldest first; NULL: zero), n = B or n_seqs;
+ * final_state (same layout, or NULL) receives the last W - 1 inputs, the
+ * initial state's own rows among them where a sequence is shorter.
+ */
+gdn_status gdn_causal_conv_fwd(const void *x, int64_t x_batch_stride, int64_t x_token_stride, const void *weight,
+                               const void *bias, gdn_dtype w_dtype, const void *initial_state,
+                               const int32_t *cu_seqlens, int n_seqs, int B, int T, int D, int W, int silu,
+                               gdn_dtype dtype, void *y, void *final_state, int32_t *device_status,
+                               gdn_stream_t stream);
+
+/*
+ * Its backward pass: dx [B, T, D] (dtype), dweight [D, W] and dbias [D] (fp32,
+ * either may be NULL), d_initial_state [n, W - 1, D] (dtype, may be NULL) from
+ * dy and, where given, d_final_state (like final_state).  The workspace
+ * (16-byte aligned, gdn_causal_conv_bwd_workspace_size() bytes) is needed for
+ * dweight or dbias only.  The same inputs give the same bits.
+ */
+size_t gdn_causal_conv_bwd_workspace_size(int B, int T, int D, int W);
+gdn_status gdn_causal_conv_bwd(const void *dy, int64_t dy_batch_stride, int64_t dy_token_stride, const void *x,
+                               int64_t x_batch_stride, int64_t x_token_stride, const void *weight, const void *bias,
+                               gdn_dtype w_dtype, const void *initial_state, const void *d_final_state,
+                               const int32_t *cu_seqlens, int n_seqs, int B, int T, int D, int W, int silu,
+                               gdn_dtype dtype, void *dx, float *dweight, float *dbias, void *d_initial_state,
+                               int32_t *device_status, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * One token of N sequences: x [N, D] (rows x_stride apart), y [N, D], state
+ * [n_states, W - 1, D] updated in place (the oldest row leaves, x enters).
+ * N at most 65535.
+ */
+gdn_status gdn_causal_conv_step(const void *x, int64_t x_stride, void *state, const int32_t *state_indices,
+                                int n_states, const void *weight, const void *bias, gdn_dtype w_dtype, int N, int D,
+                                int W, int silu, gdn_dtype dtype, void *y, gdn_stream_t stream);
+
+/*
+ * Selective state space scan with a diagonal transition: per channel d < D and
+ * state index n < N of a sequence,
+ *
+ *     h_t[d][n] = exp(s_t[d] A[d][n]) h_{t-1}[d][n] + s_t[d] x_t[d] B_t[n],
+ *     y_t[d] = (sum_n C_t[n] h_t[d][n] + D_skip[d] x_t[d]) silu(z_t[d]),
+ *     s_t[d] = f(dt_t[d] + dt_bias[d]),  f softplus or the identity.
+ *
+ * x, dt, z: [B, T, D], B_, C_: [B, T, N] in dtype, shared by all channels,
+ * each with its own batch and token strides; A fp32 [D, N], D_skip and dt_bias
+ * fp32 [D]; initial_state fp32 [n, D, N], n = B or n_seqs.  z (no gate),
+ * D_skip and dt_bias (zero), initial_state (zero) and cu_seqlens may be NULL.
+ * N at most 64, B at most 65535.  s A <= 0 is expected (a state that grows
+ * overflows as the formula does).
+ */
+typedef struct {
+    const void *x, *dt, *z, *B_, *C_;
+    const float *A, *D_skip, *dt_bias, *initial_state;
+    const int32_t *cu_seqlens;
+    int64_t x_batch_stride, x_token_stride, dt_batch_stride, dt_token_stride, z_batch_stride, z_token_stride;
+    int64_t b_batch_stride, b_token_stride, c_batch_stride, c_token_stride;
+    int32_t B, T, D, N, n_seqs, dt_softplus, dtype, reserved;
+} gdn_scan_desc;
+
+/* y [B, T, D] in dtype; final_state fp32 [n, D, N] or NULL.  The workspace is
+ * 16-byte aligned and holds gdn_selective_scan_fwd_workspace_size() bytes. */
+size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int N);
+gdn_status gdn_selective_scan_fwd(const gdn_scan_desc *desc, void *y, float *final_state, int32_t *device_status,
+                                  void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* One token of B sequences (desc->T = 1, initial_state and cu_seqlens unused):
+ * y [B, D]; state fp32 [n_states, D, N] updated in place. */
+gdn_status gdn_selective_scan_step(const gdn_scan_desc *desc, float *state, const int32_t *state_indices,
+                                   int n_states, void *y, gdn_stream_t stream);
+
+/*
+ * One token of the gated delta rule (gdn_chunk_fwd's recurrence) for N
+ * sequences: q, k [N, H, dk], v, o [N, H, dv] in dtype, g, beta fp32 [N, H],
+ * state fp32 [n_states, H, dk, dv] in the layout of final_state, updated in
+ * place.  dk, dv in {32, 64, 128}; scale <= 0 selects dk^-0.5; qk_l2norm = 1
+ * scales the rows of q and k to unit L2 norm first (eps 1e-6).  All pointers
+ * but state_indices 16-byte aligned.
+ */
+gdn_status gdn_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                          float *state, const int32_t *state_indices, int n_states, float scale, int qk_l2norm,
+                          int N, int H, int dk, int dv, gdn_dtype dtype, void *o, gdn_stream_t stream);
 
 /* The CUDA error (and, for tensor-map encoding, the driver result) behind the
  * most recent GDN_ERR_CUDA returned on the calling host thread, as text such

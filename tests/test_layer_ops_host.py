@@ -1,0 +1,110 @@
+"""Host-side refusals of the layer operators (no GPU): the C entry points
+return a status before any launch, the Python functions raise for tensors that
+are not on a CUDA device."""
+import ctypes
+
+import pytest
+import torch
+
+import chunked_prefill_gdn_gb300 as gdn
+from chunked_prefill_gdn_gb300 import build as gdn_build
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    gdn_build.build()
+    return gdn.load_library()
+
+
+P = ctypes.c_void_p(4096)   # never dereferenced: the calls are refused first
+
+
+def test_layer_norm_arguments(lib):
+    f = lib.gdn_layer_norm_fwd
+    assert f(P, 8, None, None, 1, 1e-5, 4, 0, 1, P, None, None, None) == INVALID        # no columns
+    assert f(P, 7, None, None, 1, 1e-5, 4, 8, 1, P, None, None, None) == INVALID        # rows overlap
+    assert f(P, 8, None, None, 1, -1.0, 4, 8, 1, P, None, None, None) == INVALID        # eps
+    assert f(P, 8, None, None, 1, float("nan"), 4, 8, 1, P, None, None, None) == INVALID
+    assert f(P, 8, None, None, 1, 1e-5, 4, 8, 7, P, None, None, None) == INVALID        # type
+    assert f(None, 8, None, None, 1, 1e-5, 4, 8, 1, P, None, None, None) == INVALID
+    assert f(ctypes.c_void_p(4098), 8, None, None, 1, 1e-5, 4, 8, 1, P, None, None, None) == INVALID   # fp32 at 2 bytes
+    assert f(None, 8, None, None, 1, 1e-5, 0, 8, 1, None, None, None, None) == 0        # no rows
+    b = lib.gdn_layer_norm_bwd
+    size = lib.gdn_layer_norm_bwd_workspace_size(4, 8)
+    assert size >= 64 and lib.gdn_layer_norm_bwd_workspace_size(4, 0) == 0
+    assert b(P, 8, P, 8, P, P, None, 1, 4, 8, 1, P, P, P, P, size - 1, None) == WORKSPACE
+    assert b(P, 8, P, 8, P, P, None, 1, 4, 8, 1, P, P, P, None, 0, None) == INVALID
+    assert b(P, 8, P, 8, None, P, None, 1, 4, 8, 1, P, P, P, P, size, None) == INVALID
+
+
+def test_causal_conv_arguments(lib):
+    f = lib.gdn_causal_conv_fwd
+
+    def fwd(x=P, sb=64, st=8, w=P, wd=1, cu=None, n=0, B=1, T=8, D=8, W=4, dt=1, y=P):
+        return f(x, sb, st, w, None, wd, None, cu, n, B, T, D, W, 1, dt, y, None, None, None)
+
+    assert fwd(W=1) == UNSUPPORTED and fwd(W=5) == UNSUPPORTED
+    assert fwd(st=7) == INVALID and fwd(D=0) == INVALID and fwd(T=-1) == INVALID and fwd(w=None) == INVALID
+    assert fwd(x=None) == INVALID and fwd(y=None) == INVALID and fwd(dt=2) == INVALID
+    assert fwd(cu=P, n=0) == INVALID and fwd(cu=P, n=2, B=2) == INVALID
+    assert fwd(wd=0) == INVALID                      # bf16 weights with fp32 activations
+    assert fwd(B=0) == 0
+    size = lib.gdn_causal_conv_bwd_workspace_size(1, 8, 8, 4)
+    assert size > 0 and lib.gdn_causal_conv_bwd_workspace_size(1, 8, 8, 5) == 0
+    assert lib.gdn_causal_conv_bwd(P, 64, 8, P, 64, 8, P, None, 1, None, None, None, 0, 1, 8, 8, 4, 1, 1, P, P, P, None,
+                                   None, P, size - 1, None) == WORKSPACE
+    s = lib.gdn_causal_conv_step
+    assert s(P, 8, P, None, 3, P, None, 1, 4, 8, 4, 1, 1, P, None) == INVALID     # four rows, three states
+    assert s(P, 8, None, None, 4, P, None, 1, 4, 8, 4, 1, 1, P, None) == INVALID
+    assert s(P, 8, P, None, 0, P, None, 1, 0, 8, 4, 1, 1, P, None) == 0
+
+
+def scan_desc(**kw):
+    d = gdn.GdnScanDesc(4096, 4096, None, 4096, 4096, 4096, None, None, None, None, 64, 8, 64, 8, 0, 8, 128, 16, 128, 16,
+                        1, 8, 8, 16, 1, 1, 1, 0)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def test_selective_scan_arguments(lib):
+    f = lambda **kw: lib.gdn_selective_scan_fwd(scan_desc(**kw), P, None, None, None, 0, None)   # noqa: E731
+    assert f(N=65) == UNSUPPORTED and f(N=0) == INVALID and f(D=0) == INVALID
+    assert f(x=None) == INVALID and f(A=None) == INVALID and f(dtype=3) == INVALID
+    assert f(x_token_stride=7) == INVALID and f(b_token_stride=15) == INVALID and f(x_batch_stride=-1) == INVALID
+    assert f(cu_seqlens=4096, n_seqs=0) == INVALID and f(cu_seqlens=4096, n_seqs=2, B=2) == INVALID
+    assert f(B=0) == 0
+    assert lib.gdn_selective_scan_fwd(None, P, None, None, None, 0, None) == INVALID
+    size = lib.gdn_selective_scan_fwd_workspace_size(1, 4096, 8, 16)
+    assert size > 16
+    assert lib.gdn_selective_scan_fwd(scan_desc(T=4096), P, None, None, P, size - 1, None) == WORKSPACE
+    s = lib.gdn_selective_scan_step
+    assert s(scan_desc(T=2), P, None, 1, P, None) == INVALID
+    assert s(scan_desc(T=1), P, None, 0, P, None) == INVALID
+
+
+def test_delta_step_arguments(lib):
+    def f(q=P, n=2, N=2, H=2, dk=32, dv=32, dt=1):
+        return lib.gdn_delta_step(q, P, P, P, P, P, None, n, 0.0, 0, N, H, dk, dv, dt, P, None)
+
+    assert f(dk=48) == UNSUPPORTED and f(dv=256) == UNSUPPORTED
+    assert f(q=None) == INVALID and f(n=1) == INVALID and f(H=0) == INVALID and f(dt=9) == INVALID
+    assert f(q=ctypes.c_void_p(4100)) == INVALID
+    assert f(N=0, n=0) == 0
+
+
+def test_python_functions_refuse_host_tensors(lib):
+    x = torch.zeros(1, 4, 8)
+    w = torch.zeros(8, 4)
+    with pytest.raises(ValueError):
+        gdn.layer_norm_fwd(x)
+    with pytest.raises(ValueError):
+        gdn.causal_conv_fwd(x, w)
+    with pytest.raises(ValueError):
+        gdn.causal_conv_step(x[0], torch.zeros(4, 3, 8), w)
+    with pytest.raises(ValueError):
+        gdn.selective_scan_fwd(x, x, w, x, x)
+    with pytest.raises(ValueError):
+        gdn.gated_delta_step(x, x, x, x, x, torch.zeros(1, 4, 8, 8))
