@@ -123,9 +123,11 @@ __device__ __forceinline__ void store_pairs(float *row, int n0, int N, const F2 
     }
 }
 
-cudaError_t launch_scan_fwd(ScanArgs a, int dtype, cudaStream_t s);
-cudaError_t launch_scan_bwd(ScanArgs a, int dtype, void *dB, void *dC, float *dA, float *dskip, float *dbias,
+// The backward pass with its maps, partial sums and outputs placed in `a`;
+// channels per block of its main kernel.
+cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, void *dB, void *dC, float *dA, float *dskip, float *dbias,
                             cudaStream_t s);
+int scan_bwd_channels(int N);
 cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s);
 
 // Threads over n of the scanning kernels: eight n each.

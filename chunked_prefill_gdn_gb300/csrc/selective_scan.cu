@@ -513,3 +513,82 @@ extern "C" gdn_status gdn_selective_scan_step(const gdn_scan_desc *desc, float *
     }
     return GDN_OK;
 }
+
+namespace gdn {
+namespace {
+
+// How the backward pass cuts a problem: tiles per row, segments of tiles that
+// one block walks, blocks of channels.
+struct BwdPlan {
+    int row_tiles, segs, seg_tokens, chan_blocks;
+    size_t maps, part_a, part_v, part_bc;
+};
+BwdPlan bwd_plan(int B, int T, int D, int N) {
+    BwdPlan p;
+    const size_t np = 8 * (size_t)scan_parts(N);
+    const int ch = scan_bwd_channels(N);
+    p.row_tiles = (T + kTile - 1) / kTile;
+    p.chan_blocks = (D + ch - 1) / ch;
+    // one tile per block until there are many more blocks than the SMs hold (two
+    // each); then longer walks, with fewer partial sums of dA
+    const long long blocks = (long long)B * std::max(1, p.row_tiles) * p.chan_blocks;
+    const int per = (int)std::max<long long>(1, std::min<long long>(blocks / (16ll * device_sm_count()), 64));
+    p.segs = std::max(1, (p.row_tiles + per - 1) / per);
+    p.seg_tokens = per * kTile;
+    p.maps = maps_bytes((long long)B * p.row_tiles, D, N, 2);
+    p.part_a = round16((size_t)B * p.segs * D * np * 4);
+    p.part_v = round16((size_t)B * p.segs * 2 * D * 4);
+    p.part_bc = round16((size_t)p.chan_blocks * B * T * 2 * np * 4);
+    return p;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int N) {
+    if (B < 0 || T < 0 || D < 1 || N < 1 || N > 64) return 0;
+    const gdn::BwdPlan p = gdn::bwd_plan(B, T, D, N);
+    return std::max<size_t>(16, p.maps + p.part_a + p.part_v + p.part_bc);
+}
+
+extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_desc *desc, const void *dy, int64_t dy_batch_stride,
+                                             int64_t dy_token_stride, const float *d_final_state, void *dx, void *ddt,
+                                             float *dA, void *dB, void *dC, float *dD_skip, void *dz,
+                                             float *ddt_bias, float *d_initial_state, int32_t *device_status,
+                                             void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    using namespace gdn;
+    const gdn_status st = scan_desc_ok(desc);
+    if (st != GDN_OK) return st;
+    const gdn_scan_desc &p = *desc;
+    if (p.B == 0) return GDN_OK;
+    if (dy_token_stride < p.D || dy_batch_stride < 0 || !dA) return GDN_ERR_INVALID_ARG;
+    if (p.T > 0 && (!dy || !dx || !ddt || !dB || !dC || (p.z && !dz))) return GDN_ERR_INVALID_ARG;
+    const uintptr_t em = p.dtype == GDN_F32 ? 3 : 1;
+    const void *elems[] = {dy, dx, ddt, dB, dC, dz};
+    for (const void *q : elems)
+        if (reinterpret_cast<uintptr_t>(q) & em) return GDN_ERR_INVALID_ARG;
+    const void *f32[] = {d_final_state, dA, dD_skip, ddt_bias, d_initial_state, device_status};
+    for (const void *q : f32)
+        if (reinterpret_cast<uintptr_t>(q) & 3) return GDN_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+    if (workspace_bytes < gdn_selective_scan_bwd_workspace_size(p.B, p.T, p.D, p.N)) return GDN_ERR_WORKSPACE;
+    ScanArgs a = scan_args(p);
+    const int per = p.dtype == GDN_F32 ? 4 : 8;
+    const void *wide[] = {dy, dx, ddt, dz};
+    const int64_t ws[] = {dy_batch_stride, dy_token_stride};
+    a.vec = a.vec && all_aligned(wide, 4, ws, 2, per);
+    a.dy = dy, a.dy_batch = dy_batch_stride, a.dy_token = dy_token_stride, a.d_final = d_final_state;
+    a.out = dx, a.ddt = ddt, a.dz = dz, a.dinit = d_initial_state, a.status = device_status;
+    const BwdPlan plan = bwd_plan(p.B, p.T, p.D, p.N);
+    a.row_tiles = plan.row_tiles, a.segs = plan.segs, a.seg_tokens = plan.seg_tokens, a.chan_blocks = plan.chan_blocks;
+    char *at = place_maps(a, static_cast<char *>(workspace), (long long)p.B * plan.row_tiles, 2);
+    a.part_a = reinterpret_cast<float *>(at), at += plan.part_a;
+    a.part_v = reinterpret_cast<float *>(at), at += plan.part_v;
+    a.part_bc = reinterpret_cast<float *>(at);
+    const cudaError_t e = launch_scan_bwd(a, p.dtype, dB, dC, dA, dD_skip, ddt_bias, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        set_error_detail("launch selective_scan_bwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}

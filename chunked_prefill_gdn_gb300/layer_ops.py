@@ -28,7 +28,7 @@ from typing import Optional
 import torch
 
 __all__ = ["layer_norm_fwd", "layer_norm_bwd", "layer_norm", "causal_conv_fwd", "causal_conv_bwd", "causal_conv_step",
-           "causal_conv", "selective_scan_fwd", "selective_scan_step",
+           "causal_conv", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step", "selective_scan",
            "gated_delta_step", "GdnScanDesc"]
 
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
@@ -61,6 +61,8 @@ def bind(lib):
             ("gdn_causal_conv_step", i32, [vp, i64, vp, vp, i32, vp, vp] + [i32] * 6 + [vp, vp]),
             ("gdn_selective_scan_fwd_workspace_size", sz, [i32] * 4),
             ("gdn_selective_scan_fwd", i32, [desc, vp, vp, vp, vp, sz, vp]),
+            ("gdn_selective_scan_bwd_workspace_size", sz, [i32] * 4),
+            ("gdn_selective_scan_bwd", i32, [desc, vp, i64, i64] + [vp] * 12 + [sz, vp]),
             ("gdn_selective_scan_step", i32, [desc, vp, vp, i32, vp, vp]),
             ("gdn_delta_step", i32, [vp] * 7 + [i32, f32] + [i32] * 6 + [vp, vp])):
         fn = getattr(lib, name)
@@ -488,6 +490,40 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     return y, final
 
 
+def selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
+                       initial_state=None, cu_seqlens=None, d_final_state=None, workspace=None,
+                       stream: Optional[torch.cuda.Stream] = None, check: bool = False):
+    """Gradients of selective_scan_fwd from dy and, where the final state is
+    used, d_final_state: (dx, ddt, dA, dB, dC, dD, dz, d_dt_bias,
+    d_initial_state); dz is None without z.  dA, dD, d_dt_bias and the state's
+    gradient are float32, the others in x's type."""
+    desc, n = _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
+    dev, dtype = x.device, x.dtype
+    _like("dy", dy, x.shape, dtype, dev, strided=True)
+    if d_final_state is not None:
+        _like("d_final_state", d_final_state, (n, desc.D, desc.N), _F32, dev)
+    gb, gt = _strides("dy", dy)
+    lib = _lib()
+    on = _On(dev, stream)
+    try:
+        dx, ddt = on.empty(x.shape, dtype), on.empty(x.shape, dtype)
+        dz = on.empty(x.shape, dtype) if z is not None else None
+        dB, dC = on.empty(B.shape, dtype), on.empty(C.shape, dtype)
+        dA, dv, ds = on.empty(A.shape, _F32), on.empty((2, desc.D), _F32), on.empty((n, desc.D, desc.N), _F32)
+        ws = _workspace(on, workspace, lib.gdn_selective_scan_bwd_workspace_size(desc.B, desc.T, desc.D, desc.N))
+        word = _status_word(on, check, cu_seqlens)
+        p = dv.data_ptr()
+        rc = lib.gdn_selective_scan_bwd(desc, dy.data_ptr(), gb, gt, _p(d_final_state), dx.data_ptr(), ddt.data_ptr(),
+                                        dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), p, _p(dz), p + 4 * desc.D,
+                                        ds.data_ptr(), _p(word), ws.data_ptr(), ws.numel(), on.raw)
+        if rc != 0:
+            _raise(rc, "gdn_selective_scan_bwd")
+        _read_status(word, on, "gdn_selective_scan_bwd")
+    finally:
+        on.done()
+    return dx, ddt, dA, dB, dC, dv[0], dz, dv[1], ds
+
+
 def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
                         state_indices=None, out=None, stream: Optional[torch.cuda.Stream] = None):
     """One token of Bt sequences through the scan: x, dt, z [Bt, D], B, C
@@ -512,6 +548,34 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     finally:
         on.done()
     return y
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens):
+        y, final = selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
+        ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens)
+        ctx.dt_softplus = dt_softplus
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    def backward(ctx, dy, d_final):
+        x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
+        dx, ddt, dA, dB, dC, dD, dz, db, ds = selective_scan_bwd(
+            dy, x, dt, A, B, C, D, z, dt_bias, ctx.dt_softplus, initial_state, cu_seqlens,
+            d_final.contiguous() if d_final is not None else None)
+        return (dx, ddt, dA, dB, dC, dD if D is not None else None, dz, db if dt_bias is not None else None, None,
+                ds if initial_state is not None else None, None)
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True, initial_state=None,
+                   output_final_state: bool = False, cu_seqlens=None):
+    """selective_scan_fwd with autograd (every tensor but cu_seqlens); returns
+    (y, final_state or None)."""
+    y, final = _SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
+    return y, (final if output_final_state else None)
 
 
 # -------------------------------------------------- one token of the delta rule

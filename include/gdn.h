@@ -658,6 +658,21 @@ size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int N);
 gdn_status gdn_selective_scan_fwd(const gdn_scan_desc *desc, void *y, float *final_state, int32_t *device_status,
                                   void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * Its backward pass, from dy [B, T, D] (dtype, with its strides) and
+ * d_final_state (fp32 [n, D, N], or NULL): dx, ddt, dz [B, T, D] and dB, dC
+ * [B, T, N] in dtype, contiguous (dz NULL without a gate); dA fp32 [D, N];
+ * dD_skip, ddt_bias fp32 [D] and d_initial_state fp32 [n, D, N], each may be
+ * NULL.  ddt is the gradient of dt before bias and softplus.  The states are
+ * recomputed.  Workspace as above.  The same inputs give the same bits.
+ */
+size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int N);
+gdn_status gdn_selective_scan_bwd(const gdn_scan_desc *desc, const void *dy, int64_t dy_batch_stride,
+                                  int64_t dy_token_stride, const float *d_final_state, void *dx, void *ddt, float *dA,
+                                  void *dB, void *dC, float *dD_skip, void *dz, float *ddt_bias,
+                                  float *d_initial_state, int32_t *device_status, void *workspace,
+                                  size_t workspace_bytes, gdn_stream_t stream);
+
 /* One token of B sequences (desc->T = 1, initial_state and cu_seqlens unused):
  * y [B, D]; state fp32 [n_states, D, N] updated in place. */
 gdn_status gdn_selective_scan_step(const gdn_scan_desc *desc, float *state, const int32_t *state_indices,

@@ -312,6 +312,77 @@ def test_selective_scan(case, gate, dtype, layout):
     close("state", last, last0, lm, 8 * (T + 8))
 
 
+GRADS = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dbias", "dstate")
+
+
+def check_scan_grads(c, got, dtype, T, gate=True, softplus=True, with_final=True):
+    want = ref.selective_scan_backward(num(c["dy"]), **scan_ref(c, use_softplus=softplus), z=num(c["z"]) if gate else None,
+                                       d_last=num(c["dl"]) if with_final else None)
+    g = np.abs(num(c["dy"])) * (np.abs(silu(num(c["z"]))) if gate else 1.0)
+    mags = list(ref.selective_scan_backward(g, **scan_ref(c, np.abs, use_softplus=softplus), magnitude=True,
+                                            d_last=np.abs(num(c["dl"])) if with_final else None))
+    ym, _ = ref.selective_scan(**scan_ref(c, np.abs, use_softplus=softplus))
+    mags[6] = 1.1 * np.abs(num(c["dy"])) * ym
+    types = (dtype, dtype, "f32", dtype, dtype, "f32", dtype, "f32", "f32")
+    for name, x, w, m, t in zip(GRADS, got, want, mags, types):
+        if name == "dz" and not gate:
+            assert x is None
+            continue
+        close(name, x, w, m, 8 * (3 * T + 32), t)
+
+
+@pytest.mark.parametrize("dtype,layout", [("bf16", lambda t: t), ("bf16", wide), ("f32", odd), ("f32", lambda t: t)])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("case", SCAN)
+def test_selective_scan_backward(case, gate, dtype, layout):
+    c = scan_case(*case, dtype)
+    for k in ("x", "dt", "z", "B", "C", "dy"):
+        c[k] = layout(c[k])
+    got = gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c, gate=gate),
+                                 d_final_state=c["dl"], check=True)
+    check_scan_grads(c, got, dtype, case[1], gate)
+
+
+def test_selective_scan_backward_over_many_blocks():
+    """More channels than a block of any kernel holds and longer than a segment,
+    twice with the same bits; plain steps without a bias."""
+    c = scan_case(1, 150, 300, 16, [0, 40, 150], "f32")
+    c["bias"] = torch.zeros_like(c["bias"])
+    c["dt"] = 0.3 * c["dt"].abs()
+    run = lambda: gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c, softplus=False),   # noqa: E731
+                                         d_final_state=c["dl"])
+    got, again = run(), run()
+    check_scan_grads(c, got, "f32", 150, softplus=False)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_selective_scan_autograd():
+    c = scan_case(1, 70, 40, 16, [0, 3, 70], "f32")
+    names = ("x", "dt", "A", "B", "C", "D", "z", "bias")
+    leaves = [c[k].clone().requires_grad_() for k in names] + [c["s"].clone().requires_grad_()]
+    y, last = gdn.selective_scan(*leaves[:8], True, leaves[8], True, c["cu"])
+    ((y * c["dy"]).sum() + (last * c["dl"]).sum()).backward()
+    want = gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c), d_final_state=c["dl"])
+    for leaf, g in zip(leaves, want):
+        assert torch.equal(leaf.grad, g)
+    # without options, through y alone
+    leaves = [c[k].clone().requires_grad_() for k in ("x", "dt", "A", "B", "C")]
+    y, last = gdn.selective_scan(*leaves)
+    assert last is None
+    (y * c["dy"]).sum().backward()
+    want = gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"])
+    for leaf, g in zip(leaves, want):
+        assert torch.equal(leaf.grad, g)
+
+
+def test_selective_scan_backward_of_no_tokens():
+    c = scan_case(2, 40, 8, 16, None, "f32")
+    e = lambda t: t[:, :0]   # noqa: E731
+    got = gdn.selective_scan_bwd(e(c["dy"]), e(c["x"]), e(c["dt"]), c["A"], e(c["B"]), e(c["C"]), D=c["D"],
+                                 initial_state=c["s"], d_final_state=c["dl"])
+    assert torch.equal(got[8], c["dl"]) and not got[2].any() and not got[5].any() and not got[7].any()
+
+
 def test_selective_scan_plain_steps_and_no_options():
     """dt used as it is (positive and zero steps, no bias), no skip, no gate, no state."""
     c = scan_case(2, 70, 12, 16, None, "f32")
@@ -550,4 +621,7 @@ def test_bad_cu_seqlens_is_reported(cu):
     B, A = normal(g, 1, 6, 8), -normal(g, 32, 8).abs()
     with pytest.raises(gdn.GdnError) as e:
         gdn.selective_scan_fwd(x, x, A, B, B, initial_state=normal(g, n, 32, 8), cu_seqlens=cu, check=True)
+    assert e.value.status == 5
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.selective_scan_bwd(x, x, x, A, B, B, initial_state=normal(g, n, 32, 8), cu_seqlens=cu, check=True)
     assert e.value.status == 5

@@ -80,6 +80,12 @@ def test_selective_scan_arguments(lib):
     size = lib.gdn_selective_scan_fwd_workspace_size(1, 4096, 8, 16)
     assert size > 16
     assert lib.gdn_selective_scan_fwd(scan_desc(T=4096), P, None, None, P, size - 1, None) == WORKSPACE
+    size = lib.gdn_selective_scan_bwd_workspace_size(1, 64, 8, 16)
+    assert size > 16 and lib.gdn_selective_scan_bwd_workspace_size(1, 64, 8, 65) == 0
+    b = lambda dy=P, st=8, ws=P, size=size, dA=P, **kw: lib.gdn_selective_scan_bwd(   # noqa: E731
+        scan_desc(T=64, **kw), dy, 512, st, None, P, P, dA, P, P, None, None, None, None, None, ws, size, None)
+    assert b(size=size - 1) == WORKSPACE and b(ws=None) == INVALID and b(dy=None) == INVALID and b(dA=None) == INVALID
+    assert b(st=7) == INVALID and b(z=4096) == INVALID and b(N=65) == UNSUPPORTED     # a gate without dz
     s = lib.gdn_selective_scan_step
     assert s(scan_desc(T=2), P, None, 1, P, None) == INVALID
     assert s(scan_desc(T=1), P, None, 0, P, None) == INVALID
