@@ -130,6 +130,27 @@ __device__ __forceinline__ void store_some(T *p, const float *x, int n) {
         if (i < n) p[i] = from_f32<T>(x[i]);
 }
 
+// Eight neighbouring elements of which `live` exist, on their way into shared
+// memory: asynchronously where the address allows, else (and for what does not
+// exist, which is zero) by plain stores.  The thread that copies is the one that
+// reads, after copy_commit and copy_wait.
+template <typename T>
+__device__ __forceinline__ void copy8_async(T *dst, const T *src, int live, bool vec) {
+    if (vec && live >= 8) {
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(dst);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * i), "l"(src + i * 16 / (int)sizeof(T)) : "memory");
+    } else {
+        store_raw<T, 8>(dst, live > 0 ? load_some<T, 8>(src, live) : zero_raw<T, 8>());
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+}
+
 // sigmoid(x); x * sigmoid(x) is SiLU.  exp(-x) overflows to +inf below -88,
 // where the quotient is the right zero.
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }

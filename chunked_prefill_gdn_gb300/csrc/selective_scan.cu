@@ -12,12 +12,9 @@
 // channel).  ex2 runs at 32 lanes per clock and SM, FP32 FMA at 128 (measured
 // on a GB300), so both pipes are full at the same rate, 32 (token, channel, n)
 // per clock and SM; the arithmetic is written on pairs (two-wide FP32), which
-// leaves issue slots for the rest.  A thread keeps eight n of one channel in
-// registers, LP threads share a channel.  B and C of a tile of tokens are read
-// from shared memory by every channel of the block, and what is per (token,
-// channel) only (softplus, the gate) is computed once, by the threads that load
-// the tile, not by the LP threads that scan it.  The next tile is loaded into
-// registers during the scan of the current one.
+// leaves issue slots for the rest.  A thread keeps 16 n of one channel in
+// registers (N above 16: LP threads share a channel); B and C of a tile of
+// tokens are read from shared memory by all lanes at once.
 //
 // When the (sequence, channel) pairs do not fill the GPU, the token axis is cut
 // into segments: a first pass gives every segment's end state from a zero
@@ -32,24 +29,39 @@ namespace gdn {
 
 namespace {
 
-constexpr int kScanThreads = 64;
+// One warp per block and 32 / LP channels per warp; NPL values of n per thread.
+// Inputs are staged tile by tile: asynchronous copies of the raw rows, two tiles
+// in flight, each piece read back by the lane that copied it.
+constexpr int kScanTile = 16;   // tokens per staged tile
 
-// STATE_ONLY: the end state from a zero start and the sum of the steps of every
-// segment; else the full pass.
-template <typename T, int LP, bool STATE_ONLY>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
-    constexpr int CH = kScanThreads / LP;          // channels of the block
-    constexpr int NP = 8 * LP;                     // n, padded
-    constexpr int VPR = CH / 8;                    // loads of eight channels per row
-    constexpr int RPP = kScanThreads / VPR;        // rows per pass of the loading threads
-    constexpr int PASSES = RPP >= kTile ? 1 : kTile / RPP;
-    __shared__ __align__(16) float2 sd[kTile][CH]; // step, step * x
-    __shared__ __align__(16) float bc[kTile][2][NP];
-    __shared__ __align__(16) float ys[STATE_ONLY ? 1 : kTile][CH];
+template <typename T, int NPL, int LP, bool STATE_ONLY>
+struct ScanShape {
+    static constexpr int CW = 32 / LP;             // channels of the warp
+    static constexpr int NP = NPL * LP;            // n, padded
+    static constexpr int VPR = CW / 8;             // vectors of eight channels per row
+    static constexpr int RPP = 32 / VPR;           // rows per pass of the copying lanes
+    static constexpr int PASSES = kScanTile / RPP > 0 ? kScanTile / RPP : 1;
+    static constexpr int BCV = kScanTile * 2 * (NP / 8) / 32 > 0 ? kScanTile * 2 * (NP / 8) / 32 : 1;   // vectors of B, C per lane
+    static constexpr int ARRAYS = STATE_ONLY ? 2 : 3;
+    // rows of 16-byte entries per channel, shifted by half a bank row so that two
+    // rows written together do not meet in a bank
+    static constexpr int SD = CW * 4 + 16;
+    static constexpr int YS = CW + 4;
+};
+
+template <typename T, int NPL, int LP, bool STATE_ONLY>
+__global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
+    using S = ScanShape<T, NPL, LP, STATE_ONLY>;
+    constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPL / 2;
+    __shared__ __align__(16) T rows[2][S::ARRAYS][PASSES][32][8];   // raw x, dt, z: one vector per lane and pass
+    __shared__ __align__(16) T bcr[2][S::BCV][32][8];
+    __shared__ __align__(16) float sd[kScanTile][S::SD];            // step, step, step * x, step * x
+    __shared__ __align__(16) float bc[kScanTile][2][NP];
+    __shared__ __align__(16) float ys[STATE_ONLY ? 1 : kScanTile][S::YS];
 
     if (!STATE_ONLY && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
-    const int tid = threadIdx.x;
-    const int chan0 = (blockIdx.x % a.chan_blocks) * CH;
+    const int lane = threadIdx.x;
+    const int chan0 = (blockIdx.x % a.chan_blocks) * CW;
     // the last segment of a row needs no map
     const int spr = STATE_ONLY ? a.segs - 1 : a.segs;
     Span r;
@@ -58,12 +70,16 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
     r.t0 = (seg - r.b * a.segs) * a.seg_tokens;
     r.t1 = min(a.T, r.t0 + a.seg_tokens);
 
-    const int part = tid % LP, n0 = part * 8, chl = tid / LP, ch = chan0 + chl;
+    // copying: lane -> (row of the pass, eight channels).  Scanning: the channels
+    // in the order in which the copying lanes lay them down, so that neither side
+    // meets in a bank.
+    const int lv = lane % VPR, lrow = lane / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
+    const int part = lane % LP, n0 = part * NPL, pos = lane / LP, ch = chan0 + pos % VPR * 8 + pos / VPR;
     const bool live = ch < a.D;
     if (!STATE_ONLY && a.final_state && live) {    // a sequence without a token keeps its state
         auto keep = [&](int n) {
             const long long at = ((long long)n * a.D + ch) * a.N;
-            F2 v[4];
+            F2 v[M];
             load_pairs(a.init ? a.init + at : nullptr, n0, a.N, true, v);
             store_pairs(a.final_state + at, n0, a.N, v);
         };
@@ -73,10 +89,34 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
     }
     if (r.t0 >= r.t1) return;
 
-    F2 A2[4], h[4];
+    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + lc;
+    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + lc;
+    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + lc;
+    const bool gated = !STATE_ONLY && a.z != nullptr;
+    auto stage = [&](int t, int buf) {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int q = t + i * RPP + lrow;
+            const int n = i * RPP + lrow < kScanTile && q < r.t1 ? lrest : 0;
+            copy8_async<T>(rows[buf][0][i][lane], px + q * a.x_token, n, a.vec);
+            copy8_async<T>(rows[buf][1][i][lane], pd + q * a.dt_token, n, a.vec);
+            if (!STATE_ONLY) copy8_async<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + q * a.z_token, gated ? n : 0, a.vec);
+        }
+#pragma unroll
+        for (int i = 0; i < S::BCV; ++i) {
+            const int j = i * 32 + lane, v = j % (NP / 8), c = j / (NP / 8) % 2, q = t + j / (NP / 4);
+            const T *src = c ? static_cast<const T *>(a.Cm) + r.b * a.c_batch + q * a.c_token
+                             : static_cast<const T *>(a.Bm) + r.b * a.b_batch + q * a.b_token;
+            copy8_async<T>(bcr[buf][i][lane], src + v * 8, j / (NP / 4) < kScanTile && q < r.t1 ? a.N - v * 8 : 0, a.bc_vec);
+        }
+        copy_commit();
+    };
+    stage(r.t0, 0);
+
+    F2 A2[M], h[M];
     load_pairs(a.A + (long long)ch * a.N, n0, a.N, live, A2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = mul2(A2[i], pair(kLog2e, kLog2e));
+    for (int i = 0; i < M; ++i) A2[i] = mul2(A2[i], both(kLog2e));
     span_find(a, r);
     const bool starts = r.begin == r.t0;
     bool inside = false;
@@ -86,98 +126,67 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
     if (starts) initial(r.n);
     else load_pairs(!STATE_ONLY && a.has_carry ? a.hloc + ((long long)seg * a.D + ch) * NP : nullptr, n0, NP, live, h);
     float step_sum = 0.f;
+    F2 bias[4], skip[4];
+    load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
+    load_pairs(!STATE_ONLY && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
 
-    // loading: thread -> (row of the pass, eight channels)
-    const int lv = tid % VPR, lrow = tid / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
-    const bool loads = lrow < kTile;
-    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + lc;
-    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + lc;
-    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + lc;
-    const bool gated = !STATE_ONLY && a.z != nullptr;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = a.bias && i < lrest ? a.bias[lc + i] : 0.f;
-        skip[i] = !STATE_ONLY && a.skip && i < lrest ? a.skip[lc + i] : 0.f;
-    }
-    Raw<T, 8> rx[PASSES], rd[PASSES], rz[PASSES], rbc[LP];
-    auto load_tile = [&](int t) {
+    int buf = 0;
+    for (int t = r.t0; t < r.t1; t += kScanTile, buf ^= 1) {
+        stage(t + kScanTile, buf ^ 1);
+        copy_wait<1>();
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            const int q = t + i * RPP + lrow;
-            const int n = loads && q < r.t1 ? lrest : 0;
-            rx[i] = load8<T>(px + q * a.x_token, n, a.vec);
-            rd[i] = load8<T>(pd + q * a.dt_token, n, a.vec);
-            rz[i] = load8<T>(pz + q * a.z_token, gated ? n : 0, a.vec);
-        }
-#pragma unroll
-        for (int i = 0; i < LP; ++i) {             // rows of B and C, eight n each
-            const int j = i * kScanThreads + tid, v = j % LP, c = j / LP % 2, q = t + j / (2 * LP);
-            const T *src = c ? static_cast<const T *>(a.Cm) + r.b * a.c_batch + q * a.c_token
-                             : static_cast<const T *>(a.Bm) + r.b * a.b_batch + q * a.b_token;
-            rbc[i] = load8<T>(src + v * 8, q < r.t1 ? a.N - v * 8 : 0, a.bc_vec);
-        }
-    };
-    load_tile(r.t0);
-    for (int t = r.t0; t < r.t1; t += kTile) {
-        Raw<T, 8> cx[PASSES], cz[PASSES];
-        // (the threads' last reads of sd and bc lie before the barrier after the scan)
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            cx[i] = rx[i];
-            cz[i] = rz[i];
             const int q = i * RPP + lrow;
-            float x[8], d[8];
-            unpack<T, 8>(rx[i], x);
-            unpack<T, 8>(rd[i], d);
-            if (loads) {
+            if (q >= kScanTile) continue;
+            F2 x[4], d[4];
+            unpack_pairs<T>(load_raw<T, 8>(rows[buf][0][i][lane]), x);
+            unpack_pairs<T>(load_raw<T, 8>(rows[buf][1][i][lane]), d);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float p0 = d[e] + bias[e], p1 = d[e + 1] + bias[e + 1];
-                    const float s0 = a.softplus ? softplus_f32(p0) : p0, s1 = a.softplus ? softplus_f32(p1) : p1;
-                    *reinterpret_cast<float4 *>(&sd[q][lv * 8 + e]) = make_float4(s0, s0 * x[e], s1, s1 * x[e + 1]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                d[e] = add2(d[e], bias[e]);
+                const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
+                *reinterpret_cast<float4 *>(&sd[q][(2 * e * VPR + lv) * 4]) = make_float4(lo(s), lo(s), lo(sx), lo(sx));
+                *reinterpret_cast<float4 *>(&sd[q][((2 * e + 1) * VPR + lv) * 4]) = make_float4(hi(s), hi(s), hi(sx), hi(sx));
             }
         }
 #pragma unroll
-        for (int i = 0; i < LP; ++i) {
-            const int j = i * kScanThreads + tid, v = j % LP, c = j / LP % 2, q = j / (2 * LP);
-            float f[8];
-            unpack<T, 8>(rbc[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<float4 *>(&bc[q][c][v * 8 + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        for (int i = 0; i < S::BCV; ++i) {
+            const int j = i * 32 + lane, v = j % (NP / 8), c = j / (NP / 8) % 2, q = j / (NP / 4);
+            if (q >= kScanTile) continue;
+            F2 f[4];
+            unpack_pairs<T>(load_raw<T, 8>(bcr[buf][i][lane]), f);
+            *reinterpret_cast<ulonglong2 *>(&bc[q][c][v * 8]) = make_ulonglong2(f[0], f[1]);
+            *reinterpret_cast<ulonglong2 *>(&bc[q][c][v * 8 + 4]) = make_ulonglong2(f[2], f[3]);
         }
-        load_tile(t + kTile);
-        __syncthreads();
-        const int stop = min(r.t1, t + kTile);
+        __syncwarp();
+        const int stop = min(r.t1, t + kScanTile);
         for (int q = t; q < stop;) {
             const int run_end = min(stop, r.end);
 #pragma unroll 4
             for (int k = q - t; k < run_end - t; ++k) {
-                const float2 s = sd[k][chl];
-                const F2 ss = pair(s.x, s.x), sx = pair(s.y, s.y);
+                const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(&sd[k][pos * 4]);
                 const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(&bc[k][0][n0]);
                 const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(&bc[k][1][n0]);
-                F2 y = pair(0.f, 0.f);
+                F2 y0 = both(0.f), y1 = both(0.f);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < M / 2; ++i) {
                     const ulonglong2 b = Bk[i];
-                    h[2 * i] = fma2(exp2_pair(mul2(ss, A2[2 * i])), h[2 * i], mul2(sx, b.x));
-                    h[2 * i + 1] = fma2(exp2_pair(mul2(ss, A2[2 * i + 1])), h[2 * i + 1], mul2(sx, b.y));
+                    h[2 * i] = fma2(exp2_pair(mul2(s.x, A2[2 * i])), h[2 * i], mul2(s.y, b.x));
+                    h[2 * i + 1] = fma2(exp2_pair(mul2(s.x, A2[2 * i + 1])), h[2 * i + 1], mul2(s.y, b.y));
                     if (!STATE_ONLY) {
                         const ulonglong2 c = Ck[i];
-                        y = fma2(c.x, h[2 * i], y);
-                        y = fma2(c.y, h[2 * i + 1], y);
+                        y0 = i ? fma2(c.x, h[2 * i], y0) : mul2(c.x, h[0]);
+                        y1 = i ? fma2(c.y, h[2 * i + 1], y1) : mul2(c.y, h[1]);
                     }
                 }
                 if (STATE_ONLY) {
-                    step_sum += s.x;
+                    step_sum += lo(s.x);
                 } else {
-                    float v = lo(y) + hi(y);
+                    y0 = add2(y0, y1);
+                    float v = lo(y0) + hi(y0);
 #pragma unroll
                     for (int off = 1; off < LP; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                    if (part == 0) ys[k][chl] = v;
+                    if (LP == 1 || part == 0) ys[k][pos] = v;
                 }
             }
             q = run_end;
@@ -191,27 +200,26 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
                 }
             }
         }
-        __syncthreads();
+        __syncwarp();
         if (!STATE_ONLY) {
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int q = i * RPP + lrow;
-                if (!loads || t + q >= r.t1) continue;
-                float x[8], z[8], o[8];
-                unpack<T, 8>(cx[i], x);
-                unpack<T, 8>(cz[i], z);
+                if (q >= kScanTile || t + q >= r.t1) continue;
+                F2 x[4], z[4];
+                float o[8];
+                unpack_pairs<T>(load_raw<T, 8>(rows[buf][0][i][lane]), x);
+                unpack_pairs<T>(load_raw<T, 8>(rows[buf][S::ARRAYS - 1][i][lane]), z);
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&ys[q][lv * 8 + e]);
-                    o[e] = v.x, o[e + 1] = v.y, o[e + 2] = v.z, o[e + 3] = v.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o[e] = fmaf(skip[e], x[e], o[e]);
-                    if (gated) o[e] *= z[e] * sigmoid_f32(z[e]);
+                for (int e = 0; e < 4; ++e) {
+                    F2 y = pair(ys[q][2 * e * VPR + lv], ys[q][(2 * e + 1) * VPR + lv]);
+                    y = fma2(skip[e], x[e], y);
+                    if (gated) y = mul2(y, mul2(z[e], sigmoid_pair(z[e])));
+                    o[2 * e] = lo(y), o[2 * e + 1] = hi(y);
                 }
                 store8<T>(static_cast<T *>(a.out) + ((long long)r.b * a.T + t + q) * a.D + lc, o, lrest, a.vec);
             }
+            __syncwarp();   // ys is written again by the next tile
         }
     }
     if (STATE_ONLY) {
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(ScanArgs a) {
             store_pairs(a.hloc + ((long long)seg * a.D + ch) * NP, n0, NP, h);
             if (part == 0) a.sums[(long long)seg * a.D + ch] = step_sum;
         }
-        if (chan0 == 0 && tid == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
+        if (chan0 == 0 && lane == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
     }
 }
 
@@ -317,28 +325,29 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     }
 }
 
-template <typename T, int LP>
+template <typename T, int NPL, int LP>
 cudaError_t launch_scan_parts(ScanArgs a, cudaStream_t s) {
-    constexpr int CH = kScanThreads / LP;
-    a.chan_blocks = (a.D + CH - 1) / CH;
+    constexpr int CW = 32 / LP;
+    a.chan_blocks = (a.D + CW - 1) / CW;
     a.has_carry = a.segs > 1;
     if (a.segs > 1) {
-        scan_kernel<T, LP, true><<<(unsigned)((long long)a.chan_blocks * a.B * (a.segs - 1)), kScanThreads, 0, s>>>(a);
+        scan_kernel<T, NPL, LP, true><<<(unsigned)((long long)a.chan_blocks * a.B * (a.segs - 1)), 32, 0, s>>>(a);
         const cudaError_t e = launch_scan_combine(a, a.segs, false, s);
         if (e != cudaSuccess) return e;
     }
-    scan_kernel<T, LP, false><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), kScanThreads, 0, s>>>(a);
+    scan_kernel<T, NPL, LP, false><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 
+// Channels of a warp by N, as launch_scan_typed picks them.
+int scan_warp_channels(int N) { return N <= 16 ? 32 : N <= 32 ? 16 : 8; }
+
 template <typename T>
 cudaError_t launch_scan_typed(const ScanArgs &a, cudaStream_t s) {
-    switch (scan_parts(a.N)) {
-        case 1: return launch_scan_parts<T, 1>(a, s);
-        case 2: return launch_scan_parts<T, 2>(a, s);
-        case 4: return launch_scan_parts<T, 4>(a, s);
-        default: return launch_scan_parts<T, 8>(a, s);
-    }
+    if (a.N <= 8) return launch_scan_parts<T, 8, 1>(a, s);
+    if (a.N <= 16) return launch_scan_parts<T, 16, 1>(a, s);
+    if (a.N <= 32) return launch_scan_parts<T, 16, 2>(a, s);
+    return launch_scan_parts<T, 16, 4>(a, s);
 }
 
 template <typename T>
@@ -353,21 +362,18 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 }
 
 // Segments per row in the forward pass.  One segment takes each exponential
-// once; several take it twice but put that many times the blocks to work.  An
-// SM is busy with about eight blocks of two warps (one warp of every two
-// schedulers hides the other's latency); segments are cut when whole rows
-// leave it with less than half of that.
+// once; several take it twice but put that many times the warps to work.
 int scan_segments(int B, int T, int D, int N) {
-    const int ch = kScanThreads / scan_parts(N), tiles = (T + kTile - 1) / kTile;
-    const long long blocks = (long long)B * ((D + ch - 1) / ch), wanted = 8ll * device_sm_count();
-    if (tiles <= 1 || 2 * blocks >= wanted) return 1;
-    const int segs = (int)std::min<long long>((wanted + blocks - 1) / blocks, tiles);
+    const int ch = scan_warp_channels(N), tiles = (T + kScanTile - 1) / kScanTile;
+    const long long warps = (long long)B * ((D + ch - 1) / ch), wanted = 8ll * device_sm_count();
+    if (tiles <= 1 || 2 * warps >= wanted) return 1;
+    const int segs = (int)std::min<long long>((wanted + warps - 1) / warps, tiles);
     const int len = (tiles + segs - 1) / segs;
     return (tiles + len - 1) / len;
 }
 int scan_segment_tokens(int T, int segs) {
-    const int tiles = (T + kTile - 1) / kTile;
-    return std::max(1, (tiles + segs - 1) / segs) * kTile;
+    const int tiles = (T + kScanTile - 1) / kScanTile;
+    return std::max(1, (tiles + segs - 1) / segs) * kScanTile;
 }
 
 }  // namespace
