@@ -135,12 +135,16 @@ __device__ __forceinline__ void store_some(T *p, const float *x, int n) {
 // exist, which is zero) by plain stores.  The thread that copies is the one that
 // reads, after copy_commit and copy_wait.
 template <typename T>
+__device__ __forceinline__ void copy8_whole(T *dst, const T *src) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(dst);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * i), "l"(src + i * 16 / (int)sizeof(T)) : "memory");
+}
+template <typename T>
 __device__ __forceinline__ void copy8_async(T *dst, const T *src, int live, bool vec) {
     if (vec && live >= 8) {
-        const uint32_t at = (uint32_t)__cvta_generic_to_shared(dst);
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * i), "l"(src + i * 16 / (int)sizeof(T)) : "memory");
+        copy8_whole<T>(dst, src);
     } else {
         store_raw<T, 8>(dst, live > 0 ? load_some<T, 8>(src, live) : zero_raw<T, 8>());
     }

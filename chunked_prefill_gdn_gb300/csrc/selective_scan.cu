@@ -43,9 +43,9 @@ struct ScanShape {
     static constexpr int PASSES = kScanTile / RPP > 0 ? kScanTile / RPP : 1;
     static constexpr int BCV = kScanTile * 2 * (NP / 8) / 32 > 0 ? kScanTile * 2 * (NP / 8) / 32 : 1;   // vectors of B, C per lane
     static constexpr int ARRAYS = STATE_ONLY ? 2 : 3;
-    // rows of 16-byte entries per channel, shifted by half a bank row so that two
-    // rows written together do not meet in a bank
-    static constexpr int SD = CW * 4 + 16;
+    // rows of 8-byte entries per channel, shifted by a quarter of a bank row so that
+    // the four rows written together do not meet in a bank
+    static constexpr int SD = CW * 2 + 8;
     static constexpr int YS = CW + 4;
 };
 
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
     constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPL / 2;
     __shared__ __align__(16) T rows[2][S::ARRAYS][PASSES][32][8];   // raw x, dt, z: one vector per lane and pass
     __shared__ __align__(16) T bcr[2][S::BCV][32][8];
-    __shared__ __align__(16) float sd[kScanTile][S::SD];            // step, step, step * x, step * x
+    __shared__ __align__(16) float sd[kScanTile][S::SD];            // step, step * x
     __shared__ __align__(16) float bc[kScanTile][2][NP];
     __shared__ __align__(16) float ys[STATE_ONLY ? 1 : kScanTile][S::YS];
 
@@ -89,26 +89,49 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
     }
     if (r.t0 >= r.t1) return;
 
-    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + lc;
-    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + lc;
-    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + lc;
     const bool gated = !STATE_ONLY && a.z != nullptr;
-    auto stage = [&](int t, int buf) {
+    const long long first = r.t0 + lrow;
+    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + first * a.x_token + lc;
+    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + first * a.dt_token + lc;
+    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + first * a.z_token + lc;
+    // the lane's piece of a tile's rows of B and C
+    constexpr int BCR = NP / 4;                    // vectors per row of both
+    const int bcc = lane / (NP / 8) % 2, bcn = lane % (NP / 8) * 8;
+    const long long bc_token = bcc ? a.c_token : a.b_token;
+    const T *pbc = (bcc ? static_cast<const T *>(a.Cm) + r.b * a.c_batch : static_cast<const T *>(a.Bm) + r.b * a.b_batch) +
+                   (long long)(r.t0 + lane / BCR) * bc_token + bcn;
+    const bool whole = a.vec && lrest >= 8 && a.bc_vec && a.N - bcn >= 8;
+    auto stage = [&](int t, int buf) {             // copies tile t and moves the pointers on to the next
+        if (whole && t + kScanTile <= r.t1) {
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int q = t + i * RPP + lrow;
-            const int n = i * RPP + lrow < kScanTile && q < r.t1 ? lrest : 0;
-            copy8_async<T>(rows[buf][0][i][lane], px + q * a.x_token, n, a.vec);
-            copy8_async<T>(rows[buf][1][i][lane], pd + q * a.dt_token, n, a.vec);
-            if (!STATE_ONLY) copy8_async<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + q * a.z_token, gated ? n : 0, a.vec);
-        }
+            for (int i = 0; i < PASSES; ++i) {
+                if (RPP > kScanTile && lrow >= kScanTile) break;
+                copy8_whole<T>(rows[buf][0][i][lane], px + i * RPP * a.x_token);
+                copy8_whole<T>(rows[buf][1][i][lane], pd + i * RPP * a.dt_token);
+                if (gated) copy8_whole<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + i * RPP * a.z_token);
+            }
 #pragma unroll
-        for (int i = 0; i < S::BCV; ++i) {
-            const int j = i * 32 + lane, v = j % (NP / 8), c = j / (NP / 8) % 2, q = t + j / (NP / 4);
-            const T *src = c ? static_cast<const T *>(a.Cm) + r.b * a.c_batch + q * a.c_token
-                             : static_cast<const T *>(a.Bm) + r.b * a.b_batch + q * a.b_token;
-            copy8_async<T>(bcr[buf][i][lane], src + v * 8, j / (NP / 4) < kScanTile && q < r.t1 ? a.N - v * 8 : 0, a.bc_vec);
+            for (int i = 0; i < S::BCV; ++i)
+                if (32 / BCR <= kScanTile || lane / BCR < kScanTile)
+                    copy8_whole<T>(bcr[buf][i][lane], pbc + i * (32 / BCR) * bc_token);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int q = i * RPP + lrow, n = q < kScanTile && t + q < r.t1 ? lrest : 0;
+                copy8_async<T>(rows[buf][0][i][lane], px + i * RPP * a.x_token, n, a.vec);
+                copy8_async<T>(rows[buf][1][i][lane], pd + i * RPP * a.dt_token, n, a.vec);
+                if (!STATE_ONLY)
+                    copy8_async<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + i * RPP * a.z_token, gated ? n : 0, a.vec);
+            }
+#pragma unroll
+            for (int i = 0; i < S::BCV; ++i) {
+                const int q = i * (32 / BCR) + lane / BCR;
+                copy8_async<T>(bcr[buf][i][lane], pbc + i * (32 / BCR) * bc_token,
+                               q < kScanTile && t + q < r.t1 ? a.N - bcn : 0, a.bc_vec);
+            }
         }
+        px += kScanTile * a.x_token, pd += kScanTile * a.dt_token, pz += kScanTile * a.z_token;
+        pbc += kScanTile * bc_token;
         copy_commit();
     };
     stage(r.t0, 0);
@@ -130,6 +153,7 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
     load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
     load_pairs(!STATE_ONLY && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
 
+    T *py = STATE_ONLY ? nullptr : static_cast<T *>(a.out) + ((long long)r.b * a.T + r.t0 + lrow) * a.D + lc;
     int buf = 0;
     for (int t = r.t0; t < r.t1; t += kScanTile, buf ^= 1) {
         stage(t + kScanTile, buf ^ 1);
@@ -145,18 +169,18 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
             for (int e = 0; e < 4; ++e) {
                 d[e] = add2(d[e], bias[e]);
                 const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
-                *reinterpret_cast<float4 *>(&sd[q][(2 * e * VPR + lv) * 4]) = make_float4(lo(s), lo(s), lo(sx), lo(sx));
-                *reinterpret_cast<float4 *>(&sd[q][((2 * e + 1) * VPR + lv) * 4]) = make_float4(hi(s), hi(s), hi(sx), hi(sx));
+                *reinterpret_cast<float2 *>(&sd[q][(2 * e * VPR + lv) * 2]) = make_float2(lo(s), lo(sx));
+                *reinterpret_cast<float2 *>(&sd[q][((2 * e + 1) * VPR + lv) * 2]) = make_float2(hi(s), hi(sx));
             }
         }
 #pragma unroll
         for (int i = 0; i < S::BCV; ++i) {
-            const int j = i * 32 + lane, v = j % (NP / 8), c = j / (NP / 8) % 2, q = j / (NP / 4);
+            const int q = i * (32 / BCR) + lane / BCR;
             if (q >= kScanTile) continue;
             F2 f[4];
             unpack_pairs<T>(load_raw<T, 8>(bcr[buf][i][lane]), f);
-            *reinterpret_cast<ulonglong2 *>(&bc[q][c][v * 8]) = make_ulonglong2(f[0], f[1]);
-            *reinterpret_cast<ulonglong2 *>(&bc[q][c][v * 8 + 4]) = make_ulonglong2(f[2], f[3]);
+            *reinterpret_cast<ulonglong2 *>(&bc[q][bcc][bcn]) = make_ulonglong2(f[0], f[1]);
+            *reinterpret_cast<ulonglong2 *>(&bc[q][bcc][bcn + 4]) = make_ulonglong2(f[2], f[3]);
         }
         __syncwarp();
         const int stop = min(r.t1, t + kScanTile);
@@ -164,7 +188,8 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
             const int run_end = min(stop, r.end);
 #pragma unroll 4
             for (int k = q - t; k < run_end - t; ++k) {
-                const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(&sd[k][pos * 4]);
+                const float2 sv = *reinterpret_cast<const float2 *>(&sd[k][pos * 2]);
+                const ulonglong2 s = make_ulonglong2(both(sv.x), both(sv.y));
                 const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(&bc[k][0][n0]);
                 const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(&bc[k][1][n0]);
                 F2 y0 = both(0.f), y1 = both(0.f);
@@ -180,7 +205,7 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
                     }
                 }
                 if (STATE_ONLY) {
-                    step_sum += lo(s.x);
+                    step_sum += sv.x;
                 } else {
                     y0 = add2(y0, y1);
                     float v = lo(y0) + hi(y0);
@@ -217,8 +242,9 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
                     if (gated) y = mul2(y, mul2(z[e], sigmoid_pair(z[e])));
                     o[2 * e] = lo(y), o[2 * e + 1] = hi(y);
                 }
-                store8<T>(static_cast<T *>(a.out) + ((long long)r.b * a.T + t + q) * a.D + lc, o, lrest, a.vec);
+                store8<T>(py + (long long)i * RPP * a.D, o, lrest, a.vec);
             }
+            py += (long long)kScanTile * a.D;
             __syncwarp();   // ys is written again by the next tile
         }
     }
