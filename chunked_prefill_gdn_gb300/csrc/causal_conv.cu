@@ -48,32 +48,33 @@ __device__ __forceinline__ float conv_param(const void *p, long long i, int f32)
     return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
+// Weights and bias of a thread's VEC channels, as pairs of channels.
 template <int W, int VEC>
-__device__ __forceinline__ void load_weights(const ConvArgs &a, int c, int live, float (*w)[VEC], float *b) {
+__device__ __forceinline__ void load_weights(const ConvArgs &a, int c, bool live, F2 (&w)[W][(VEC + 1) / 2],
+                                             F2 (&b)[(VEC + 1) / 2]) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int p = 0; p < (VEC + 1) / 2; ++p) {
+        const bool two = live && VEC > 1;
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i][e] = live ? conv_param(a.w, (long long)(c + e) * W + i, a.w_f32) : 0.f;
-        b[e] = live && a.bias ? conv_param(a.bias, c + e, a.w_f32) : 0.f;
+        for (int i = 0; i < W; ++i)
+            w[i][p] = pair(live ? conv_param(a.w, (long long)(c + 2 * p) * W + i, a.w_f32) : 0.f,
+                           two ? conv_param(a.w, (long long)(c + 2 * p + 1) * W + i, a.w_f32) : 0.f);
+        b[p] = pair(live && a.bias ? conv_param(a.bias, c + 2 * p, a.w_f32) : 0.f,
+                    two && a.bias ? conv_param(a.bias, c + 2 * p + 1, a.w_f32) : 0.f);
     }
 }
 
-// Rows of a sequence's state as the window before its first token.
+// Row r of sequence n's state.
 template <typename T, int W, int VEC>
-__device__ __forceinline__ void state_window(const ConvArgs &a, int n, int c, bool live, float (*win)[VEC]) {
-#pragma unroll
-    for (int r = 0; r < W - 1; ++r) {
-        if (live && a.init)
-            unpack<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.init) + ((long long)n * (W - 1) + r) * a.D + c), win[r]);
-        else
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) win[r][e] = 0.f;
-    }
+__device__ __forceinline__ void state_row(const ConvArgs &a, const void *state, int n, int r, int c, bool live,
+                                          F2 (&v)[(VEC + 1) / 2]) {
+    unpack_pairs<T, VEC>(live && state ? load_raw<T, VEC>(static_cast<const T *>(state) + ((long long)n * (W - 1) + r) * a.D + c)
+                                       : zero_raw<T, VEC>(), v);
 }
 
 // Where a run of tokens [t0, t1) of batch row b lies.
 struct Run {
-    int b, t0, t1, n, begin, end;   // begin, end: of the sequence that holds t0
+    int b, t0, t1, n, begin, end;   // begin, end: of the sequence that holds the current token
 };
 
 __device__ __forceinline__ void enter_seq(const ConvArgs &a, Run &r, int t) {
@@ -85,22 +86,41 @@ __device__ __forceinline__ void enter_seq(const ConvArgs &a, Run &r, int t) {
 
 // The window before token t0: rows of the run's sequence, or of its state.
 template <typename T, int W, int VEC>
-__device__ __forceinline__ void first_window(const ConvArgs &a, const Run &r, int c, bool live, float (*win)[VEC]) {
+__device__ __forceinline__ void first_window(const ConvArgs &a, const Run &r, int c, bool live,
+                                             F2 (&win)[W - 1][(VEC + 1) / 2]) {
     const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         const int t = r.t0 - (W - 1) + i;
-        const int s = (W - 1) + t - r.begin;   // the state's row when t < begin
+        if (t >= r.begin) unpack_pairs<T, VEC>(live ? load_raw<T, VEC>(x + t * a.x_token) : zero_raw<T, VEC>(), win[i]);
+        else state_row<T, W, VEC>(a, a.init, r.n, (W - 1) + t - r.begin, c, live, win[i]);
+    }
+}
+
+// u of a token whose row is x, and the window moved on.
+template <int W, int P>
+__device__ __forceinline__ void conv_sum(const F2 (&w)[W][P], const F2 (&bias)[P], const F2 (&win)[W - 1][P],
+                                         const F2 (&x)[P], F2 (&u)[P]) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) win[i][e] = 0.f;
-        if (live && t >= r.begin) unpack<T, VEC>(load_raw<T, VEC>(x + t * a.x_token), win[i]);
-        else if (live && a.init)
-            unpack<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(a.init) + ((long long)r.n * (W - 1) + s) * a.D + c), win[i]);
+    for (int p = 0; p < P; ++p) {
+        u[p] = fma2(w[W - 1][p], x[p], bias[p]);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) u[p] = fma2(w[k][p], win[k][p], u[p]);
+    }
+}
+template <int W, int P>
+__device__ __forceinline__ void move_window(F2 (&win)[W - 1][P], const F2 (&x)[P]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+        for (int k = 0; k < W - 2; ++k) win[k][p] = win[k + 1][p];
+        win[W - 2][p] = x[p];
     }
 }
 
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
+    constexpr int P = (VEC + 1) / 2;
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
@@ -111,76 +131,76 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
     r.b = tile / per_row;
     r.t0 = (tile % per_row) * a.run;
     r.t1 = min(a.T, r.t0 + a.run);
-    // states of empty sequences, dealt over the runs
-    if (a.cu && a.last && live) {
-        for (int n = tile; n < a.n_seqs; n += a.groups * kConvWarps) {
-            if (__ldg(a.cu + n) < __ldg(a.cu + n + 1)) continue;
-            float win[W - 1][VEC];
-            state_window<T, W, VEC>(a, n, c, true, win);
+    T *last = static_cast<T *>(a.last);
+    // a sequence without a token keeps its state: packed ones are dealt over the runs
+    if (last && live) {
+        auto keep = [&](int n) {
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i)
-                store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)n * (W - 1) + i) * a.D + c, pack<T, VEC>(win[i]));
-        }
+            for (int i = 0; i < W - 1; ++i) {
+                F2 v[P];
+                state_row<T, W, VEC>(a, a.init, n, i, c, true, v);
+                store_raw<T, VEC>(last + ((long long)n * (W - 1) + i) * a.D + c, pack_pairs<T, VEC>(v));
+            }
+        };
+        for (int n = tile; a.cu && n < a.n_seqs; n += a.groups * kConvWarps)
+            if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) keep(n);
+        if (!a.cu && a.T == 0 && r.t0 == 0) keep(r.b);
     }
-    if (r.t0 >= r.t1) {
-        // batched rows without a token keep their state
-        if (!a.cu && a.T == 0 && a.last && live && r.t0 == 0) {
-            float win[W - 1][VEC];
-            state_window<T, W, VEC>(a, r.b, c, true, win);
+    if (r.t0 >= r.t1 || !live) return;
+    const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + r.t0 * a.x_token + c;   // the next row to load
+    T *y = static_cast<T *>(a.out) + ((long long)r.b * a.T + r.t0) * a.D + c;            // the next to store
+    Raw<T, VEC> ring[kSub];
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i)
-                store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)r.b * (W - 1) + i) * a.D + c, pack<T, VEC>(win[i]));
-        }
-        return;
+    for (int i = 0; i < kSub; ++i) {
+        ring[i] = r.t0 + i < r.t1 ? load_raw<T, VEC>(x) : zero_raw<T, VEC>();
+        x += a.x_token;
     }
-    const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
-    T *y = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
-    Raw<T, VEC> next[kSub];
-    auto load_rows = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < kSub; ++i)
-            next[i] = live && t + i < r.t1 ? load_raw<T, VEC>(x + (t + i) * a.x_token) : zero_raw<T, VEC>();
-    };
-    load_rows(r.t0);
-    float w[W][VEC], bias[VEC], win[W - 1][VEC];
+    F2 w[W][P], bias[P], win[W - 1][P];
     load_weights<W, VEC>(a, c, live, w, bias);
     r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
     r.begin = 0, r.end = a.T;
     enter_seq(a, r, r.t0);
     first_window<T, W, VEC>(a, r, c, live, win);
-    for (int t = r.t0; t < r.t1; t += kSub) {
-        Raw<T, VEC> cur[kSub];
+    auto token = [&](int i) {   // computes row i of the ring
+        F2 xv[P], u[P];
+        unpack_pairs<T, VEC>(ring[i], xv);
+        conv_sum<W, P>(w, bias, win, xv, u);
+        move_window<W, P>(win, xv);
+        if (a.silu) {
 #pragma unroll
-        for (int i = 0; i < kSub; ++i) cur[i] = next[i];
-        load_rows(t + kSub);
+            for (int p = 0; p < P; ++p) u[p] = mul2(u[p], sigmoid_pair(u[p]));
+        }
+        store_raw<T, VEC>(y, pack_pairs<T, VEC>(u));
+        y += a.D;
+    };
+    for (int t = r.t0; t < r.t1; t += kSub) {
+        if (t + kSub < min(r.end, r.t1) && t + 2 * kSub <= r.t1) {
+            // no boundary among these rows, and as many to follow
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+                token(i);
+                ring[i] = load_raw<T, VEC>(x);
+                x += a.x_token;
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < kSub; ++i) {
-            if (t + i >= r.t1) break;
-            if (t + i == r.end) {   // the next sequence that has a token
-                while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= t + i) ++r.n;
-                enter_seq(a, r, t + i);
-                state_window<T, W, VEC>(a, r.n, c, live, win);
+            const int q = t + i;
+            if (q >= r.t1) break;
+            if (q == r.end) {   // the next sequence that has a token
+                while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= q) ++r.n;
+                enter_seq(a, r, q);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) state_row<T, W, VEC>(a, a.init, r.n, k, c, true, win[k]);
             }
-            float xv[VEC], u[VEC];
-            unpack<T, VEC>(cur[i], xv);
+            token(i);
+            if (q + kSub < r.t1) ring[i] = load_raw<T, VEC>(x);
+            x += a.x_token;
+            if (last && q + 1 == r.end) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                u[e] = fmaf(w[W - 1][e], xv[e], bias[e]);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) u[e] = fmaf(w[k][e], win[k][e], u[e]);
-                if (a.silu) u[e] *= sigmoid_f32(u[e]);
-#pragma unroll
-                for (int k = 0; k < W - 2; ++k) win[k][e] = win[k + 1][e];
-                win[W - 2][e] = xv[e];
-            }
-            if (live) {
-                store_raw<T, VEC>(y + (long long)(t + i) * a.D, pack<T, VEC>(u));
-                if (a.last && t + i + 1 == r.end) {
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-                        store_raw<T, VEC>(static_cast<T *>(a.last) + ((long long)r.n * (W - 1) + k) * a.D + c,
-                                          pack<T, VEC>(win[k]));
-                }
+                for (int k = 0; k < W - 1; ++k)
+                    store_raw<T, VEC>(last + ((long long)r.n * (W - 1) + k) * a.D + c, pack_pairs<T, VEC>(win[k]));
             }
         }
     }
@@ -188,6 +208,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
 
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
+    constexpr int P = (VEC + 1) / 2;
     __shared__ float sum[kConvWarps][W + 1][32 * VEC];
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -201,85 +222,124 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
     r.t0 = (tile % per_row) * a.run;
     r.t1 = min(a.T, r.t0 + a.run);
     T *dinit = static_cast<T *>(a.last);
-    const T *dfin = static_cast<const T *>(a.d_final);
     // a sequence without a token hands the gradient of its final state on
-    auto pass_on = [&](int n) {
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-            const long long at = ((long long)n * (W - 1) + i) * a.D + c;
-            store_raw<T, VEC>(dinit + at, dfin ? load_raw<T, VEC>(dfin + at) : zero_raw<T, VEC>());
-        }
-    };
     if (dinit && live) {
-        if (a.cu) {
-            for (int n = tile; n < a.n_seqs; n += a.groups * kConvWarps)
-                if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) pass_on(n);
-        } else if (a.T == 0 && r.t0 == 0) {
-            pass_on(r.b);
-        }
-    }
-    float dw[W][VEC], db[VEC];
+        auto pass_on = [&](int n) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        db[e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
-    }
-    if (r.t0 < r.t1) {
-        const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + c;
-        const T *dy = static_cast<const T *>(a.dy) + r.b * a.dy_batch + c;
-        T *dx = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
-        const int stop = min(a.T, r.t1 + W - 1);
-        Raw<T, VEC> nx[kSubB], ng[kSubB];
-        auto load_rows = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < kSubB; ++i) {
-                const bool in = live && t + i < stop;
-                nx[i] = in ? load_raw<T, VEC>(x + (t + i) * a.x_token) : zero_raw<T, VEC>();
-                ng[i] = in ? load_raw<T, VEC>(dy + (t + i) * a.dy_token) : zero_raw<T, VEC>();
+            for (int i = 0; i < W - 1; ++i) {
+                F2 v[P];
+                state_row<T, W, VEC>(a, a.d_final, n, i, c, true, v);
+                store_raw<T, VEC>(dinit + ((long long)n * (W - 1) + i) * a.D + c, pack_pairs<T, VEC>(v));
             }
         };
-        load_rows(r.t0);
-        float w[W][VEC], bias[VEC], win[W - 1][VEC], acc[W][VEC];
+        for (int n = tile; a.cu && n < a.n_seqs; n += a.groups * kConvWarps)
+            if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) pass_on(n);
+        if (!a.cu && a.T == 0 && r.t0 == 0) pass_on(r.b);
+    }
+    F2 dw[W][P], db[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        db[p] = both(0.f);
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][p] = both(0.f);
+    }
+    if (r.t0 < r.t1 && live) {
+        // dx of a token needs the W - 1 tokens after it: the walk goes on past the run
+        const int stop = min(a.T, r.t1 + W - 1);
+        const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + r.t0 * a.x_token + c;
+        const T *dy = static_cast<const T *>(a.dy) + r.b * a.dy_batch + r.t0 * a.dy_token + c;
+        T *dx = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
+        Raw<T, VEC> rx[kSubB], rg[kSubB];
+#pragma unroll
+        for (int i = 0; i < kSubB; ++i) {
+            rx[i] = r.t0 + i < stop ? load_raw<T, VEC>(x) : zero_raw<T, VEC>();
+            rg[i] = r.t0 + i < stop ? load_raw<T, VEC>(dy) : zero_raw<T, VEC>();
+            x += a.x_token, dy += a.dy_token;
+        }
+        F2 w[W][P], bias[P], win[W - 1][P], acc[W][P];
         load_weights<W, VEC>(a, c, live, w, bias);
         r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
         r.begin = 0, r.end = a.T;
         enter_seq(a, r, r.t0);
         first_window<T, W, VEC>(a, r, c, live, win);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
+        for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
+            for (int k = 0; k < W; ++k) acc[k][p] = both(0.f);
+        // row i of the ring; acc[k] gathers dx of position (its own) - (W - 1) + k
+        auto token = [&](int i, bool mine) {
+            F2 xv[P], u[P], du[P];
+            unpack_pairs<T, VEC>(rx[i], xv);
+            unpack_pairs<T, VEC>(rg[i], du);
+            if (a.silu) {
+                conv_sum<W, P>(w, bias, win, xv, u);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    // silu' = s + u s (1 - s) = s (1 + u (1 - s))
+                    const F2 s = sigmoid_pair(u[p]);
+                    const F2 g = fma2(u[p], fma2(s, both(-1.f), both(1.f)), both(1.f));
+                    du[p] = mul2(du[p], mul2(s, g));
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+                for (int k = 0; k < W; ++k) acc[k][p] = fma2(w[k][p], du[p], acc[k][p]);
+                if (mine) {   // tokens past the run belong to the next one's sums
+                    db[p] = add2(db[p], du[p]);
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) dw[k][p] = fma2(du[p], win[k][p], dw[k][p]);
+                    dw[W - 1][p] = fma2(du[p], xv[p], dw[W - 1][p]);
+                }
+            }
+            move_window<W, P>(win, xv);
+        };
+        auto shift = [&] {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) acc[k][p] = acc[k + 1][p];
+                acc[W - 1][p] = both(0.f);
+            }
+        };
         // the complete sum of position q, to whom it belongs
-        auto emit = [&](int q, const float *v) {
-            if (!live) return;
+        auto emit = [&](int q, const F2 (&v)[P]) {
             if (q >= r.begin) {
-                if (q >= r.t0 && q < r.t1) store_raw<T, VEC>(dx + (long long)q * a.D, pack<T, VEC>(v));
+                if (q >= r.t0 && q < r.t1) store_raw<T, VEC>(dx + (long long)q * a.D, pack_pairs<T, VEC>(v));
             } else if (dinit && r.begin >= r.t0 && r.begin < r.t1) {
-                store_raw<T, VEC>(dinit + ((long long)r.n * (W - 1) + (W - 1) + q - r.begin) * a.D + c, pack<T, VEC>(v));
+                store_raw<T, VEC>(dinit + ((long long)r.n * (W - 1) + (W - 1) + q - r.begin) * a.D + c, pack_pairs<T, VEC>(v));
             }
         };
         // the last W - 1 positions before a sequence's end (at t): no token follows
         auto flush = [&](int t) {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
-                if (dfin && live) {
-                    float f[VEC];
-                    unpack<T, VEC>(load_raw<T, VEC>(dfin + ((long long)r.n * (W - 1) + k) * a.D + c), f);
+                F2 f[P];
+                state_row<T, W, VEC>(a, a.d_final, r.n, k, c, true, f);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[k][e] += f[e];
-                }
+                for (int p = 0; p < P; ++p) acc[k][p] = add2(acc[k][p], f[p]);
                 emit(t - (W - 1) + k, acc[k]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
+                for (int p = 0; p < P; ++p) acc[k][p] = both(0.f);
             }
         };
         bool done = false;
         for (int t = r.t0; t < stop && !done; t += kSubB) {
-            Raw<T, VEC> cx[kSubB], cg[kSubB];
+            if (t - (W - 1) >= max(r.begin, r.t0) && t + kSubB <= min(r.end, r.t1) && t + 2 * kSubB <= stop) {
+                // tokens and the positions they complete in the run and the sequence
+                T *out = dx + (long long)(t - (W - 1)) * a.D;
 #pragma unroll
-            for (int i = 0; i < kSubB; ++i) cx[i] = nx[i], cg[i] = ng[i];
-            load_rows(t + kSubB);
+                for (int i = 0; i < kSubB; ++i) {
+                    token(i, true);
+                    store_raw<T, VEC>(out, pack_pairs<T, VEC>(acc[0]));
+                    out += a.D;
+                    shift();
+                    rx[i] = load_raw<T, VEC>(x);
+                    rg[i] = load_raw<T, VEC>(dy);
+                    x += a.x_token, dy += a.dy_token;
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kSubB; ++i) {
                 const int q = t + i;
@@ -292,38 +352,17 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
                     }
                     while (r.n + 1 < a.n_seqs && __ldg(a.cu + r.n + 1) <= q) ++r.n;
                     enter_seq(a, r, q);
-                    state_window<T, W, VEC>(a, r.n, c, live, win);
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) state_row<T, W, VEC>(a, a.init, r.n, k, c, true, win[k]);
                 }
-                float xv[VEC], gv[VEC];
-                unpack<T, VEC>(cx[i], xv);
-                unpack<T, VEC>(cg[i], gv);
-                const float mine = q < r.t1 ? 1.f : 0.f;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float du = gv[e];
-                    if (a.silu) {
-                        float u = fmaf(w[W - 1][e], xv[e], bias[e]);
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) u = fmaf(w[k][e], win[k][e], u);
-                        const float sg = sigmoid_f32(u);
-                        du *= sg * fmaf(u, 1.f - sg, 1.f);
-                    }
-#pragma unroll
-                    for (int k = 0; k < W; ++k) acc[k][e] = fmaf(w[k][e], du, acc[k][e]);
-                    const float own = du * mine;   // tokens past the run belong to the next one's sums
-                    db[e] += own;
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(own, win[k][e], dw[k][e]);
-                    dw[W - 1][e] = fmaf(own, xv[e], dw[W - 1][e]);
-#pragma unroll
-                    for (int k = 0; k < W - 2; ++k) win[k][e] = win[k + 1][e];
-                    win[W - 2][e] = xv[e];
-                }
+                token(i, q < r.t1);
                 emit(q - (W - 1), acc[0]);
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[k][e] = k + 1 < W ? acc[k + 1 < W ? k + 1 : k][e] : 0.f;
+                shift();
+                if (q + kSubB < stop) {
+                    rx[i] = load_raw<T, VEC>(x);
+                    rg[i] = load_raw<T, VEC>(dy);
+                }
+                x += a.x_token, dy += a.dy_token;
             }
         }
         if (!done && stop == r.end) flush(stop);
@@ -332,8 +371,8 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) sum[warp][k][lane * VEC + e] = dw[k][e];
-        sum[warp][W][lane * VEC + e] = db[e];
+        for (int k = 0; k < W; ++k) sum[warp][k][lane * VEC + e] = e & 1 ? hi(dw[k][e / 2]) : lo(dw[k][e / 2]);
+        sum[warp][W][lane * VEC + e] = e & 1 ? hi(db[e / 2]) : lo(db[e / 2]);
     }
     __syncthreads();
     const int c0 = (blockIdx.x % a.chan_blocks) * 32 * VEC;
@@ -387,20 +426,21 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) row[k] = load_raw<T, VEC>(state + (long long)k * a.D);
     row[W - 1] = load_raw<T, VEC>(static_cast<const T *>(a.x) + n * a.x_batch + c);
-    float w[W][VEC], u[VEC];
-    load_weights<W, VEC>(a, c, 1, w, u);
+    constexpr int P = (VEC + 1) / 2;
+    F2 w[W][P], u[P];
+    load_weights<W, VEC>(a, c, true, w, u);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        float v[VEC];
-        unpack<T, VEC>(row[k], v);
+        F2 v[P];
+        unpack_pairs<T, VEC>(row[k], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) u[e] = fmaf(w[k][e], v[e], u[e]);
+        for (int p = 0; p < P; ++p) u[p] = fma2(w[k][p], v[p], u[p]);
     }
     if (a.silu) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) u[e] *= sigmoid_f32(u[e]);
+        for (int p = 0; p < P; ++p) u[p] = mul2(u[p], sigmoid_pair(u[p]));
     }
-    store_raw<T, VEC>(y, pack<T, VEC>(u));
+    store_raw<T, VEC>(y, pack_pairs<T, VEC>(u));
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) store_raw<T, VEC>(state + (long long)k * a.D, row[k + 1]);
 }

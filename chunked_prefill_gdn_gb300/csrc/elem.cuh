@@ -155,9 +155,78 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
 }
 
-// sigmoid(x); x * sigmoid(x) is SiLU.  exp(-x) overflows to +inf below -88,
-// where the quotient is the right zero.
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Two fp32 values in one 64-bit register; mul, add and fma act on both.
+using F2 = unsigned long long;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo(F2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// 2^x, at most 2^-22 off relatively; results below 2^-126 are zero.
+__device__ __forceinline__ float exp2_f32(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ F2 exp2_pair(F2 x) { return pair(exp2_f32(lo(x)), exp2_f32(hi(x))); }
+
+__device__ __forceinline__ float rcp_f32(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ F2 rcp_pair(F2 x) { return pair(rcp_f32(lo(x)), rcp_f32(hi(x))); }
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+
+// 1 / (1 + exp(-x)); exp(-x) = inf gives the right zero.
+__device__ __forceinline__ F2 sigmoid_pair(F2 x) {
+    return rcp_pair(add2(exp2_pair(mul2(x, both(-kLog2e))), both(1.f)));
+}
+
+// E neighbouring values as pairs (a single value: its pair's second half is
+// zero), and back, rounded once.
+template <typename T, int E = 8>
+__device__ __forceinline__ void unpack_pairs(const Raw<T, E> &r, F2 (&v)[(E + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) {
+        if constexpr (E == 1)
+            v[i] = pair(__uint_as_float(sizeof(T) == 2 ? r.w[0] << 16 : r.w[0]), 0.f);
+        else if constexpr (sizeof(T) == 2)
+            v[i] = pair(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+        else
+            v[i] = pair(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    }
+}
+template <typename T, int E>
+__device__ __forceinline__ Raw<T, E> pack_pairs(const F2 (&v)[(E + 1) / 2]) {
+    float x[E + 1];
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) x[2 * i] = lo(v[i]), x[2 * i + 1] = hi(v[i]);
+    return pack<T, E>(x);
+}
+
+// 1 / (1 + exp(-x)), x times which is SiLU.
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_f32(1.f + exp2_f32(x * -kLog2e)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -1,60 +1,12 @@
-// What the selective scan's kernels share: pairs of fp32 values in one 64-bit
-// register (mul / fma act on both), the exponential and softplus, the
-// arguments, and where a tile of tokens lies among the sequences.
+// What the selective scan's kernels share: softplus, the arguments, and where a
+// tile of tokens lies among the sequences.
 #pragma once
 
 #include "elem.cuh"
 
 namespace gdn {
 
-using F2 = unsigned long long;
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 32;   // tokens per tile
-
-__device__ __forceinline__ F2 pair(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float lo(F2 v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// 2^x, at most 2^-22 off relatively; results below 2^-126 are zero.
-__device__ __forceinline__ float exp2_f32(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ F2 exp2_pair(F2 x) { return pair(exp2_f32(lo(x)), exp2_f32(hi(x))); }
-
-__device__ __forceinline__ float rcp_f32(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ F2 rcp_pair(F2 x) { return pair(rcp_f32(lo(x)), rcp_f32(hi(x))); }
-__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
-
-// 1 / (1 + exp(-x)); exp(-x) = inf gives the right zero.
-__device__ __forceinline__ F2 sigmoid_pair(F2 x) {
-    return rcp_pair(add2(exp2_pair(mul2(x, both(-kLog2e))), both(1.f)));
-}
 
 // log(1 + exp(x)) = max(x, 0) + log(1 + t), t = exp(-|x|) in [0, 1], with
 // log(1 + t) = 2 artanh(r), r = t / (2 + t) <= 1/3: no cancellation at either
@@ -71,18 +23,6 @@ __device__ __forceinline__ F2 softplus_pair(F2 x) {
     return fma2(r, p, pair(fmaxf(lo(x), 0.f), fmaxf(hi(x), 0.f)));
 }
 __device__ __forceinline__ float softplus_f32(float x) { return lo(softplus_pair(pair(x, 0.f))); }
-
-// Words of two bf16 values, or two fp32 values, as a pair; and back.
-template <typename T>
-__device__ __forceinline__ void unpack_pairs(const Raw<T, 8> &r, F2 (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2)
-            v[i] = pair(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
-        else
-            v[i] = pair(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
-    }
-}
 
 struct ScanArgs {
     const void *x, *dt, *z, *Bm, *Cm, *dy;
