@@ -15,8 +15,9 @@
 // and own their columns: the weights stay in registers over all rows of a
 // block, and in the backward pass so do the sums of dw and db, which leave the
 // block once, as one partial row per block; a second kernel adds those rows in
-// a fixed order, so the result does not depend on the launch.  The next row is
-// loaded before the current one is reduced.  Rows wider than 8192 are read
+// a fixed order, so the result does not depend on the launch.  The next rows come
+// in by asynchronous copies (up to four rows in flight, each
+// thread reading back what it copied) while the current one is reduced.  Rows wider than 8192 are read
 // three times instead (layer_norm_wide_*).
 #include <algorithm>
 
@@ -69,69 +70,142 @@ __device__ __forceinline__ void row_sums(float (&v)[NSUM], float (*red)[32]) {
 constexpr int norm_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
 constexpr int norm_blocks_per_sm(int tpr, bool bwd) { return (bwd ? 512 : 768) / norm_threads(tpr); }
 
+// Rows in flight per row of threads: as many as 64 KB per block hold, at most
+// four.  (Unaligned rows are loaded element by element, one row ahead.)
+template <typename T, int TPR, int VEC, int NV, int ARRAYS>
+struct NormStages {
+    static constexpr bool async = VEC * sizeof(T) == 16;
+    static constexpr int bytes = norm_threads(TPR) * NV * ARRAYS * 16;   // one stage of a block
+    static constexpr int count = !async ? 1 : 65536 / bytes >= 4 ? 4 : 65536 / bytes;
+    static constexpr int smem = async ? count * bytes : 0;
+};
+
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// A thread's element e of a row (of NV vectors of VEC elements, TPR vectors
+// apart) is in the row; elements 2p and 2p + 1 are pair p.
+template <int TPR, int VEC>
+__device__ __forceinline__ bool live_col(int e, int t, int D) {
+    return (e / VEC * TPR + t) * VEC + (VEC > 1 ? 0 : e % VEC) < D;   // a vector lies in the row or past it
+}
+__device__ __forceinline__ float half(F2 v, int e) { return e & 1 ? hi(v) : lo(v); }
+
+template <int TPR, int VEC, int NV>
+__device__ __forceinline__ void load_param_pairs(const void *p, int f32, int D, int t, float none, F2 (&v)[NV * VEC / 2]) {
+    float x[NV * VEC];
+#pragma unroll
+    for (int e = 0; e < NV * VEC; ++e)
+        x[e] = p && live_col<TPR, VEC>(e, t, D) ? load_param(p, (e / VEC * TPR + t) * VEC + e % VEC, f32) : none;
+#pragma unroll
+    for (int i = 0; i < NV * VEC / 2; ++i) v[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+
+template <typename T, int TPR, int VEC, int NV, typename F>
+__device__ __forceinline__ void unpack_row(int D, int t, F2 (&v)[NV * VEC / 2], F load) {
+    if constexpr (VEC > 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            F2 u[VEC / 2];
+            unpack_pairs<T, VEC>(live_col<TPR, VEC>(i * VEC, t, D) ? load(i) : zero_raw<T, VEC>(), u);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) v[i * (VEC / 2) + j] = u[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) {
+            float a, b;
+            unpack<T, 1>(load(2 * i), &a);
+            unpack<T, 1>(load(2 * i + 1), &b);
+            v[i] = pair(a, b);
+        }
+    }
+}
+
+template <typename T, int TPR, int VEC, int NV>
+__device__ __forceinline__ void store_row(T *row, int D, int t, const F2 (&v)[NV * VEC / 2]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        if (c >= D) continue;
+        if constexpr (VEC > 1) {
+            F2 u[VEC / 2];
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) u[j] = v[i * (VEC / 2) + j];
+            store_raw<T, VEC>(row + c, pack_pairs<T, VEC>(u));
+        } else {
+            row[c] = from_f32<T>(half(v[i / 2], i));
+        }
+    }
+}
+
 // TPR threads per row, NV vectors of VEC elements per thread.
 template <typename T, int TPR, int VEC, int NV>
 __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, false)) layer_norm_fwd_kernel(NormArgs a) {
+    using St = NormStages<T, TPR, VEC, NV, 1>;
     constexpr int RPB = norm_threads(TPR) / TPR;   // rows per block
+    constexpr int S = St::count, NT = norm_threads(TPR), NP = NV * VEC / 2;
     __shared__ float red[2][1][32];
+    extern __shared__ uint4 stages[];              // [S][NV][thread]
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.out);
-    Raw<T, VEC> next[NV];
-    auto load_row = [&](long long r) {
+    Raw<T, VEC> next[St::async ? 1 : NV];
+    auto load_row = [&](long long r, int slot) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
-            next[i] = r < a.rows && c < a.D ? load_raw<T, VEC>(x + r * a.x_stride + c) : zero_raw<T, VEC>();
-        }
-    };
-    load_row(row);
-    float w[NV * VEC], b[NV * VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (i * TPR + t) * VEC + j;
-            w[i * VEC + j] = a.w && c < a.D ? load_param(a.w, c, a.w_f32) : 1.f;
-            b[i * VEC + j] = a.b && c < a.D ? load_param(a.b, c, a.w_f32) : 0.f;
-        }
-    }
-    const float inv_d = 1.f / (float)a.D;
-    // a row group without a row of its own still takes part in the block's sums
-    for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
-        float v[NV * VEC];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) unpack<T, VEC>(next[i], v + i * VEC);
-        load_row(row + step);
-        float s[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < NV * VEC; ++i) s[0] += v[i];
-        row_sums<TPR, 1>(s, red[0]);
-        const float mean = s[0] * inv_d;
-        float q[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = (i * TPR + t) * VEC < a.D;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                v[i * VEC + j] = in ? v[i * VEC + j] - mean : 0.f;
-                q[0] = fmaf(v[i * VEC + j], v[i * VEC + j], q[0]);
+            const bool in = r < a.rows && c < a.D;
+            if constexpr (St::async) {
+                if (in) copy16(stages + (slot * NV + i) * NT + threadIdx.x, x + r * a.x_stride + c);
+            } else {
+                next[i] = in ? load_raw<T, VEC>(x + r * a.x_stride + c) : zero_raw<T, VEC>();
             }
         }
+        copy_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    F2 w[NP], b[NP];
+    load_param_pairs<TPR, VEC, NV>(a.w, a.w_f32, a.D, t, 1.f, w);
+    load_param_pairs<TPR, VEC, NV>(a.b, a.w_f32, a.D, t, 0.f, b);
+    const float inv_d = 1.f / (float)a.D;
+    // (with several rows per block a row is a warp's own: it may leave the loop alone)
+    for (int slot = 0; row < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1) {
+        F2 v[NP];
+        if constexpr (St::async) {
+            load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+            unpack_row<T, TPR, VEC, NV>(a.D, t, v, [&](int i) {
+                return load_raw<T, VEC>(reinterpret_cast<const T *>(stages + (slot * NV + i) * NT + threadIdx.x));
+            });
+        } else {
+            unpack_row<T, TPR, VEC, NV>(a.D, t, v, [&](int i) { return next[i]; });
+            load_row(row + step, 0);
+        }
+        F2 s2 = v[0];
+#pragma unroll
+        for (int p = 1; p < NP; ++p) s2 = add2(s2, v[p]);
+        float s[1] = {lo(s2) + hi(s2)};
+        row_sums<TPR, 1>(s, red[0]);
+        const float mean = s[0] * inv_d;
+        F2 q2 = both(0.f);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            v[p] = add2(v[p], both(-mean));
+            if (!live_col<TPR, VEC>(2 * p, t, a.D)) v[p] = v[p] & 0xFFFFFFFF00000000ull;
+            if (!live_col<TPR, VEC>(2 * p + 1, t, a.D)) v[p] = v[p] & 0x00000000FFFFFFFFull;
+            q2 = fma2(v[p], v[p], q2);
+        }
+        float q[1] = {lo(q2) + hi(q2)};
         row_sums<TPR, 1>(q, red[1]);
         const float rstd = rsqrtf(q[0] * inv_d + a.eps);
-        if (row >= a.rows) continue;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (c >= a.D) continue;
-            float o[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] = fmaf(v[i * VEC + j] * rstd, w[i * VEC + j], b[i * VEC + j]);
-            store_raw<T, VEC>(y + row * a.D + c, pack<T, VEC>(o));
-        }
+        for (int p = 0; p < NP; ++p) v[p] = fma2(mul2(v[p], both(rstd)), w[p], b[p]);
+        store_row<T, TPR, VEC, NV>(y + row * a.D, a.D, t, v);
         if (t == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -141,78 +215,73 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, fal
 
 template <typename T, int TPR, int VEC, int NV>
 __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, true)) layer_norm_bwd_kernel(NormArgs a) {
+    using St = NormStages<T, TPR, VEC, NV, 2>;
     constexpr int RPB = norm_threads(TPR) / TPR;
+    constexpr int S = St::count, NT = norm_threads(TPR), NP = NV * VEC / 2;
     __shared__ float red[2][2][32];
+    extern __shared__ uint4 stages[];              // [S][x, dy][NV][thread]
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.out);
-    Raw<T, VEC> nx[NV], ng[NV];
-    float nmean = 0.f, nrstd = 0.f;
-    auto load_row = [&](long long r) {
+    Raw<T, VEC> nx[St::async ? 1 : NV], ng[St::async ? 1 : NV];
+    auto load_row = [&](long long r, int slot) {
         const bool live = r < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
-            nx[i] = live && c < a.D ? load_raw<T, VEC>(x + r * a.x_stride + c) : zero_raw<T, VEC>();
-            ng[i] = live && c < a.D ? load_raw<T, VEC>(dy + r * a.dy_stride + c) : zero_raw<T, VEC>();
+            const bool in = live && c < a.D;
+            if constexpr (St::async) {
+                uint4 *at = stages + (slot * 2 * NV + i) * NT + threadIdx.x;
+                if (in) copy16(at, x + r * a.x_stride + c), copy16(at + NV * NT, dy + r * a.dy_stride + c);
+            } else {
+                nx[i] = in ? load_raw<T, VEC>(x + r * a.x_stride + c) : zero_raw<T, VEC>();
+                ng[i] = in ? load_raw<T, VEC>(dy + r * a.dy_stride + c) : zero_raw<T, VEC>();
+            }
         }
-        nmean = live ? a.mean[r] : 0.f;
-        nrstd = live ? a.rstd[r] : 0.f;
+        copy_commit();
     };
-    load_row(row);
-    float w[NV * VEC], dw[NV * VEC], db[NV * VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    float nmean = row < a.rows ? a.mean[row] : 0.f, nrstd = row < a.rows ? a.rstd[row] : 0.f;
+    F2 w[NP], dw[NP], db[NP];
+    load_param_pairs<TPR, VEC, NV>(a.w, a.w_f32, a.D, t, 1.f, w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int c = (i * TPR + t) * VEC + j;
-            w[i * VEC + j] = a.w && c < a.D ? load_param(a.w, c, a.w_f32) : 1.f;
-            dw[i * VEC + j] = db[i * VEC + j] = 0.f;
-        }
-    }
+    for (int p = 0; p < NP; ++p) dw[p] = db[p] = both(0.f);
     const float inv_d = 1.f / (float)a.D;
     int phase = 0;
-    for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step, phase ^= 1) {
-        float xh[NV * VEC], g[NV * VEC];
+    for (int slot = 0; row < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1, phase ^= 1) {
+        F2 xh[NP], g[NP];   // zero past D, where g = 0 keeps xh out of every sum
         const float mean = nmean, rstd = nrstd;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack<T, VEC>(nx[i], xh + i * VEC);
-            unpack<T, VEC>(ng[i], g + i * VEC);
+        if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
+        if constexpr (St::async) {
+            load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+            const uint4 *at = stages + slot * 2 * NV * NT + threadIdx.x;
+            unpack_row<T, TPR, VEC, NV>(a.D, t, xh, [&](int i) { return load_raw<T, VEC>(reinterpret_cast<const T *>(at + i * NT)); });
+            unpack_row<T, TPR, VEC, NV>(a.D, t, g, [&](int i) { return load_raw<T, VEC>(reinterpret_cast<const T *>(at + (NV + i) * NT)); });
+        } else {
+            unpack_row<T, TPR, VEC, NV>(a.D, t, xh, [&](int i) { return nx[i]; });
+            unpack_row<T, TPR, VEC, NV>(a.D, t, g, [&](int i) { return ng[i]; });
+            load_row(row + step, 0);
         }
-        load_row(row + step);
-        float s[2] = {0.f, 0.f};
+        F2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = (i * TPR + t) * VEC < a.D;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int e = i * VEC + j;
-                xh[e] = in ? (xh[e] - mean) * rstd : 0.f;
-                dw[e] = fmaf(g[e], xh[e], dw[e]);
-                db[e] += g[e];
-                g[e] *= w[e];
-                s[0] += g[e];
-                s[1] = fmaf(g[e], xh[e], s[1]);
-            }
+        for (int p = 0; p < NP; ++p) {
+            xh[p] = mul2(add2(xh[p], both(-mean)), both(rstd));
+            dw[p] = fma2(g[p], xh[p], dw[p]);
+            db[p] = add2(db[p], g[p]);
+            g[p] = mul2(g[p], w[p]);
+            s0 = add2(s0, g[p]);
+            s1 = fma2(g[p], xh[p], s1);
         }
+        float s[2] = {lo(s0) + hi(s0), lo(s1) + hi(s1)};
         row_sums<TPR, 2>(s, red[phase]);
-        if (row >= a.rows) continue;
         const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (c >= a.D) continue;
-            float o[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int e = i * VEC + j;
-                o[j] = rstd * (g[e] - m1 - xh[e] * m2);
-            }
-            store_raw<T, VEC>(dx + row * a.D + c, pack<T, VEC>(o));
-        }
+        for (int p = 0; p < NP; ++p) g[p] = mul2(fma2(xh[p], both(-m2), add2(g[p], both(-m1))), both(rstd));
+        store_row<T, TPR, VEC, NV>(dx + row * a.D, a.D, t, g);
     }
     if (!a.partial) return;
     float *pw = a.partial + 2ll * blockIdx.x * a.D, *pb = pw + a.D;
@@ -220,7 +289,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, tru
 #pragma unroll
         for (int i = 0; i < NV * VEC; ++i) {
             const int c = (i / VEC * TPR + t) * VEC + i % VEC;
-            if (c < a.D) pw[c] = dw[i], pb[c] = db[i];
+            if (c < a.D) pw[c] = half(dw[i / 2], i), pb[c] = half(db[i / 2], i);
         }
     } else {
         // the warps' sums, added in the warps' order
@@ -231,8 +300,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, tru
 #pragma unroll
                 for (int i = 0; i < NV * VEC; ++i) {
                     const int c = (i / VEC * TPR + t) * VEC + i % VEC;
-                    sum[0][c] = (r ? sum[0][c] : 0.f) + dw[i];
-                    sum[1][c] = (r ? sum[1][c] : 0.f) + db[i];
+                    sum[0][c] = (r ? sum[0][c] : 0.f) + half(dw[i / 2], i);
+                    sum[1][c] = (r ? sum[1][c] : 0.f) + half(db[i / 2], i);
                 }
             }
             __syncthreads();
@@ -303,17 +372,18 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_bwd_kernel(NormArgs a) {
     }
 }
 
-// dw, db from the blocks' partial rows, in the blocks' order: eight row groups
-// of 32 columns per block, then the groups in order.
-__global__ void __launch_bounds__(256) layer_norm_reduce_kernel(const float *partial, int rows, int D, float *dw,
-                                                                float *db) {
-    __shared__ float sum[2][8][32];
+// dw, db from the blocks' partial rows, in the blocks' order: 32 row groups of
+// 32 columns per block, then the groups in order.
+__global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const float *partial, int rows, int D, float *dw,
+                                                                 float *db) {
+    __shared__ float sum[2][32][32];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s0 = 0.f, s1 = 0.f;
+    grid_dependency_wait();
     if (c < D) {
 #pragma unroll 4
-        for (int r = grp; r < rows; r += 8) {
+        for (int r = grp; r < rows; r += 32) {
             s0 += partial[2ll * r * D + c];
             s1 += partial[(2ll * r + 1) * D + c];
         }
@@ -324,7 +394,7 @@ __global__ void __launch_bounds__(256) layer_norm_reduce_kernel(const float *par
     if (grp < 2 && c < D) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sum[grp][i][lane];
+        for (int i = 0; i < 32; ++i) s += sum[grp][i][lane];
         float *out = grp ? db : dw;
         if (out) out[c] = s;
     }
@@ -342,13 +412,23 @@ int norm_grid(long long rows, int D, bool bwd) {
     return (int)std::min<long long>((rows + rpb - 1) / rpb, (long long)device_sm_count() * norm_blocks_per_sm(tpr, bwd));
 }
 
+template <typename T, int TPR, int VEC, int NV, bool BWD>
+cudaError_t launch_norm_one(const NormArgs &a, int grid, cudaStream_t s) {
+    constexpr int smem = NormStages<T, TPR, VEC, NV, BWD ? 2 : 1>::smem;
+    void (*kernel)(NormArgs);
+    if constexpr (BWD) kernel = layer_norm_bwd_kernel<T, TPR, VEC, NV>;
+    else kernel = layer_norm_fwd_kernel<T, TPR, VEC, NV>;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<grid, norm_threads(TPR), smem, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, int VEC, bool BWD>
 cudaError_t launch_norm(const NormArgs &a, int grid, cudaStream_t s) {
-#define GDN_NORM(TPR, EPT)                                                                                      \
-    do {                                                                                                        \
-        if constexpr (BWD) layer_norm_bwd_kernel<T, TPR, VEC, (EPT) / VEC><<<grid, norm_threads(TPR), 0, s>>>(a); \
-        else layer_norm_fwd_kernel<T, TPR, VEC, (EPT) / VEC><<<grid, norm_threads(TPR), 0, s>>>(a);               \
-    } while (0)
+#define GDN_NORM(TPR, EPT) return launch_norm_one<T, TPR, VEC, (EPT) / VEC, BWD>(a, grid, s)
     if (a.D <= 256) GDN_NORM(32, 8);
     else if (a.D <= 512) GDN_NORM(32, 16);
     else if (a.D <= 1024) GDN_NORM(128, 8);
@@ -441,9 +521,8 @@ extern "C" gdn_status gdn_layer_norm_bwd(const void *dy, int64_t dy_stride, cons
                               : gdn::launch_norm_typed<float, true>(a, grid, s);
     }
     if (e == cudaSuccess && params) {  // no rows: the sums are zero
-        gdn::layer_norm_reduce_kernel<<<(D + 31) / 32, 256, 0, s>>>(static_cast<const float *>(workspace),
-                                                                   rows > 0 ? grid : 0, D, dweight, dbias);
-        e = cudaGetLastError();
+        e = gdn::launch_dependent(gdn::layer_norm_reduce_kernel, dim3((D + 31) / 32), dim3(1024), 0, s,
+                                  static_cast<const float *>(workspace), rows > 0 ? grid : 0, D, dweight, dbias);
     }
     if (e != cudaSuccess) {
         gdn::set_error_detail("launch layer_norm_bwd", e);

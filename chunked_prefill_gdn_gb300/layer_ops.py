@@ -67,13 +67,20 @@ def bind(lib):
             ("gdn_delta_step", i32, [vp] * 7 + [i32, f32] + [i32] * 6 + [vp, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
+    global _bound
+    _bound = lib
 
 
 # ------------------------------------------------------------------ arguments
 
+_bound = None   # the loaded library
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    if _bound is None:
+        from . import load_library
+        load_library()
+    return _bound
 
 
 def _raise(status, where):
@@ -146,7 +153,7 @@ class _On:
         if device.index != torch.cuda.current_device():
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
-        self.raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+        self.raw = _current_raw_stream(device.index) if stream is None else stream.cuda_stream
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
@@ -158,6 +165,12 @@ class _On:
         if self.guard is not None:
             self.guard.__exit__(None, None, None)
             self.guard = None
+
+
+# torch.cuda.current_stream(device).cuda_stream without the Stream object in
+# between (2 us of a single-token call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _p(t):
@@ -235,12 +248,10 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None,
     on = _On(dev, stream)
     try:
         y = out if out is not None else on.empty(x.shape, dtype)
-        stats = on.empty((2, *lead), _F32)
-        mean, rstd = stats[0], stats[1]
+        mean, rstd = on.empty(lead, _F32), on.empty(lead, _F32)
         rows = mean.numel()
-        p = stats.data_ptr()
         st = _lib().gdn_layer_norm_fwd(x.data_ptr(), stride, _p(weight), _p(bias), wcode, eps, rows, D, _CODE[dtype],
-                                       y.data_ptr(), p, p + 4 * rows, on.raw)
+                                       y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), on.raw)
         if st != 0:
             _raise(st, "gdn_layer_norm_fwd")
     finally:
@@ -437,31 +448,35 @@ def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activ
 # ------------------------------------------------------- selective state space scan
 
 def _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens):
-    """Checks the scan's inputs ([Bt, T, D] activations) and fills the
-    descriptor; returns (descriptor, number of sequences)."""
+    """Checks the scan's inputs (activations [Bt, T, D], or [Bt, D] for one
+    token) and fills the descriptor; returns (descriptor, number of sequences)."""
     _act("x", x)
-    if x.dim() != 3 or A.dim() != 2:
-        raise ValueError("x must be [B, T, D] and A [D, N]")
-    Bt, T, Dn = x.shape
-    N, dev, dtype = A.shape[1], x.device, x.dtype
+    lead, dev, dtype = x.shape[:-1], x.device, x.dtype
+    Dn, N = A.shape
+    one = len(lead) == 1
     _like("dt", dt, x.shape, dtype, dev, strided=True)
-    _like("A", A, (Dn, N), _F32, dev)
-    _like("B", B, (Bt, T, N), dtype, dev, strided=True)
-    _like("C", C, (Bt, T, N), dtype, dev, strided=True)
+    _like("A", A, (x.shape[-1], N), _F32, dev)
+    _like("B", B, (*lead, N), dtype, dev, strided=True)
+    _like("C", C, (*lead, N), dtype, dev, strided=True)
     if z is not None:
         _like("z", z, x.shape, dtype, dev, strided=True)
     if D is not None:
         _like("D", D, (Dn,), _F32, dev)
     if dt_bias is not None:
         _like("dt_bias", dt_bias, (Dn,), _F32, dev)
+    Bt, T = (lead[0], 1) if one else lead
     n = _sequences(cu_seqlens, Bt, dev)
     if initial_state is not None:
         _like("initial_state", initial_state, (n, Dn, N), _F32, dev)
-    zs = _strides("z", z) if z is not None else (0, Dn)
+    if one:
+        strides = (x.stride(0), Dn, dt.stride(0), Dn, z.stride(0) if z is not None else 0, Dn, B.stride(0), N,
+                   C.stride(0), N)
+    else:
+        strides = (*_strides("x", x), *_strides("dt", dt), *(_strides("z", z) if z is not None else (0, Dn)),
+                   *_strides("B", B), *_strides("C", C))
     return GdnScanDesc(x.data_ptr(), dt.data_ptr(), _p(z), B.data_ptr(), C.data_ptr(), A.data_ptr(), _p(D),
-                       _p(dt_bias), _p(initial_state), _p(cu_seqlens), *_strides("x", x), *_strides("dt", dt), *zs,
-                       *_strides("B", B), *_strides("C", C), Bt, T, Dn, N, n, 1 if dt_softplus else 0, _CODE[dtype],
-                       0), n
+                       _p(dt_bias), _p(initial_state), _p(cu_seqlens), *strides, Bt, T, Dn, N, n,
+                       1 if dt_softplus else 0, _CODE[dtype], 0), n
 
 
 def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = True, initial_state=None,
@@ -469,6 +484,8 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
                        check: bool = False):
     """Selective scan of x [Bt, T, D] (dt, z alike) with A [D, N] float32 and
     B, C [Bt, T, N]; returns (y, final_state), final_state float32 [n, D, N]."""
+    if x.dim() != 3 or A.dim() != 2:
+        raise ValueError("x must be [B, T, D] and A [D, N]")
     desc, n = _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     if out is not None:
         _like("out", out, x.shape, x.dtype, x.device)
@@ -497,6 +514,8 @@ def selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
     used, d_final_state: (dx, ddt, dA, dB, dC, dD, dz, d_dt_bias,
     d_initial_state); dz is None without z.  dA, dD, d_dt_bias and the state's
     gradient are float32, the others in x's type."""
+    if x.dim() != 3 or A.dim() != 2:
+        raise ValueError("x must be [B, T, D] and A [D, N]")
     desc, n = _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     dev, dtype = x.device, x.dtype
     _like("dy", dy, x.shape, dtype, dev, strided=True)
@@ -530,10 +549,9 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     [Bt, N], state float32 [S, D, N] updated in place (row r uses
     state_indices[r], or r); returns y [Bt, D].  A row whose index is outside
     [0, S) is padding: y is zero there."""
-    if x.dim() != 2:
-        raise ValueError("x must be [N, D]")
-    one = lambda t: t.unsqueeze(1) if t is not None and t.dim() == 2 else t   # noqa: E731
-    desc, _ = _scan_desc(one(x), one(dt), A, one(B), one(C), D, one(z), dt_bias, dt_softplus, None, None)
+    if x.dim() != 2 or A.dim() != 2:
+        raise ValueError("x must be [N, D] and A [D, N]")
+    desc, _ = _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, None, None)
     _like("state", state, (state.shape[0], desc.D, desc.N), _F32, x.device)
     _slots(state, state_indices, desc.B, x.device)
     if out is not None:
