@@ -32,8 +32,7 @@ namespace {
 
 // Measured at 65536 packed tokens x 6144 channels forward, 4 x 4095 x 4096
 // backward (bf16): 4 warps and runs of 64 give 313 / 117 us, 8 warps 289 / 115,
-// with runs of 128 too 275 / 110 (more would leave small problems without
-// warps: 16 warps 361, runs of 256 279); four rows ahead 318 us forward, 16 348;
+// with runs of 128 too 275 / 110 (16 warps 361, runs of 256 279); four rows ahead 318 us forward, 16 348;
 // four rows of both inputs ahead backward 110 us, six 103, eight (with runs of
 // 64) 121.  Eight channels per thread instead of four: 320 / 135 us, for want of
 // registers.
@@ -478,15 +477,23 @@ cudaError_t launch_conv(ConvArgs a, int W, bool vec, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Tokens per warp: fewer than kConvRun where the problem would not give every SM
-// about 16 warps.
-int conv_run(int B, int T, int D, int vec) {
-    const long long warps_wanted = 16ll * device_sm_count();
-    const int chan = (D + 32 * vec - 1) / (32 * vec);
-    int run = kConvRun;
-    while (run > kSub && (long long)B * ((T + run - 1) / run) * chan < warps_wanted) run >>= 1;
+// Tokens per warp: the run that gives the shortest schedule when an SM holds
+// `resident` blocks, counting for each run its tokens and about 16 more (halo,
+// weights, filling and draining the ring of rows).  At 4 x 4095 tokens x 4096
+// channels the backward pass runs 1.7 waves of blocks with runs of 128 and 2.95
+// with runs of 74.
+int conv_run(int B, int T, int D, int vec, int resident) {
+    const long long chan = (D + 32 * vec - 1) / (32 * vec), slots = (long long)resident * device_sm_count();
+    long long best = -1;
+    int run = kSub;
+    for (int r = kSub; r <= kConvRun; r += 2) {
+        const long long blocks = B * chan * ((T + r * kConvWarps - 1) / (r * kConvWarps));
+        const long long cost = (blocks + slots - 1) / slots * (r + 16);
+        if (best < 0 || cost < best) best = cost, run = r;
+    }
     return run;
 }
+constexpr int kConvResident = 3, kConvResidentB = 2;   // blocks per SM by registers
 
 // Groups of kConvWarps runs over all batch rows (at least one per row).
 int conv_groups(int B, int T, int run) { return B * std::max(1, (T + run * kConvWarps - 1) / (run * kConvWarps)); }
@@ -541,7 +548,7 @@ extern "C" gdn_status gdn_causal_conv_fwd(const void *x, int64_t x_batch_stride,
     a.x = x, a.w = weight, a.bias = bias, a.init = initial_state, a.out = y, a.last = final_state;
     a.cu = cu_seqlens, a.status = device_status, a.x_batch = x_batch_stride, a.x_token = x_token_stride;
     a.B = B, a.T = T, a.D = D, a.n_seqs = cu_seqlens ? n_seqs : B, a.w_f32 = w_dtype == GDN_F32, a.silu = silu != 0;
-    a.run = conv_run(B, T, D, vec ? 4 : 1);
+    a.run = conv_run(B, T, D, vec ? 4 : 1, kConvResident);
     a.groups = conv_groups(B, T, a.run);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == GDN_BF16 ? launch_conv<Conv::kFwd, __nv_bfloat16>(a, W, vec, s)
@@ -556,7 +563,8 @@ extern "C" gdn_status gdn_causal_conv_fwd(const void *x, int64_t x_batch_stride,
 extern "C" size_t gdn_causal_conv_bwd_workspace_size(int B, int T, int D, int W) {
     if (B < 0 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
     // the narrower of the two layouts needs more groups: room for either
-    const int g4 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 4)), g1 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 1));
+    const int g4 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 4, gdn::kConvResidentB));
+    const int g1 = gdn::conv_groups(B, T, gdn::conv_run(B, T, D, 1, gdn::kConvResidentB));
     return std::max<size_t>(16, (size_t)std::max(g4, g1) * (W + 1) * (size_t)D * sizeof(float));
 }
 
@@ -593,7 +601,7 @@ extern "C" gdn_status gdn_causal_conv_bwd(const void *dy, int64_t dy_batch_strid
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (B > 0) {
-        a.run = conv_run(B, T, D, vec ? 4 : 1);
+        a.run = conv_run(B, T, D, vec ? 4 : 1, kConvResidentB);
         a.groups = conv_groups(B, T, a.run);
         e = dtype == GDN_BF16 ? launch_conv<Conv::kBwd, __nv_bfloat16>(a, W, vec, s)
                               : launch_conv<Conv::kBwd, float>(a, W, vec, s);

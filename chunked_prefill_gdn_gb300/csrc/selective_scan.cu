@@ -29,38 +29,56 @@ namespace gdn {
 
 namespace {
 
-// One warp per block and 32 / LP channels per warp; NPL values of n per thread.
-// Inputs are staged tile by tile: asynchronous copies of the raw rows, two tiles
-// in flight, each piece read back by the lane that copied it.
-constexpr int kScanTile = 16;   // tokens per staged tile
+constexpr int kScanTile = 16;   // tokens per tile
 
-template <typename T, int NPL, int LP, bool STATE_ONLY>
+// 32 channels per block.  NW warps scan, a lane per channel, sharing out the n,
+// NPT per thread; one more warp feeds them: it copies the raw rows in
+// asynchronously (three tiles in flight, each piece read back by the lane that
+// copied it), prepares the steps and B and C of the next tile in fp32, and
+// finishes the outputs of the last one, all while the current tile is scanned.
+template <typename T, int NPT, int NW, bool STATE_ONLY>
 struct ScanShape {
-    static constexpr int CW = 32 / LP;             // channels of the warp
-    static constexpr int NP = NPL * LP;            // n, padded
-    static constexpr int VPR = CW / 8;             // vectors of eight channels per row
-    static constexpr int RPP = 32 / VPR;           // rows per pass of the copying lanes
-    static constexpr int PASSES = kScanTile / RPP > 0 ? kScanTile / RPP : 1;
-    static constexpr int BCV = kScanTile * 2 * (NP / 8) / 32 > 0 ? kScanTile * 2 * (NP / 8) / 32 : 1;   // vectors of B, C per lane
+    static constexpr int CW = 32;
+    static constexpr int NP = NPT * NW;                     // n, padded
+    static constexpr int VPR = CW / 8;                      // vectors of eight channels per row
+    static constexpr int RPP = 32 / VPR;                    // rows per pass of the feeding warp
+    static constexpr int PASSES = kScanTile / RPP;
+    static constexpr int BCR = NP / 4;                      // vectors of eight n per row of B and C
+    static constexpr int BCP = 32 / BCR;                    // rows of B and C per pass
+    static constexpr int BCV = kScanTile / BCP;
     static constexpr int ARRAYS = STATE_ONLY ? 2 : 3;
     // rows of 8-byte entries per channel, shifted by a quarter of a bank row so that
     // the four rows written together do not meet in a bank
     static constexpr int SD = CW * 2 + 8;
     static constexpr int YS = CW + 4;
+    static constexpr size_t rows_bytes = 3 * ARRAYS * PASSES * 32 * 8 * sizeof(T);
+    static constexpr size_t bcr_bytes = 2 * BCV * 32 * 8 * sizeof(T);
+    static constexpr size_t smem = rows_bytes + bcr_bytes + 2 * kScanTile * (SD + 2 * NP + (STATE_ONLY ? 0 : NW * YS)) * 4;
 };
 
-template <typename T, int NPL, int LP, bool STATE_ONLY>
-__global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
-    using S = ScanShape<T, NPL, LP, STATE_ONLY>;
-    constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPL / 2;
-    __shared__ __align__(16) T rows[2][S::ARRAYS][PASSES][32][8];   // raw x, dt, z: one vector per lane and pass
-    __shared__ __align__(16) T bcr[2][S::BCV][32][8];
-    __shared__ __align__(16) float sd[kScanTile][S::SD];            // step, step * x
-    __shared__ __align__(16) float bc[kScanTile][2][NP];
-    __shared__ __align__(16) float ys[STATE_ONLY ? 1 : kScanTile][S::YS];
+template <typename T, int NPT, int NW, bool STATE_ONLY>
+__global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) scan_kernel(ScanArgs a) {
+    using S = ScanShape<T, NPT, NW, STATE_ONLY>;
+    constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPT / 2, TILE = kScanTile;
+    extern __shared__ __align__(16) unsigned char smem[];
+    using Piece = T[8];
+    Piece *rows = reinterpret_cast<Piece *>(smem);                              // [3][ARRAYS][PASSES][lane]
+    Piece *bcr = reinterpret_cast<Piece *>(smem + S::rows_bytes);               // [2][BCV][lane]
+    float *sd = reinterpret_cast<float *>(smem + S::rows_bytes + S::bcr_bytes); // [2][TILE][SD]: step, step * x
+    float *bc = sd + 2 * TILE * S::SD;                                          // [2][TILE][2][NP]
+    float *ys = bc + 2 * TILE * 2 * NP;                                         // [2][NW][TILE][YS]
 
     if (!STATE_ONLY && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
-    const int lane = threadIdx.x;
+    const int lane = threadIdx.x & 31;
+    int warp = threadIdx.x >> 5;
+    if (NW == 1) {
+        // Two warps of a block lie on neighbouring schedulers of the SM's four: were the
+        // first one always the scanning one, half of the schedulers would feed only.
+        __shared__ unsigned slot;
+        if (threadIdx.x == 0) asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+        __syncthreads();
+        warp ^= slot >> 2 & 1;
+    }
     const int chan0 = (blockIdx.x % a.chan_blocks) * CW;
     // the last segment of a row needs no map
     const int spr = STATE_ONLY ? a.segs - 1 : a.segs;
@@ -69,12 +87,123 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
     const int seg = r.b * a.segs + blockIdx.x / a.chan_blocks % spr;
     r.t0 = (seg - r.b * a.segs) * a.seg_tokens;
     r.t1 = min(a.T, r.t0 + a.seg_tokens);
+    const int tiles = r.t0 < r.t1 ? (r.t1 - r.t0 + TILE - 1) / TILE : 0;
 
-    // copying: lane -> (row of the pass, eight channels).  Scanning: the channels
-    // in the order in which the copying lanes lay them down, so that neither side
-    // meets in a bank.
-    const int lv = lane % VPR, lrow = lane / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
-    const int part = lane % LP, n0 = part * NPL, pos = lane / LP, ch = chan0 + pos % VPR * 8 + pos / VPR;
+    if (warp == NW) {   // the feeding warp: lane -> (row of the pass, eight channels)
+        if (tiles == 0) return;
+        const int lv = lane % VPR, lrow = lane / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
+        const bool gated = !STATE_ONLY && a.z != nullptr;
+        const long long first = r.t0 + lrow;
+        const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + first * a.x_token + lc;
+        const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + first * a.dt_token + lc;
+        const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + first * a.z_token + lc;
+        T *py = STATE_ONLY ? nullptr : static_cast<T *>(a.out) + ((long long)r.b * a.T + first) * a.D + lc;
+        const int bcc = lane / (NP / 8) % 2, bcn = lane % (NP / 8) * 8, bcrow = lane / S::BCR;
+        const long long bc_token = bcc ? a.c_token : a.b_token;
+        const T *pbc = (bcc ? static_cast<const T *>(a.Cm) + r.b * a.c_batch : static_cast<const T *>(a.Bm) + r.b * a.b_batch) +
+                       (r.t0 + bcrow) * bc_token + bcn;
+        const bool whole = a.vec && lrest >= 8 && a.bc_vec && a.N - bcn >= 8;
+        auto piece = [&](int k, int array, int i) -> T * { return rows[((k % 3 * S::ARRAYS + array) * PASSES + i) * 32 + lane]; };
+        auto bc_piece = [&](int k, int i) -> T * { return bcr[(k % 2 * S::BCV + i) * 32 + lane]; };
+        F2 bias[4], skip[4];
+        load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
+        load_pairs(!STATE_ONLY && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
+        auto stage = [&](int k) {   // copies tile k and moves the pointers on to the next
+            const int t = r.t0 + k * TILE;
+            if (whole && t + TILE <= r.t1) {
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {
+                    copy8_whole<T>(piece(k, 0, i), px + i * RPP * a.x_token);
+                    copy8_whole<T>(piece(k, 1, i), pd + i * RPP * a.dt_token);
+                    if (gated) copy8_whole<T>(piece(k, 2, i), pz + i * RPP * a.z_token);
+                }
+#pragma unroll
+                for (int i = 0; i < S::BCV; ++i) copy8_whole<T>(bc_piece(k, i), pbc + i * S::BCP * bc_token);
+            } else if (t < r.t1) {
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {
+                    const int n = t + i * RPP + lrow < r.t1 ? lrest : 0;
+                    copy8_async<T>(piece(k, 0, i), px + i * RPP * a.x_token, n, a.vec);
+                    copy8_async<T>(piece(k, 1, i), pd + i * RPP * a.dt_token, n, a.vec);
+                    if (gated) copy8_async<T>(piece(k, 2, i), pz + i * RPP * a.z_token, n, a.vec);
+                }
+#pragma unroll
+                for (int i = 0; i < S::BCV; ++i)
+                    copy8_async<T>(bc_piece(k, i), pbc + i * S::BCP * bc_token,
+                                   t + i * S::BCP + bcrow < r.t1 ? a.N - bcn : 0, a.bc_vec);
+            }
+            px += TILE * a.x_token, pd += TILE * a.dt_token, pz += TILE * a.z_token;
+            pbc += TILE * bc_token;
+            copy_commit();
+        };
+        auto prepare = [&](int k) {
+            float *s_at = sd + k % 2 * TILE * S::SD, *bc_at = bc + k % 2 * TILE * 2 * NP;
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                float *at = s_at + (i * RPP + lrow) * S::SD + lv * 2;
+                F2 x[4], d[4];
+                unpack_pairs<T>(load_raw<T, 8>(piece(k, 0, i)), x);
+                unpack_pairs<T>(load_raw<T, 8>(piece(k, 1, i)), d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    d[e] = add2(d[e], bias[e]);
+                    const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
+                    *reinterpret_cast<float2 *>(at + 2 * e * VPR * 2) = make_float2(lo(s), lo(sx));
+                    *reinterpret_cast<float2 *>(at + (2 * e + 1) * VPR * 2) = make_float2(hi(s), hi(sx));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < S::BCV; ++i) {
+                F2 f[4];
+                unpack_pairs<T>(load_raw<T, 8>(bc_piece(k, i)), f);
+                ulonglong2 *at = reinterpret_cast<ulonglong2 *>(bc_at + ((i * S::BCP + bcrow) * 2 + bcc) * NP + bcn);
+                at[0] = make_ulonglong2(f[0], f[1]);
+                at[1] = make_ulonglong2(f[2], f[3]);
+            }
+        };
+        auto finish = [&](int k) {
+            const float *y_at = ys + k % 2 * NW * TILE * S::YS;
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int q = i * RPP + lrow;
+                if (r.t0 + k * TILE + q >= r.t1) continue;
+                F2 x[4], z[4];
+                float o[8];
+                unpack_pairs<T>(load_raw<T, 8>(piece(k, 0, i)), x);
+                if (gated) unpack_pairs<T>(load_raw<T, 8>(piece(k, 2, i)), z);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *at = y_at + q * S::YS + 2 * e * VPR + lv;
+                    F2 y = pair(at[0], at[VPR]);
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) y = add2(y, pair(at[w * TILE * S::YS], at[w * TILE * S::YS + VPR]));
+                    y = fma2(skip[e], x[e], y);
+                    if (gated) y = mul2(y, mul2(z[e], sigmoid_pair(z[e])));
+                    o[2 * e] = lo(y), o[2 * e + 1] = hi(y);
+                }
+                store8<T>(py + (long long)i * RPP * a.D, o, lrest, a.vec);
+            }
+            py += (long long)TILE * a.D;
+        };
+        stage(0);
+        stage(1);
+        copy_wait<1>();
+        prepare(0);
+        __syncthreads();
+        for (int k = 0; k < tiles; ++k) {
+            if (!STATE_ONLY && k > 0) finish(k - 1);
+            stage(k + 2);
+            copy_wait<1>();
+            if (k + 1 < tiles) prepare(k + 1);
+            __syncthreads();
+        }
+        if (!STATE_ONLY) finish(tiles - 1);
+        return;
+    }
+
+    // a scanning warp: the channels in the order in which the feeding lanes lay
+    // them down, so that neither side meets in a bank
+    const int n0 = warp * NPT, ch = chan0 + lane % VPR * 8 + lane / VPR;
     const bool live = ch < a.D;
     if (!STATE_ONLY && a.final_state && live) {    // a sequence without a token keeps its state
         auto keep = [&](int n) {
@@ -87,55 +216,7 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
         for (int n = seg; a.cu && n < a.n_seqs; n += a.segs)
             if (__ldg(a.cu + n) >= __ldg(a.cu + n + 1)) keep(n);
     }
-    if (r.t0 >= r.t1) return;
-
-    const bool gated = !STATE_ONLY && a.z != nullptr;
-    const long long first = r.t0 + lrow;
-    const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + first * a.x_token + lc;
-    const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + first * a.dt_token + lc;
-    const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + first * a.z_token + lc;
-    // the lane's piece of a tile's rows of B and C
-    constexpr int BCR = NP / 4;                    // vectors per row of both
-    const int bcc = lane / (NP / 8) % 2, bcn = lane % (NP / 8) * 8;
-    const long long bc_token = bcc ? a.c_token : a.b_token;
-    const T *pbc = (bcc ? static_cast<const T *>(a.Cm) + r.b * a.c_batch : static_cast<const T *>(a.Bm) + r.b * a.b_batch) +
-                   (long long)(r.t0 + lane / BCR) * bc_token + bcn;
-    const bool whole = a.vec && lrest >= 8 && a.bc_vec && a.N - bcn >= 8;
-    auto stage = [&](int t, int buf) {             // copies tile t and moves the pointers on to the next
-        if (whole && t + kScanTile <= r.t1) {
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                if (RPP > kScanTile && lrow >= kScanTile) break;
-                copy8_whole<T>(rows[buf][0][i][lane], px + i * RPP * a.x_token);
-                copy8_whole<T>(rows[buf][1][i][lane], pd + i * RPP * a.dt_token);
-                if (gated) copy8_whole<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + i * RPP * a.z_token);
-            }
-#pragma unroll
-            for (int i = 0; i < S::BCV; ++i)
-                if (32 / BCR <= kScanTile || lane / BCR < kScanTile)
-                    copy8_whole<T>(bcr[buf][i][lane], pbc + i * (32 / BCR) * bc_token);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int q = i * RPP + lrow, n = q < kScanTile && t + q < r.t1 ? lrest : 0;
-                copy8_async<T>(rows[buf][0][i][lane], px + i * RPP * a.x_token, n, a.vec);
-                copy8_async<T>(rows[buf][1][i][lane], pd + i * RPP * a.dt_token, n, a.vec);
-                if (!STATE_ONLY)
-                    copy8_async<T>(rows[buf][S::ARRAYS - 1][i][lane], pz + i * RPP * a.z_token, gated ? n : 0, a.vec);
-            }
-#pragma unroll
-            for (int i = 0; i < S::BCV; ++i) {
-                const int q = i * (32 / BCR) + lane / BCR;
-                copy8_async<T>(bcr[buf][i][lane], pbc + i * (32 / BCR) * bc_token,
-                               q < kScanTile && t + q < r.t1 ? a.N - bcn : 0, a.bc_vec);
-            }
-        }
-        px += kScanTile * a.x_token, pd += kScanTile * a.dt_token, pz += kScanTile * a.z_token;
-        pbc += kScanTile * bc_token;
-        copy_commit();
-    };
-    stage(r.t0, 0);
-
+    if (tiles == 0) return;
     F2 A2[M], h[M];
     load_pairs(a.A + (long long)ch * a.N, n0, a.N, live, A2);
 #pragma unroll
@@ -149,70 +230,42 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
     if (starts) initial(r.n);
     else load_pairs(!STATE_ONLY && a.has_carry ? a.hloc + ((long long)seg * a.D + ch) * NP : nullptr, n0, NP, live, h);
     float step_sum = 0.f;
-    F2 bias[4], skip[4];
-    load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
-    load_pairs(!STATE_ONLY && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
-
-    T *py = STATE_ONLY ? nullptr : static_cast<T *>(a.out) + ((long long)r.b * a.T + r.t0 + lrow) * a.D + lc;
-    int buf = 0;
-    for (int t = r.t0; t < r.t1; t += kScanTile, buf ^= 1) {
-        stage(t + kScanTile, buf ^ 1);
-        copy_wait<1>();
+    auto token = [&](int j, const float *s_at, const float *bc_at, float *y_at) {
+        const float2 sv = *reinterpret_cast<const float2 *>(s_at + j * S::SD);
+        const F2 ss = both(sv.x), sx = both(sv.y);
+        const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP);
+        const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP + NP);
+        F2 y0 = both(0.f), y1 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int q = i * RPP + lrow;
-            if (q >= kScanTile) continue;
-            F2 x[4], d[4];
-            unpack_pairs<T>(load_raw<T, 8>(rows[buf][0][i][lane]), x);
-            unpack_pairs<T>(load_raw<T, 8>(rows[buf][1][i][lane]), d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[e] = add2(d[e], bias[e]);
-                const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
-                *reinterpret_cast<float2 *>(&sd[q][(2 * e * VPR + lv) * 2]) = make_float2(lo(s), lo(sx));
-                *reinterpret_cast<float2 *>(&sd[q][((2 * e + 1) * VPR + lv) * 2]) = make_float2(hi(s), hi(sx));
+        for (int i = 0; i < M / 2; ++i) {
+            const ulonglong2 b = Bk[i];
+            h[2 * i] = fma2(exp2_pair(mul2(ss, A2[2 * i])), h[2 * i], mul2(sx, b.x));
+            h[2 * i + 1] = fma2(exp2_pair(mul2(ss, A2[2 * i + 1])), h[2 * i + 1], mul2(sx, b.y));
+            if (!STATE_ONLY) {
+                const ulonglong2 c = Ck[i];
+                y0 = i ? fma2(c.x, h[2 * i], y0) : mul2(c.x, h[0]);
+                y1 = i ? fma2(c.y, h[2 * i + 1], y1) : mul2(c.y, h[1]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < S::BCV; ++i) {
-            const int q = i * (32 / BCR) + lane / BCR;
-            if (q >= kScanTile) continue;
-            F2 f[4];
-            unpack_pairs<T>(load_raw<T, 8>(bcr[buf][i][lane]), f);
-            *reinterpret_cast<ulonglong2 *>(&bc[q][bcc][bcn]) = make_ulonglong2(f[0], f[1]);
-            *reinterpret_cast<ulonglong2 *>(&bc[q][bcc][bcn + 4]) = make_ulonglong2(f[2], f[3]);
+        if (STATE_ONLY) {
+            step_sum += sv.x;
+        } else {
+            y0 = add2(y0, y1);
+            y_at[j * S::YS] = lo(y0) + hi(y0);
         }
-        __syncwarp();
-        const int stop = min(r.t1, t + kScanTile);
+    };
+    __syncthreads();
+    for (int k = 0; k < tiles; ++k) {
+        const int t = r.t0 + k * TILE, stop = min(r.t1, t + TILE);
+        const float *s_at = sd + k % 2 * TILE * S::SD + lane * 2, *bc_at = bc + k % 2 * TILE * 2 * NP + n0;
+        float *y_at = ys + (k % 2 * NW + warp) * TILE * S::YS + lane;
         for (int q = t; q < stop;) {
             const int run_end = min(stop, r.end);
-#pragma unroll 4
-            for (int k = q - t; k < run_end - t; ++k) {
-                const float2 sv = *reinterpret_cast<const float2 *>(&sd[k][pos * 2]);
-                const ulonglong2 s = make_ulonglong2(both(sv.x), both(sv.y));
-                const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(&bc[k][0][n0]);
-                const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(&bc[k][1][n0]);
-                F2 y0 = both(0.f), y1 = both(0.f);
+            if (run_end - q == TILE) {   // the usual case, with addresses known
 #pragma unroll
-                for (int i = 0; i < M / 2; ++i) {
-                    const ulonglong2 b = Bk[i];
-                    h[2 * i] = fma2(exp2_pair(mul2(s.x, A2[2 * i])), h[2 * i], mul2(s.y, b.x));
-                    h[2 * i + 1] = fma2(exp2_pair(mul2(s.x, A2[2 * i + 1])), h[2 * i + 1], mul2(s.y, b.y));
-                    if (!STATE_ONLY) {
-                        const ulonglong2 c = Ck[i];
-                        y0 = i ? fma2(c.x, h[2 * i], y0) : mul2(c.x, h[0]);
-                        y1 = i ? fma2(c.y, h[2 * i + 1], y1) : mul2(c.y, h[1]);
-                    }
-                }
-                if (STATE_ONLY) {
-                    step_sum += sv.x;
-                } else {
-                    y0 = add2(y0, y1);
-                    float v = lo(y0) + hi(y0);
-#pragma unroll
-                    for (int off = 1; off < LP; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                    if (LP == 1 || part == 0) ys[k][pos] = v;
-                }
+                for (int j = 0; j < TILE; ++j) token(j, s_at, bc_at, y_at);
+            } else {
+                for (int j = q - t; j < run_end - t; ++j) token(j, s_at, bc_at, y_at);
             }
             q = run_end;
             if (q == r.end) {   // the sequence is complete
@@ -225,35 +278,14 @@ __global__ void __launch_bounds__(32) scan_kernel(ScanArgs a) {
                 }
             }
         }
-        __syncwarp();
-        if (!STATE_ONLY) {
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int q = i * RPP + lrow;
-                if (q >= kScanTile || t + q >= r.t1) continue;
-                F2 x[4], z[4];
-                float o[8];
-                unpack_pairs<T>(load_raw<T, 8>(rows[buf][0][i][lane]), x);
-                unpack_pairs<T>(load_raw<T, 8>(rows[buf][S::ARRAYS - 1][i][lane]), z);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    F2 y = pair(ys[q][2 * e * VPR + lv], ys[q][(2 * e + 1) * VPR + lv]);
-                    y = fma2(skip[e], x[e], y);
-                    if (gated) y = mul2(y, mul2(z[e], sigmoid_pair(z[e])));
-                    o[2 * e] = lo(y), o[2 * e + 1] = hi(y);
-                }
-                store8<T>(py + (long long)i * RPP * a.D, o, lrest, a.vec);
-            }
-            py += (long long)kScanTile * a.D;
-            __syncwarp();   // ys is written again by the next tile
-        }
+        __syncthreads();
     }
     if (STATE_ONLY) {
         if (live) {
             store_pairs(a.hloc + ((long long)seg * a.D + ch) * NP, n0, NP, h);
-            if (part == 0) a.sums[(long long)seg * a.D + ch] = step_sum;
+            if (warp == 0) a.sums[(long long)seg * a.D + ch] = step_sum;
         }
-        if (chan0 == 0 && lane == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
+        if (chan0 == 0 && warp == 0 && lane == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
     }
 }
 
@@ -351,22 +383,30 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     }
 }
 
-template <typename T, int NPL, int LP>
-cudaError_t launch_scan_parts(ScanArgs a, cudaStream_t s) {
-    constexpr int CW = 32 / LP;
-    a.chan_blocks = (a.D + CW - 1) / CW;
-    a.has_carry = a.segs > 1;
-    if (a.segs > 1) {
-        scan_kernel<T, NPL, LP, true><<<(unsigned)((long long)a.chan_blocks * a.B * (a.segs - 1)), 32, 0, s>>>(a);
-        const cudaError_t e = launch_scan_combine(a, a.segs, false, s);
+template <typename T, int NPT, int NW, bool STATE_ONLY>
+cudaError_t launch_scan_one(const ScanArgs &a, int segs, cudaStream_t s) {
+    using S = ScanShape<T, NPT, NW, STATE_ONLY>;
+    if (S::smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, NPT, NW, STATE_ONLY>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
         if (e != cudaSuccess) return e;
     }
-    scan_kernel<T, NPL, LP, false><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), 32, 0, s>>>(a);
+    scan_kernel<T, NPT, NW, STATE_ONLY>
+        <<<(unsigned)((long long)a.chan_blocks * a.B * segs), 32 * (NW + 1), S::smem, s>>>(a);
     return cudaGetLastError();
 }
 
-// Channels of a warp by N, as launch_scan_typed picks them.
-int scan_warp_channels(int N) { return N <= 16 ? 32 : N <= 32 ? 16 : 8; }
+template <typename T, int NPT, int NW>
+cudaError_t launch_scan_parts(ScanArgs a, cudaStream_t s) {
+    a.chan_blocks = (a.D + 31) / 32;
+    a.has_carry = a.segs > 1;
+    if (a.segs > 1) {
+        cudaError_t e = launch_scan_one<T, NPT, NW, true>(a, a.segs - 1, s);
+        if (e == cudaSuccess) e = launch_scan_combine(a, a.segs, false, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_scan_one<T, NPT, NW, false>(a, a.segs, s);
+}
 
 template <typename T>
 cudaError_t launch_scan_typed(const ScanArgs &a, cudaStream_t s) {
@@ -390,8 +430,8 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 // Segments per row in the forward pass.  One segment takes each exponential
 // once; several take it twice but put that many times the warps to work.
 int scan_segments(int B, int T, int D, int N) {
-    const int ch = scan_warp_channels(N), tiles = (T + kScanTile - 1) / kScanTile;
-    const long long warps = (long long)B * ((D + ch - 1) / ch), wanted = 8ll * device_sm_count();
+    const int tiles = (T + kScanTile - 1) / kScanTile;
+    const long long warps = (long long)B * ((D + 31) / 32) * (N <= 16 ? 1 : N <= 32 ? 2 : 4), wanted = 7ll * device_sm_count();
     if (tiles <= 1 || 2 * warps >= wanted) return 1;
     const int segs = (int)std::min<long long>((wanted + warps - 1) / warps, tiles);
     const int len = (tiles + segs - 1) / segs;
