@@ -6,7 +6,7 @@
 
 namespace gdn {
 
-constexpr int kTile = 32;   // tokens per tile
+constexpr int kTile = 16;   // tokens per tile
 
 // log(1 + exp(x)) = max(x, 0) + log(1 + t), t = exp(-|x|) in [0, 1], with
 // log(1 + t) = 2 artanh(r), r = t / (2 + t) <= 1/3: no cancellation at either
@@ -33,13 +33,17 @@ struct ScanArgs {
     float *final_state;
     void *ddt, *dz;
     float *dinit;
-    // workspace: per segment (forward) or per tile (backward) and channel
-    float *hloc, *gloc, *sums;       // [maps][D][NP], [maps][D][NP], [maps][D]
-    int32_t *flags;                  // [maps]: bit 0 a sequence starts at its first token, bit 1 at a later one
+    // workspace: the segments' maps, [segments][D][NP] and [segments][D]
+    float *hloc, *gloc, *sums;
+    int32_t *flags;                  // [segments]: bit 0 a sequence starts at its first token, bit 1 at a later one
+    // backward: every tile's start state and the steps before it, from a zero start
+    // of its segment, [tiles][D][NP] and [tiles][D] (nothing for a segment's first)
+    float *htile, *stile;
+    int32_t *exact;                  // [tiles]: a sequence starts in the segment before the tile
     float *part_a, *part_v, *part_bc;   // [segments][D][NP], [segments][2][D], [chan_blocks][tokens][2][NP]
     long long x_batch, x_token, dt_batch, dt_token, z_batch, z_token, b_batch, b_token, c_batch, c_token, dy_batch,
         dy_token;
-    int B, T, D, N, n_seqs, softplus, vec, bc_vec, chan_blocks, segs, seg_tokens, row_tiles, pool, has_carry;
+    int B, T, D, N, n_seqs, softplus, vec, bc_vec, chan_blocks, segs, seg_tokens, row_tiles, span_tokens, pool, has_carry;
 };
 
 // Tokens [t0, t1) of row b, and the sequence that holds the current one.
@@ -106,9 +110,27 @@ __device__ __forceinline__ void store_pairs(float *row, int n0, int N, const F2 
 cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, void *dB, void *dC, float *dA, float *dskip, float *dbias,
                             cudaStream_t s);
 int scan_bwd_channels(int N);
+// The segments' maps and the tiles' start states for the backward pass.
+cudaError_t launch_scan_maps(const ScanArgs &a, int dtype, cudaStream_t s);
+// A row of padded n, 16-byte aligned.
+template <int M>
+__device__ __forceinline__ void store_aligned(float *row, const F2 (&h)[M]) {
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) reinterpret_cast<ulonglong2 *>(row)[i] = make_ulonglong2(h[2 * i], h[2 * i + 1]);
+}
+template <int M>
+__device__ __forceinline__ void load_aligned(const float *row, bool live, F2 (&h)[M]) {
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) {
+        const ulonglong2 v = live ? reinterpret_cast<const ulonglong2 *>(row)[i] : make_ulonglong2(0, 0);
+        h[2 * i] = v.x, h[2 * i + 1] = v.y;
+    }
+}
+
 cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s);
 
-// Threads over n of the scanning kernels: eight n each.
+// Eights of n, rounded up to a power of two: the state of a channel is padded to
+// that many in the workspace and in registers.
 inline int scan_parts(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
 
 }  // namespace gdn

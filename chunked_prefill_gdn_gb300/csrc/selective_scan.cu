@@ -22,6 +22,7 @@
 // h + end), and the full pass starts every segment from its exact state.  Each
 // exponential is then taken twice.
 #include <algorithm>
+#include <type_traits>
 
 #include "scan_pairs.cuh"
 
@@ -29,46 +30,52 @@ namespace gdn {
 
 namespace {
 
-constexpr int kScanTile = 16;   // tokens per tile
+// kFull: the outputs and final states.  kState: the end state from a zero start
+// and the sum of the steps of every segment.  kMaps: the same for the backward
+// pass, whose segments are shorter than what a block of this kernel walks
+// (span_tokens), with the gradient at a segment's start that the outputs of its
+// tokens give, and the state and the sum so far before each of its tiles.
+enum ScanMode { kFull, kState, kMaps };
 
 // 32 channels per block.  NW warps scan, a lane per channel, sharing out the n,
 // NPT per thread; one more warp feeds them: it copies the raw rows in
 // asynchronously (three tiles in flight, each piece read back by the lane that
 // copied it), prepares the steps and B and C of the next tile in fp32, and
 // finishes the outputs of the last one, all while the current tile is scanned.
-template <typename T, int NPT, int NW, bool STATE_ONLY>
+template <typename T, int NPT, int NW, int MODE>
 struct ScanShape {
     static constexpr int CW = 32;
     static constexpr int NP = NPT * NW;                     // n, padded
     static constexpr int VPR = CW / 8;                      // vectors of eight channels per row
     static constexpr int RPP = 32 / VPR;                    // rows per pass of the feeding warp
-    static constexpr int PASSES = kScanTile / RPP;
+    static constexpr int PASSES = kTile / RPP;
     static constexpr int BCR = NP / 4;                      // vectors of eight n per row of B and C
     static constexpr int BCP = 32 / BCR;                    // rows of B and C per pass
-    static constexpr int BCV = kScanTile / BCP;
-    static constexpr int ARRAYS = STATE_ONLY ? 2 : 3;
+    static constexpr int BCV = kTile / BCP;
+    static constexpr int ARRAYS = MODE == kState ? 2 : MODE == kFull ? 3 : 4;
     // rows of 8-byte entries per channel, shifted by a quarter of a bank row so that
     // the four rows written together do not meet in a bank
     static constexpr int SD = CW * 2 + 8;
     static constexpr int YS = CW + 4;
     static constexpr size_t rows_bytes = 3 * ARRAYS * PASSES * 32 * 8 * sizeof(T);
     static constexpr size_t bcr_bytes = 2 * BCV * 32 * 8 * sizeof(T);
-    static constexpr size_t smem = rows_bytes + bcr_bytes + 2 * kScanTile * (SD + 2 * NP + (STATE_ONLY ? 0 : NW * YS)) * 4;
+    static constexpr size_t smem = rows_bytes + bcr_bytes + 2 * kTile * (SD + 2 * NP + (MODE == kFull ? NW * YS : MODE == kMaps ? CW : 0)) * 4;
 };
 
-template <typename T, int NPT, int NW, bool STATE_ONLY>
-__global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) scan_kernel(ScanArgs a) {
-    using S = ScanShape<T, NPT, NW, STATE_ONLY>;
-    constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPT / 2, TILE = kScanTile;
+template <typename T, int NPT, int NW, int MODE>
+__global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 7) : NW == 2 ? 4 : 2) scan_kernel(ScanArgs a) {
+    using S = ScanShape<T, NPT, NW, MODE>;
+    constexpr int CW = S::CW, NP = S::NP, VPR = S::VPR, RPP = S::RPP, PASSES = S::PASSES, M = NPT / 2, TILE = kTile;
     extern __shared__ __align__(16) unsigned char smem[];
     using Piece = T[8];
     Piece *rows = reinterpret_cast<Piece *>(smem);                              // [3][ARRAYS][PASSES][lane]
     Piece *bcr = reinterpret_cast<Piece *>(smem + S::rows_bytes);               // [2][BCV][lane]
     float *sd = reinterpret_cast<float *>(smem + S::rows_bytes + S::bcr_bytes); // [2][TILE][SD]: step, step * x
     float *bc = sd + 2 * TILE * S::SD;                                          // [2][TILE][2][NP]
-    float *ys = bc + 2 * TILE * 2 * NP;                                         // [2][NW][TILE][YS]
+    float *ys = bc + 2 * TILE * 2 * NP;                                         // kFull: [2][NW][TILE][YS], y
+    float *gs = ys;                                                             // kMaps: [2][TILE][CW], dy through the gate
 
-    if (!STATE_ONLY && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
+    if (MODE == kFull && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31;
     int warp = threadIdx.x >> 5;
     if (NW == 1) {
@@ -81,23 +88,25 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
     }
     const int chan0 = (blockIdx.x % a.chan_blocks) * CW;
     // the last segment of a row needs no map
-    const int spr = STATE_ONLY ? a.segs - 1 : a.segs;
+    const int spr = MODE == kState ? a.segs - 1 : a.segs;
     Span r;
     r.b = blockIdx.x / a.chan_blocks / spr;
     const int seg = r.b * a.segs + blockIdx.x / a.chan_blocks % spr;
-    r.t0 = (seg - r.b * a.segs) * a.seg_tokens;
-    r.t1 = min(a.T, r.t0 + a.seg_tokens);
+    const int walked = MODE == kMaps ? a.span_tokens : a.seg_tokens;
+    r.t0 = (seg - r.b * a.segs) * walked;
+    r.t1 = min(a.T, r.t0 + walked);
     const int tiles = r.t0 < r.t1 ? (r.t1 - r.t0 + TILE - 1) / TILE : 0;
 
     if (warp == NW) {   // the feeding warp: lane -> (row of the pass, eight channels)
         if (tiles == 0) return;
         const int lv = lane % VPR, lrow = lane / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
-        const bool gated = !STATE_ONLY && a.z != nullptr;
+        const bool gated = MODE != kState && a.z != nullptr;
         const long long first = r.t0 + lrow;
         const T *px = static_cast<const T *>(a.x) + r.b * a.x_batch + first * a.x_token + lc;
         const T *pd = static_cast<const T *>(a.dt) + r.b * a.dt_batch + first * a.dt_token + lc;
         const T *pz = static_cast<const T *>(a.z) + r.b * a.z_batch + first * a.z_token + lc;
-        T *py = STATE_ONLY ? nullptr : static_cast<T *>(a.out) + ((long long)r.b * a.T + first) * a.D + lc;
+        const T *pg = MODE == kMaps ? static_cast<const T *>(a.dy) + r.b * a.dy_batch + first * a.dy_token + lc : nullptr;
+        T *py = MODE != kFull ? nullptr : static_cast<T *>(a.out) + ((long long)r.b * a.T + first) * a.D + lc;
         const int bcc = lane / (NP / 8) % 2, bcn = lane % (NP / 8) * 8, bcrow = lane / S::BCR;
         const long long bc_token = bcc ? a.c_token : a.b_token;
         const T *pbc = (bcc ? static_cast<const T *>(a.Cm) + r.b * a.c_batch : static_cast<const T *>(a.Bm) + r.b * a.b_batch) +
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
         auto bc_piece = [&](int k, int i) -> T * { return bcr[(k % 2 * S::BCV + i) * 32 + lane]; };
         F2 bias[4], skip[4];
         load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
-        load_pairs(!STATE_ONLY && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
+        load_pairs(MODE == kFull && a.skip ? a.skip + lc : nullptr, 0, lrest, true, skip);
         auto stage = [&](int k) {   // copies tile k and moves the pointers on to the next
             const int t = r.t0 + k * TILE;
             if (whole && t + TILE <= r.t1) {
@@ -116,6 +125,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
                     copy8_whole<T>(piece(k, 0, i), px + i * RPP * a.x_token);
                     copy8_whole<T>(piece(k, 1, i), pd + i * RPP * a.dt_token);
                     if (gated) copy8_whole<T>(piece(k, 2, i), pz + i * RPP * a.z_token);
+                    if (MODE == kMaps) copy8_whole<T>(piece(k, 3, i), pg + i * RPP * a.dy_token);
                 }
 #pragma unroll
                 for (int i = 0; i < S::BCV; ++i) copy8_whole<T>(bc_piece(k, i), pbc + i * S::BCP * bc_token);
@@ -126,6 +136,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
                     copy8_async<T>(piece(k, 0, i), px + i * RPP * a.x_token, n, a.vec);
                     copy8_async<T>(piece(k, 1, i), pd + i * RPP * a.dt_token, n, a.vec);
                     if (gated) copy8_async<T>(piece(k, 2, i), pz + i * RPP * a.z_token, n, a.vec);
+                    if (MODE == kMaps) copy8_async<T>(piece(k, 3, i), pg + i * RPP * a.dy_token, n, a.vec);
                 }
 #pragma unroll
                 for (int i = 0; i < S::BCV; ++i)
@@ -133,6 +144,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
                                    t + i * S::BCP + bcrow < r.t1 ? a.N - bcn : 0, a.bc_vec);
             }
             px += TILE * a.x_token, pd += TILE * a.dt_token, pz += TILE * a.z_token;
+            if (MODE == kMaps) pg += TILE * a.dy_token;
             pbc += TILE * bc_token;
             copy_commit();
         };
@@ -150,6 +162,17 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
                     const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
                     *reinterpret_cast<float2 *>(at + 2 * e * VPR * 2) = make_float2(lo(s), lo(sx));
                     *reinterpret_cast<float2 *>(at + (2 * e + 1) * VPR * 2) = make_float2(hi(s), hi(sx));
+                }
+                if (MODE == kMaps) {
+                    float *g_at = gs + (k % 2 * TILE + i * RPP + lrow) * CW + lv;
+                    F2 g[4], z[4];
+                    unpack_pairs<T>(load_raw<T, 8>(piece(k, 3, i)), g);
+                    if (gated) unpack_pairs<T>(load_raw<T, 8>(piece(k, 2, i)), z);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (gated) g[e] = mul2(g[e], mul2(z[e], sigmoid_pair(z[e])));
+                        g_at[2 * e * VPR] = lo(g[e]), g_at[(2 * e + 1) * VPR] = hi(g[e]);
+                    }
                 }
             }
 #pragma unroll
@@ -191,13 +214,13 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
         prepare(0);
         __syncthreads();
         for (int k = 0; k < tiles; ++k) {
-            if (!STATE_ONLY && k > 0) finish(k - 1);
+            if (MODE == kFull && k > 0) finish(k - 1);
             stage(k + 2);
             copy_wait<1>();
             if (k + 1 < tiles) prepare(k + 1);
             __syncthreads();
         }
-        if (!STATE_ONLY) finish(tiles - 1);
+        if (MODE == kFull) finish(tiles - 1);
         return;
     }
 
@@ -205,7 +228,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
     // them down, so that neither side meets in a bank
     const int n0 = warp * NPT, ch = chan0 + lane % VPR * 8 + lane / VPR;
     const bool live = ch < a.D;
-    if (!STATE_ONLY && a.final_state && live) {    // a sequence without a token keeps its state
+    if (MODE == kFull && a.final_state && live) {    // a sequence without a token keeps its state
         auto keep = [&](int n) {
             const long long at = ((long long)n * a.D + ch) * a.N;
             F2 v[M];
@@ -222,67 +245,109 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
 #pragma unroll
     for (int i = 0; i < M; ++i) A2[i] = mul2(A2[i], both(kLog2e));
     span_find(a, r);
-    const bool starts = r.begin == r.t0;
-    bool inside = false;
+    bool starts = r.begin == r.t0, inside = false;
     auto initial = [&](int n) {
         load_pairs(a.init ? a.init + ((long long)n * a.D + ch) * a.N : nullptr, n0, a.N, live, h);
     };
     if (starts) initial(r.n);
-    else load_pairs(!STATE_ONLY && a.has_carry ? a.hloc + ((long long)seg * a.D + ch) * NP : nullptr, n0, NP, live, h);
+    else load_aligned(a.hloc + ((long long)seg * a.D + ch) * NP + n0, live && MODE == kFull && a.has_carry, h);
     float step_sum = 0.f;
-    auto token = [&](int j, const float *s_at, const float *bc_at, float *y_at) {
+    F2 p[M], G[M];   // kMaps: the product of the a's so far, the gradient at the tile's start
+    auto token = [&](auto with_g, int j, const float *s_at, const float *bc_at, float *y_at) {
         const float2 sv = *reinterpret_cast<const float2 *>(s_at + j * S::SD);
         const F2 ss = both(sv.x), sx = both(sv.y);
         const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP);
         const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP + NP);
-        F2 y0 = both(0.f), y1 = both(0.f);
+        F2 y0 = both(0.f), y1 = both(0.f), gg = both(0.f);
+        if (with_g) gg = both(y_at[j * CW]);
 #pragma unroll
         for (int i = 0; i < M / 2; ++i) {
             const ulonglong2 b = Bk[i];
-            h[2 * i] = fma2(exp2_pair(mul2(ss, A2[2 * i])), h[2 * i], mul2(sx, b.x));
-            h[2 * i + 1] = fma2(exp2_pair(mul2(ss, A2[2 * i + 1])), h[2 * i + 1], mul2(sx, b.y));
-            if (!STATE_ONLY) {
+            const F2 e0 = exp2_pair(mul2(ss, A2[2 * i])), e1 = exp2_pair(mul2(ss, A2[2 * i + 1]));
+            h[2 * i] = fma2(e0, h[2 * i], mul2(sx, b.x));
+            h[2 * i + 1] = fma2(e1, h[2 * i + 1], mul2(sx, b.y));
+            if (MODE == kFull) {
                 const ulonglong2 c = Ck[i];
                 y0 = i ? fma2(c.x, h[2 * i], y0) : mul2(c.x, h[0]);
                 y1 = i ? fma2(c.y, h[2 * i + 1], y1) : mul2(c.y, h[1]);
             }
+            if (with_g) {
+                const ulonglong2 c = Ck[i];
+                p[2 * i] = mul2(p[2 * i], e0);
+                p[2 * i + 1] = mul2(p[2 * i + 1], e1);
+                G[2 * i] = fma2(p[2 * i], mul2(gg, c.x), G[2 * i]);
+                G[2 * i + 1] = fma2(p[2 * i + 1], mul2(gg, c.y), G[2 * i + 1]);
+            }
         }
-        if (STATE_ONLY) {
-            step_sum += sv.x;
-        } else {
+        if (MODE == kFull) {
             y0 = add2(y0, y1);
             y_at[j * S::YS] = lo(y0) + hi(y0);
+        } else {
+            step_sum += sv.x;
         }
     };
+    using Yes = std::integral_constant<bool, MODE == kMaps>;
+    using No = std::integral_constant<bool, false>;
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
         const int t = r.t0 + k * TILE, stop = min(r.t1, t + TILE);
         const float *s_at = sd + k % 2 * TILE * S::SD + lane * 2, *bc_at = bc + k % 2 * TILE * 2 * NP + n0;
-        float *y_at = ys + (k % 2 * NW + warp) * TILE * S::YS + lane;
+        float *y_at = MODE == kFull ? ys + (k % 2 * NW + warp) * TILE * S::YS + lane : gs + k % 2 * TILE * CW + lane;
+        if (MODE == kMaps) {
+            const bool here = r.begin == t;
+            if (t % a.seg_tokens == 0) {   // a new segment
+                starts = here, inside = false, step_sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < M; ++i) p[i] = both(1.f), G[i] = h[i] = both(0.f);
+            } else if (here) {
+                inside = true;
+            }
+            if (here) initial(r.n);
+            if (live && t % a.seg_tokens != 0) {
+                const long long tile = (long long)r.b * a.row_tiles + t / TILE;
+                store_aligned(a.htile + (tile * a.D + ch) * NP + n0, h);
+                if (warp == 0) a.stile[tile * a.D + ch] = step_sum;
+                if (chan0 == 0 && warp == 0 && lane == 0) a.exact[tile] = starts || inside;
+            }
+        }
         for (int q = t; q < stop;) {
             const int run_end = min(stop, r.end);
-            if (run_end - q == TILE) {   // the usual case, with addresses known
+            if (run_end - q == TILE && !(MODE == kMaps && inside)) {   // the usual case, with addresses known
 #pragma unroll
-                for (int j = 0; j < TILE; ++j) token(j, s_at, bc_at, y_at);
+                for (int j = 0; j < TILE; ++j) token(Yes(), j, s_at, bc_at, y_at);
+            } else if (MODE == kMaps && !inside) {
+                for (int j = q - t; j < run_end - t; ++j) token(Yes(), j, s_at, bc_at, y_at);
             } else {
-                for (int j = q - t; j < run_end - t; ++j) token(j, s_at, bc_at, y_at);
+                for (int j = q - t; j < run_end - t; ++j) token(No(), j, s_at, bc_at, y_at);
             }
             q = run_end;
             if (q == r.end) {   // the sequence is complete
-                if (!STATE_ONLY && a.final_state && live)
-                    store_pairs(a.final_state + ((long long)r.n * a.D + ch) * a.N, n0, a.N, h);
+                const long long at = ((long long)r.n * a.D + ch) * a.N;
+                if (MODE == kFull && a.final_state && live) store_pairs(a.final_state + at, n0, a.N, h);
+                if (MODE == kMaps && !inside && a.d_final) {
+                    F2 f[M];
+                    load_pairs(a.d_final + at, n0, a.N, live, f);
+#pragma unroll
+                    for (int i = 0; i < M; ++i) G[i] = fma2(p[i], f[i], G[i]);
+                }
                 if (q < r.t1) {
                     span_next(a, r, q);
-                    initial(r.n);
-                    inside = true;
+                    if (MODE != kMaps || q < stop) initial(r.n), inside = true;   // (a tile's start: at its top)
                 }
             }
         }
+        if (MODE == kMaps && live && (stop % a.seg_tokens == 0 || stop == a.T)) {   // the segment is complete
+            const long long at = (long long)r.b * ((a.T + a.seg_tokens - 1) / a.seg_tokens) + t / a.seg_tokens;
+            store_aligned(a.hloc + (at * a.D + ch) * NP + n0, h);
+            store_aligned(a.gloc + (at * a.D + ch) * NP + n0, G);
+            if (warp == 0) a.sums[at * a.D + ch] = step_sum;
+            if (chan0 == 0 && warp == 0 && lane == 0) a.flags[at] = (starts ? 1 : 0) | (inside ? 2 : 0);
+        }
         __syncthreads();
     }
-    if (STATE_ONLY) {
+    if (MODE == kState) {
         if (live) {
-            store_pairs(a.hloc + ((long long)seg * a.D + ch) * NP, n0, NP, h);
+            store_aligned(a.hloc + ((long long)seg * a.D + ch) * NP + n0, h);
             if (warp == 0) a.sums[(long long)seg * a.D + ch] = step_sum;
         }
         if (chan0 == 0 && warp == 0 && lane == 0) a.flags[seg] = (starts ? 1 : 0) | (inside ? 2 : 0);
@@ -293,36 +358,41 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? 7 : NW == 2 ? 4 : 2) 
 // map's start gradient by the gradient at its end.  A thread per (row, channel,
 // n); eight maps are loaded ahead.
 template <bool GRAD>
-__global__ void __launch_bounds__(128) scan_combine_kernel(ScanArgs a, int maps, int NP) {
+__global__ void __launch_bounds__(64) scan_combine_kernel(ScanArgs a, int maps, int NP) {
     constexpr int AHEAD = 8;
-    const long long at = (long long)blockIdx.x * 128 + threadIdx.x, size = (long long)a.D * NP;
+    const long long at = (long long)blockIdx.x * 64 + threadIdx.x, size = (long long)a.D * NP;
     if (at >= size) return;
     const int ch = (int)(at / NP), n = (int)(at % NP);
     const float A2 = n < a.N ? a.A[(long long)ch * a.N + n] * kLog2e : 0.f;
     const bool back = GRAD && blockIdx.z == 1;
-    float *maps_at = (back ? a.gloc : a.hloc) + (long long)blockIdx.y * maps * size + at;
-    const float *sums = a.sums + (long long)blockIdx.y * maps * a.D + ch;
-    const int32_t *flags = a.flags + (long long)blockIdx.y * maps;
-    float carry = 0.f;
-    for (int m0 = 0; m0 < maps; m0 += AHEAD) {
-        float v[AHEAD], s[AHEAD];
-        int f[AHEAD];
+    // the walk's first map and its direction
+    const long long m0 = (long long)blockIdx.y * maps + (back ? maps - 1 : 0), dir = back ? -1 : 1;
+    float *at_map = (back ? a.gloc : a.hloc) + m0 * size + at;
+    const float *at_sum = a.sums + m0 * a.D + ch;
+    const int32_t *at_flag = a.flags + m0;
+    const long long map_step = dir * size, sum_step = dir * a.D;
+    const int there = GRAD ? maps : maps - 1;   // forward only: the last map is not there
+    float v[AHEAD], s[AHEAD], carry = 0.f;
+    int f[AHEAD];
+    float *ahead = at_map;
+    auto load = [&](int i, int m) {
+        const bool in = m < there;
+        v[i] = in ? *ahead : 0.f;
+        s[i] = in ? *at_sum : 0.f;
+        f[i] = in ? *at_flag : 0;
+        ahead += map_step, at_sum += sum_step, at_flag += dir;
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load(i, i);
+    for (int m = 0; m < maps; m += AHEAD) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int m = back ? maps - 1 - m0 - i : m0 + i;
-            const bool in = m0 + i < maps && (GRAD || m + 1 < maps);   // forward only: the last map is not there
-            v[i] = in ? maps_at[m * size] : 0.f;
-            s[i] = in ? sums[(long long)m * a.D] : 0.f;
-            f[i] = in ? flags[m] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            if (m0 + i >= maps) break;
-            const int m = back ? maps - 1 - m0 - i : m0 + i;
-            maps_at[m * size] = carry;
-            const float through = exp2_f32(A2 * s[i]);
-            if (back) carry = f[i] & 1 ? 0.f : f[i] & 2 ? v[i] : fmaf(through, carry, v[i]);
-            else carry = f[i] ? v[i] : fmaf(through, carry, v[i]);
+            if (m + i >= maps) break;
+            *at_map = carry;
+            at_map += map_step;
+            const float through = fmaf(exp2_f32(A2 * s[i]), carry, v[i]);
+            carry = back ? (f[i] & 1 ? 0.f : f[i] & 2 ? v[i] : through) : f[i] ? v[i] : through;
+            load(i, m + AHEAD + i);
         }
     }
 }
@@ -383,15 +453,15 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     }
 }
 
-template <typename T, int NPT, int NW, bool STATE_ONLY>
+template <typename T, int NPT, int NW, int MODE>
 cudaError_t launch_scan_one(const ScanArgs &a, int segs, cudaStream_t s) {
-    using S = ScanShape<T, NPT, NW, STATE_ONLY>;
+    using S = ScanShape<T, NPT, NW, MODE>;
     if (S::smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, NPT, NW, STATE_ONLY>,
+        const cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, NPT, NW, MODE>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
         if (e != cudaSuccess) return e;
     }
-    scan_kernel<T, NPT, NW, STATE_ONLY>
+    scan_kernel<T, NPT, NW, MODE>
         <<<(unsigned)((long long)a.chan_blocks * a.B * segs), 32 * (NW + 1), S::smem, s>>>(a);
     return cudaGetLastError();
 }
@@ -401,11 +471,11 @@ cudaError_t launch_scan_parts(ScanArgs a, cudaStream_t s) {
     a.chan_blocks = (a.D + 31) / 32;
     a.has_carry = a.segs > 1;
     if (a.segs > 1) {
-        cudaError_t e = launch_scan_one<T, NPT, NW, true>(a, a.segs - 1, s);
+        cudaError_t e = launch_scan_one<T, NPT, NW, kState>(a, a.segs - 1, s);
         if (e == cudaSuccess) e = launch_scan_combine(a, a.segs, false, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_scan_one<T, NPT, NW, false>(a, a.segs, s);
+    return launch_scan_one<T, NPT, NW, kFull>(a, a.segs, s);
 }
 
 template <typename T>
@@ -430,7 +500,7 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 // Segments per row in the forward pass.  One segment takes each exponential
 // once; several take it twice but put that many times the warps to work.
 int scan_segments(int B, int T, int D, int N) {
-    const int tiles = (T + kScanTile - 1) / kScanTile;
+    const int tiles = (T + kTile - 1) / kTile;
     const long long warps = (long long)B * ((D + 31) / 32) * (N <= 16 ? 1 : N <= 32 ? 2 : 4), wanted = 7ll * device_sm_count();
     if (tiles <= 1 || 2 * warps >= wanted) return 1;
     const int segs = (int)std::min<long long>((wanted + warps - 1) / warps, tiles);
@@ -438,17 +508,35 @@ int scan_segments(int B, int T, int D, int N) {
     return (tiles + len - 1) / len;
 }
 int scan_segment_tokens(int T, int segs) {
-    const int tiles = (T + kScanTile - 1) / kScanTile;
-    return std::max(1, (tiles + segs - 1) / segs) * kScanTile;
+    const int tiles = (T + kTile - 1) / kTile;
+    return std::max(1, (tiles + segs - 1) / segs) * kTile;
 }
 
 }  // namespace
 
+cudaError_t launch_scan_maps(const ScanArgs &p, int dtype, cudaStream_t s) {
+    ScanArgs a = p;
+    a.chan_blocks = (a.D + 31) / 32;
+    // segments per block: as many as leave every SM seven blocks
+    const int per_seg = a.seg_tokens / kTile, row_segs = (a.row_tiles + per_seg - 1) / per_seg;
+    const long long all = (long long)a.B * row_segs * a.chan_blocks;
+    const int per = (int)std::max<long long>(1, std::min<long long>(all / (7ll * device_sm_count()), row_segs));
+    a.segs = (row_segs + per - 1) / per;
+    a.span_tokens = per * a.seg_tokens;
+#define GDN_MAPS(NPT, NW) \
+    (dtype == GDN_BF16 ? launch_scan_one<__nv_bfloat16, NPT, NW, kMaps>(a, a.segs, s) : launch_scan_one<float, NPT, NW, kMaps>(a, a.segs, s))
+    if (a.N <= 8) return GDN_MAPS(8, 1);
+    if (a.N <= 16) return GDN_MAPS(16, 1);
+    if (a.N <= 32) return GDN_MAPS(16, 2);
+    return GDN_MAPS(16, 4);
+#undef GDN_MAPS
+}
+
 cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s) {
     const int NP = 8 * scan_parts(a.N);
-    const dim3 grid((unsigned)(((long long)a.D * NP + 127) / 128), a.B, grad ? 2 : 1);
-    if (grad) scan_combine_kernel<true><<<grid, 128, 0, s>>>(a, maps, NP);
-    else scan_combine_kernel<false><<<grid, 128, 0, s>>>(a, maps, NP);
+    const dim3 grid((unsigned)(((long long)a.D * NP + 63) / 64), a.B, grad ? 2 : 1);
+    if (grad) scan_combine_kernel<true><<<grid, 64, 0, s>>>(a, maps, NP);
+    else scan_combine_kernel<false><<<grid, 64, 0, s>>>(a, maps, NP);
     return cudaGetLastError();
 }
 
@@ -590,10 +678,10 @@ namespace gdn {
 namespace {
 
 // How the backward pass cuts a problem: tiles per row, segments of tiles that
-// one block walks, blocks of channels.
+// one block of the main kernel walks, blocks of channels.
 struct BwdPlan {
     int row_tiles, segs, seg_tokens, chan_blocks;
-    size_t maps, part_a, part_v, part_bc;
+    size_t maps, htile, stile, exact, part_a, part_v, part_bc;
 };
 BwdPlan bwd_plan(int B, int T, int D, int N) {
     BwdPlan p;
@@ -601,13 +689,23 @@ BwdPlan bwd_plan(int B, int T, int D, int N) {
     const int ch = scan_bwd_channels(N);
     p.row_tiles = (T + kTile - 1) / kTile;
     p.chan_blocks = (D + ch - 1) / ch;
-    // one tile per block until there are many more blocks than the SMs hold (two
-    // each); then longer walks, with fewer partial sums of dA
-    const long long blocks = (long long)B * std::max(1, p.row_tiles) * p.chan_blocks;
-    const int per = (int)std::max<long long>(1, std::min<long long>(blocks / (16ll * device_sm_count()), 64));
+    // tiles per segment: what gives the shortest schedule on two blocks per SM,
+    // with half a tile's time for a block's own start and end
+    const long long slots = 2ll * device_sm_count();
+    int per = 1;
+    double best = 0;
+    for (int m = 1; m <= 16 && m <= std::max(1, p.row_tiles); ++m) {
+        const long long blocks = (long long)B * ((p.row_tiles + m - 1) / m) * p.chan_blocks;
+        const double cost = (double)((blocks + slots - 1) / slots) * (m + 0.5);
+        if (m == 1 || cost < best) best = cost, per = m;
+    }
     p.segs = std::max(1, (p.row_tiles + per - 1) / per);
     p.seg_tokens = per * kTile;
-    p.maps = maps_bytes((long long)B * p.row_tiles, D, N, 2);
+    const size_t tiles = (size_t)B * p.row_tiles;
+    p.maps = maps_bytes((long long)B * p.segs, D, N, 2);
+    p.htile = round16(tiles * D * np * 4);
+    p.stile = round16(tiles * D * 4);
+    p.exact = round16(tiles * 4);
     p.part_a = round16((size_t)B * p.segs * D * np * 4);
     p.part_v = round16((size_t)B * p.segs * 2 * D * 4);
     p.part_bc = round16((size_t)p.chan_blocks * B * T * 2 * np * 4);
@@ -620,7 +718,7 @@ BwdPlan bwd_plan(int B, int T, int D, int N) {
 extern "C" size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int N) {
     if (B < 0 || T < 0 || D < 1 || N < 1 || N > 64) return 0;
     const gdn::BwdPlan p = gdn::bwd_plan(B, T, D, N);
-    return std::max<size_t>(16, p.maps + p.part_a + p.part_v + p.part_bc);
+    return std::max<size_t>(16, p.maps + p.htile + p.stile + p.exact + p.part_a + p.part_v + p.part_bc);
 }
 
 extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_desc *desc, const void *dy, int64_t dy_batch_stride,
@@ -653,7 +751,10 @@ extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_desc *desc, const vo
     a.out = dx, a.ddt = ddt, a.dz = dz, a.dinit = d_initial_state, a.status = device_status;
     const BwdPlan plan = bwd_plan(p.B, p.T, p.D, p.N);
     a.row_tiles = plan.row_tiles, a.segs = plan.segs, a.seg_tokens = plan.seg_tokens, a.chan_blocks = plan.chan_blocks;
-    char *at = place_maps(a, static_cast<char *>(workspace), (long long)p.B * plan.row_tiles, 2);
+    char *at = place_maps(a, static_cast<char *>(workspace), (long long)p.B * plan.segs, 2);
+    a.htile = reinterpret_cast<float *>(at), at += plan.htile;
+    a.stile = reinterpret_cast<float *>(at), at += plan.stile;
+    a.exact = reinterpret_cast<int32_t *>(at), at += plan.exact;
     a.part_a = reinterpret_cast<float *>(at), at += plan.part_a;
     a.part_v = reinterpret_cast<float *>(at), at += plan.part_v;
     a.part_bc = reinterpret_cast<float *>(at);

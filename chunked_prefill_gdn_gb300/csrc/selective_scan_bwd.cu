@@ -8,149 +8,36 @@
 //     ds_t = sum_n q_t A + x_t u_t,    dx_t = s_t u_t + D g_t,   u_t = sum_n dh_t B_t,
 //     dz_t = dout_t y_t silu'(z_t),    dD = sum_t g_t x_t,   ddt = ds softplus'.
 //
-// Both recurrences run over tiles of 32 tokens in parallel.  A first kernel
-// gives every tile's two maps from one pass over its exponentials: the end
-// state from a zero start, and the gradient at its start from a zero gradient
-// at its end, which needs no reversed pass: with the running product p_t of
-// the a's it is sum_t p_t C_t g_t.  scan_combine_kernel turns the maps into
-// every tile's exact start state and end gradient.  The main kernel walks a
-// tile forward, keeping the state at every fourth token in shared memory, then
-// backward in blocks of four tokens whose states it recomputes in registers.
+// Both recurrences run over segments of a few tiles of 16 tokens in parallel.  A
+// first kernel (scan_kernel in its kMaps mode) gives every segment's two maps
+// from one pass over its exponentials: the end state from a zero start, and the
+// gradient at its start from a zero gradient at its end, which needs no reversed
+// pass: with the running product p_t of the a's it is sum_t p_t C_t g_t.  It also
+// keeps the state before every tile.  scan_combine_kernel turns the maps into
+// every segment's exact start state and end gradient; a tile's start state is
+// what the first kernel kept plus exp(A sum s) times the segment's.  The main
+// kernel takes a segment's tiles from the last to the first: each is walked
+// forward, keeping the state at every second token in shared memory, then
+// backward two tokens at a time, whose states are recomputed in registers.
 //
-// The sums over n (for the gradients per channel) and over channels (for dB
-// and dC) decide the thread layout: a thread holds four n of CS channels, so
-// that both sums are first taken in registers, and each remaining exchange
-// between lanes halves the values it still carries (a reduce-scatter); a layout
-// with all n or all channels in one lane would pay twice the shuffles.
-// Sums over warps, blocks and tokens are added in a fixed order: no atomics,
-// the same inputs give the same bits.
+// What bounds the main kernel is the instructions around its 14 multiply-adds and
+// two exponentials per (token, channel, n): the sums over n (for the gradients
+// per channel) and over channels (for dB and dC).  A thread holds eight n of CS
+// channels, so that both sums are first taken in registers and what is per
+// (token, channel) serves eight n; each exchange between lanes then halves the
+// values still carried (a reduce-scatter).  The first two exchanges of dB and dC
+// need no selection of the half to keep: the lanes hold their n in different
+// orders, so that every lane keeps the same registers.  Sums over warps, blocks
+// and tokens are added in a fixed order: no atomics, the same inputs give the
+// same bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "scan_pairs.cuh"
 
 namespace gdn {
 
 namespace {
-
-constexpr int kMapThreads = 64;
-
-template <typename T, int LP>
-__global__ void __launch_bounds__(kMapThreads) scan_tile_maps_kernel(ScanArgs a) {
-    constexpr int CH = kMapThreads / LP;
-    constexpr int NP = 8 * LP;
-    constexpr int VPR = CH / 8;
-    constexpr int RPP = kMapThreads / VPR;
-    constexpr int PASSES = RPP >= kTile ? 1 : kTile / RPP;
-    __shared__ __align__(16) float4 sd[kTile][CH];   // step, step * x, dy through the gate, -
-    __shared__ __align__(16) float bc[kTile][2][NP];
-    const int tid = threadIdx.x;
-    const int chan0 = (blockIdx.x % a.chan_blocks) * CH;
-    const int tile = blockIdx.x / a.chan_blocks;     // over all rows
-    Span r;
-    r.b = tile / a.row_tiles;
-    r.t0 = (tile - r.b * a.row_tiles) * kTile;
-    r.t1 = min(a.T, r.t0 + kTile);
-
-    const int lv = tid % VPR, lrow = tid / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
-    const long long row = r.b;
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int q = i * RPP + lrow, t = r.t0 + q;
-        const int n = q < kTile && t < r.t1 ? lrest : 0;
-        float x[8], d[8], z[8], g[8];
-        unpack<T, 8>(load8<T>(static_cast<const T *>(a.x) + row * a.x_batch + t * a.x_token + lc, n, a.vec), x);
-        unpack<T, 8>(load8<T>(static_cast<const T *>(a.dt) + row * a.dt_batch + t * a.dt_token + lc, n, a.vec), d);
-        unpack<T, 8>(load8<T>(static_cast<const T *>(a.z) + row * a.z_batch + t * a.z_token + lc, a.z ? n : 0, a.vec), z);
-        unpack<T, 8>(load8<T>(static_cast<const T *>(a.dy) + row * a.dy_batch + t * a.dy_token + lc, n, a.vec), g);
-        if (q < kTile) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float pre = d[e] + (a.bias && e < lrest ? a.bias[lc + e] : 0.f);
-                const float s = a.softplus ? softplus_f32(pre) : pre;
-                const float gate = a.z ? z[e] * sigmoid_f32(z[e]) : 1.f;
-                sd[q][lv * 8 + e] = make_float4(s, s * x[e], g[e] * gate, 0.f);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < LP; ++i) {
-        const int j = i * kMapThreads + tid, v = j % LP, c = j / LP % 2, q = j / (2 * LP), t = r.t0 + q;
-        const T *src = c ? static_cast<const T *>(a.Cm) + row * a.c_batch + t * a.c_token
-                         : static_cast<const T *>(a.Bm) + row * a.b_batch + t * a.b_token;
-        float f[8];
-        unpack<T, 8>(load8<T>(src + v * 8, t < r.t1 ? a.N - v * 8 : 0, a.bc_vec), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) bc[q][c][v * 8 + e] = f[e];
-    }
-    const int part = tid % LP, n0 = part * 8, chl = tid / LP, ch = chan0 + chl;
-    const bool live = ch < a.D;
-    F2 A2[4], h[4], p[4], G[4];
-    load_pairs(a.A + (long long)ch * a.N, n0, a.N, live, A2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        A2[i] = mul2(A2[i], pair(kLog2e, kLog2e));
-        h[i] = G[i] = pair(0.f, 0.f);
-        p[i] = pair(1.f, 1.f);
-    }
-    span_find(a, r);
-    const bool starts = r.begin == r.t0;
-    bool inside = false;
-    auto initial = [&](int n) {
-        load_pairs(a.init ? a.init + ((long long)n * a.D + ch) * a.N : nullptr, n0, a.N, live, h);
-    };
-    if (starts) initial(r.n);
-    float sum = 0.f;
-    __syncthreads();
-    for (int q = r.t0; q < r.t1;) {
-        const int run_end = min(r.t1, r.end);
-        if (!inside) {
-#pragma unroll 4
-            for (int k = q - r.t0; k < run_end - r.t0; ++k) {
-                const float4 s = sd[k][chl];
-                const F2 ss = pair(s.x, s.x), sx = pair(s.y, s.y), gg = pair(s.z, s.z);
-                const F2 *Bk = reinterpret_cast<const F2 *>(&bc[k][0][n0]), *Ck = reinterpret_cast<const F2 *>(&bc[k][1][n0]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 e = exp2_pair(mul2(ss, A2[i]));
-                    h[i] = fma2(e, h[i], mul2(sx, Bk[i]));
-                    p[i] = mul2(p[i], e);
-                    G[i] = fma2(p[i], mul2(gg, Ck[i]), G[i]);
-                }
-                sum += s.x;
-            }
-        } else {
-#pragma unroll 4
-            for (int k = q - r.t0; k < run_end - r.t0; ++k) {
-                const float4 s = sd[k][chl];
-                const F2 ss = pair(s.x, s.x), sx = pair(s.y, s.y);
-                const F2 *Bk = reinterpret_cast<const F2 *>(&bc[k][0][n0]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = fma2(exp2_pair(mul2(ss, A2[i])), h[i], mul2(sx, Bk[i]));
-            }
-        }
-        q = run_end;
-        if (q == r.end) {
-            if (!inside && a.d_final) {
-                F2 f[4];
-                load_pairs(a.d_final + ((long long)r.n * a.D + ch) * a.N, n0, a.N, live, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) G[i] = fma2(p[i], f[i], G[i]);
-            }
-            if (q < r.t1) {
-                span_next(a, r, q);
-                initial(r.n);
-                inside = true;
-            }
-        }
-    }
-    if (live) {
-        const long long at = ((long long)tile * a.D + ch) * NP;
-        store_pairs(a.hloc + at, n0, NP, h);
-        store_pairs(a.gloc + at, n0, NP, G);
-        if (part == 0) a.sums[(long long)tile * a.D + ch] = sum;
-    }
-    if (chan0 == 0 && tid == 0) a.flags[tile] = (starts ? 1 : 0) | (inside ? 2 : 0);
-}
 
 // V values per lane summed over the lanes that differ in the bits MASK, MASK / 2,
 // ..., LAST: each exchange hands half of the values over and keeps the other
@@ -177,42 +64,78 @@ __device__ __forceinline__ void reduce_scatter(float *v, int lane, int &base) {
 
 constexpr int kBwdThreads = 128;
 constexpr int kBwdWarps = kBwdThreads / 32;
-constexpr int kBlock = 4;                      // tokens per block of the backward walk
+constexpr int kBlock = 2;                      // tokens per block of the backward walk
 constexpr int kBlocks = kTile / kBlock;
 
-// NL lanes share a channel (four n each), CS channels per lane.
+// NL lanes share a channel (eight n each), CS channels per lane.
 template <int NL>
 struct BwdShape {
-    static constexpr int CS = NL == 2 ? 2 : 4;
-    static constexpr int CL = 32 / NL;                   // lanes over channels
+    static constexpr int CS = NL == 1 ? 1 : 2;
+    static constexpr int CL = 32 / NL;                   // lanes over channels, four at least
     static constexpr int WC = CL * CS;                   // channels of a warp
     static constexpr int CH = WC * kBwdWarps;            // of the block
-    static constexpr int NP = 4 * NL;
-    static constexpr int VL = 4 * 8 / CL > 0 ? 4 * 8 / CL : 1;   // dB, dC sums left per lane and block of tokens
-    // a block's dB and dC sums go where its states were; block 0 has none of its own
-    static constexpr int REGIONS = 32 * NL * 2 <= CS * 32 * 4 ? kBlocks - 1 : kBlocks;
-    static constexpr int REGION = kBwdWarps * CS * 32;   // float4
-    static constexpr size_t smem = REGIONS * REGION * 16 + 3 * kTile * CH * 4 + kTile * 2 * NP * 4 + kTile * 4 + 16;
+    static constexpr int NP = 8 * NL;
+    static constexpr int VL = 32 / CL;                   // dB, dC sums left per lane and block of tokens
+    // float4 per warp and block of tokens: the states before it, later its dB and
+    // dC sums (2 tokens x 2 x NP; those of block 0 behind those of block 1)
+    static constexpr int REGION = CS * 2 * 32;
+    static constexpr int VPR = CH / 8;                   // vectors of eight channels per row
+    static constexpr int PASSES = kBwdThreads / VPR >= kTile ? 1 : kTile * VPR / kBwdThreads;
+    static constexpr int BCV = (kTile * 2 * NL + kBwdThreads - 1) / kBwdThreads;
+    static constexpr size_t smem = (kBlocks - 1) * kBwdWarps * REGION * 16 + 3 * kTile * CH * 4 + kTile * 2 * NP * 4 +
+                                   kTile * 4 + 16;
+    // raw x, dt, z, dy, B and C of the next tile: where two blocks per SM have the
+    // room (16-bit inputs)
+    template <typename T>
+    static constexpr size_t staged = sizeof(T) == 2 ? (4 * PASSES + BCV) * kBwdThreads * 8 * sizeof(T) : 0;
+    static_assert(2 * 4 * NP <= REGION * 4, "sums of two blocks of tokens in one region");
 };
+
+// Pairs of eight n of a row from n0: slot i holds pair i ^ perm.
+__device__ __forceinline__ void load_perm(const float *row, int n0, int perm, int N, bool live, F2 (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 2 * (i ^ perm);
+        h[i] = pair(row && live && n < N ? row[n] : 0.f, row && live && n + 1 < N ? row[n + 1] : 0.f);
+    }
+}
+__device__ __forceinline__ void store_perm(float *row, int n0, int perm, int N, const F2 (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 2 * (i ^ perm);
+        if (n < N) row[n] = lo(h[i]);
+        if (n + 1 < N) row[n + 1] = hi(h[i]);
+    }
+}
+// The same from a padded row, eight bytes at a time.
+__device__ __forceinline__ void load_padded(const float *row, int n0, int perm, bool live, F2 (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = live ? *reinterpret_cast<const F2 *>(row + n0 + 2 * (i ^ perm)) : both(0.f);
+}
+__device__ __forceinline__ F2 shfl_pair(F2 v, int mask) {
+    return pair(__shfl_xor_sync(0xffffffffu, lo(v), mask), __shfl_xor_sync(0xffffffffu, hi(v), mask));
+}
 
 template <typename T, int NL>
 __global__ void __launch_bounds__(kBwdThreads, 2) scan_bwd_kernel(ScanArgs a) {
     using S = BwdShape<NL>;
     constexpr int CS = S::CS, CL = S::CL, CH = S::CH, NP = S::NP, VL = S::VL;
-    constexpr int VPR = CH / 8, RPP = kBwdThreads / VPR, PASSES = kTile / RPP;
-    static_assert(RPP <= kTile && RPP * PASSES == kTile, "rows of the loading threads");
+    constexpr int VPR = S::VPR, RPP = kBwdThreads / VPR, PASSES = S::PASSES;
+    constexpr bool STAGED = sizeof(T) == 2;
     extern __shared__ __align__(16) unsigned char raw[];
-    float4 *ck = reinterpret_cast<float4 *>(raw);                       // [REGIONS][warp][cs][lane]
-    float *st = reinterpret_cast<float *>(ck + S::REGIONS * S::REGION); // [kTile][CH]: step, then ds
+    float4 *ck = reinterpret_cast<float4 *>(raw);                       // [kBlocks - 1][warp][cs][2][lane]
+    float *st = reinterpret_cast<float *>(ck + (kBlocks - 1) * kBwdWarps * S::REGION);   // [kTile][CH]: step, then ds
     float *xs = st + kTile * CH;                                        // x, then dx
     float *gs = xs + kTile * CH;                                        // g, then y
     float *bc = gs + kTile * CH;                                        // [kTile][2][NP]
     int *seq = reinterpret_cast<int *>(bc + kTile * 2 * NP);            // [kTile] the token's sequence
     unsigned *masks = reinterpret_cast<unsigned *>(seq + kTile);        // tokens that start / end one
+    using Piece = T[8];
+    Piece *ahead = reinterpret_cast<Piece *>(masks + 4);                // [4 * PASSES + BCV][thread]
 
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nl = lane % NL, cl = lane / NL, n0 = nl * 4;
+    const int nl = lane % NL, cl = lane / NL, n0 = nl * 8, perm = (cl & 1) * 2 | (cl >> 1 & 1);
     const int chan_block = blockIdx.x % a.chan_blocks, chan0 = chan_block * CH;
     const int seg = blockIdx.x / a.chan_blocks;
     const int b = seg / a.segs;
@@ -234,240 +157,316 @@ __global__ void __launch_bounds__(kBwdThreads, 2) scan_bwd_kernel(ScanArgs a) {
     }
     if (a.T == 0) return;
 
-    F2 A2[CS][2], dA[CS][2], dh[CS][2];
+    F2 A2[CS][4], dA[CS][4], dh[CS][4];
+    float skip[CS];
 #pragma unroll
     for (int cs = 0; cs < CS; ++cs) {
         const bool live = channel(cs) < a.D;
-        load_pairs(a.A + (long long)channel(cs) * a.N, n0, a.N, live, A2[cs]);
-        load_pairs(a.gloc + (((long long)b * a.row_tiles + last_tile) * a.D + channel(cs)) * NP, n0, NP, live, dh[cs]);
+        load_perm(a.A + (long long)channel(cs) * a.N, n0, perm, a.N, live, A2[cs]);
+        load_padded(a.gloc + ((long long)seg * a.D + channel(cs)) * NP, n0, perm, live, dh[cs]);
+        skip[cs] = a.skip && live ? a.skip[channel(cs)] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            A2[cs][i] = mul2(A2[cs][i], pair(kLog2e, kLog2e));
-            dA[cs][i] = pair(0.f, 0.f);
+        for (int i = 0; i < 4; ++i) {
+            A2[cs][i] = mul2(A2[cs][i], both(kLog2e));
+            dA[cs][i] = both(0.f);
         }
     }
     const int lv = tid % VPR, lrow = tid / VPR, lc = chan0 + lv * 8, lrest = a.D - lc;
-    float bias[8], dbias[8], dskip[8];
+    F2 bias[4], dbias[4], dskip[4];
+    load_pairs(a.bias ? a.bias + lc : nullptr, 0, lrest, true, bias);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bias[e] = a.bias && e < lrest ? a.bias[lc + e] : 0.f;
-        dbias[e] = dskip[e] = 0.f;
-    }
+    for (int e = 0; e < 4; ++e) dbias[e] = dskip[e] = both(0.f);
     const T *px = static_cast<const T *>(a.x) + b * a.x_batch + lc, *pd = static_cast<const T *>(a.dt) + b * a.dt_batch + lc;
     const T *pz = static_cast<const T *>(a.z) + b * a.z_batch + lc, *pg = static_cast<const T *>(a.dy) + b * a.dy_batch + lc;
 
+    // raw row pieces of a tile: i = array * PASSES + pass for x, dt, z, dy, then B and C
+    auto source = [&](int i, int t0, int &n) -> const T * {
+        if (i < 4 * PASSES) {
+            const int q = i % PASSES * RPP + lrow, t = t0 + q;
+            n = q < kTile && t < a.T ? lrest : 0;
+            switch (i / PASSES) {
+                case 0: return px + t * a.x_token;
+                case 1: return pd + t * a.dt_token;
+                case 2: n = a.z ? n : 0; return pz + t * a.z_token;
+                default: return pg + t * a.dy_token;
+            }
+        }
+        const int j = (i - 4 * PASSES) * kBwdThreads + tid, v = j % NL, c = j / NL % 2, q = j / (2 * NL), t = t0 + q;
+        n = q < kTile && t < a.T ? a.N - v * 8 : 0;
+        return v * 8 + (c ? static_cast<const T *>(a.Cm) + b * a.c_batch + t * a.c_token
+                          : static_cast<const T *>(a.Bm) + b * a.b_batch + t * a.b_token);
+    };
+    auto stage = [&](int tile) {
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < 4 * PASSES + S::BCV; ++i) {
+                int n;
+                const T *src = source(i, tile * kTile, n);
+                copy8_async<T>(ahead[i * kBwdThreads + tid], src, n, i < 4 * PASSES ? a.vec : a.bc_vec);
+            }
+            copy_commit();
+        }
+    };
+    auto fetch = [&](int i, int t0) -> Raw<T, 8> {
+        if constexpr (STAGED) return load_raw<T, 8>(ahead[i * kBwdThreads + tid]);
+        int n;
+        const T *src = source(i, t0, n);
+        return load8<T>(src, n, i < 4 * PASSES ? a.vec : a.bc_vec);
+    };
+    stage(last_tile);
     for (int tile = last_tile; tile >= first_tile; --tile) {
         const int t0 = tile * kTile, t1 = min(a.T, t0 + kTile);
+        if (STAGED) copy_wait<0>();
         __syncthreads();   // the tile after this one has left shared memory
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int q = i * RPP + lrow, t = t0 + q;
-            const bool in = t < t1;
-            const int n = in ? lrest : 0;
-            float x[8], d[8], z[8], g[8];
-            unpack<T, 8>(load8<T>(px + t * a.x_token, n, a.vec), x);
-            unpack<T, 8>(load8<T>(pd + t * a.dt_token, n, a.vec), d);
-            unpack<T, 8>(load8<T>(pz + t * a.z_token, a.z ? n : 0, a.vec), z);
-            unpack<T, 8>(load8<T>(pg + t * a.dy_token, n, a.vec), g);
+            if (q >= kTile) continue;
+            F2 x[4], d[4], z[4], g[4];
+            unpack_pairs<T>(fetch(i, t0), x);
+            unpack_pairs<T>(fetch(PASSES + i, t0), d);
+            unpack_pairs<T>(fetch(2 * PASSES + i, t0), z);
+            unpack_pairs<T>(fetch(3 * PASSES + i, t0), g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float pre = d[e] + bias[e];
-                d[e] = in ? (a.softplus ? softplus_f32(pre) : pre) : 0.f;   // a token past the end: step 0
-                if (a.z) g[e] *= z[e] * sigmoid_f32(z[e]);
-                dskip[e] = fmaf(g[e], x[e], dskip[e]);
+            for (int e = 0; e < 4; ++e) {
+                d[e] = add2(d[e], bias[e]);
+                if (a.softplus) d[e] = softplus_pair(d[e]);
+                if (t >= t1) d[e] = both(0.f);   // a token past the end: step 0
+                if (a.z) g[e] = mul2(g[e], mul2(z[e], sigmoid_pair(z[e])));
+                dskip[e] = fma2(g[e], x[e], dskip[e]);
             }
+            const int at = q * CH + lv * 8;
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const int at = q * CH + lv * 8 + e;
-                *reinterpret_cast<float4 *>(st + at) = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
-                *reinterpret_cast<float4 *>(xs + at) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                *reinterpret_cast<float4 *>(gs + at) = make_float4(g[e], g[e + 1], g[e + 2], g[e + 3]);
+            for (int e = 0; e < 2; ++e) {
+                reinterpret_cast<ulonglong2 *>(st + at)[e] = make_ulonglong2(d[2 * e], d[2 * e + 1]);
+                reinterpret_cast<ulonglong2 *>(xs + at)[e] = make_ulonglong2(x[2 * e], x[2 * e + 1]);
+                reinterpret_cast<ulonglong2 *>(gs + at)[e] = make_ulonglong2(g[2 * e], g[2 * e + 1]);
             }
         }
-        for (int j = tid; j < kTile * 2 * (NP / 8); j += kBwdThreads) {
-            const int v = j % (NP / 8), c = j / (NP / 8) % 2, q = j / (2 * (NP / 8)), t = t0 + q;
-            const T *src = c ? static_cast<const T *>(a.Cm) + b * a.c_batch + t * a.c_token
-                             : static_cast<const T *>(a.Bm) + b * a.b_batch + t * a.b_token;
-            float f[8];
-            unpack<T, 8>(load8<T>(src + v * 8, t < t1 ? a.N - v * 8 : 0, a.bc_vec), f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) bc[(q * 2 + c) * NP + v * 8 + e] = f[e];
+        for (int i = 0; i < S::BCV; ++i) {
+            const int j = i * kBwdThreads + tid;
+            if (j >= kTile * 2 * NL) continue;
+            F2 f[4];
+            unpack_pairs<T>(fetch(4 * PASSES + i, t0), f);
+            ulonglong2 *at = reinterpret_cast<ulonglong2 *>(bc + j / NL * NP + j % NL * 8);
+            at[0] = make_ulonglong2(f[0], f[1]);
+            at[1] = make_ulonglong2(f[2], f[3]);
         }
+        if (tile > first_tile) stage(tile - 1);
         if (warp == 0) {
             const int t = min(t0 + lane, a.T - 1);
             const int n = a.cu ? find_seq(a.cu, a.n_seqs, t) : b;
             const bool starts = a.cu ? __ldg(a.cu + n) == t : t == 0, ends = a.cu ? __ldg(a.cu + n + 1) == t + 1 : t == a.T - 1;
             const unsigned ms = __ballot_sync(0xffffffffu, starts && t0 + lane < t1);
             const unsigned me = __ballot_sync(0xffffffffu, ends && t0 + lane < t1);
-            seq[lane] = n;
+            if (lane < kTile) seq[lane] = n;
             if (lane == 0) masks[0] = ms, masks[1] = me;
         }
         __syncthreads();
         const unsigned ms = masks[0], me = masks[1];
-        auto initial = [&](int j, int cs, F2 (&h)[2]) {
-            load_pairs(a.init ? a.init + ((long long)seq[j] * a.D + channel(cs)) * a.N : nullptr, n0, a.N,
-                       channel(cs) < a.D, h);
+        auto initial = [&](int j, int cs, F2 (&h)[4]) {
+            load_perm(a.init ? a.init + ((long long)seq[j] * a.D + channel(cs)) * a.N : nullptr, n0, perm, a.N,
+                      channel(cs) < a.D, h);
         };
-        const long long map = ((long long)b * a.row_tiles + tile) * a.D;
-        // forward: the state before every block of tokens but the first
+        // row j's B (c = 0) or C (c = 1) in the lane's order of pairs
+        auto load_bc = [&](int j, int c, F2 (&v)[4]) {
 #pragma unroll
-        for (int cs = 0; cs < CS; ++cs) {
-            F2 h[2];
-            load_pairs(a.hloc + (map + channel(cs)) * NP, n0, NP, channel(cs) < a.D, h);
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const F2 *>(bc + (j * 2 + c) * NP + n0 + 2 * (i ^ perm));
+        };
+        // the tile's start state: the segment's, moved on to the tile
+        auto start_state = [&](int cs, F2 (&h)[4]) {
+            const bool ok = channel(cs) < a.D;
+            if (tile == first_tile) {
+                load_padded(a.hloc + ((long long)seg * a.D + channel(cs)) * NP, n0, perm, ok, h);
+                return;
+            }
+            const long long at = ((long long)b * a.row_tiles + tile) * a.D + channel(cs);
+            load_padded(a.htile + at * NP, n0, perm, ok, h);
+            if (a.exact[(long long)b * a.row_tiles + tile]) return;
+            const float sum = ok ? a.stile[at] : 0.f;
+            F2 first[4];
+            load_padded(a.hloc + ((long long)seg * a.D + channel(cs)) * NP, n0, perm, ok, first);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = fma2(exp2_pair(mul2(both(sum), A2[cs][i])), first[i], h[i]);
+        };
+        // forward: the state before every block of tokens but the first
+        {
+            F2 h[CS][4];
+#pragma unroll
+            for (int cs = 0; cs < CS; ++cs) start_state(cs, h[cs]);
+#pragma unroll 1
             for (int kb = 0; kb < kBlocks - 1; ++kb) {
 #pragma unroll
                 for (int k = 0; k < kBlock; ++k) {
                     const int j = kb * kBlock + k;
-                    const float s = st[j * CH + local(cs)], sx = s * xs[j * CH + local(cs)];
-                    const ulonglong2 B = *reinterpret_cast<const ulonglong2 *>(bc + j * 2 * NP + n0);
-                    if (ms >> j & 1) initial(j, cs, h);
-                    h[0] = fma2(exp2_pair(mul2(pair(s, s), A2[cs][0])), h[0], mul2(pair(sx, sx), B.x));
-                    h[1] = fma2(exp2_pair(mul2(pair(s, s), A2[cs][1])), h[1], mul2(pair(sx, sx), B.y));
+                    F2 B[4];
+                    load_bc(j, 0, B);
+                    if (ms >> j & 1) {
+#pragma unroll
+                        for (int cs = 0; cs < CS; ++cs) initial(j, cs, h[cs]);
+                    }
+#pragma unroll
+                    for (int cs = 0; cs < CS; ++cs) {
+                        const float s = st[j * CH + local(cs)], sx = s * xs[j * CH + local(cs)];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            h[cs][i] = fma2(exp2_pair(mul2(both(s), A2[cs][i])), h[cs][i], mul2(both(sx), B[i]));
+                    }
                 }
-                ck[((kb * kBwdWarps + warp) * CS + cs) * 32 + lane] = make_float4(lo(h[0]), hi(h[0]), lo(h[1]), hi(h[1]));
+#pragma unroll
+                for (int cs = 0; cs < CS; ++cs) {
+                    ulonglong2 *at = reinterpret_cast<ulonglong2 *>(ck + (kb * kBwdWarps + warp) * S::REGION + cs * 64 + lane);
+                    at[0] = make_ulonglong2(h[cs][0], h[cs][1]);
+                    at[32] = make_ulonglong2(h[cs][2], h[cs][3]);
+                }
             }
         }
         // backward
-        for (int kb = kBlocks - 1; kb >= 0; --kb) {
-            float acc[kBlock * 8];   // [token][dB, dC][four n], over this lane's channels
+        F2 acc[kBlock][2][4];   // dB, dC over this lane's channels
+        auto walk = [&](auto plain, int kb) {   // plain: no sequence starts or ends in the block
+            F2 B[kBlock][4], C[kBlock][4];
 #pragma unroll
-            for (int i = 0; i < kBlock * 8; ++i) acc[i] = 0.f;
-            ulonglong2 B[kBlock], C[kBlock];
-#pragma unroll
-            for (int k = 0; k < kBlock; ++k) {
-                B[k] = *reinterpret_cast<const ulonglong2 *>(bc + (kb * kBlock + k) * 2 * NP + n0);
-                C[k] = *reinterpret_cast<const ulonglong2 *>(bc + (kb * kBlock + k) * 2 * NP + NP + n0);
-            }
+            for (int k = 0; k < kBlock; ++k) load_bc(kb * kBlock + k, 0, B[k]), load_bc(kb * kBlock + k, 1, C[k]);
 #pragma unroll
             for (int cs = 0; cs < CS; ++cs) {
                 const int chl = local(cs), ch = channel(cs);
-                F2 h[2], e[kBlock][2], p[kBlock][2];
+                F2 h[4], e[kBlock][4], p[kBlock][4];
                 float s[kBlock], x[kBlock], g[kBlock], y[kBlock], u[kBlock], w[kBlock];
                 if (kb == 0) {
-                    load_pairs(a.hloc + (map + ch) * NP, n0, NP, ch < a.D, h);
+                    start_state(cs, h);
                 } else {
-                    const float4 v = ck[(((kb - 1) * kBwdWarps + warp) * CS + cs) * 32 + lane];
-                    h[0] = pair(v.x, v.y), h[1] = pair(v.z, v.w);
+                    const ulonglong2 *at = reinterpret_cast<const ulonglong2 *>(ck + ((kb - 1) * kBwdWarps + warp) * S::REGION + cs * 64 + lane);
+                    const ulonglong2 v0 = at[0], v1 = at[32];
+                    h[0] = v0.x, h[1] = v0.y, h[2] = v1.x, h[3] = v1.y;
                 }
 #pragma unroll
                 for (int k = 0; k < kBlock; ++k) {
                     const int j = kb * kBlock + k;
                     s[k] = st[j * CH + chl], x[k] = xs[j * CH + chl], g[k] = gs[j * CH + chl];
-                    const float sx = s[k] * x[k];
-                    if (ms >> j & 1) initial(j, cs, h);
-                    e[k][0] = exp2_pair(mul2(pair(s[k], s[k]), A2[cs][0]));
-                    e[k][1] = exp2_pair(mul2(pair(s[k], s[k]), A2[cs][1]));
-                    p[k][0] = mul2(e[k][0], h[0]);
-                    p[k][1] = mul2(e[k][1], h[1]);
-                    h[0] = fma2(pair(sx, sx), B[k].x, p[k][0]);
-                    h[1] = fma2(pair(sx, sx), B[k].y, p[k][1]);
-                    const F2 yy = fma2(C[k].y, h[1], mul2(C[k].x, h[0]));
+                    const F2 ss = both(s[k]), sx = both(s[k] * x[k]), gg = both(g[k]);
+                    if (!plain && (ms >> j & 1)) initial(j, cs, h);
+                    F2 yy = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[k][i] = exp2_pair(mul2(ss, A2[cs][i]));
+                        p[k][i] = mul2(e[k][i], h[i]);
+                        h[i] = fma2(sx, B[k][i], p[k][i]);
+                        yy = i ? fma2(C[k][i], h[i], yy) : mul2(C[k][i], h[i]);
+                        acc[k][1][i] = cs ? fma2(gg, h[i], acc[k][1][i]) : mul2(gg, h[i]);
+                    }
                     y[k] = lo(yy) + hi(yy);
-                    // dC, while the state is at hand
-                    const F2 gg = pair(g[k], g[k]);
-                    F2 c0 = pair(acc[k * 8 + 4], acc[k * 8 + 5]), c1 = pair(acc[k * 8 + 6], acc[k * 8 + 7]);
-                    c0 = fma2(gg, h[0], c0), c1 = fma2(gg, h[1], c1);
-                    acc[k * 8 + 4] = lo(c0), acc[k * 8 + 5] = hi(c0), acc[k * 8 + 6] = lo(c1), acc[k * 8 + 7] = hi(c1);
                 }
 #pragma unroll
                 for (int k = kBlock - 1; k >= 0; --k) {
                     const int j = kb * kBlock + k;
-                    const float sx = s[k] * x[k];
-                    const F2 gg = pair(g[k], g[k]), ss = pair(s[k], s[k]), sxx = pair(sx, sx);
-                    if (me >> j & 1 && a.d_final) {
-                        F2 f[2];
-                        load_pairs(a.d_final + ((long long)seq[j] * a.D + ch) * a.N, n0, a.N, ch < a.D, f);
-                        dh[cs][0] = add2(dh[cs][0], f[0]), dh[cs][1] = add2(dh[cs][1], f[1]);
+                    const F2 gg = both(g[k]), ss = both(s[k]), sx = both(s[k] * x[k]);
+                    if (!plain && (me >> j & 1) && a.d_final) {
+                        F2 f[4];
+                        load_perm(a.d_final + ((long long)seq[j] * a.D + ch) * a.N, n0, perm, a.N, ch < a.D, f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dh[cs][i] = add2(dh[cs][i], f[i]);
                     }
-                    dh[cs][0] = fma2(gg, C[k].x, dh[cs][0]);
-                    dh[cs][1] = fma2(gg, C[k].y, dh[cs][1]);
-                    F2 b0 = pair(acc[k * 8], acc[k * 8 + 1]), b1 = pair(acc[k * 8 + 2], acc[k * 8 + 3]);
-                    b0 = fma2(sxx, dh[cs][0], b0), b1 = fma2(sxx, dh[cs][1], b1);
-                    acc[k * 8] = lo(b0), acc[k * 8 + 1] = hi(b0), acc[k * 8 + 2] = lo(b1), acc[k * 8 + 3] = hi(b1);
-                    const F2 uu = fma2(dh[cs][1], B[k].y, mul2(dh[cs][0], B[k].x));
-                    const F2 q0 = mul2(dh[cs][0], p[k][0]), q1 = mul2(dh[cs][1], p[k][1]);
-                    dA[cs][0] = fma2(ss, q0, dA[cs][0]);
-                    dA[cs][1] = fma2(ss, q1, dA[cs][1]);
-                    const F2 ww = fma2(q1, A2[cs][1], mul2(q0, A2[cs][0]));
+                    F2 uu = both(0.f), ww = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dh[cs][i] = fma2(gg, C[k][i], dh[cs][i]);
+                        acc[k][0][i] = cs ? fma2(sx, dh[cs][i], acc[k][0][i]) : mul2(sx, dh[cs][i]);
+                        uu = i ? fma2(dh[cs][i], B[k][i], uu) : mul2(dh[cs][i], B[k][i]);
+                        const F2 q = mul2(dh[cs][i], p[k][i]);
+                        dA[cs][i] = fma2(ss, q, dA[cs][i]);
+                        ww = i ? fma2(q, A2[cs][i], ww) : mul2(q, A2[cs][i]);
+                        dh[cs][i] = mul2(dh[cs][i], e[k][i]);
+                    }
                     u[k] = lo(uu) + hi(uu);
                     w[k] = lo(ww) + hi(ww);
-                    dh[cs][0] = mul2(dh[cs][0], e[k][0]);
-                    dh[cs][1] = mul2(dh[cs][1], e[k][1]);
-                    if (ms >> j & 1) {   // the gradient of the sequence's initial state
+                    if (!plain && (ms >> j & 1)) {   // the gradient of the sequence's initial state
                         if (a.dinit && ch < a.D)
-                            store_pairs(a.dinit + ((long long)seq[j] * a.D + ch) * a.N, n0, a.N, dh[cs]);
-                        dh[cs][0] = dh[cs][1] = pair(0.f, 0.f);
+                            store_perm(a.dinit + ((long long)seq[j] * a.D + ch) * a.N, n0, perm, a.N, dh[cs]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dh[cs][i] = both(0.f);
                     }
                 }
-                // over the lanes of the channel; each is left with its token or tokens
+                // over the lanes of the channel; each is left with its token (or both)
                 int k0 = 0, k1 = 0, k2 = 0;
                 reduce_scatter<kBlock, NL / 2, 1>(u, lane, k0);
                 reduce_scatter<kBlock, NL / 2, 1>(w, lane, k1);
                 if (a.z) reduce_scatter<kBlock, NL / 2, 1>(y, lane, k2);
                 __syncwarp();
-                constexpr int KEPT = NL >= kBlock ? 1 : kBlock / NL;
-                const float skip = a.skip && ch < a.D ? a.skip[ch] : 0.f;
+                constexpr int KEPT = NL == 1 ? kBlock : 1;
 #pragma unroll
                 for (int i = 0; i < KEPT; ++i) {
-                    float sk = 0.f, xk = 0.f, gk = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kBlock; ++k)
-                        if (k == k0 + i) sk = s[k], xk = x[k], gk = g[k];
+                    const float sk = k0 + i ? s[1] : s[0], xk = k0 + i ? x[1] : x[0], gk = k0 + i ? g[1] : g[0];
                     const int at = (kb * kBlock + k0 + i) * CH + chl;
                     st[at] = fmaf(u[i], xk, w[i] * kLn2);
-                    xs[at] = fmaf(u[i], sk, skip * gk);
-                    gs[at] = fmaf(skip, xk, y[i]);
+                    xs[at] = fmaf(u[i], sk, skip[cs] * gk);
+                    gs[at] = fmaf(skip[cs], xk, y[i]);
                 }
             }
-            // dB, dC over the lanes of the warp's channels
-            int base = 0;
-            reduce_scatter<kBlock * 8, 16, NL>(acc, lane, base);
-            __syncwarp();
-            constexpr int OWN = S::REGIONS == kBlocks ? kBlocks - 1 : 0;   // where block 0's go
-            float *res = reinterpret_cast<float *>(ck + ((kb ? kb - 1 : OWN) * kBwdWarps + warp) * CS * 32) +
-                         (kb == 0 && S::REGIONS != kBlocks ? 32 * NL : 0);
+        };
+#pragma unroll 1
+        for (int kb = kBlocks - 1; kb >= 0; --kb) {
+            if (((ms | me) >> kb * kBlock & ((1u << kBlock) - 1)) == 0) walk(std::true_type(), kb);
+            else walk(std::false_type(), kb);
+            // dB, dC over the lanes of the warp's channels: every lane keeps its slots 0
+            // and 1, then 0, of four
+            float v[kBlock * 2 * 2];
 #pragma unroll
-            for (int i = 0; i < VL; ++i) res[nl * 32 + base + i] = acc[i];
+            for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const F2 a0 = add2(acc[k][c][0], shfl_pair(acc[k][c][2], NL)), a1 = add2(acc[k][c][1], shfl_pair(acc[k][c][3], NL));
+                    const F2 a2 = add2(a0, shfl_pair(a1, 2 * NL));
+                    v[(k * 2 + c) * 2] = lo(a2), v[(k * 2 + c) * 2 + 1] = hi(a2);
+                }
+            int base = 0;
+            reduce_scatter<kBlock * 4, 16, 4 * NL>(v, lane, base);
+            __syncwarp();
+            float *res = reinterpret_cast<float *>(ck + ((kb ? kb - 1 : 0) * kBwdWarps + warp) * S::REGION) + (kb ? 0 : 4 * NP);
+#pragma unroll
+            for (int i = 0; i < VL; ++i) res[((base + i) / 2) * NP + n0 + 2 * perm + (base + i) % 2] = v[i];
         }
         __syncthreads();
         // dB, dC of the tile over the block's channels
         const long long tokens = (long long)a.B * a.T;
         for (int i = tid; i < (t1 - t0) * 2 * NP; i += kBwdThreads) {
             const int n = i % NP, c = i / NP % 2, j = i / (2 * NP), kb = j / kBlock;
-            const int at = (n / 4) * 32 + (j % kBlock) * 8 + c * 4 + n % 4;
-            constexpr int OWN = S::REGIONS == kBlocks ? kBlocks - 1 : 0;
             float v = 0.f;
 #pragma unroll
             for (int wp = 0; wp < kBwdWarps; ++wp)
-                v += (reinterpret_cast<const float *>(ck + ((kb ? kb - 1 : OWN) * kBwdWarps + wp) * CS * 32) +
-                      (kb == 0 && S::REGIONS != kBlocks ? 32 * NL : 0))[at];
+                v += (reinterpret_cast<const float *>(ck + ((kb ? kb - 1 : 0) * kBwdWarps + wp) * S::REGION) +
+                      (kb ? 0 : 4 * NP))[(j % kBlock * 2 + c) * NP + n];
             a.part_bc[((chan_block * tokens + (long long)b * a.T + t0 + j) * 2 + c) * NP + n] = v;
         }
         // dx, ddt, dz
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int q = i * RPP + lrow, t = t0 + q;
-            if (t >= t1 || lrest <= 0) continue;
-            float d[8], z[8], g[8], o[8];
+            if (q >= kTile || t >= t1 || lrest <= 0) continue;
+            float o[8];
             const long long at = ((long long)b * a.T + t) * a.D + lc;
             const int in = q * CH + lv * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = xs[in + e];
             store8<T>(static_cast<T *>(a.out) + at, o, lrest, a.vec);
-            unpack<T, 8>(load8<T>(pd + t * a.dt_token, lrest, a.vec), d);
+            F2 d[4], z[4], g[4];
+            unpack_pairs<T>(load8<T>(pd + t * a.dt_token, lrest, a.vec), d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                o[e] = st[in + e] * (a.softplus ? sigmoid_f32(d[e] + bias[e]) : 1.f);
-                dbias[e] += o[e];
+            for (int e = 0; e < 4; ++e) {
+                F2 v = *reinterpret_cast<const F2 *>(st + in + 2 * e);
+                if (a.softplus) v = mul2(v, sigmoid_pair(add2(d[e], bias[e])));
+                dbias[e] = add2(dbias[e], v);
+                o[2 * e] = lo(v), o[2 * e + 1] = hi(v);
             }
             store8<T>(static_cast<T *>(a.ddt) + at, o, lrest, a.vec);
             if (a.z) {
-                unpack<T, 8>(load8<T>(pz + t * a.z_token, lrest, a.vec), z);
-                unpack<T, 8>(load8<T>(pg + t * a.dy_token, lrest, a.vec), g);
+                unpack_pairs<T>(load8<T>(pz + t * a.z_token, lrest, a.vec), z);
+                unpack_pairs<T>(load8<T>(pg + t * a.dy_token, lrest, a.vec), g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float sg = sigmoid_f32(z[e]);
-                    o[e] = g[e] * gs[in + e] * sg * fmaf(z[e], 1.f - sg, 1.f);
+                for (int e = 0; e < 4; ++e) {
+                    const F2 sg = sigmoid_pair(z[e]), y = *reinterpret_cast<const F2 *>(gs + in + 2 * e);
+                    const F2 v = mul2(mul2(g[e], y), mul2(sg, fma2(z[e], fma2(sg, both(-1.f), both(1.f)), both(1.f))));
+                    o[2 * e] = lo(v), o[2 * e + 1] = hi(v);
                 }
                 store8<T>(static_cast<T *>(a.dz) + at, o, lrest, a.vec);
             }
@@ -476,13 +475,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) scan_bwd_kernel(ScanArgs a) {
     // the segment's sums over tokens
 #pragma unroll
     for (int cs = 0; cs < CS; ++cs)
-        if (channel(cs) < a.D) store_pairs(a.part_a + ((long long)seg * a.D + channel(cs)) * NP, n0, NP, dA[cs]);
+        if (channel(cs) < a.D) store_perm(a.part_a + ((long long)seg * a.D + channel(cs)) * NP, n0, perm, NP, dA[cs]);
     __syncthreads();
     float *sum = reinterpret_cast<float *>(raw);   // [2][RPP][CH]
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        sum[lrow * CH + lv * 8 + e] = dskip[e];
-        sum[(RPP + lrow) * CH + lv * 8 + e] = dbias[e];
+    for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<F2 *>(sum + lrow * CH + lv * 8 + 2 * e) = dskip[e];
+        *reinterpret_cast<F2 *>(sum + (RPP + lrow) * CH + lv * 8 + 2 * e) = dbias[e];
     }
     __syncthreads();
     for (int i = tid; i < 2 * CH; i += kBwdThreads) {
@@ -537,20 +536,13 @@ __global__ void __launch_bounds__(256) scan_bwd_param_kernel(const float *part_a
     }
 }
 
-template <typename T, int LP>
-cudaError_t launch_maps(ScanArgs a, cudaStream_t s) {
-    a.chan_blocks = (a.D + kMapThreads / LP - 1) / (kMapThreads / LP);
-    scan_tile_maps_kernel<T, LP><<<(unsigned)((long long)a.chan_blocks * a.B * a.row_tiles), kMapThreads, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
 template <typename T, int NL>
 cudaError_t launch_main(ScanArgs a, cudaStream_t s) {
     using S = BwdShape<NL>;
-    const cudaError_t attr =
-        cudaFuncSetAttribute(scan_bwd_kernel<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+    constexpr size_t smem = S::smem + S::template staged<T>;
+    const cudaError_t attr = cudaFuncSetAttribute(scan_bwd_kernel<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (attr != cudaSuccess) return attr;
-    scan_bwd_kernel<T, NL><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), kBwdThreads, S::smem, s>>>(a);
+    scan_bwd_kernel<T, NL><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), kBwdThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -560,20 +552,15 @@ cudaError_t launch_bwd_typed(const ScanArgs &a, T *dB, T *dC, float *dA, float *
     const long long tokens = (long long)a.B * a.T;
     cudaError_t e = cudaSuccess;
     if (tokens > 0) {
-        switch (parts) {
-            case 1: e = launch_maps<T, 1>(a, s); break;
-            case 2: e = launch_maps<T, 2>(a, s); break;
-            case 4: e = launch_maps<T, 4>(a, s); break;
-            default: e = launch_maps<T, 8>(a, s);
-        }
-        if (e == cudaSuccess) e = launch_scan_combine(a, a.row_tiles, true, s);
+        e = launch_scan_maps(a, sizeof(T) == 2 ? GDN_BF16 : GDN_F32, s);
+        if (e == cudaSuccess) e = launch_scan_combine(a, a.segs, true, s);
         if (e != cudaSuccess) return e;
     }
     switch (parts) {
-        case 1: e = launch_main<T, 2>(a, s); break;
-        case 2: e = launch_main<T, 4>(a, s); break;
-        case 4: e = launch_main<T, 8>(a, s); break;
-        default: e = launch_main<T, 16>(a, s);
+        case 1: e = launch_main<T, 1>(a, s); break;
+        case 2: e = launch_main<T, 2>(a, s); break;
+        case 4: e = launch_main<T, 4>(a, s); break;
+        default: e = launch_main<T, 8>(a, s);
     }
     if (e != cudaSuccess) return e;
     if (tokens > 0) {
@@ -589,7 +576,14 @@ cudaError_t launch_bwd_typed(const ScanArgs &a, T *dB, T *dC, float *dA, float *
 
 }  // namespace
 
-int scan_bwd_channels(int N) { return N <= 8 ? BwdShape<2>::CH : N <= 16 ? BwdShape<4>::CH : N <= 32 ? BwdShape<8>::CH : BwdShape<16>::CH; }
+int scan_bwd_channels(int N) {
+    switch (scan_parts(N)) {
+        case 1: return BwdShape<1>::CH;
+        case 2: return BwdShape<2>::CH;
+        case 4: return BwdShape<4>::CH;
+        default: return BwdShape<8>::CH;
+    }
+}
 
 cudaError_t launch_scan_bwd(const ScanArgs &a, int dtype, void *dB, void *dC, float *dA, float *dskip, float *dbias,
                             cudaStream_t s) {
