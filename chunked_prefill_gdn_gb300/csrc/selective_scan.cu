@@ -53,13 +53,12 @@ struct ScanShape {
     static constexpr int BCP = 32 / BCR;                    // rows of B and C per pass
     static constexpr int BCV = kTile / BCP;
     static constexpr int ARRAYS = MODE == kState ? 2 : MODE == kFull ? 3 : 4;
-    // rows of 8-byte entries per channel, shifted by a quarter of a bank row so that
-    // the four rows written together do not meet in a bank
-    static constexpr int SD = CW * 2 + 8;
-    static constexpr int YS = CW + 4;
+    // rows of a value per channel, shifted by a quarter of a bank row so that the four
+    // rows that a pass writes or reads together do not meet in a bank
+    static constexpr int ROW = CW + 8;
     static constexpr size_t rows_bytes = 3 * ARRAYS * PASSES * 32 * 8 * sizeof(T);
     static constexpr size_t bcr_bytes = 2 * BCV * 32 * 8 * sizeof(T);
-    static constexpr size_t smem = rows_bytes + bcr_bytes + 2 * kTile * (SD + 2 * NP + (MODE == kFull ? NW * YS : MODE == kMaps ? CW : 0)) * 4;
+    static constexpr size_t smem = rows_bytes + bcr_bytes + 2 * kTile * (2 * ROW + 2 * NP + (MODE == kFull ? NW * ROW : MODE == kMaps ? ROW : 0)) * 4;
 };
 
 template <typename T, int NPT, int NW, int MODE>
@@ -70,10 +69,10 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
     using Piece = T[8];
     Piece *rows = reinterpret_cast<Piece *>(smem);                              // [3][ARRAYS][PASSES][lane]
     Piece *bcr = reinterpret_cast<Piece *>(smem + S::rows_bytes);               // [2][BCV][lane]
-    float *sd = reinterpret_cast<float *>(smem + S::rows_bytes + S::bcr_bytes); // [2][TILE][SD]: step, step * x
-    float *bc = sd + 2 * TILE * S::SD;                                          // [2][TILE][2][NP]
-    float *ys = bc + 2 * TILE * 2 * NP;                                         // kFull: [2][NW][TILE][YS], y
-    float *gs = ys;                                                             // kMaps: [2][TILE][CW], dy through the gate
+    float *sd = reinterpret_cast<float *>(smem + S::rows_bytes + S::bcr_bytes); // [2][TILE][2][ROW]: step, step * x
+    float *bc = sd + 2 * TILE * 2 * S::ROW;                                     // [2][TILE][2][NP]
+    float *ys = bc + 2 * TILE * 2 * NP;                                         // kFull: [2][NW][TILE][ROW], y
+    float *gs = ys;                                                             // kMaps: [2][TILE][ROW], dy through the gate
 
     if (MODE == kFull && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31;
@@ -149,29 +148,29 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
             copy_commit();
         };
         auto prepare = [&](int k) {
-            float *s_at = sd + k % 2 * TILE * S::SD, *bc_at = bc + k % 2 * TILE * 2 * NP;
+            float *s_at = sd + k % 2 * TILE * 2 * S::ROW, *bc_at = bc + k % 2 * TILE * 2 * NP;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
-                float *at = s_at + (i * RPP + lrow) * S::SD + lv * 2;
+                float *at = s_at + (i * RPP + lrow) * 2 * S::ROW + lv * 2;
                 F2 x[4], d[4];
                 unpack_pairs<T>(load_raw<T, 8>(piece(k, 0, i)), x);
                 unpack_pairs<T>(load_raw<T, 8>(piece(k, 1, i)), d);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     d[e] = add2(d[e], bias[e]);
-                    const F2 s = a.softplus ? softplus_pair(d[e]) : d[e], sx = mul2(s, x[e]);
-                    *reinterpret_cast<float2 *>(at + 2 * e * VPR * 2) = make_float2(lo(s), lo(sx));
-                    *reinterpret_cast<float2 *>(at + (2 * e + 1) * VPR * 2) = make_float2(hi(s), hi(sx));
+                    const F2 s = a.softplus ? softplus_pair(d[e]) : d[e];
+                    *reinterpret_cast<F2 *>(at + e * VPR * 2) = s;
+                    *reinterpret_cast<F2 *>(at + S::ROW + e * VPR * 2) = mul2(s, x[e]);
                 }
                 if (MODE == kMaps) {
-                    float *g_at = gs + (k % 2 * TILE + i * RPP + lrow) * CW + lv;
+                    float *g_at = gs + (k % 2 * TILE + i * RPP + lrow) * S::ROW + lv * 2;
                     F2 g[4], z[4];
                     unpack_pairs<T>(load_raw<T, 8>(piece(k, 3, i)), g);
                     if (gated) unpack_pairs<T>(load_raw<T, 8>(piece(k, 2, i)), z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (gated) g[e] = mul2(g[e], mul2(z[e], sigmoid_pair(z[e])));
-                        g_at[2 * e * VPR] = lo(g[e]), g_at[(2 * e + 1) * VPR] = hi(g[e]);
+                        *reinterpret_cast<F2 *>(g_at + e * VPR * 2) = g[e];
                     }
                 }
             }
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
             }
         };
         auto finish = [&](int k) {
-            const float *y_at = ys + k % 2 * NW * TILE * S::YS;
+            const float *y_at = ys + k % 2 * NW * TILE * S::ROW + lv * 2;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int q = i * RPP + lrow;
@@ -196,10 +195,10 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
                 if (gated) unpack_pairs<T>(load_raw<T, 8>(piece(k, 2, i)), z);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float *at = y_at + q * S::YS + 2 * e * VPR + lv;
-                    F2 y = pair(at[0], at[VPR]);
+                    const float *at = y_at + q * S::ROW + e * VPR * 2;
+                    F2 y = *reinterpret_cast<const F2 *>(at);
 #pragma unroll
-                    for (int w = 1; w < NW; ++w) y = add2(y, pair(at[w * TILE * S::YS], at[w * TILE * S::YS + VPR]));
+                    for (int w = 1; w < NW; ++w) y = add2(y, *reinterpret_cast<const F2 *>(at + w * TILE * S::ROW));
                     y = fma2(skip[e], x[e], y);
                     if (gated) y = mul2(y, mul2(z[e], sigmoid_pair(z[e])));
                     o[2 * e] = lo(y), o[2 * e + 1] = hi(y);
@@ -224,9 +223,9 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
         return;
     }
 
-    // a scanning warp: the channels in the order in which the feeding lanes lay
-    // them down, so that neither side meets in a bank
-    const int n0 = warp * NPT, ch = chan0 + lane % VPR * 8 + lane / VPR;
+    // a scanning warp: the channels in the order in which the feeding lanes lay them
+    // down, pair e of vector v at place e VPR + v
+    const int n0 = warp * NPT, ch = chan0 + lane / 2 % VPR * 8 + lane / 2 / VPR * 2 + lane % 2;
     const bool live = ch < a.D;
     if (MODE == kFull && a.final_state && live) {    // a sequence without a token keeps its state
         auto keep = [&](int n) {
@@ -254,12 +253,12 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
     float step_sum = 0.f;
     F2 p[M], G[M];   // kMaps: the product of the a's so far, the gradient at the tile's start
     auto token = [&](auto with_g, int j, const float *s_at, const float *bc_at, float *y_at) {
-        const float2 sv = *reinterpret_cast<const float2 *>(s_at + j * S::SD);
-        const F2 ss = both(sv.x), sx = both(sv.y);
+        const float step = s_at[j * 2 * S::ROW];
+        const F2 ss = both(step), sx = both(s_at[j * 2 * S::ROW + S::ROW]);
         const ulonglong2 *Bk = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP);
         const ulonglong2 *Ck = reinterpret_cast<const ulonglong2 *>(bc_at + j * 2 * NP + NP);
         F2 y0 = both(0.f), y1 = both(0.f), gg = both(0.f);
-        if (with_g) gg = both(y_at[j * CW]);
+        if (with_g) gg = both(y_at[j * S::ROW]);
 #pragma unroll
         for (int i = 0; i < M / 2; ++i) {
             const ulonglong2 b = Bk[i];
@@ -281,9 +280,9 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
         }
         if (MODE == kFull) {
             y0 = add2(y0, y1);
-            y_at[j * S::YS] = lo(y0) + hi(y0);
+            y_at[j * S::ROW] = lo(y0) + hi(y0);
         } else {
-            step_sum += sv.x;
+            step_sum += step;
         }
     };
     using Yes = std::integral_constant<bool, MODE == kMaps>;
@@ -291,8 +290,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
         const int t = r.t0 + k * TILE, stop = min(r.t1, t + TILE);
-        const float *s_at = sd + k % 2 * TILE * S::SD + lane * 2, *bc_at = bc + k % 2 * TILE * 2 * NP + n0;
-        float *y_at = MODE == kFull ? ys + (k % 2 * NW + warp) * TILE * S::YS + lane : gs + k % 2 * TILE * CW + lane;
+        const float *s_at = sd + k % 2 * TILE * 2 * S::ROW + lane, *bc_at = bc + k % 2 * TILE * 2 * NP + n0;
+        float *y_at = MODE == kFull ? ys + (k % 2 * NW + warp) * TILE * S::ROW + lane : gs + k % 2 * TILE * S::ROW + lane;
         if (MODE == kMaps) {
             const bool here = r.begin == t;
             if (t % a.seg_tokens == 0) {   // a new segment
@@ -453,6 +452,9 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     }
 }
 
+// Blocks of the scanning kernels that an SM holds, by N.
+int scan_resident(int N) { return N <= 16 ? 7 : N <= 32 ? 4 : 2; }
+
 template <typename T, int NPT, int NW, int MODE>
 cudaError_t launch_scan_one(const ScanArgs &a, int segs, cudaStream_t s) {
     using S = ScanShape<T, NPT, NW, MODE>;
@@ -498,12 +500,14 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 }
 
 // Segments per row in the forward pass.  One segment takes each exponential
-// once; several take it twice but put that many times the warps to work.
+// once; several take it twice but put that many times the blocks to work: they
+// are cut when whole rows leave half of the SMs' room free, as many as fill it
+// once.
 int scan_segments(int B, int T, int D, int N) {
     const int tiles = (T + kTile - 1) / kTile;
-    const long long warps = (long long)B * ((D + 31) / 32) * (N <= 16 ? 1 : N <= 32 ? 2 : 4), wanted = 7ll * device_sm_count();
-    if (tiles <= 1 || 2 * warps >= wanted) return 1;
-    const int segs = (int)std::min<long long>((wanted + warps - 1) / warps, tiles);
+    const long long blocks = (long long)B * ((D + 31) / 32), room = (long long)scan_resident(N) * device_sm_count();
+    if (tiles <= 1 || 2 * blocks > room) return 1;
+    const int segs = (int)std::min<long long>(room / blocks, tiles);
     const int len = (tiles + segs - 1) / segs;
     return (tiles + len - 1) / len;
 }
@@ -517,10 +521,10 @@ int scan_segment_tokens(int T, int segs) {
 cudaError_t launch_scan_maps(const ScanArgs &p, int dtype, cudaStream_t s) {
     ScanArgs a = p;
     a.chan_blocks = (a.D + 31) / 32;
-    // segments per block: as many as leave every SM seven blocks
+    // segments per block: as many as leave every SM six blocks
     const int per_seg = a.seg_tokens / kTile, row_segs = (a.row_tiles + per_seg - 1) / per_seg;
     const long long all = (long long)a.B * row_segs * a.chan_blocks;
-    const int per = (int)std::max<long long>(1, std::min<long long>(all / (7ll * device_sm_count()), row_segs));
+    const int per = (int)std::max<long long>(1, std::min<long long>(all / (6ll * device_sm_count()), row_segs));
     a.segs = (row_segs + per - 1) / per;
     a.span_tokens = per * a.seg_tokens;
 #define GDN_MAPS(NPT, NW) \
@@ -689,14 +693,17 @@ BwdPlan bwd_plan(int B, int T, int D, int N) {
     const int ch = scan_bwd_channels(N);
     p.row_tiles = (T + kTile - 1) / kTile;
     p.chan_blocks = (D + ch - 1) / ch;
-    // tiles per segment: what gives the shortest schedule on two blocks per SM,
-    // with half a tile's time for a block's own start and end
-    const long long slots = 2ll * device_sm_count();
+    // tiles per segment: what gives the shortest schedule of the main kernel (two
+    // blocks per SM, half a tile's time for a block's own start and end) and of the
+    // maps (a tile's time), whose tile takes about 2/11 as long
+    const long long slots = 2ll * device_sm_count(), map_slots = 6ll * device_sm_count();
     int per = 1;
     double best = 0;
     for (int m = 1; m <= 16 && m <= std::max(1, p.row_tiles); ++m) {
-        const long long blocks = (long long)B * ((p.row_tiles + m - 1) / m) * p.chan_blocks;
-        const double cost = (double)((blocks + slots - 1) / slots) * (m + 0.5);
+        const long long segs = (long long)B * ((p.row_tiles + m - 1) / m), blocks = segs * p.chan_blocks;
+        const long long map_blocks = segs * ((D + 31) / 32);
+        const double cost = (double)((blocks + slots - 1) / slots) * (m + 0.5) +
+                            (double)((map_blocks + map_slots - 1) / map_slots) * (m + 1) * (2.0 / 11);
         if (m == 1 || cost < best) best = cost, per = m;
     }
     p.segs = std::max(1, (p.row_tiles + per - 1) / per);
