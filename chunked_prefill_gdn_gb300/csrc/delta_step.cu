@@ -29,7 +29,7 @@ struct DeltaArgs {
     const int32_t *slots;
     void *o;
     int H, dk, dv, pool, l2norm;
-    long long units;
+    long long units, q_token, k_token, v_token;
     float scale;
 };
 
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_step_kernel(DeltaArgs a) 
         float qv[DK / 32], kv[DK / 32], qq = 0.f, kk = 0.f, qk = 0.f;
 #pragma unroll
         for (int i = 0; i < DK / 32; ++i) {
-            qv[i] = to_f32(static_cast<const T *>(a.q)[unit * DK + i * 32 + lane]);
-            kv[i] = to_f32(static_cast<const T *>(a.k)[unit * DK + i * 32 + lane]);
+            qv[i] = to_f32(static_cast<const T *>(a.q)[n * a.q_token + h * DK + i * 32 + lane]);
+            kv[i] = to_f32(static_cast<const T *>(a.k)[n * a.k_token + h * DK + i * 32 + lane]);
             qq = fmaf(qv[i], qv[i], qq);
             kk = fmaf(kv[i], kv[i], kk);
         }
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_step_kernel(DeltaArgs a) 
     }
     const float qk = dots[0], alpha = dots[1], beta = dots[2];
     float vv[4];
-    const T *v = static_cast<const T *>(a.v) + unit * a.dv + col0 + cg * 4;
+    const T *v = static_cast<const T *>(a.v) + n * a.v_token + (long long)h * a.dv + col0 + cg * 4;
 #pragma unroll
     for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[e]);
     float4 u;
@@ -161,8 +161,8 @@ cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s) {
 
 }  // namespace gdn
 
-extern "C" gdn_status gdn_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
-                                     float *state, const int32_t *state_indices, int n_states, float scale,
+extern "C" gdn_status gdn_delta_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                     int64_t v_stride, const float *g, const float *beta, float *state, const int32_t *state_indices, int n_states, float scale,
                                      int qk_l2norm, int N, int H, int dk, int dv, gdn_dtype dtype, void *o,
                                      gdn_stream_t stream) {
     using namespace gdn;
@@ -173,13 +173,18 @@ extern "C" gdn_status gdn_delta_step(const void *q, const void *k, const void *v
     if ((long long)N * H > (1ll << 28)) return GDN_ERR_UNSUPPORTED;
     if (N == 0) return GDN_OK;
     if (!q || !k || !v || !g || !beta || !state || !o) return GDN_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(state) ||
-        !aligned16(o))
-        return GDN_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)H * dk || k_stride < (int64_t)H * dk || v_stride < (int64_t)H * dv) return GDN_ERR_INVALID_ARG;
+    const uintptr_t em = dtype == GDN_F32 ? 3 : 1;
+    const void *elems[] = {q, k, v, o}, *f32[] = {g, beta, state_indices};
+    for (const void *p : elems)
+        if (reinterpret_cast<uintptr_t>(p) & em) return GDN_ERR_INVALID_ARG;
+    for (const void *p : f32)
+        if (reinterpret_cast<uintptr_t>(p) & 3) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(state)) return GDN_ERR_INVALID_ARG;
     DeltaArgs a = {};
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.state = state, a.slots = state_indices, a.o = o;
     a.H = H, a.dk = dk, a.dv = dv, a.pool = n_states, a.l2norm = qk_l2norm != 0;
-    a.units = (long long)N * H;
+    a.units = (long long)N * H, a.q_token = q_stride, a.k_token = k_stride, a.v_token = v_stride;
     a.scale = scale > 0.f ? scale : 1.f / sqrtf((float)dk);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == GDN_BF16 ? launch_delta<__nv_bfloat16>(a, s) : launch_delta<float>(a, s);

@@ -64,7 +64,7 @@ def bind(lib):
             ("gdn_selective_scan_bwd_workspace_size", sz, [i32] * 4),
             ("gdn_selective_scan_bwd", i32, [desc, vp, i64, i64] + [vp] * 12 + [sz, vp]),
             ("gdn_selective_scan_step", i32, [desc, vp, vp, i32, vp, vp]),
-            ("gdn_delta_step", i32, [vp] * 7 + [i32, f32] + [i32] * 6 + [vp, vp])):
+            ("gdn_delta_step", i32, [vp, i64, vp, i64, vp, i64] + [vp] * 4 + [i32, f32] + [i32] * 6 + [vp, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     global _bound
@@ -139,6 +139,18 @@ def _row_stride(name, t):
     if at[-1][1] < D:
         raise ValueError("%s: rows overlap" % name)
     return at[-1][1]
+
+
+def _head_stride(name, t):
+    """The distance between the tokens of a [N, H, d] tensor whose heads lie
+    next to each other."""
+    N, H, d = t.shape
+    st = t.stride()
+    if H > 1 and st[1] != d:
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if N > 1 and st[0] < H * d:
+        raise ValueError("%s: tokens overlap" % name)
+    return st[0] if N > 1 else H * d
 
 
 class _On:
@@ -601,17 +613,17 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
 def gated_delta_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_kernel: bool = False, state_indices=None,
                      out=None, stream: Optional[torch.cuda.Stream] = None):
     """One token of the gated delta rule for N sequences, chunk_fwd's recurrence
-    on a cached state: q, k [N, H, dk], v [N, H, dv] (bf16 or fp32), g, beta
-    [N, H] float32, state float32 [S, H, dk, dv] updated in place (row r uses
+    on a cached state: q, k [N, H, dk], v [N, H, dv] (bf16 or fp32, each token's
+    heads contiguous), g, beta [N, H] float32, state float32 [S, H, dk, dv] updated in place (row r uses
     state_indices[r], or r); returns o [N, H, dv].  A row whose index is outside
     [0, S) is padding: o is zero there."""
     _act("q", q)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q and k must be [N, H, dk], v [N, H, dv] and state [S, H, dk, dv]")
     (N, H, dk), dv, dev, dtype = q.shape, v.shape[2], q.device, q.dtype
-    _like("q", q, q.shape, dtype, dev)
-    _like("k", k, q.shape, dtype, dev)
-    _like("v", v, (N, H, dv), dtype, dev)
+    _like("k", k, q.shape, dtype, dev, strided=True)
+    _like("v", v, (N, H, dv), dtype, dev, strided=True)
+    sq, sk, sv = _head_stride("q", q), _head_stride("k", k), _head_stride("v", v)
     _like("g", g, (N, H), _F32, dev)
     _like("beta", beta, (N, H), _F32, dev)
     _like("state", state, (state.shape[0], H, dk, dv), _F32, dev)
@@ -621,7 +633,7 @@ def gated_delta_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_kerne
     on = _On(dev, stream)
     try:
         o = out if out is not None else on.empty(v.shape, dtype)
-        rc = _lib().gdn_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        rc = _lib().gdn_delta_step(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
                                    state.data_ptr(), _p(state_indices), state.shape[0],
                                    float(scale) if scale is not None else 0.0, 1 if use_qk_l2norm_in_kernel else 0,
                                    N, H, dk, dv, _CODE[dtype], o.data_ptr(), on.raw)

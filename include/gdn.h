@@ -680,15 +680,17 @@ gdn_status gdn_selective_scan_step(const gdn_scan_desc *desc, float *state, cons
 
 /*
  * One token of the gated delta rule (gdn_chunk_fwd's recurrence) for N
- * sequences: q, k [N, H, dk], v, o [N, H, dv] in dtype, g, beta fp32 [N, H],
- * state fp32 [n_states, H, dk, dv] in the layout of final_state, updated in
+ * sequences: q, k [N, H, dk], v [N, H, dv] in dtype, the tokens' rows of H heads
+ * q_stride (k_stride, v_stride) elements apart, so that slices of one projection
+ * can be used as they lie; o [N, H, dv] in dtype, g, beta fp32 [N, H]; state fp32
+ * [n_states, H, dk, dv] in the layout of final_state, 16-byte aligned, updated in
  * place.  dk, dv in {32, 64, 128}; scale <= 0 selects dk^-0.5; qk_l2norm = 1
- * scales the rows of q and k to unit L2 norm first (eps 1e-6).  All pointers
- * but state_indices 16-byte aligned.
+ * scales the rows of q and k to unit L2 norm first (eps 1e-6).
  */
-gdn_status gdn_delta_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
-                          float *state, const int32_t *state_indices, int n_states, float scale, int qk_l2norm,
-                          int N, int H, int dk, int dv, gdn_dtype dtype, void *o, gdn_stream_t stream);
+gdn_status gdn_delta_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                          int64_t v_stride, const float *g, const float *beta, float *state,
+                          const int32_t *state_indices, int n_states, float scale, int qk_l2norm, int N, int H,
+                          int dk, int dv, gdn_dtype dtype, void *o, gdn_stream_t stream);
 
 /* The CUDA error (and, for tensor-map encoding, the driver result) behind the
  * most recent GDN_ERR_CUDA returned on the calling host thread, as text such

@@ -485,6 +485,19 @@ def test_delta_step(N, H, dk, dv, dtype, norm):
         assert not o[1].any()
 
 
+def test_delta_step_takes_slices_of_one_projection():
+    g = rng(21)
+    N, H, d = 5, 3, 64
+    qkv = normal(g, N, 3, H, d, to="bf16")
+    gate, beta, S = -normal(g, N, H).abs(), torch.sigmoid(normal(g, N, H)), normal(g, N, H, d, d)
+    S2 = S.clone()
+    o = gdn.gated_delta_step(*qkv.unbind(1), gate, beta, S, use_qk_l2norm_in_kernel=True)
+    o2 = gdn.gated_delta_step(*(t.contiguous() for t in qkv.unbind(1)), gate, beta, S2, use_qk_l2norm_in_kernel=True)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    with pytest.raises(ValueError):
+        gdn.gated_delta_step(*(normal(g, N, H, 2 * d)[..., :d] for _ in range(3)), gate, beta, S)   # heads apart
+
+
 def test_delta_steps_continue_a_prompt():
     """chunk_fwd's final state goes on token by token as the longer prompt does
     (the parity bar of the prefill path: 5e-3 relative, 2e-2 largest)."""

@@ -92,12 +92,12 @@ def test_selective_scan_arguments(lib):
 
 
 def test_delta_step_arguments(lib):
-    def f(q=P, n=2, N=2, H=2, dk=32, dv=32, dt=1):
-        return lib.gdn_delta_step(q, P, P, P, P, P, None, n, 0.0, 0, N, H, dk, dv, dt, P, None)
+    def f(q=P, n=2, N=2, H=2, dk=32, dv=32, dt=1, st=64, state=P):
+        return lib.gdn_delta_step(q, st, P, 64, P, 64, P, P, state, None, n, 0.0, 0, N, H, dk, dv, dt, P, None)
 
     assert f(dk=48) == UNSUPPORTED and f(dv=256) == UNSUPPORTED
     assert f(q=None) == INVALID and f(n=1) == INVALID and f(H=0) == INVALID and f(dt=9) == INVALID
-    assert f(q=ctypes.c_void_p(4100)) == INVALID
+    assert f(q=ctypes.c_void_p(4098)) == INVALID and f(state=ctypes.c_void_p(4100)) == INVALID and f(st=63) == INVALID
     assert f(N=0, n=0) == 0
 
 
