@@ -518,13 +518,30 @@ int scan_segment_tokens(int T, int segs) {
 
 }  // namespace
 
+namespace {
+
+// Segments of `tiles` tiles that a block of the maps walks: what gives the
+// shortest schedule on six blocks per SM, with a tile's time for a block's own
+// start and end; that schedule's length in tiles.
+int maps_per_block(int B, int row_segs, int tiles, int chan_blocks, long long *cost) {
+    const long long slots = 6ll * device_sm_count();
+    int per = 1;
+    for (int m = 1; m <= row_segs && m <= 64; ++m) {
+        const long long blocks = (long long)B * ((row_segs + m - 1) / m) * chan_blocks;
+        const long long c = (blocks + slots - 1) / slots * (m * tiles + 1);
+        if (m == 1 || c < *cost) *cost = c, per = m;
+    }
+    return per;
+}
+
+}  // namespace
+
 cudaError_t launch_scan_maps(const ScanArgs &p, int dtype, cudaStream_t s) {
     ScanArgs a = p;
     a.chan_blocks = (a.D + 31) / 32;
-    // segments per block: as many as leave every SM six blocks
     const int per_seg = a.seg_tokens / kTile, row_segs = (a.row_tiles + per_seg - 1) / per_seg;
-    const long long all = (long long)a.B * row_segs * a.chan_blocks;
-    const int per = (int)std::max<long long>(1, std::min<long long>(all / (6ll * device_sm_count()), row_segs));
+    long long cost = 0;
+    const int per = maps_per_block(a.B, row_segs, per_seg, a.chan_blocks, &cost);
     a.segs = (row_segs + per - 1) / per;
     a.span_tokens = per * a.seg_tokens;
 #define GDN_MAPS(NPT, NW) \
@@ -695,15 +712,16 @@ BwdPlan bwd_plan(int B, int T, int D, int N) {
     p.chan_blocks = (D + ch - 1) / ch;
     // tiles per segment: what gives the shortest schedule of the main kernel (two
     // blocks per SM, half a tile's time for a block's own start and end) and of the
-    // maps (a tile's time), whose tile takes about 2/11 as long
-    const long long slots = 2ll * device_sm_count(), map_slots = 6ll * device_sm_count();
+    // maps, whose tile takes about 2/11 as long
+    const long long slots = 2ll * device_sm_count();
     int per = 1;
     double best = 0;
     for (int m = 1; m <= 16 && m <= std::max(1, p.row_tiles); ++m) {
-        const long long segs = (long long)B * ((p.row_tiles + m - 1) / m), blocks = segs * p.chan_blocks;
-        const long long map_blocks = segs * ((D + 31) / 32);
-        const double cost = (double)((blocks + slots - 1) / slots) * (m + 0.5) +
-                            (double)((map_blocks + map_slots - 1) / map_slots) * (m + 1) * (2.0 / 11);
+        const int row_segs = (p.row_tiles + m - 1) / m;
+        const long long blocks = (long long)B * row_segs * p.chan_blocks;
+        long long maps = 0;
+        maps_per_block(B, row_segs, m, (D + 31) / 32, &maps);
+        const double cost = (double)((blocks + slots - 1) / slots) * (m + 0.5) + maps * (2.0 / 11);
         if (m == 1 || cost < best) best = cost, per = m;
     }
     p.segs = std::max(1, (p.row_tiles + per - 1) / per);
