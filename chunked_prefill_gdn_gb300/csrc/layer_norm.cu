@@ -9,16 +9,22 @@
 //     dw = sum_rows dy xh,    db = sum_rows dy.
 //
 // Both passes are streams bound by HBM: x (and dy) are read once, y (or dx)
-// written once.  A row is held in registers (by a warp up to 512 columns, by
-// a block of 128, 256 or 512 threads above), so the variance is the two-pass one
+// written once.  A row is held in registers (by a warp up to 512 columns, by a
+// block of 128, 256 or 512 threads above), so the variance is the two-pass one
 // around the exact fp32 mean without a second read.  The blocks are persistent
-// and own their columns: the weights stay in registers over all rows of a
-// block, and in the backward pass so do the sums of dw and db, which leave the
-// block once, as one partial row per block; a second kernel adds those rows in
-// a fixed order, so the result does not depend on the launch.  The next rows come
-// in by asynchronous copies (up to four rows in flight, each
-// thread reading back what it copied) while the current one is reduced.  Rows wider than 8192 are read
-// three times instead (layer_norm_wide_*).
+// and own their columns: the weights stay in registers over all rows of a block,
+// and in the backward pass so do the sums of dw and db, which leave the block
+// once, as one partial row per block; a second kernel adds those rows in a fixed
+// order, so the result does not depend on the launch.  The next rows come in by
+// asynchronous copies (up to four in flight, each thread reading back what it
+// copied) while the current one is reduced.  The arithmetic is on pairs of
+// columns (two-wide FP32): unpaired, the backward pass was held up by its own
+// instructions between the barriers (163 us where it now takes 142).  Rows wider
+// than 8192 are read three times instead (layer_norm_wide_*).
+//
+// Measured (bf16, fp32 weights, 32768 x 4096): forward 97 us, 5.5 TB/s, 83% of
+// the measured copy rate; backward 142 us, 5.7 TB/s (85%), of it 7 us the sum
+// over the blocks; 16 rows of 4096 2.5 us.
 #include <algorithm>
 
 #include "elem.cuh"

@@ -9,12 +9,24 @@
 //
 // What bounds the forward pass is arithmetic, not memory: one exponential and
 // four multiply-adds per (token, channel, n) against about 8 bytes per (token,
-// channel).  ex2 runs at 32 lanes per clock and SM, FP32 FMA at 128 (measured
-// on a GB300), so both pipes are full at the same rate, 32 (token, channel, n)
-// per clock and SM; the arithmetic is written on pairs (two-wide FP32), which
-// leaves issue slots for the rest.  A thread keeps 16 n of one channel in
-// registers (N above 16: LP threads share a channel); B and C of a tile of
-// tokens are read from shared memory by all lanes at once.
+// channel).  ex2 runs at 32 lanes per clock and SM, FP32 FMA at 128 (measured on
+// a GB300), so both pipes are full at the same rate, 32 (token, channel, n) per
+// clock and SM; a loop of exactly these instructions, with B and C in shared
+// memory, reaches 20 of them with four warps per scheduler, 16 with two, 11 with
+// one.  The arithmetic is written on pairs (two-wide FP32), which leaves issue
+// slots for the rest.  B and C of a tile of tokens are read from shared memory by
+// all channels of a block at once, and what is per (token, channel) only
+// (softplus, the gate) is computed once, by a warp of its own.
+//
+// Measured (bf16, 16 n): 8 x 1024 tokens x 4096 channels 174 us (12 per clock and
+// SM): 6.7 scanning warps per SM are what 32768 channels give, and without the
+// feeding warps' work they alone take 136 us.  A row of 32768 tokens x 1024
+// channels 294 us, of it 118 the maps and 7 their combination.  Tried and dropped:
+// eight n per thread and twice the warps (lanes or warps sharing a channel: 213
+// and 199 us where 16 n took 197), two channels x eight n per thread, which halves
+// the reads of B and C (201 / 298 us: the same rate per SM, but blocks of 64
+// channels fill the SMs less evenly), tiles of 8 or 32 tokens, the exponentials of
+// the next token computed ahead (181 us).
 //
 // When the (sequence, channel) pairs do not fill the GPU, the token axis is cut
 // into segments: a first pass gives every segment's end state from a zero
@@ -311,8 +323,11 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
         }
         for (int q = t; q < stop;) {
             const int run_end = min(stop, r.end);
-            if (run_end - q == TILE && !(MODE == kMaps && inside)) {   // the usual case, with addresses known
-#pragma unroll
+            if (run_end - q == TILE && !(MODE == kMaps && inside)) {
+                // the usual case, with addresses known: unrolled whole (179 us on the batch
+                // of prompts where four at a time take 197), but for the longer token of
+                // kMaps (16 at a time miss the instruction cache: 322 us against 314)
+#pragma unroll(MODE == kMaps ? 4 : TILE)
                 for (int j = 0; j < TILE; ++j) token(Yes(), j, s_at, bc_at, y_at);
             } else if (MODE == kMaps && !inside) {
                 for (int j = q - t; j < run_end - t; ++j) token(Yes(), j, s_at, bc_at, y_at);
@@ -396,7 +411,9 @@ __global__ void __launch_bounds__(64) scan_combine_kernel(ScanArgs a, int maps, 
     }
 }
 
-// One token of each sequence: 4 n per thread, LANES threads per channel.
+// One token of each sequence: 4 n per thread, LANES threads per channel, so that a
+// warp reads and writes 512 contiguous bytes of the states; bound by their traffic
+// (32 x 4096 x 16, 18 MB: 5 us).
 template <typename T, int LANES>
 __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     const int part = threadIdx.x % LANES, ch = (int)((blockIdx.x * 128ll + threadIdx.x) / LANES);
@@ -421,8 +438,13 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = n0 + i < a.N ? state[i] : 0.f, av[i] = n0 + i < a.N ? A[i] : 0.f;
         }
+        if (a.bc_vec && n0 + 4 <= a.N) {
+            unpack<T, 4>(load_raw<T, 4>(B), Bv);
+            unpack<T, 4>(load_raw<T, 4>(C), Cv);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Bv[i] = n0 + i < a.N ? to_f32(B[i]) : 0.f, Cv[i] = n0 + i < a.N ? to_f32(C[i]) : 0.f;
+            for (int i = 0; i < 4; ++i) Bv[i] = n0 + i < a.N ? to_f32(B[i]) : 0.f, Cv[i] = n0 + i < a.N ? to_f32(C[i]) : 0.f;
+        }
         x = to_f32(static_cast<const T *>(a.x)[b * a.x_batch + ch]);
         float s = to_f32(static_cast<const T *>(a.dt)[b * a.dt_batch + ch]) + (a.bias ? a.bias[ch] : 0.f);
         if (a.softplus) s = softplus_f32(s);
