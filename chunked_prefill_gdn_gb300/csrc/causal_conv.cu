@@ -25,8 +25,8 @@
 // pass issues about 13 instructions per element against 4 bytes, the backward
 // pass 22 against 6.
 //
-// Measured (bf16, W = 4, SiLU): 65536 packed tokens x 6144 channels 276 us, 5.9
-// TB/s, 88% of the measured copy rate; backward 4 x 4095 x 4096 102 us, 4.0 TB/s
+// Measured (bf16, W = 4, SiLU): 65536 packed tokens x 6144 channels 266 us, 6.1
+// TB/s, 91% of the measured copy rate; backward 4 x 4095 x 4096 102 us, 4.0 TB/s
 // (59%): there the 128 registers of a thread leave 16 warps per SM, and what the
 // counters show is issue (1.7 per clock) and waiting for rows; one token of 64
 // sequences x 12288 channels 3.4 us, 3.7 TB/s.
@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
         y += a.D;
     };
     for (int t = r.t0; t < r.t1; t += kSub) {
-        if (t + kSub < min(r.end, r.t1) && t + 2 * kSub <= r.t1) {
-            // no boundary among these rows, and as many to follow
+        if (t + kSub <= r.t1 && t + kSub < r.end) {   // no boundary among these rows
+            const int more = r.t1 - t - kSub;
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
                 token(i);
-                ring[i] = load_raw<T, VEC>(x);
+                if (i < more) ring[i] = load_raw<T, VEC>(x);
                 x += a.x_token;
             }
             continue;
@@ -359,8 +359,10 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         };
         bool done = false;
         for (int t = r.t0; t < stop && !done; t += kSubB) {
+            // tokens and the positions they complete in the run and the sequence (predicated
+            // stores for the run's first positions or loads for its last rows would take more
+            // tokens through here, but cost 3 and 6 us of 102)
             if (t - (W - 1) >= max(r.begin, r.t0) && t + kSubB <= min(r.end, r.t1) && t + 2 * kSubB <= stop) {
-                // tokens and the positions they complete in the run and the sequence
                 T *out = dx + (long long)(t - (W - 1)) * a.D;
 #pragma unroll
                 for (int i = 0; i < kSubB; ++i) {
