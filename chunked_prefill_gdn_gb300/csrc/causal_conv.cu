@@ -47,7 +47,8 @@ namespace {
 constexpr int kConvWarps = 8;   // token runs per block
 constexpr int kConvRun = 128;   // tokens of a run, at most
 constexpr int kSub = 8;         // rows loaded ahead (forward)
-constexpr int kSubB = 6;        // rows of x and dy loaded ahead (backward)
+constexpr int kSubB = 4;        // rows of an unrolled step (backward)
+constexpr int kAheadBytes = 16; // element size x rows of x and dy on their way (backward)
 
 struct ConvArgs {
     const void *x, *dy, *w, *bias, *init, *d_final;
@@ -129,6 +130,17 @@ __device__ __forceinline__ void first_window(const ConvArgs &a, const Run &r, in
         if (t >= r.begin) unpack_pairs<T, VEC>(live ? load_raw<T, VEC>(x + t * a.x_token) : zero_raw<T, VEC>(), win[i]);
         else state_row<T, W, VEC>(a, a.init, r.n, (W - 1) + t - r.begin, c, live, win[i]);
     }
+}
+
+// VEC elements on their way into shared memory (a single 2-byte one by way of a
+// register).
+template <typename T, int VEC>
+__device__ __forceinline__ void copy_piece(T *dst, const T *src) {
+    constexpr int bytes = VEC * (int)sizeof(T);
+    if constexpr (bytes >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "n"(bytes) : "memory");
+    else
+        *dst = *src;
 }
 
 // u of a token whose row is x, and the window moved on.
@@ -243,7 +255,13 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
     constexpr int P = (VEC + 1) / 2;
-    __shared__ float sum[kConvWarps][W + 1][32 * VEC];
+    constexpr int kAhead = kAheadBytes / (int)sizeof(T);
+    using Piece = T[VEC];
+    using Rows = Piece[kAhead][2][32];               // of a warp
+    using Sums = float[W + 1][32 * VEC];             // of a warp, when it is done with its rows
+    __shared__ __align__(16) unsigned char shared[kConvWarps * (sizeof(Rows) > sizeof(Sums) ? sizeof(Rows) : sizeof(Sums))];
+    Piece *ring = reinterpret_cast<Rows *>(shared)[threadIdx.x >> 5][0][0];
+    Sums *sum = reinterpret_cast<Sums *>(shared);
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
@@ -283,13 +301,21 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + r.t0 * a.x_token + c;
         const T *dy = static_cast<const T *>(a.dy) + r.b * a.dy_batch + r.t0 * a.dy_token + c;
         T *dx = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
-        Raw<T, VEC> rx[kSubB], rg[kSubB];
-#pragma unroll
-        for (int i = 0; i < kSubB; ++i) {
-            rx[i] = r.t0 + i < stop ? load_raw<T, VEC>(x) : zero_raw<T, VEC>();
-            rg[i] = r.t0 + i < stop ? load_raw<T, VEC>(dy) : zero_raw<T, VEC>();
+        // rows of x and dy come in kAhead ahead, asynchronously where the address allows;
+        // a lane reads back what it copied
+        int loaded = 0;
+        auto load_row = [&](int t) {
+            Piece *at = ring + (loaded % kAhead * 2) * 32 + lane;
+            if (t < stop) {
+                copy_piece<T, VEC>(at[0], x);
+                copy_piece<T, VEC>(at[32], dy);
+            }
+            copy_commit();
             x += a.x_token, dy += a.dy_token;
-        }
+            ++loaded;
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_row(r.t0 + i);
         F2 w[W][P], bias[P], win[W - 1][P], acc[W][P];
         load_weights<W, VEC>(a, c, live, w, bias);
         r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
@@ -300,11 +326,14 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int k = 0; k < W; ++k) acc[k][p] = both(0.f);
-        // row i of the ring; acc[k] gathers dx of position (its own) - (W - 1) + k
-        auto token = [&](int i, bool mine) {
+        // the row of token t; acc[k] gathers dx of position t - (W - 1) + k
+        auto token = [&](int t, bool mine) {
             F2 xv[P], u[P], du[P];
-            unpack_pairs<T, VEC>(rx[i], xv);
-            unpack_pairs<T, VEC>(rg[i], du);
+            copy_wait<kAhead - 1>();
+            const Piece *at = ring + (loaded % kAhead * 2) * 32 + lane;
+            unpack_pairs<T, VEC>(load_raw<T, VEC>(at[0]), xv);
+            unpack_pairs<T, VEC>(load_raw<T, VEC>(at[32]), du);
+            load_row(t + kAhead);
             if (a.silu) {
                 conv_sum<W, P>(w, bias, win, xv, u);
 #pragma unroll
@@ -359,24 +388,18 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         };
         bool done = false;
         for (int t = r.t0; t < stop && !done; t += kSubB) {
-            // tokens and the positions they complete in the run and the sequence (predicated
-            // stores for the run's first positions or loads for its last rows would take more
-            // tokens through here, but cost 3 and 6 us of 102)
-            if (t - (W - 1) >= max(r.begin, r.t0) && t + kSubB <= min(r.end, r.t1) && t + 2 * kSubB <= stop) {
+            // tokens and the positions they complete in the run and the sequence
+            if (t - (W - 1) >= max(r.begin, r.t0) && t + kSubB <= min(r.end, r.t1)) {
                 T *out = dx + (long long)(t - (W - 1)) * a.D;
 #pragma unroll
                 for (int i = 0; i < kSubB; ++i) {
-                    token(i, true);
+                    token(t + i, true);
                     store_raw<T, VEC>(out, pack_pairs<T, VEC>(acc[0]));
                     out += a.D;
                     shift();
-                    rx[i] = load_raw<T, VEC>(x);
-                    rg[i] = load_raw<T, VEC>(dy);
-                    x += a.x_token, dy += a.dy_token;
                 }
                 continue;
             }
-#pragma unroll
             for (int i = 0; i < kSubB; ++i) {
                 const int q = t + i;
                 if (q >= stop || done) break;
@@ -391,19 +414,16 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) state_row<T, W, VEC>(a, a.init, r.n, k, c, true, win[k]);
                 }
-                token(i, q < r.t1);
+                token(q, q < r.t1);
                 emit(q - (W - 1), acc[0]);
                 shift();
-                if (q + kSubB < stop) {
-                    rx[i] = load_raw<T, VEC>(x);
-                    rg[i] = load_raw<T, VEC>(dy);
-                }
-                x += a.x_token, dy += a.dy_token;
             }
         }
+        copy_wait<0>();
         if (!done && stop == r.end) flush(stop);
     }
     if (!a.partial) return;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
 #pragma unroll
