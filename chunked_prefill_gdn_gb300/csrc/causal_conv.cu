@@ -555,6 +555,8 @@ struct ConvShape {
 gdn_status conv_shape_ok(const ConvShape &p, int64_t batch_stride, int64_t token_stride) {
     if (p.B < 0 || p.T < 0 || p.D < 1) return GDN_ERR_INVALID_ARG;
     if (p.W < 2 || p.W > 4) return GDN_ERR_UNSUPPORTED;
+    // token and channel indices are 32-bit, and so is the number of blocks
+    if (p.T > (1 << 30) || p.D > (1 << 30) || (long long)p.B * (p.T / kSub + 1) > (1ll << 30)) return GDN_ERR_UNSUPPORTED;
     if ((p.dtype != GDN_BF16 && p.dtype != GDN_F32) || (p.w_dtype != GDN_F32 && p.w_dtype != p.dtype))
         return GDN_ERR_INVALID_ARG;
     if (p.cu && (p.B != 1 || p.n_seqs < 1)) return GDN_ERR_INVALID_ARG;

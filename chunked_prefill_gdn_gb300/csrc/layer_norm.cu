@@ -461,6 +461,7 @@ bool elem_aligned(const void *p, int dtype) {
 
 gdn_status norm_args_ok(int64_t rows, int D, int dtype, int w_dtype, int64_t stride) {
     if (rows < 0 || D < 1 || stride < D) return GDN_ERR_INVALID_ARG;
+    if (D > (1 << 30)) return GDN_ERR_UNSUPPORTED;   // columns are counted in 32 bits
     if ((dtype != GDN_BF16 && dtype != GDN_F32) || (w_dtype != GDN_BF16 && w_dtype != GDN_F32)) return GDN_ERR_INVALID_ARG;
     return GDN_OK;
 }
@@ -472,7 +473,9 @@ gdn_status norm_args_ok(int64_t rows, int D, int dtype, int w_dtype, int64_t str
 extern "C" gdn_status gdn_layer_norm_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias,
                                          gdn_dtype w_dtype, float eps, int64_t rows, int D, gdn_dtype dtype, void *y,
                                          float *mean, float *rstd, gdn_stream_t stream) {
-    if (gdn::norm_args_ok(rows, D, dtype, w_dtype, x_stride) != GDN_OK || !(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = gdn::norm_args_ok(rows, D, dtype, w_dtype, x_stride);
+    if (st != GDN_OK) return st;
+    if (!(eps >= 0.f)) return GDN_ERR_INVALID_ARG;
     if (rows == 0) return GDN_OK;
     if (!x || !y || !gdn::elem_aligned(x, dtype) || !gdn::elem_aligned(y, dtype) ||
         !gdn::elem_aligned(weight, w_dtype) || !gdn::elem_aligned(bias, w_dtype) ||
@@ -501,7 +504,9 @@ extern "C" gdn_status gdn_layer_norm_bwd(const void *dy, int64_t dy_stride, cons
                                          const float *mean, const float *rstd, const void *weight, gdn_dtype w_dtype,
                                          int64_t rows, int D, gdn_dtype dtype, void *dx, float *dweight, float *dbias,
                                          void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
-    if (gdn::norm_args_ok(rows, D, dtype, w_dtype, x_stride) != GDN_OK || dy_stride < D) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = gdn::norm_args_ok(rows, D, dtype, w_dtype, x_stride);
+    if (st != GDN_OK) return st;
+    if (dy_stride < D) return GDN_ERR_INVALID_ARG;
     const bool params = dweight || dbias;
     if (!gdn::elem_aligned(dweight, GDN_F32) || !gdn::elem_aligned(dbias, GDN_F32) ||
         !gdn::elem_aligned(weight, w_dtype))

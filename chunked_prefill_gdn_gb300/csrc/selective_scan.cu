@@ -588,7 +588,8 @@ namespace {
 gdn_status scan_desc_ok(const gdn_scan_desc *p) {
     if (!p || p->B < 0 || p->T < 0 || p->D < 1 || p->N < 1) return GDN_ERR_INVALID_ARG;
     if (p->dtype != GDN_BF16 && p->dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
-    if (p->N > 64 || p->B > 65535) return GDN_ERR_UNSUPPORTED;
+    // token and channel indices are 32-bit
+    if (p->N > 64 || p->B > 65535 || p->T > (1 << 30) || p->D > (1 << 26)) return GDN_ERR_UNSUPPORTED;
     if (p->cu_seqlens && (p->B != 1 || p->n_seqs < 1)) return GDN_ERR_INVALID_ARG;
     if (p->B > 0 && (!p->A || (p->T > 0 && (!p->x || !p->dt || !p->B_ || !p->C_)))) return GDN_ERR_INVALID_ARG;
     const int64_t chan[] = {p->x_token_stride, p->dt_token_stride, p->z ? p->z_token_stride : p->D};
@@ -777,9 +778,8 @@ extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_desc *desc, const vo
     const gdn_status st = scan_desc_ok(desc);
     if (st != GDN_OK) return st;
     const gdn_scan_desc &p = *desc;
-    if (p.B == 0) return GDN_OK;
     if (dy_token_stride < p.D || dy_batch_stride < 0 || !dA) return GDN_ERR_INVALID_ARG;
-    if (p.T > 0 && (!dy || !dx || !ddt || !dB || !dC || (p.z && !dz))) return GDN_ERR_INVALID_ARG;
+    if (p.B > 0 && p.T > 0 && (!dy || !dx || !ddt || !dB || !dC || (p.z && !dz))) return GDN_ERR_INVALID_ARG;
     const uintptr_t em = p.dtype == GDN_F32 ? 3 : 1;
     const void *elems[] = {dy, dx, ddt, dB, dC, dz};
     for (const void *q : elems)

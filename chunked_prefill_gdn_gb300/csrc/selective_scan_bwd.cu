@@ -563,11 +563,13 @@ cudaError_t launch_bwd_typed(const ScanArgs &a, T *dB, T *dC, float *dA, float *
         if (e == cudaSuccess) e = launch_scan_combine(a, a.segs, true, s);
         if (e != cudaSuccess) return e;
     }
-    switch (parts) {
-        case 1: e = launch_main<T, 1>(a, s); break;
-        case 2: e = launch_main<T, 2>(a, s); break;
-        case 4: e = launch_main<T, 4>(a, s); break;
-        default: e = launch_main<T, 8>(a, s);
+    if (a.B > 0) {   // (without tokens: the gradients of the states)
+        switch (parts) {
+            case 1: e = launch_main<T, 1>(a, s); break;
+            case 2: e = launch_main<T, 2>(a, s); break;
+            case 4: e = launch_main<T, 4>(a, s); break;
+            default: e = launch_main<T, 8>(a, s);
+        }
     }
     if (e != cudaSuccess) return e;
     if (tokens > 0) {

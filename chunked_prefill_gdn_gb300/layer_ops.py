@@ -307,6 +307,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layer_norm_bwd(dy.contiguous(), x, mean, rstd, weight)
@@ -440,6 +441,7 @@ class _CausalConv(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, d_final):
         x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -590,6 +592,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, d_final):
         x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()

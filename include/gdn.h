@@ -563,7 +563,7 @@ gdn_status gdn_chunk_bwd_check(const void *workspace, gdn_stream_t stream);
  *
  * var the mean squared deviation.  x: `rows` rows, x_stride elements apart;
  * y: [rows, D]; weight, bias: [D] in w_dtype, either may be NULL (one, zero);
- * mean, rstd: fp32 [rows] outputs, either may be NULL.  eps >= 0.  Any D.
+ * mean, rstd: fp32 [rows] outputs, either may be NULL.  eps >= 0, D at most 2^30.
  */
 gdn_status gdn_layer_norm_fwd(const void *x, int64_t x_stride, const void *weight, const void *bias,
                               gdn_dtype w_dtype, float eps, int64_t rows, int D, gdn_dtype dtype, void *y,
@@ -591,7 +591,8 @@ gdn_status gdn_layer_norm_bwd(const void *dy, int64_t dy_stride, const void *x, 
  *
  *     u_t = bias + sum_{i < W} w_i x_{t - (W-1) + i},  y = silu ? u sigmoid(u) : u,
  *
- * W in {2, 3, 4}.  x: [B, T, D] with the given batch and token strides;
+ * W in {2, 3, 4}, T and D at most 2^30.  x: [B, T, D] with the given batch and
+ * token strides;
  * weight: [D, W], bias: [D] or NULL, in w_dtype (fp32 or dtype); y: [B, T, D].
  * The inputs before a sequence's first token are the rows of initial_state
  * [n, W - 1, D] (dtype, oldest first; NULL: zero), n = B or n_seqs;
@@ -640,8 +641,10 @@ gdn_status gdn_causal_conv_step(const void *x, int64_t x_stride, void *state, co
  * each with its own batch and token strides; A fp32 [D, N], D_skip and dt_bias
  * fp32 [D]; initial_state fp32 [n, D, N], n = B or n_seqs.  z (no gate),
  * D_skip and dt_bias (zero), initial_state (zero) and cu_seqlens may be NULL.
- * N at most 64, B at most 65535.  s A <= 0 is expected (a state that grows
- * overflows as the formula does).
+ * N at most 64, B at most 65535, T at most 2^30, D at most 2^26.  s A <= 0 is
+ * expected (a state that grows overflows as the formula does).  A step or x that
+ * is not finite makes its channel's outputs non-finite from that token to the
+ * end of its sequence, and no other channel's.
  */
 typedef struct {
     const void *x, *dt, *z, *B_, *C_;

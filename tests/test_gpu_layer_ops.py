@@ -383,6 +383,41 @@ def test_selective_scan_backward_of_no_tokens():
     assert torch.equal(got[8], c["dl"]) and not got[2].any() and not got[5].any() and not got[7].any()
 
 
+def test_no_sequences_give_zero_parameter_gradients():
+    c = scan_case(2, 5, 8, 16, None, "f32")
+    none = lambda t: t[:0]   # noqa: E731
+    y, last = gdn.selective_scan_fwd(none(c["x"]), none(c["dt"]), c["A"], none(c["B"]), none(c["C"]))
+    assert y.shape == (0, 5, 8) and last.shape == (0, 8, 16)
+    got = gdn.selective_scan_bwd(none(c["dy"]), none(c["x"]), none(c["dt"]), c["A"], none(c["B"]), none(c["C"]))
+    assert not got[2].any() and not got[5].any() and not got[7].any()
+    x, w = torch.empty(0, 5, 8, device="cuda"), normal(rng(1), 8, 4)
+    assert gdn.causal_conv_fwd(x, w)[0].shape == (0, 5, 8)
+    _, dw, db, _ = gdn.causal_conv_bwd(x, x, w)
+    assert not dw.any() and not db.any()
+    assert gdn.causal_conv_step(x[:, 0], torch.empty(0, 3, 8, device="cuda"), w).shape == (0, 8)
+    q = torch.empty(0, 2, 32, device="cuda")
+    assert gdn.gated_delta_step(q, q, q, q[..., 0], q[..., 0], torch.empty(0, 2, 32, 32, device="cuda")).shape == (0, 2, 32)
+
+
+@pytest.mark.parametrize("N", [16, 24])
+def test_selective_scan_channels_stand_alone(N):
+    """A NaN in one channel's input, or an infinite one, leaves the others' outputs,
+    states and gradients as they are."""
+    c = scan_case(1, 60, 40, N, [0, 20, 60], "f32")
+    run = lambda: gdn.selective_scan_fwd(c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c))   # noqa: E731
+    grads = lambda: gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c))   # noqa: E731
+    (y, last), g = run(), grads()
+    c["x"][0, 30, 7], c["dt"][0, 31, 9] = float("nan"), float("inf")
+    (y2, last2), g2 = run(), grads()
+    others = [i for i in range(40) if i not in (7, 9)]
+    assert torch.equal(y[..., others], y2[..., others]) and torch.equal(last[:, others], last2[:, others])
+    assert torch.equal(y[:, :20], y2[:, :20])                 # and the sequence before
+    assert not torch.isfinite(y2[0, 30:, 7]).any()
+    for i in (0, 1, 6):
+        assert torch.equal(g[i][..., others], g2[i][..., others])
+    assert torch.equal(g[2][others], g2[2][others]) and torch.equal(g[8][:, others], g2[8][:, others])
+
+
 def test_selective_scan_plain_steps_and_no_options():
     """dt used as it is (positive and zero steps, no bias), no skip, no gate, no state."""
     c = scan_case(2, 70, 12, 16, None, "f32")

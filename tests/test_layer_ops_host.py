@@ -30,6 +30,7 @@ def test_layer_norm_arguments(lib):
     assert f(P, 8, None, None, 1, 1e-5, 4, 8, 7, P, None, None, None) == INVALID        # type
     assert f(None, 8, None, None, 1, 1e-5, 4, 8, 1, P, None, None, None) == INVALID
     assert f(ctypes.c_void_p(4098), 8, None, None, 1, 1e-5, 4, 8, 1, P, None, None, None) == INVALID   # fp32 at 2 bytes
+    assert f(P, 1 << 31, None, None, 1, 1e-5, 4, (1 << 30) + 1, 1, P, None, None, None) == UNSUPPORTED
     assert f(None, 8, None, None, 1, 1e-5, 0, 8, 1, None, None, None, None) == 0        # no rows
     b = lib.gdn_layer_norm_bwd
     size = lib.gdn_layer_norm_bwd_workspace_size(4, 8)
@@ -51,6 +52,7 @@ def test_causal_conv_arguments(lib):
     assert fwd(cu=P, n=0) == INVALID and fwd(cu=P, n=2, B=2) == INVALID
     assert fwd(wd=0) == INVALID                      # bf16 weights with fp32 activations
     assert fwd(B=0) == 0
+    assert fwd(T=(1 << 30) + 1) == UNSUPPORTED and fwd(B=1 << 30, T=64) == UNSUPPORTED
     size = lib.gdn_causal_conv_bwd_workspace_size(1, 8, 8, 4)
     assert size > 0 and lib.gdn_causal_conv_bwd_workspace_size(1, 8, 8, 5) == 0
     assert lib.gdn_causal_conv_bwd(P, 64, 8, P, 64, 8, P, None, 1, None, None, None, 0, 1, 8, 8, 4, 1, 1, P, P, P, None,
@@ -71,6 +73,7 @@ def scan_desc(**kw):
 
 def test_selective_scan_arguments(lib):
     f = lambda **kw: lib.gdn_selective_scan_fwd(scan_desc(**kw), P, None, None, None, 0, None)   # noqa: E731
+    assert f(T=(1 << 30) + 1) == UNSUPPORTED and f(B=65536) == UNSUPPORTED
     assert f(N=65) == UNSUPPORTED and f(N=0) == INVALID and f(D=0) == INVALID
     assert f(x=None) == INVALID and f(A=None) == INVALID and f(dtype=3) == INVALID
     assert f(x_token_stride=7) == INVALID and f(b_token_stride=15) == INVALID and f(x_batch_stride=-1) == INVALID
