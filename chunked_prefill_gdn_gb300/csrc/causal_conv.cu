@@ -21,15 +21,13 @@
 // W partial sums of the dx that are not complete yet, so dy and x are read
 // once; dw and dbias stay in registers over the run, are added over the block's
 // warps and leave as one partial row per block that a second kernel adds in
-// order.  All arithmetic is on pairs of channels (two-wide FP32): the forward
-// pass issues about 13 instructions per element against 4 bytes, the backward
-// pass 22 against 6.
+// order.  All arithmetic is on pairs of channels (two-wide FP32).
 //
 // Measured (bf16, W = 4, SiLU): 65536 packed tokens x 6144 channels 266 us, 6.1
-// TB/s, 91% of the measured copy rate; backward 4 x 4095 x 4096 102 us, 4.0 TB/s
-// (59%): there the 128 registers of a thread leave 16 warps per SM, and what the
-// counters show is issue (1.7 per clock) and waiting for rows; one token of 64
-// sequences x 12288 channels 3.4 us, 3.7 TB/s.
+// TB/s, 91% of the measured copy rate; backward 4 x 4095 x 4096 93 us, 4.4 TB/s
+// (65%): there the 116 registers of a thread leave 16 warps per SM, which issue 2.3
+// instructions per clock, 28 per element; one token of 64 sequences x 12288
+// channels 3.3 us, 3.8 TB/s.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -39,11 +37,12 @@ namespace gdn {
 namespace {
 
 // Measured at 65536 packed tokens x 6144 channels forward, 4 x 4095 x 4096
-// backward (bf16): 4 warps and runs of 64 give 313 / 117 us, 8 warps 289 / 115,
-// with runs of 128 too 275 / 110 (16 warps 361, runs of 256 279); four rows ahead 318 us forward, 16 348;
-// four rows of both inputs ahead backward 110 us, six 103, eight (with runs of
-// 64) 121.  Eight channels per thread instead of four: 320 / 135 us, for want of
-// registers.
+// backward (bf16).  Forward: 4 warps and runs of 64 give 313 us, 8 warps 289, with
+// runs of 128 too 275 (16 warps 361, runs of 256 279; four rows ahead 318, 16 348;
+// eight channels per thread instead of four 320), with the run's last rows on the
+// boundary-free path 266.  Backward: rows in registers 102 us (eight channels per
+// thread 135), eight rows on their way into shared memory 93 (four or twelve 96;
+// steps of eight rows 98, of two 100).
 constexpr int kConvWarps = 8;   // token runs per block
 constexpr int kConvRun = 128;   // tokens of a run, at most
 constexpr int kSub = 8;         // rows loaded ahead (forward)
@@ -256,6 +255,7 @@ template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
     constexpr int P = (VEC + 1) / 2;
     constexpr int kAhead = kAheadBytes / (int)sizeof(T);
+    static_assert(kAhead % kSubB == 0, "a step's rows in neighbouring slots");
     using Piece = T[VEC];
     using Rows = Piece[kAhead][2][32];               // of a warp
     using Sums = float[W + 1][32 * VEC];             // of a warp, when it is done with its rows
@@ -301,21 +301,19 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         const T *x = static_cast<const T *>(a.x) + r.b * a.x_batch + r.t0 * a.x_token + c;
         const T *dy = static_cast<const T *>(a.dy) + r.b * a.dy_batch + r.t0 * a.dy_token + c;
         T *dx = static_cast<T *>(a.out) + (long long)r.b * a.T * a.D + c;
-        // rows of x and dy come in kAhead ahead, asynchronously where the address allows;
-        // a lane reads back what it copied
-        int loaded = 0;
-        auto load_row = [&](int t) {
-            Piece *at = ring + (loaded % kAhead * 2) * 32 + lane;
+        // rows of x and dy come in kAhead ahead, asynchronously where the address allows,
+        // row t in slot t - t0 modulo kAhead; a lane reads back what it copied
+        auto load_row = [&](Piece *at, int t) {
             if (t < stop) {
                 copy_piece<T, VEC>(at[0], x);
                 copy_piece<T, VEC>(at[32], dy);
             }
             copy_commit();
             x += a.x_token, dy += a.dy_token;
-            ++loaded;
         };
+        Piece *slots = ring + lane;   // the unrolled step's first slot
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_row(r.t0 + i);
+        for (int i = 0; i < kAhead; ++i) load_row(slots + i * 64, r.t0 + i);
         F2 w[W][P], bias[P], win[W - 1][P], acc[W][P];
         load_weights<W, VEC>(a, c, live, w, bias);
         r.n = a.cu ? find_seq(a.cu, a.n_seqs, r.t0) : r.b;
@@ -326,14 +324,14 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int k = 0; k < W; ++k) acc[k][p] = both(0.f);
-        // the row of token t; acc[k] gathers dx of position t - (W - 1) + k
-        auto token = [&](int t, bool mine) {
+        // row i of the step, that of token t; acc[k] gathers dx of position t - (W - 1) + k
+        auto token = [&](int i, int t, bool mine) {
             F2 xv[P], u[P], du[P];
+            Piece *at = slots + i * 64;
             copy_wait<kAhead - 1>();
-            const Piece *at = ring + (loaded % kAhead * 2) * 32 + lane;
             unpack_pairs<T, VEC>(load_raw<T, VEC>(at[0]), xv);
             unpack_pairs<T, VEC>(load_raw<T, VEC>(at[32]), du);
-            load_row(t + kAhead);
+            load_row(at, t + kAhead);
             if (a.silu) {
                 conv_sum<W, P>(w, bias, win, xv, u);
 #pragma unroll
@@ -387,13 +385,13 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
             }
         };
         bool done = false;
-        for (int t = r.t0; t < stop && !done; t += kSubB) {
+        for (int t = r.t0; t < stop && !done; t += kSubB, slots = kAhead == kSubB ? slots : ring + lane + (t - r.t0) % kAhead * 64) {
             // tokens and the positions they complete in the run and the sequence
             if (t - (W - 1) >= max(r.begin, r.t0) && t + kSubB <= min(r.end, r.t1)) {
                 T *out = dx + (long long)(t - (W - 1)) * a.D;
 #pragma unroll
                 for (int i = 0; i < kSubB; ++i) {
-                    token(t + i, true);
+                    token(i, t + i, true);
                     store_raw<T, VEC>(out, pack_pairs<T, VEC>(acc[0]));
                     out += a.D;
                     shift();
@@ -414,7 +412,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) state_row<T, W, VEC>(a, a.init, r.n, k, c, true, win[k]);
                 }
-                token(q, q < r.t1);
+                token(i, q, q < r.t1);
                 emit(q - (W - 1), acc[0]);
                 shift();
             }

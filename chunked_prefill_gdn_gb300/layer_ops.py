@@ -246,11 +246,11 @@ def _slots(state, state_indices, N, device):
 
 # ------------------------------------------------------------------ layer norm
 
-def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None,
+def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats: bool = True,
                    stream: Optional[torch.cuda.Stream] = None):
     """Layer norm over the last axis of x [..., D]; returns (y, mean, rstd),
-    mean and rstd float32 [...] for the backward pass.  weight and bias: [D] in
-    float32 or x's type, or None."""
+    mean and rstd float32 [...] for the backward pass (None without stats).
+    weight and bias: [D] in float32 or x's type, or None."""
     _act("x", x)
     D, lead, dev, dtype = x.shape[-1], x.shape[:-1], x.device, x.dtype
     wcode = _params(D, dev, dtype, weight, bias, (D,))
@@ -260,10 +260,12 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None,
     on = _On(dev, stream)
     try:
         y = out if out is not None else on.empty(x.shape, dtype)
-        mean, rstd = on.empty(lead, _F32), on.empty(lead, _F32)
-        rows = mean.numel()
+        mean = rstd = None
+        if stats:
+            mean, rstd = on.empty(lead, _F32), on.empty(lead, _F32)
+        rows = y.numel() // D if D else 0
         st = _lib().gdn_layer_norm_fwd(x.data_ptr(), stride, _p(weight), _p(bias), wcode, eps, rows, D, _CODE[dtype],
-                                       y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), on.raw)
+                                       y.data_ptr(), _p(mean), _p(rstd), on.raw)
         if st != 0:
             _raise(st, "gdn_layer_norm_fwd")
     finally:
@@ -317,6 +319,8 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """Layer norm over the last axis with autograd (x, weight, bias)."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))):
+        return layer_norm_fwd(x, weight, bias, eps, stats=False)[0]
     return _LayerNorm.apply(x, weight, bias, eps)
 
 

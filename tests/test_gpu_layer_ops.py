@@ -157,6 +157,8 @@ def test_layer_norm_autograd_and_determinism():
     again = gdn.layer_norm_bwd(dy, x, mean, rstd, w)
     for leaf, a, c in zip(leaves, first, again):
         assert torch.equal(a, c) and torch.equal(leaf.grad, a)
+    y, none, _ = gdn.layer_norm_fwd(x, w, b, stats=False)
+    assert none is None and torch.equal(y, gdn.layer_norm(x, w, b)) and torch.equal(y, gdn.layer_norm_fwd(x, w, b)[0])
 
 
 # ---------------------------------------------------- short causal convolution
