@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float *partial, 
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
     float s = 0.f;
+    grid_dependency_wait();
     if (c < D) {
 #pragma unroll 4
         for (int g = grp; g < groups; g += 8) s += partial[((long long)g * (W + 1) + k) * D + c];
@@ -656,9 +657,8 @@ extern "C" gdn_status gdn_causal_conv_bwd(const void *dy, int64_t dy_batch_strid
                               : launch_conv<Conv::kBwd, float>(a, W, vec, s);
     }
     if (e == cudaSuccess && params) {
-        conv_reduce_kernel<<<dim3((D + 31) / 32, W + 1), 256, 0, s>>>(static_cast<const float *>(workspace),
-                                                                     B > 0 ? a.groups : 0, W, D, dweight, dbias);
-        e = cudaGetLastError();
+        e = launch_dependent(conv_reduce_kernel, dim3((D + 31) / 32, W + 1), dim3(256), 0, s,
+                             static_cast<const float *>(workspace), B > 0 ? a.groups : 0, W, D, dweight, dbias);
     }
     if (e != cudaSuccess) {
         set_error_detail("launch causal_conv_bwd", e);

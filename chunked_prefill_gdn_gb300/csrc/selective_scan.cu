@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
     float *ys = bc + 2 * TILE * 2 * NP;                                         // kFull: [2][NW][TILE][ROW], y
     float *gs = ys;                                                             // kMaps: [2][TILE][ROW], dy through the gate
 
+    if (MODE == kFull) grid_dependency_wait();   // (the segments' start states)
     if (MODE == kFull && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31;
     int warp = threadIdx.x >> 5;
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
 template <bool GRAD>
 __global__ void __launch_bounds__(64) scan_combine_kernel(ScanArgs a, int maps, int NP) {
     constexpr int AHEAD = 8;
+    grid_dependency_wait();
     const long long at = (long long)blockIdx.x * 64 + threadIdx.x, size = (long long)a.D * NP;
     if (at >= size) return;
     const int ch = (int)(at / NP), n = (int)(at % NP);
@@ -485,8 +487,9 @@ cudaError_t launch_scan_one(const ScanArgs &a, int segs, cudaStream_t s) {
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
         if (e != cudaSuccess) return e;
     }
-    scan_kernel<T, NPT, NW, MODE>
-        <<<(unsigned)((long long)a.chan_blocks * a.B * segs), 32 * (NW + 1), S::smem, s>>>(a);
+    const dim3 grid((unsigned)((long long)a.chan_blocks * a.B * segs));
+    if (MODE == kFull && a.has_carry) return launch_dependent(scan_kernel<T, NPT, NW, MODE>, grid, dim3(32 * (NW + 1)), S::smem, s, a);
+    scan_kernel<T, NPT, NW, MODE><<<grid, 32 * (NW + 1), S::smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -578,9 +581,8 @@ cudaError_t launch_scan_maps(const ScanArgs &p, int dtype, cudaStream_t s) {
 cudaError_t launch_scan_combine(const ScanArgs &a, int maps, bool grad, cudaStream_t s) {
     const int NP = 8 * scan_parts(a.N);
     const dim3 grid((unsigned)(((long long)a.D * NP + 63) / 64), a.B, grad ? 2 : 1);
-    if (grad) scan_combine_kernel<true><<<grid, 64, 0, s>>>(a, maps, NP);
-    else scan_combine_kernel<false><<<grid, 64, 0, s>>>(a, maps, NP);
-    return cudaGetLastError();
+    return grad ? launch_dependent(scan_combine_kernel<true>, grid, dim3(64), 0, s, a, maps, NP)
+                : launch_dependent(scan_combine_kernel<false>, grid, dim3(64), 0, s, a, maps, NP);
 }
 
 namespace {

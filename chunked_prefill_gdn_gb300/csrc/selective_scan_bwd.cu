@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) scan_bwd_kernel(ScanArgs a) {
     using Piece = T[8];
     Piece *ahead = reinterpret_cast<Piece *>(masks + 4);                // [4 * PASSES + BCV][thread]
 
+    grid_dependency_wait();
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % NL, cl = lane / NL, n0 = nl * 8, perm = (cl & 1) * 2 | (cl >> 1 & 1);
@@ -500,31 +501,31 @@ __global__ void __launch_bounds__(kBwdThreads, 2) scan_bwd_kernel(ScanArgs a) {
     }
 }
 
-// dB, dC in the activations' type, over the blocks of channels.
+// The sums over blocks: the first `bc_blocks` blocks add dB and dC, in the
+// activations' type, over the blocks of channels; the others dA, dD and ddt_bias
+// over the segments, eight groups of segments per 32 values, then the groups in
+// order.
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const float *part, int blocks, long long tokens, int N, int NP,
-                                                          T *dB, T *dC) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, size = tokens * 2 * NP;
-    if (i >= size) return;
-    const int n = (int)(i % NP), c = (int)(i / NP % 2);
-    if (n >= N) return;
-    float v = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < blocks; ++k) v += part[k * size + i];
-    (c ? dC : dB)[i / (2 * NP) * N + n] = from_f32<T>(v);
-}
-
-// dA, dD and ddt_bias over the segments: eight groups of segments per 32
-// values, then the groups in order.
-__global__ void __launch_bounds__(256) scan_bwd_param_kernel(const float *part_a, const float *part_v, int segs, int D,
-                                                             int N, int NP, float *dA, float *dskip, float *dbias) {
+__global__ void __launch_bounds__(256) scan_bwd_sum_kernel(ScanArgs a, int bc_blocks, int chan_blocks, int segs, int NP,
+                                                           T *dB, T *dC, float *dA, float *dskip, float *dbias) {
     __shared__ float sum[8][32];
+    grid_dependency_wait();
+    if ((int)blockIdx.x < bc_blocks) {
+        const long long i = (long long)blockIdx.x * 256 + threadIdx.x, size = (long long)a.B * a.T * 2 * NP;
+        const int n = (int)(i % NP), c = (int)(i / NP % 2);
+        if (i >= size || n >= a.N) return;
+        float v = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < chan_blocks; ++k) v += a.part_bc[k * size + i];
+        (c ? dC : dB)[i / (2 * NP) * a.N + n] = from_f32<T>(v);
+        return;
+    }
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const long long i = (long long)blockIdx.x * 32 + lane, na = (long long)D * NP, total = na + 2 * D;
+    const long long i = (long long)(blockIdx.x - bc_blocks) * 32 + lane, na = (long long)a.D * NP, total = na + 2 * a.D;
     float v = 0.f;
     if (i < total) {
-        const float *p = i < na ? part_a + i : part_v + (i - na);
-        const long long step = i < na ? na : 2 * D;
+        const float *p = i < na ? a.part_a + i : a.part_v + (i - na);
+        const long long step = i < na ? na : 2 * a.D;
 #pragma unroll 4
         for (int s = grp; s < segs; s += 8) v += p[s * step];
     }
@@ -535,11 +536,11 @@ __global__ void __launch_bounds__(256) scan_bwd_param_kernel(const float *part_a
 #pragma unroll
     for (int k = 0; k < 8; ++k) v += sum[k][lane];
     if (i < na) {
-        if (i % NP < N) dA[i / NP * N + i % NP] = v;
-    } else if (i - na < D) {
+        if (i % NP < a.N) dA[i / NP * a.N + i % NP] = v;
+    } else if (i - na < a.D) {
         if (dskip) dskip[i - na] = v;
     } else if (dbias) {
-        dbias[i - na - D] = v;
+        dbias[i - na - a.D] = v;
     }
 }
 
@@ -549,8 +550,8 @@ cudaError_t launch_main(ScanArgs a, cudaStream_t s) {
     constexpr size_t smem = S::smem + S::template staged<T>;
     const cudaError_t attr = cudaFuncSetAttribute(scan_bwd_kernel<T, NL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (attr != cudaSuccess) return attr;
-    scan_bwd_kernel<T, NL><<<(unsigned)((long long)a.chan_blocks * a.B * a.segs), kBwdThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(scan_bwd_kernel<T, NL>, dim3((unsigned)((long long)a.chan_blocks * a.B * a.segs)),
+                            dim3(kBwdThreads), smem, s, a);
 }
 
 template <typename T>
@@ -572,15 +573,9 @@ cudaError_t launch_bwd_typed(const ScanArgs &a, T *dB, T *dC, float *dA, float *
         }
     }
     if (e != cudaSuccess) return e;
-    if (tokens > 0) {
-        scan_bwd_bc_kernel<T><<<(unsigned)((tokens * 2 * NP + 255) / 256), 256, 0, s>>>(a.part_bc, a.chan_blocks, tokens,
-                                                                                       a.N, NP, dB, dC);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    scan_bwd_param_kernel<<<(unsigned)(((long long)a.D * (NP + 2) + 31) / 32), 256, 0, s>>>(
-        a.part_a, a.part_v, tokens > 0 ? a.B * a.segs : 0, a.D, a.N, NP, dA, dskip, dbias);
-    return cudaGetLastError();
+    const int bc_blocks = (int)((tokens * 2 * NP + 255) / 256);
+    return launch_dependent(scan_bwd_sum_kernel<T>, dim3((unsigned)(bc_blocks + ((long long)a.D * (NP + 2) + 31) / 32)), dim3(256), 0, s,
+                            a, bc_blocks, a.chan_blocks, tokens > 0 ? a.B * a.segs : 0, NP, dB, dC, dA, dskip, dbias);
 }
 
 }  // namespace
