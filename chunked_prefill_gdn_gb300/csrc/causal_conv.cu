@@ -166,6 +166,7 @@ __device__ __forceinline__ void move_window(F2 (&win)[W - 1][P], const F2 (&x)[P
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_fwd_kernel(ConvArgs a) {
     constexpr int P = (VEC + 1) / 2;
+    grid_dependency_wait();
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_bwd_kernel(ConvArgs a) {
     __shared__ __align__(16) unsigned char shared[kConvWarps * (sizeof(Rows) > sizeof(Sums) ? sizeof(Rows) : sizeof(Sums))];
     Piece *ring = reinterpret_cast<Rows *>(shared)[threadIdx.x >> 5][0][0];
     Sums *sum = reinterpret_cast<Sums *>(shared);
+    grid_dependency_wait();
     if (a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = ((blockIdx.x % a.chan_blocks) * 32 + lane) * VEC;
@@ -469,6 +471,7 @@ template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
     const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
     const int n = blockIdx.y;
+    grid_dependency_wait();
     if (c >= a.D) return;
     T *y = static_cast<T *>(a.out) + (long long)n * a.D + c;
     const int slot = a.slots ? __ldg(a.slots + n) : n;
@@ -503,13 +506,13 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
 enum class Conv { kFwd, kBwd, kStep };
 
 template <Conv OP, typename T, int W, int VEC>
-void launch_conv_one(const ConvArgs &a, cudaStream_t s) {
+cudaError_t launch_conv_one(const ConvArgs &a, cudaStream_t s) {
     if constexpr (OP == Conv::kStep) {
-        conv_step_kernel<T, W, VEC><<<dim3((a.D + 128 * VEC - 1) / (128 * VEC), a.B), 128, 0, s>>>(a);
+        return launch_dependent(conv_step_kernel<T, W, VEC>, dim3((a.D + 128 * VEC - 1) / (128 * VEC), a.B), dim3(128), 0, s, a);
     } else {
-        const unsigned grid = (unsigned)((long long)a.groups * a.chan_blocks);
-        if constexpr (OP == Conv::kFwd) conv_fwd_kernel<T, W, VEC><<<grid, 32 * kConvWarps, 0, s>>>(a);
-        else conv_bwd_kernel<T, W, VEC><<<grid, 32 * kConvWarps, 0, s>>>(a);
+        const dim3 grid((unsigned)((long long)a.groups * a.chan_blocks)), block(32 * kConvWarps);
+        if constexpr (OP == Conv::kFwd) return launch_dependent(conv_fwd_kernel<T, W, VEC>, grid, block, 0, s, a);
+        else return launch_dependent(conv_bwd_kernel<T, W, VEC>, grid, block, 0, s, a);
     }
 }
 
@@ -518,11 +521,8 @@ cudaError_t launch_conv(ConvArgs a, int W, bool vec, cudaStream_t s) {
     const int per_block = 32 * (vec ? 4 : 1);
     a.chan_blocks = (a.D + per_block - 1) / per_block;
 #define GDN_CONV(WW) (vec ? launch_conv_one<OP, T, WW, 4>(a, s) : launch_conv_one<OP, T, WW, 1>(a, s))
-    if (W == 2) GDN_CONV(2);
-    else if (W == 3) GDN_CONV(3);
-    else GDN_CONV(4);
+    return W == 2 ? GDN_CONV(2) : W == 3 ? GDN_CONV(3) : GDN_CONV(4);
 #undef GDN_CONV
-    return cudaGetLastError();
 }
 
 // Tokens per warp: the run that gives the shortest schedule when an SM holds

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_step_kernel(DeltaArgs a) 
     constexpr int RPW = 32 / CG;                       // rows of one warp's sweep
     __shared__ float qs[DK], ks[DK], dots[3];
     __shared__ float4 sum[2][WARPS][CG];
+    grid_dependency_wait();
     const int parts = a.dv / COLS;
     const long long unit = blockIdx.x / parts;         // n * H + h
     const int col0 = (int)(blockIdx.x % parts) * COLS;
@@ -143,21 +144,18 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_step_kernel(DeltaArgs a) 
 }
 
 template <typename T, int DK>
-void launch_delta_dk(const DeltaArgs &a, int cols, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.units * (a.dv / cols));
-    if (cols == 32) delta_step_kernel<T, DK, 32><<<grid, kDeltaThreads, 0, s>>>(a);
-    else if (cols == 64) delta_step_kernel<T, DK, 64><<<grid, kDeltaThreads, 0, s>>>(a);
-    else delta_step_kernel<T, DK, 128><<<grid, kDeltaThreads, 0, s>>>(a);
+cudaError_t launch_delta_dk(const DeltaArgs &a, int cols, cudaStream_t s) {
+    void (*kernel)(DeltaArgs) = cols == 32 ? delta_step_kernel<T, DK, 32>
+                              : cols == 64 ? delta_step_kernel<T, DK, 64> : delta_step_kernel<T, DK, 128>;
+    return launch_dependent(kernel, dim3((unsigned)(a.units * (a.dv / cols))), dim3(kDeltaThreads), 0, s, a);
 }
 
 template <typename T>
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s) {
     int cols = a.dv;
     while (cols > 32 && a.units * (a.dv / cols) < 2ll * device_sm_count()) cols >>= 1;
-    if (a.dk == 32) launch_delta_dk<T, 32>(a, cols, s);
-    else if (a.dk == 64) launch_delta_dk<T, 64>(a, cols, s);
-    else launch_delta_dk<T, 128>(a, cols, s);
-    return cudaGetLastError();
+    return a.dk == 32 ? launch_delta_dk<T, 32>(a, cols, s)
+         : a.dk == 64 ? launch_delta_dk<T, 64>(a, cols, s) : launch_delta_dk<T, 128>(a, cols, s);
 }
 
 }  // namespace

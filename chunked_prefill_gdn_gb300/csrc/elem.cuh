@@ -1,6 +1,11 @@
 // Element access shared by the layer operators (norm, convolution, scan, step):
 // bf16 or fp32 in memory, fp32 in registers, eight or four neighbouring
 // elements at a time where the address allows 16-byte accesses.
+//
+// Every kernel of these operators is launched with programmatic stream
+// serialisation (launch_dependent) and starts with grid_dependency_wait(): its
+// launch overlaps the end of whatever kernel is before it on the stream, and it
+// reads nothing before that kernel is done (2 to 3 us per kernel boundary).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, fal
     extern __shared__ uint4 stages[];              // [S][NV][thread]
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
+    grid_dependency_wait();
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.out);
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, tru
     extern __shared__ uint4 stages[];              // [S][x, dy][NV][thread]
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
+    grid_dependency_wait();
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.out);
@@ -322,6 +324,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) layer_norm_wide_fwd_kernel(NormArgs a) {
     __shared__ float red[2][1][32];
     const float inv_d = 1.f / (float)a.D;
+    grid_dependency_wait();
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
         T *y = static_cast<T *>(a.out) + row * a.D;
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_bwd_kernel(NormArgs a) {
     const float inv_d = 1.f / (float)a.D;
     float *pw = a.partial ? a.partial + 2ll * blockIdx.x * a.D : nullptr;
     int phase = 0;
+    grid_dependency_wait();
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, phase ^= 1) {
         const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
         const T *dy = static_cast<const T *>(a.dy) + row * a.dy_stride;
@@ -378,31 +382,28 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_bwd_kernel(NormArgs a) {
     }
 }
 
-// dw, db from the blocks' partial rows, in the blocks' order: 32 row groups of
-// 32 columns per block, then the groups in order.
+// dw (blockIdx.y = 0) and db from the blocks' partial rows, in the blocks' order:
+// 32 row groups of 32 columns per block, then the groups in order.
 __global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const float *partial, int rows, int D, float *dw,
                                                                  float *db) {
-    __shared__ float sum[2][32][32];
+    __shared__ float sum[32][32];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float s0 = 0.f, s1 = 0.f;
+    float s = 0.f;
     grid_dependency_wait();
     if (c < D) {
-#pragma unroll 4
-        for (int r = grp; r < rows; r += 32) {
-            s0 += partial[2ll * r * D + c];
-            s1 += partial[(2ll * r + 1) * D + c];
-        }
+        const float *p = partial + (long long)blockIdx.y * D + c;
+#pragma unroll 8
+        for (int r = grp; r < rows; r += 32) s += p[2ll * r * D];
     }
-    sum[0][grp][lane] = s0;
-    sum[1][grp][lane] = s1;
+    sum[grp][lane] = s;
     __syncthreads();
-    if (grp < 2 && c < D) {
-        float s = 0.f;
+    float *out = blockIdx.y ? db : dw;
+    if (grp == 0 && c < D && out) {
+        s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += sum[grp][i][lane];
-        float *out = grp ? db : dw;
-        if (out) out[c] = s;
+        for (int i = 0; i < 32; ++i) s += sum[i][lane];
+        out[c] = s;
     }
 }
 
@@ -428,8 +429,7 @@ cudaError_t launch_norm_one(const NormArgs &a, int grid, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, norm_threads(TPR), smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), dim3(norm_threads(TPR)), smem, s, a);
 }
 
 template <typename T, int VEC, bool BWD>
@@ -441,10 +441,11 @@ cudaError_t launch_norm(const NormArgs &a, int grid, cudaStream_t s) {
     else if (a.D <= 2048) GDN_NORM(256, 8);
     else if (a.D <= 4096) GDN_NORM(256, 16);
     else if (a.D <= kNormMaxCols) GDN_NORM(512, 16);
-    else if constexpr (BWD) layer_norm_wide_bwd_kernel<T><<<grid, 1024, 0, s>>>(a);
-    else layer_norm_wide_fwd_kernel<T><<<grid, 1024, 0, s>>>(a);
+    void (*wide)(NormArgs);
+    if constexpr (BWD) wide = layer_norm_wide_bwd_kernel<T>;
+    else wide = layer_norm_wide_fwd_kernel<T>;
+    return launch_dependent(wide, dim3(grid), dim3(1024), 0, s, a);
 #undef GDN_NORM
-    return cudaGetLastError();
 }
 
 template <typename T, bool BWD>
@@ -532,7 +533,7 @@ extern "C" gdn_status gdn_layer_norm_bwd(const void *dy, int64_t dy_stride, cons
                               : gdn::launch_norm_typed<float, true>(a, grid, s);
     }
     if (e == cudaSuccess && params) {  // no rows: the sums are zero
-        e = gdn::launch_dependent(gdn::layer_norm_reduce_kernel, dim3((D + 31) / 32), dim3(1024), 0, s,
+        e = gdn::launch_dependent(gdn::layer_norm_reduce_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, s,
                                   static_cast<const float *>(workspace), rows > 0 ? grid : 0, D, dweight, dbias);
     }
     if (e != cudaSuccess) {

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), NW == 1 ? (MODE == kMaps ? 6 : 
     float *ys = bc + 2 * TILE * 2 * NP;                                         // kFull: [2][NW][TILE][ROW], y
     float *gs = ys;                                                             // kMaps: [2][TILE][ROW], dy through the gate
 
-    if (MODE == kFull) grid_dependency_wait();   // (the segments' start states)
+    grid_dependency_wait();
     if (MODE == kFull && a.status && a.cu && blockIdx.x == 0) check_cu(a.cu, a.n_seqs, a.T, a.status);
     const int lane = threadIdx.x & 31;
     int warp = threadIdx.x >> 5;
@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     const int part = threadIdx.x % LANES, ch = (int)((blockIdx.x * 128ll + threadIdx.x) / LANES);
     const int b = blockIdx.y, n0 = part * 4;
     const bool live = ch < a.D;
+    grid_dependency_wait();
     const int slot = a.slots ? __ldg(a.slots + b) : b;
     if (slot < 0 || slot >= a.pool) {   // a padded row
         if (live && part == 0) static_cast<T *>(a.out)[(long long)b * a.D + ch] = from_f32<T>(0.f);
@@ -488,9 +489,7 @@ cudaError_t launch_scan_one(const ScanArgs &a, int segs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((long long)a.chan_blocks * a.B * segs));
-    if (MODE == kFull && a.has_carry) return launch_dependent(scan_kernel<T, NPT, NW, MODE>, grid, dim3(32 * (NW + 1)), S::smem, s, a);
-    scan_kernel<T, NPT, NW, MODE><<<grid, 32 * (NW + 1), S::smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(scan_kernel<T, NPT, NW, MODE>, grid, dim3(32 * (NW + 1)), S::smem, s, a);
 }
 
 template <typename T, int NPT, int NW>
@@ -517,11 +516,9 @@ template <typename T>
 cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
     const int lanes = a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16;
     const dim3 grid((unsigned)(((long long)a.D * lanes + 127) / 128), a.B);
-    if (lanes == 2) scan_step_kernel<T, 2><<<grid, 128, 0, s>>>(a, vec);
-    else if (lanes == 4) scan_step_kernel<T, 4><<<grid, 128, 0, s>>>(a, vec);
-    else if (lanes == 8) scan_step_kernel<T, 8><<<grid, 128, 0, s>>>(a, vec);
-    else scan_step_kernel<T, 16><<<grid, 128, 0, s>>>(a, vec);
-    return cudaGetLastError();
+    void (*kernel)(ScanArgs, int) = lanes == 2 ? scan_step_kernel<T, 2> : lanes == 4 ? scan_step_kernel<T, 4>
+                                  : lanes == 8 ? scan_step_kernel<T, 8> : scan_step_kernel<T, 16>;
+    return launch_dependent(kernel, grid, dim3(128), 0, s, a, vec);
 }
 
 // Segments per row in the forward pass.  One segment takes each exponential
