@@ -23,9 +23,9 @@
 // warps and leave as one partial row per block that a second kernel adds in
 // order.  All arithmetic is on pairs of channels (two-wide FP32).
 //
-// Measured (bf16, W = 4, SiLU): 65536 packed tokens x 6144 channels 266 us, 6.1
-// TB/s, 91% of the measured copy rate; backward 4 x 4095 x 4096 93 us, 4.4 TB/s
-// (65%): there the 116 registers of a thread leave 16 warps per SM, which issue 2.3
+// Measured (bf16, W = 4, SiLU): 65536 packed tokens x 6144 channels 264 us, 6.1
+// TB/s, 92% of the measured copy rate; backward 4 x 4095 x 4096 87 us, 4.6 TB/s
+// (69%): there the 116 registers of a thread leave 16 warps per SM, which issue 2.3
 // instructions per clock, 28 per element; one token of 64 sequences x 12288
 // channels 3.3 us, 3.8 TB/s.
 #include <algorithm>

@@ -19,12 +19,12 @@
 // asynchronous copies (up to four in flight, each thread reading back what it
 // copied) while the current one is reduced.  The arithmetic is on pairs of
 // columns (two-wide FP32): unpaired, the backward pass was held up by its own
-// instructions between the barriers (163 us where it now takes 142).  Rows wider
+// instructions between the barriers (163 us where the pairs took 142).  Rows wider
 // than 8192 are read three times instead (layer_norm_wide_*).
 //
-// Measured (bf16, fp32 weights, 32768 x 4096): forward 97 us, 5.5 TB/s, 83% of
-// the measured copy rate; backward 142 us, 5.7 TB/s (85%), of it 7 us the sum
-// over the blocks; 16 rows of 4096 2.5 us.
+// Measured (bf16, fp32 weights, 32768 x 4096): forward 95 us, 5.7 TB/s, 85% of
+// the measured copy rate; backward 139 us, 5.8 TB/s (87%), of it 6 us the sum
+// over the blocks; 16 rows of 4096 2.3 us.
 #include <algorithm>
 
 #include "elem.cuh"

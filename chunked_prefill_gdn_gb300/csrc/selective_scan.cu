@@ -18,10 +18,10 @@
 // all channels of a block at once, and what is per (token, channel) only
 // (softplus, the gate) is computed once, by a warp of its own.
 //
-// Measured (bf16, 16 n): 8 x 1024 tokens x 4096 channels 174 us (12 per clock and
+// Measured (bf16, 16 n): 8 x 1024 tokens x 4096 channels 171 us (11 per clock and
 // SM): 6.7 scanning warps per SM are what 32768 channels give, and without the
 // feeding warps' work they alone take 136 us.  A row of 32768 tokens x 1024
-// channels 294 us, of it 118 the maps and 7 their combination.  Tried and dropped:
+// channels 287 us, of it 118 the maps and 7 their combination.  Tried and dropped:
 // eight n per thread and twice the warps (lanes or warps sharing a channel: 213
 // and 199 us where 16 n took 197), two channels x eight n per thread, which halves
 // the reads of B and C (201 / 298 us: the same rate per SM, but blocks of 64

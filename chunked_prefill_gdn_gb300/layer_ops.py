@@ -262,7 +262,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats
         y = out if out is not None else on.empty(x.shape, dtype)
         mean = rstd = None
         if stats:
-            mean, rstd = on.empty(lead, _F32), on.empty(lead, _F32)
+            mean, rstd = on.empty((2, *lead), _F32).unbind(0)
         rows = y.numel() // D if D else 0
         st = _lib().gdn_layer_norm_fwd(x.data_ptr(), stride, _p(weight), _p(bias), wcode, eps, rows, D, _CODE[dtype],
                                        y.data_ptr(), _p(mean), _p(rstd), on.raw)
@@ -297,7 +297,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, workspace=None, stream: Optio
             _raise(st, "gdn_layer_norm_bwd")
     finally:
         on.done()
-    return dx, dw[0], dw[1]
+    return (dx, *dw.unbind(0))
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -558,7 +558,8 @@ def selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
         _read_status(word, on, "gdn_selective_scan_bwd")
     finally:
         on.done()
-    return dx, ddt, dA, dB, dC, dv[0], dz, dv[1], ds
+    dD, db = dv.unbind(0)
+    return dx, ddt, dA, dB, dC, dD, dz, db, ds
 
 
 def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
