@@ -529,12 +529,12 @@ cudaError_t launch_conv(ConvArgs a, int W, bool vec, cudaStream_t s) {
 // `resident` blocks, counting for each run its tokens and about 24 more (halo,
 // weights, filling and draining the ring of rows).  At 4 x 4095 tokens x 4096
 // channels the backward pass runs 1.7 waves of blocks with runs of 128 and 2.95
-// with runs of 74.
+// with runs of 76.
 int conv_run(int B, int T, int D, int vec, int resident) {
     const long long chan = (D + 32 * vec - 1) / (32 * vec), slots = (long long)resident * device_sm_count();
     long long best = -1;
     int run = kSub;
-    for (int r = kSub; r <= kConvRun; r += 2) {
+    for (int r = kSub; r <= kConvRun; r += 4) {
         const long long blocks = B * chan * ((T + r * kConvWarps - 1) / (r * kConvWarps));
         const long long cost = (blocks + slots - 1) / slots * (r + 24);
         if (best < 0 || cost < best) best = cost, run = r;

@@ -546,12 +546,15 @@ namespace {
 // shortest schedule on six blocks per SM, with a tile's time for a block's own
 // start and end; that schedule's length in tiles.
 int maps_per_block(int B, int row_segs, int tiles, int chan_blocks, long long *cost) {
-    const long long slots = 6ll * device_sm_count();
+    const long long slots = 6ll * device_sm_count(), unit = (long long)B * chan_blocks;
     int per = 1;
-    for (int m = 1; m <= row_segs && m <= 64; ++m) {
-        const long long blocks = (long long)B * ((row_segs + m - 1) / m) * chan_blocks;
-        const long long c = (blocks + slots - 1) / slots * (m * tiles + 1);
-        if (m == 1 || c < *cost) *cost = c, per = m;
+    *cost = (unit * row_segs + slots - 1) / slots * (tiles + 1);
+    for (int waves = 1; waves <= 4; ++waves) {   // the fewest segments per block that fit so many waves
+        const long long per_row = waves * slots / unit;
+        if (per_row < 1 || row_segs < 1) continue;
+        const int m = (int)((row_segs + per_row - 1) / per_row);
+        const long long c = waves * ((long long)m * tiles + 1);
+        if (c < *cost) *cost = c, per = m;
     }
     return per;
 }
