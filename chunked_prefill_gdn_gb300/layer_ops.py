@@ -19,6 +19,11 @@ Activations are bfloat16 or float32; they may be strided views as long as the
 last axis is contiguous (a slice of a wider projection), everything else is
 contiguous.  Gradients of activations come in the activations' type, gradients
 of parameters in float32.
+
+The functions run on the current stream, or on `stream`.  A given stream is not
+made to wait for the one its inputs were written on, and inputs stay alive until
+it has read them: that order is the caller's, as for any tensor used on another
+stream than its own.
 """
 from __future__ import annotations
 
@@ -154,23 +159,33 @@ def _head_stride(name, t):
 
 
 class _On:
-    """The device and stream of a call, and what it allocates there: tensors
-    made for another stream than the current one are recorded on it, so that
-    their memory is not handed out again while the call still runs."""
-    __slots__ = ("device", "stream", "raw", "guard")
+    """The device and stream of a call, and what it allocates there.  With a
+    stream of the caller's the memory comes from that stream's pool: a block of
+    the current stream's pool may still be in use by work queued there, which
+    the given stream does not wait for.  Tensors that go back to the caller are
+    also recorded on the current stream, where they are likely to be read."""
+    __slots__ = ("device", "raw", "stream", "guard", "reader")
 
     def __init__(self, device, stream):
         self.device, self.stream = device, stream
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
+        self.guard = self.reader = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("stream is on %s, expected %s" % (stream.device, device))
+            self.reader = torch.cuda.current_stream(device)
+            self.guard = torch.cuda.stream(stream)
             self.guard.__enter__()
-        self.raw = _current_raw_stream(device.index) if stream is None else stream.cuda_stream
+            self.raw = stream.cuda_stream
+        else:
+            if device.index != torch.cuda.current_device():
+                self.guard = torch.cuda.device(device)
+                self.guard.__enter__()
+            self.raw = _current_raw_stream(device.index)
 
     def empty(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.stream is not None:
-            t.record_stream(self.stream)
+        if self.reader is not None:
+            t.record_stream(self.reader)
         return t
 
     def done(self):
@@ -219,7 +234,7 @@ def _status_word(on, check, cu_seqlens):
 def _read_status(word, on, where):
     if word is None:
         return
-    torch.cuda.current_stream(on.device).synchronize() if on.stream is None else on.stream.synchronize()
+    torch.cuda.current_stream(on.device).synchronize()   # the call's own, current until done()
     st = int(word.item())
     if st != 0:
         _raise(st, where + " (device check)")

@@ -592,6 +592,33 @@ def test_operators_follow_the_stream_they_are_given():
     assert all(torch.equal(a, d) for a, d in zip(got_b, want_b))
 
 
+def test_outputs_on_a_given_stream_are_not_blocks_of_the_current_one():
+    """A block freed on the current stream may still be written by work queued
+    there; what a call on another stream allocates is not such a block, its
+    workspace included."""
+    side = torch.cuda.Stream()
+    x, w, b, dy = norm_case(4000, 1024, "bf16", "f32", lambda t: t)
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b)
+    want = gdn.layer_norm_bwd(dy, x, mean, rstd, w)
+    torch.cuda.synchronize()
+    blocks = [torch.empty_like(x) for _ in range(4)]
+    freed = {t.data_ptr() for t in blocks}
+    for t in blocks:
+        t.fill_(7.0)
+    side.wait_stream(torch.cuda.current_stream())
+    del blocks, t
+    out = gdn.layer_norm_fwd(x, w, b, stream=side)
+    got = gdn.layer_norm_bwd(dy, x, mean, rstd, w, stream=side)
+    assert out[0].data_ptr() not in freed and got[0].data_ptr() not in freed
+    assert torch.cuda.current_stream() != side
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], y) and all(torch.equal(a, d) for a, d in zip(got, want))
+    ran = torch.cuda.current_stream()
+    with pytest.raises(gdn.GdnError):
+        gdn.layer_norm_fwd(torch.zeros(2, 0, device="cuda"), stream=side)
+    assert torch.cuda.current_stream() == ran
+
+
 def test_steps_run_in_a_graph():
     c = scan_case(2, 1, 64, 16, None, "bf16")
     x, w, b = normal(rng(1), 2, 64, to="bf16"), normal(rng(2), 64, 4, to="bf16"), normal(rng(3), 64, to="bf16")
