@@ -528,7 +528,7 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 int scan_segments(int B, int T, int D, int N) {
     const int tiles = (T + kTile - 1) / kTile;
     const long long blocks = (long long)B * ((D + 31) / 32), room = (long long)scan_resident(N) * device_sm_count();
-    if (tiles <= 1 || 2 * blocks > room) return 1;
+    if (tiles <= 1 || blocks == 0 || 2 * blocks > room) return 1;
     const int segs = (int)std::min<long long>(room / blocks, tiles);
     const int len = (tiles + segs - 1) / segs;
     return (tiles + len - 1) / len;
@@ -548,6 +548,8 @@ namespace {
 int maps_per_block(int B, int row_segs, int tiles, int chan_blocks, long long *cost) {
     const long long slots = 6ll * device_sm_count(), unit = (long long)B * chan_blocks;
     int per = 1;
+    *cost = 0;
+    if (unit == 0) return per;   // no batch rows
     *cost = (unit * row_segs + slots - 1) / slots * (tiles + 1);
     for (int waves = 1; waves <= 4; ++waves) {   // the fewest segments per block that fit so many waves
         const long long per_row = waves * slots / unit;

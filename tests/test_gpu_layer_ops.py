@@ -401,6 +401,19 @@ def test_no_sequences_give_zero_parameter_gradients():
     assert gdn.gated_delta_step(q, q, q, q[..., 0], q[..., 0], torch.empty(0, 2, 32, 32, device="cuda")).shape == (0, 2, 32)
 
 
+@pytest.mark.parametrize("T", [17, 40, 600])
+def test_no_sequences_of_many_tokens(T):
+    """No batch rows of more than one tile: empty outputs, zero gradients of the
+    parameters."""
+    c = scan_case(1, 3, 40, 16, None, "f32")
+    e, bc = torch.empty(0, T, 40, device="cuda"), torch.empty(0, T, 16, device="cuda")
+    y, last = gdn.selective_scan_fwd(e, e, c["A"], bc, bc, D=c["D"], dt_bias=c["bias"])
+    assert y.shape == (0, T, 40) and last.shape == (0, 40, 16)
+    got = gdn.selective_scan_bwd(e, e, e, c["A"], bc, bc, D=c["D"], dt_bias=c["bias"])
+    assert got[0].shape == (0, T, 40) and got[3].shape == (0, T, 16) and got[8].shape == (0, 40, 16)
+    assert not got[2].any() and not got[5].any() and not got[7].any()
+
+
 @pytest.mark.parametrize("N", [16, 24])
 def test_selective_scan_channels_stand_alone(N):
     """A NaN in one channel's input, or an infinite one, leaves the others' outputs,

@@ -2,6 +2,9 @@
 return a status before any launch, the Python functions raise for tensors that
 are not on a CUDA device."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -92,6 +95,23 @@ def test_selective_scan_arguments(lib):
     s = lib.gdn_selective_scan_step
     assert s(scan_desc(T=2), P, None, 1, P, None) == INVALID
     assert s(scan_desc(T=1), P, None, 0, P, None) == INVALID
+
+
+@pytest.mark.parametrize("T", [0, 5, 16, 17, 64, 4096])
+def test_scan_plans_an_empty_batch(lib, T):
+    """No batch rows, however long: the size queries answer (in a process of
+    their own, which an integer division by zero would end)."""
+    code = ("import chunked_prefill_gdn_gb300 as gdn\n"
+            "lib = gdn.load_library()\n"
+            "for D, N in ((1, 1), (64, 16), (1024, 24), (40, 64)):\n"
+            "    print(lib.gdn_selective_scan_fwd_workspace_size(0, %d, D, N),\n"
+            "          lib.gdn_selective_scan_bwd_workspace_size(0, %d, D, N))\n" % (T, T))
+    run = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-500:]
+    sizes = [int(v) for v in run.stdout.split()]
+    assert len(sizes) == 8 and all(v >= 16 for v in sizes) and all(v == 16 for v in sizes[::2])
+    assert lib.gdn_selective_scan_fwd(scan_desc(B=0, T=T), P, None, None, None, 0, None) == 0
 
 
 def test_delta_step_arguments(lib):
