@@ -317,8 +317,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, workspace=None, stream: Optio
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, eps):
-        y, mean, rstd = layer_norm_fwd(x, weight, bias, eps)
+    def forward(ctx, x, weight, bias, eps, stats):
+        y, mean, rstd = layer_norm_fwd(x, weight, bias, eps, stats=stats)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.bias_type = bias.dtype if bias is not None else None
         return y
@@ -329,14 +329,15 @@ class _LayerNorm(torch.autograd.Function):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layer_norm_bwd(dy.contiguous(), x, mean, rstd, weight)
         return (dx, dw.to(weight.dtype) if weight is not None else None,
-                db.to(ctx.bias_type) if ctx.bias_type is not None else None, None)
+                db.to(ctx.bias_type) if ctx.bias_type is not None else None, None, None)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
-    """Layer norm over the last axis with autograd (x, weight, bias)."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))):
-        return layer_norm_fwd(x, weight, bias, eps, stats=False)[0]
-    return _LayerNorm.apply(x, weight, bias, eps)
+    """Layer norm over the last axis with autograd (x, weight, bias).  Forward-mode
+    derivatives are refused, as by the other operators."""
+    # no shortcut past the autograd function: a tangent leaves requires_grad False
+    stats = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
+    return _LayerNorm.apply(x, weight, bias, eps, stats)
 
 
 # ---------------------------------------------------- short causal convolution

@@ -137,3 +137,43 @@ def test_python_functions_refuse_host_tensors(lib):
         gdn.selective_scan_fwd(x, x, w, x, x)
     with pytest.raises(ValueError):
         gdn.gated_delta_step(x, x, x, x, x, torch.zeros(1, 4, 8, 8))
+
+
+def test_layer_norm_refuses_forward_mode(monkeypatch):
+    """A tangent of any input reaches the autograd function, which has no forward
+    mode and raises; it is never dropped.  (The kernel is replaced by torch's
+    arithmetic: no GPU.)"""
+    from torch.autograd import forward_ad
+
+    calls = []
+
+    def kernel(x, weight=None, bias=None, eps=1e-5, out=None, stats=True, stream=None):
+        calls.append(stats)
+        mean = x.mean(-1)
+        rstd = (x.var(-1, unbiased=False) + eps).rsqrt()
+        y = (x - mean[..., None]) * rstd[..., None]
+        y = y * (1.0 if weight is None else weight) + (0.0 if bias is None else bias)
+        return y, *((mean, rstd) if stats else (None, None))
+
+    monkeypatch.setattr(gdn.layer_ops, "layer_norm_fwd", kernel)
+    x, w, b = torch.randn(3, 8), torch.randn(8), torch.randn(8)
+    for args in ((x,), (x, w, b)):
+        with pytest.raises(RuntimeError):
+            torch.func.jvp(gdn.layer_norm, args, tuple(torch.ones_like(t) for t in args))
+    for grads in (True, False):
+        for i in range(3):
+            with forward_ad.dual_level(), torch.set_grad_enabled(grads):
+                args = [x, w, b]
+                args[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+                with pytest.raises(RuntimeError):
+                    gdn.layer_norm(*args)
+    # without tangents: the values, and statistics only where a backward pass will ask for them
+    del calls[:]
+    want = kernel(x, w, b)[0]
+    assert torch.equal(gdn.layer_norm(x, w, b), want) and calls[-1] is False
+    leaf = w.clone().requires_grad_()
+    y = gdn.layer_norm(x, leaf, b)
+    assert y.requires_grad and calls[-1] is True
+    with torch.no_grad():
+        y = gdn.layer_norm(x, leaf, b)
+        assert not y.requires_grad and calls[-1] is False
