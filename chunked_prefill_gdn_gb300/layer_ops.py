@@ -24,6 +24,11 @@ The functions run on the current stream, or on `stream`.  A given stream is not
 made to wait for the one its inputs were written on, and inputs stay alive until
 it has read them: that order is the caller's, as for any tensor used on another
 stream than its own.
+
+What a call writes into a tensor of the caller's (a state, `out`) counts as an
+in-place operation: autograd refuses to use that tensor's earlier value in a
+backward pass.  The functions with out=, the steps and the *_fwd and *_bwd forms
+record nothing for autograd themselves.
 """
 from __future__ import annotations
 
@@ -31,6 +36,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd.graph import increment_version as _increment_version
 
 __all__ = ["layer_norm_fwd", "layer_norm_bwd", "layer_norm", "causal_conv_fwd", "causal_conv_bwd", "causal_conv_step",
            "causal_conv", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step", "selective_scan",
@@ -204,6 +210,12 @@ def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+def _wrote(*tensors):
+    """Tells autograd that a kernel wrote into tensors of the caller's (None: not
+    given), as an in-place operation of torch's own does."""
+    _increment_version([t for t in tensors if t is not None])
+
+
 def _workspace(on, workspace, size):
     if size == 0:
         _raise(1, "workspace size")
@@ -283,6 +295,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats
                                        y.data_ptr(), _p(mean), _p(rstd), on.raw)
         if st != 0:
             _raise(st, "gdn_layer_norm_fwd")
+        _wrote(out)
     finally:
         on.done()
     return y, mean, rstd
@@ -384,6 +397,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, a
                                         _p(word), on.raw)
         if rc != 0:
             _raise(rc, "gdn_causal_conv_fwd")
+        _wrote(out)
         _read_status(word, on, "gdn_causal_conv_fwd")
     finally:
         on.done()
@@ -446,6 +460,7 @@ def causal_conv_step(x, state, weight, bias=None, activation: Optional[str] = "s
                                          y.data_ptr(), on.raw)
         if rc != 0:
             _raise(rc, "gdn_causal_conv_step")
+        _wrote(state, out)
     finally:
         on.done()
     return y
@@ -535,6 +550,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
                                         ws.numel() if ws is not None else 0, on.raw)
         if rc != 0:
             _raise(rc, "gdn_selective_scan_fwd")
+        _wrote(out)
         _read_status(word, on, "gdn_selective_scan_fwd")
     finally:
         on.done()
@@ -598,6 +614,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
                                             on.raw)
         if rc != 0:
             _raise(rc, "gdn_selective_scan_step")
+        _wrote(state, out)
     finally:
         on.done()
     return y
@@ -663,6 +680,7 @@ def gated_delta_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_kerne
                                    N, H, dk, dv, _CODE[dtype], o.data_ptr(), on.raw)
         if rc != 0:
             _raise(rc, "gdn_delta_step")
+        _wrote(state, out)
     finally:
         on.done()
     return o

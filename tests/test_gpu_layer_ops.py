@@ -495,6 +495,58 @@ def test_selective_scan_steps_continue_a_prompt(dtype, D, N):
     assert pool[[1, 3]].isnan().all()
 
 
+# ------------------------------------------------------- writes that autograd sees
+
+def test_written_tensors_count_as_modified():
+    """Every state and every out= moves its version counter; nothing else does."""
+    g = rng(31)
+    x, w = normal(g, 2, 32), normal(g, 32, 4)
+    x3, A, bc = normal(g, 1, 6, 32), -normal(g, 32, 8).abs(), normal(g, 1, 6, 8)
+    q, gate, beta = normal(g, 2, 1, 32), -normal(g, 2, 1).abs(), torch.sigmoid(normal(g, 2, 1))
+    conv, ssm, delta = normal(g, 2, 3, 32), normal(g, 2, 32, 8), normal(g, 2, 1, 32, 32)
+    b2, c2 = normal(g, 2, 8), normal(g, 2, 8)
+    like = torch.empty_like
+    calls = [
+        ((), lambda out: gdn.layer_norm_fwd(x, out=out), like(x)),
+        ((), lambda out: gdn.causal_conv_fwd(x3, w, out=out), like(x3)),
+        ((), lambda out: gdn.selective_scan_fwd(x3, x3, A, bc, bc, out=out), like(x3)),
+        ((conv,), lambda out: gdn.causal_conv_step(x, conv, w, out=out), like(x)),
+        ((ssm,), lambda out: gdn.selective_scan_step(x, x, A, b2, c2, ssm, out=out), like(x)),
+        ((delta,), lambda out: gdn.gated_delta_step(q, q, q, gate, beta, delta, out=out), like(q)),
+    ]
+    inputs = (x, w, x3, A, bc, q, gate, beta, b2, c2)
+    versions = [t._version for t in inputs]
+    for states, call, out in calls:
+        before = [t._version for t in (*states, out)]
+        call(out)
+        assert all(t._version > v for t, v in zip((*states, out), before))
+        before = [t._version for t in states]
+        call(None)
+        assert all(t._version > v for t, v in zip(states, before))
+    assert [t._version for t in inputs] == versions
+
+
+def test_a_state_moved_on_is_not_used_in_a_backward_pass():
+    """A step on a state that a recorded call has read: torch's error, not the
+    gradient at the overwritten value."""
+    g = rng(32)
+    x, w, s = normal(g, 1, 6, 32), normal(g, 32, 4).requires_grad_(), normal(g, 1, 3, 32)
+    y, _ = gdn.causal_conv(x, w, initial_state=s)
+    gdn.causal_conv_step(x[:, 0], s, w.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    A, bc, h = (-normal(g, 32, 8).abs()).requires_grad_(), normal(g, 1, 6, 8), normal(g, 1, 32, 8)
+    y, _ = gdn.selective_scan(x, x, A, bc, bc, initial_state=h)
+    gdn.selective_scan_step(x[:, 0], x[:, 0], A.detach(), bc[:, 0], bc[:, 0], h)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    wn, v = normal(g, 32).requires_grad_(), normal(g, 4, 32)
+    y = gdn.layer_norm(v, wn)
+    gdn.layer_norm_fwd(normal(g, 4, 32), out=v)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
 # -------------------------------------------------- one token of the delta rule
 
 @pytest.mark.parametrize("N,H,dk,dv,dtype,norm", [
