@@ -20,6 +20,10 @@ last axis is contiguous (a slice of a wider projection), everything else is
 contiguous.  Gradients of activations come in the activations' type, gradients
 of parameters in float32.
 
+`out` must not overlap an input (refused): only layer_norm_fwd, selective_scan_fwd
+and the steps of the convolution and the scan may be given x (the scan also dt or
+z) itself.
+
 The functions run on the current stream, or on `stream`.  A given stream is not
 made to wait for the one its inputs were written on, and inputs stay alive until
 it has read them: that order is the caller's, as for any tensor used on another
@@ -210,6 +214,30 @@ def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+def _extent(t):
+    """The first byte of a tensor and the one past its last."""
+    first = t.data_ptr()
+    if t.numel() == 0:
+        return first, first
+    return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _apart(out, inputs, same=()):
+    """Refuses an `out` in the memory of an input, which other threads may still
+    have to read when it is written.  Inputs of `same` may be out itself: there
+    every element is read only by what writes it."""
+    if out is None:
+        return
+    first, last = _extent(out)
+    for name, t in inputs:
+        if t is None:
+            continue
+        a, b = _extent(t)
+        if max(a, first) < min(b, last) and not (
+                name in same and a == first and t.shape == out.shape and t.is_contiguous()):
+            raise ValueError("out overlaps %s" % name)
+
+
 def _wrote(*tensors):
     """Tells autograd that a kernel wrote into tensors of the caller's (None: not
     given), as an in-place operation of torch's own does."""
@@ -284,6 +312,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats
     stride = _row_stride("x", x)
     if out is not None:
         _like("out", out, x.shape, dtype, dev)
+        _apart(out, (("x", x), ("weight", weight), ("bias", bias)), same=("x",))
     on = _On(dev, stream)
     try:
         y = out if out is not None else on.empty(x.shape, dtype)
@@ -387,6 +416,8 @@ def causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, a
     dev, dtype, silu = x.device, x.dtype, _silu(activation)
     if out is not None:
         _like("out", out, x.shape, dtype, dev)
+        _apart(out, (("x", x), ("weight", weight), ("bias", bias), ("initial_state", initial_state),
+                     ("cu_seqlens", cu_seqlens)))
     on = _On(dev, stream)
     try:
         y = out if out is not None else on.empty(x.shape, dtype)
@@ -451,6 +482,8 @@ def causal_conv_step(x, state, weight, bias=None, activation: Optional[str] = "s
     _slots(state, state_indices, N, dev)
     if out is not None:
         _like("out", out, (N, D), dtype, dev)
+        _apart(out, (("x", x), ("state", state), ("weight", weight), ("bias", bias), ("state_indices", state_indices)),
+               same=("x",))
     silu, stride = _silu(activation), _row_stride("x", x)
     on = _On(dev, stream)
     try:
@@ -538,6 +571,8 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     desc, n = _scan_desc(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     if out is not None:
         _like("out", out, x.shape, x.dtype, x.device)
+        _apart(out, (("x", x), ("dt", dt), ("z", z), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
+                     ("initial_state", initial_state), ("cu_seqlens", cu_seqlens)), same=("x", "dt", "z"))
     lib = _lib()
     on = _On(x.device, stream)
     try:
@@ -607,6 +642,8 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     _slots(state, state_indices, desc.B, x.device)
     if out is not None:
         _like("out", out, x.shape, x.dtype, x.device)
+        _apart(out, (("x", x), ("dt", dt), ("z", z), ("A", A), ("B", B), ("C", C), ("D", D), ("dt_bias", dt_bias),
+                     ("state", state), ("state_indices", state_indices)), same=("x", "dt", "z"))
     on = _On(x.device, stream)
     try:
         y = out if out is not None else on.empty(x.shape, x.dtype)
@@ -671,6 +708,8 @@ def gated_delta_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm_in_kerne
     _slots(state, state_indices, N, dev)
     if out is not None:
         _like("out", out, v.shape, dtype, dev)
+        _apart(out, (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state),
+                     ("state_indices", state_indices)))
     on = _On(dev, stream)
     try:
         o = out if out is not None else on.empty(v.shape, dtype)

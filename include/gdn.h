@@ -554,6 +554,13 @@ gdn_status gdn_chunk_bwd_check(const void *workspace, gdn_stream_t stream);
  * n_states there are; a row whose index is outside [0, n_states) is padding:
  * its output is zero and no state changes.  Without it row r uses state r.
  * Two rows of one call must not name the same state.
+ *
+ * Outputs and states overlap neither inputs nor one another: other threads may
+ * still have to read what one writes (the convolution's neighbouring tokens, the
+ * delta step's v).  The one exception is y at the address of a contiguous x in
+ * gdn_layer_norm_fwd, gdn_causal_conv_step, gdn_selective_scan_fwd and
+ * gdn_selective_scan_step (there also of dt or z): what writes an element is all
+ * that reads it.
  */
 
 /*

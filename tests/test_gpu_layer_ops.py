@@ -495,6 +495,62 @@ def test_selective_scan_steps_continue_a_prompt(dtype, D, N):
     assert pool[[1, 3]].isnan().all()
 
 
+# ------------------------------------------------------------- outputs and inputs
+
+def test_out_in_an_inputs_memory_is_refused():
+    """Where a value is read by others than the thread that writes in its place."""
+    g = rng(41)
+    buf = normal(g, 2, 40, 32)
+    x = buf[:, :32].contiguous()
+    flat = torch.cat([x.flatten(), x.flatten()[:64]])
+    xs, later = flat[:2048].view(2, 32, 32), flat[64:].view(2, 32, 32)      # two rows apart
+    w, s = normal(g, 32, 4), normal(g, 2, 3, 32)
+    A, bc = -normal(g, 32, 32).abs(), normal(g, 2, 32, 32)
+    for call in (lambda: gdn.causal_conv_fwd(x, w, out=x), lambda: gdn.causal_conv_fwd(xs, w, out=later),
+                 lambda: gdn.causal_conv_fwd(normal(g, 1, 3, 32), w, initial_state=s[:1], out=s[:1]),
+                 lambda: gdn.layer_norm_fwd(xs, out=later), lambda: gdn.layer_norm_fwd(x, x[0, 0], out=x),
+                 lambda: gdn.selective_scan_fwd(xs, xs, A, bc, bc, out=later),
+                 lambda: gdn.selective_scan_fwd(x, x, A, bc, bc, out=bc),
+                 lambda: gdn.causal_conv_step(x[:, 0].contiguous(), s, w, out=s.view(-1)[:64].view(2, 32)),
+                 lambda: gdn.causal_conv_step(xs[0, :2], s, w, out=flat[16:80].view(2, 32)),
+                 lambda: gdn.selective_scan_step(xs[0, :2], xs[0, :2], A, bc[0, :2], bc[0, :2], normal(g, 2, 32, 32),
+                                                 out=flat[16:80].view(2, 32))):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    q, gate, S = normal(g, 2, 2, 64), -normal(g, 2, 2).abs(), normal(g, 2, 2, 64, 64)
+    k, v = normal(g, 2, 2, 64), normal(g, 2, 2, 64)
+    before = S.clone()
+    for out in (q, k, v, S.view(-1)[:256].view(2, 2, 64)):
+        with pytest.raises(ValueError, match="overlaps"):
+            gdn.gated_delta_step(q, k, v, gate, gate, S, out=out)
+    assert torch.equal(S, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(1, 40), (70, 33), (200, 512)])
+def test_out_may_be_the_input_where_that_is_allowed(T, D, dtype):
+    c = scan_case(2, T, D, 16, None, dtype)
+    want = gdn.layer_norm_fwd(c["x"], c["D"])[0]
+    x = c["x"].clone()
+    assert torch.equal(gdn.layer_norm_fwd(x, c["D"], out=x)[0], want) and torch.equal(x, want)
+    run = lambda t, out: gdn.selective_scan_fwd(t["x"], t["dt"], c["A"], c["B"], c["C"], **scan_kw(dict(c, z=t["z"])), out=out)   # noqa: E731
+    want, last = run(c, None)
+    for k in ("x", "dt", "z"):
+        t = {n: c[n].clone() for n in ("x", "dt", "z")}
+        got, end = run(t, t[k])
+        assert got is t[k] and torch.equal(got, want) and torch.equal(end, last)
+    one = {n: c[n][:, 0].contiguous() for n in ("x", "dt", "z", "B", "C")}
+    step = lambda t, S, out: gdn.selective_scan_step(t["x"], t["dt"], c["A"], t["B"], t["C"], S, z=t["z"], out=out)   # noqa: E731
+    S0 = c["s"].clone()
+    want = step(one, S0, None)
+    for k in ("x", "dt", "z"):
+        t, S = {n: v.clone() for n, v in one.items()}, c["s"].clone()
+        assert torch.equal(step(t, S, t[k]), want) and torch.equal(S, S0)
+    w, s0, s1 = normal(rng(3), D, 4), normal(rng(4), 2, 3, D, to=dtype), normal(rng(4), 2, 3, D, to=dtype)
+    want, x = gdn.causal_conv_step(one["x"], s0, w), one["x"].clone()
+    assert torch.equal(gdn.causal_conv_step(x, s1, w, out=x), want) and torch.equal(s0, s1)
+
+
 # ------------------------------------------------------- writes that autograd sees
 
 def test_written_tensors_count_as_modified():

@@ -139,6 +139,24 @@ def test_python_functions_refuse_host_tensors(lib):
         gdn.gated_delta_step(x, x, x, x, x, torch.zeros(1, 4, 8, 8))
 
 
+def test_overlapping_memory_is_found():
+    """What counts as `out` in an input's memory: any shared byte of their extents,
+    but for an input that may be out itself."""
+    apart = gdn.layer_ops._apart
+    buf = torch.zeros(100)
+    x, out = buf[:48].view(6, 8), buf[48:96].view(6, 8)
+    apart(None, [("x", x)])
+    apart(out, [("x", x), ("bias", None), ("empty", buf[50:50])])
+    apart(out, [("cu", torch.zeros(3, dtype=torch.int32))])
+    for t in (out, out[5], out.t(), buf[47:49], buf[95:], buf.view(20, 5)[9:], buf[::7], buf[48:96].view(torch.int32)):
+        with pytest.raises(ValueError, match="overlaps x"):
+            apart(out, [("x", t)])
+    apart(out, [("x", out)], same=("x",))
+    for t in (out[:5], buf[49:97].view(6, 8), out.view(8, 6), buf[48:96].view(8, 6).t()):   # not out itself
+        with pytest.raises(ValueError, match="overlaps x"):
+            apart(out, [("x", t)], same=("x",))
+
+
 def test_layer_norm_refuses_forward_mode(monkeypatch):
     """A tangent of any input reaches the autograd function, which has no forward
     mode and raises; it is never dropped.  (The kernel is replaced by torch's
