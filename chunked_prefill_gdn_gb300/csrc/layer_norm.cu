@@ -20,7 +20,9 @@
 // copied) while the current one is reduced.  The arithmetic is on pairs of
 // columns (two-wide FP32): unpaired, the backward pass was held up by its own
 // instructions between the barriers (163 us where the pairs took 142).  Rows wider
-// than 8192 are read three times instead (layer_norm_wide_*).
+// than 8192 are read three times instead (layer_norm_wide_*).  Rows that only their
+// type aligns, or of an odd length, go element by element through the same
+// kernels, 16 elements per thread of which spill up to 200 bytes.
 //
 // Measured (bf16, fp32 weights, 32768 x 4096): forward 95 us, 5.7 TB/s, 85% of
 // the measured copy rate; backward 139 us, 5.8 TB/s (87%), of it 6 us the sum
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, tru
     const float inv_d = 1.f / (float)a.D;
     int phase = 0;
     for (int slot = 0; row < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1, phase ^= 1) {
-        F2 xh[NP], g[NP];   // zero past D, where g = 0 keeps xh out of every sum
+        F2 xh[NP], g[NP];
         const float mean = nmean, rstd = nrstd;
         if (row + step < a.rows) nmean = a.mean[row + step], nrstd = a.rstd[row + step];
         if constexpr (St::async) {
@@ -274,10 +276,25 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_blocks_per_sm(TPR, tru
             unpack_row<T, TPR, VEC, NV>(a.D, t, g, [&](int i) { return ng[i]; });
             load_row(row + step, 0);
         }
+        // Past D g is zero and xh = -mean rstd, which adds nothing unless it overflows:
+        // then 0 times it is no longer 0.  With vectors that is branched on per row:
+        // those columns take the mean itself (139 us at 32768 x 4096 bf16, as without;
+        // the sum taken again on the branch 171).  Element by element the mean is
+        // masked (4095 columns 339 us, 332 without; the branch 424).
+        if constexpr (VEC > 1) {
+            if (!(fabsf(mean * rstd) < INFINITY)) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    xh[p] = pair(live_col<TPR, VEC>(2 * p, t, a.D) ? lo(xh[p]) : mean,
+                                 live_col<TPR, VEC>(2 * p + 1, t, a.D) ? hi(xh[p]) : mean);
+            }
+        }
         F2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            xh[p] = mul2(add2(xh[p], both(-mean)), both(rstd));
+            const F2 m = VEC > 1 ? both(-mean) : pair(live_col<TPR, VEC>(2 * p, t, a.D) ? -mean : 0.f,
+                                                      live_col<TPR, VEC>(2 * p + 1, t, a.D) ? -mean : 0.f);
+            xh[p] = mul2(add2(xh[p], m), both(rstd));
             dw[p] = fma2(g[p], xh[p], dw[p]);
             db[p] = add2(db[p], g[p]);
             g[p] = mul2(g[p], w[p]);

@@ -148,6 +148,22 @@ def test_layer_norm_rows_stand_alone():
     assert dx.shape == (0, 640) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("dtype,layout", [("bf16", lambda t: t), ("bf16", odd), ("f32", lambda t: t), ("f32", odd)])
+@pytest.mark.parametrize("D", [5, 64, 128, 300, 520, 1000, 1536, 2052, 4100, 8200])
+def test_layer_norm_backward_of_a_constant_row_on_a_huge_mean(D, dtype, layout):
+    """Every deviation is zero, mean x rstd is past fp32's range: columns that a
+    thread holds past the row's end stay out of its sums."""
+    g = rng(51 + D)
+    x = layout(torch.full((3, D), 2.0 ** 120, dtype=TORCH[dtype], device="cuda"))
+    mean, rstd = torch.full((3,), 2.0 ** 120, device="cuda"), torch.full((3,), 2.0 ** 9, device="cuda")
+    dy, w = layout(normal(g, 3, D, to=dtype)), 1 + 0.3 * normal(g, D)
+    dx, dw, db = gdn.layer_norm_bwd(dy, x, mean, rstd, w)
+    gw = num(dy) * num(w)
+    close("dx", dx, 512.0 * (gw - gw.mean(-1, keepdims=True)), 512.0 * (np.abs(gw) + np.abs(gw).mean(-1, keepdims=True)), 64, dtype)
+    assert not dw.any()
+    close("db", db, num(dy).sum(0), np.abs(num(dy)).sum(0), 19)
+
+
 def test_layer_norm_autograd_and_determinism():
     x, w, b, dy = norm_case(1500, 384, "bf16", "f32", lambda t: t)
     leaves = [t.clone().requires_grad_() for t in (x, w, b)]
