@@ -148,6 +148,40 @@ def test_layer_norm_rows_stand_alone():
     assert dx.shape == (0, 640) and not dw.any() and not db.any()
 
 
+# more rows than the blocks of a full GPU take at once (8 rows per block up to 512
+# columns, else one; 6 to 1 blocks per SM): five to seven turns of every block
+MANY_ROWS = [(96, 21893), (264, 18001), (512, 15003), (520, 5001), (1000, 5500), (1536, 2500), (2056, 2203), (4096, 1999),
+             (4100, 901), (8192, 777), (8200, 611), (8193, 600)]
+
+
+@pytest.mark.parametrize("dtype,wtype,layout", [("bf16", "f32", lambda t: t), ("f32", "f32", lambda t: t),
+                                                ("bf16", "bf16", odd)])
+@pytest.mark.parametrize("D,rows", MANY_ROWS)
+def test_layer_norm_many_rows(D, rows, dtype, wtype, layout):
+    """Every block takes several rows in turn: the stages of rows in flight go round,
+    the sums of dw and db gather over a block's rows.  A sum over rows is at most 7
+    turns, 8 warps, 15 + 32 partial rows and 8 roundings of a term deep: K = 80,
+    which one row missing or taken twice exceeds."""
+    g = rng(D * 3 + rows)
+    x = layout((normal(g, rows, D, std=1.5) + torch.linspace(-1, 1, rows).cuda()[:, None]).to(TORCH[dtype]))
+    w, b = (1 + 0.3 * torch.randn(D, generator=g)).to(TORCH[wtype]).cuda(), normal(g, D, std=0.2, to=wtype)
+    dy = layout(normal(g, rows, D, to=dtype))
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b, eps=1e-5)
+    x0, w0, dy0 = num(x), num(w), num(dy)
+    y0, m0, r0 = ref.layer_norm(x0, w0, num(b))
+    top = np.abs(x0).max(-1, keepdims=True)
+    close("y", y, y0, np.abs(w0) * (r0[:, None] * top + np.abs((x0 - m0[:, None]) * r0[:, None])) + np.abs(num(b)), 64, dtype)
+    close("mean", mean, m0, top[:, 0], 64)
+    close("rstd", rstd, r0, r0 * (1 + r0 * top[:, 0]), 64)
+    dx, dw, db = gdn.layer_norm_bwd(dy, x, mean, rstd, w)
+    dx0, dw0, db0 = ref.layer_norm_backward(dy0, x0, num(mean), num(rstd), w0)
+    r = num(rstd)[:, None]
+    h, gm = np.abs((x0 - num(mean)[:, None]) * r), np.abs(dy0) * np.abs(w0)
+    close("dx", dx, dx0, r * (gm + gm.mean(-1, keepdims=True) + h * (gm * h).mean(-1, keepdims=True)), 64, dtype)
+    close("dw", dw, dw0, (np.abs(dy0) * h).sum(0), 80)
+    close("db", db, db0, np.abs(dy0).sum(0), 80)
+
+
 @pytest.mark.parametrize("dtype,layout", [("bf16", lambda t: t), ("bf16", odd), ("f32", lambda t: t), ("f32", odd)])
 @pytest.mark.parametrize("D", [5, 64, 128, 300, 520, 1000, 1536, 2052, 4100, 8200])
 def test_layer_norm_backward_of_a_constant_row_on_a_huge_mean(D, dtype, layout):
