@@ -252,6 +252,39 @@ def test_causal_conv(case, silu, dtype, wtype, layout):
         close(name, got, w0, mg, K, t)
 
 
+# large enough that a warp's run of tokens (8 at least) is several times the rows
+# that are loaded ahead; on 152 SMs, forward / backward:
+LONG_RUNS = [
+    (1, 700, 12000, 4, [0, 1, 24, 25, 47, 64, 65, 95, 97, 97, 192, 224, 226, 255, 256, 288, 500, 698, 700]),   # 24 / 32
+    (2, 1000, 4096, 3, None),                                                                                # 20 / 32
+    (1, 1999, 4096, 2, [0, 28, 61, 240, 243, 1000, 1997, 1999]),                                              # 20 / 28
+    (1, 1200, 4099, 4, [0, 40, 41, 52, 129, 700, 1200]),              # one channel per thread: 52 / 76
+]
+
+
+@pytest.mark.parametrize("dtype,wtype", [("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("case", LONG_RUNS)
+def test_causal_conv_long_runs(case, dtype, wtype):
+    """The ring of rows refilled many times, on and off the path without boundaries,
+    sequences that start and end at the edges of runs and around them.  Sums over
+    tokens are a run's 128, 8 warps, 8 + 8 groups and 10 roundings of a term deep:
+    K = 256 covers them."""
+    c = conv_case(*case, dtype, wtype)
+    y, last = gdn.causal_conv_fwd(c["x"], c["w"], c["b"], c["s"], c["cu"], "silu", output_final_state=True, check=True)
+    a = [num(c[k]) for k in ("x", "w", "b", "s")]
+    y0, last0 = ref.causal_conv(*a, c["seqs"], True)
+    m, _ = ref.causal_conv(*[np.abs(t) for t in a], c["seqs"], False)
+    close("y", y, y0, m, 64, dtype)
+    assert np.array_equal(num(last), last0)
+    got = gdn.causal_conv_bwd(c["dy"], c["x"], c["w"], c["b"], c["s"], c["cu"], "silu", c["dl"], check=True)
+    want = ref.causal_conv_backward(num(c["dy"]), *a, c["seqs"], True, num(c["dl"]))
+    mags = ref.causal_conv_backward(np.abs(num(c["dy"])) * (2 + m), *[np.abs(t) for t in a], c["seqs"], False,
+                                    np.abs(num(c["dl"])))
+    for name, x, w0, mg, K, t in zip(("dx", "dw", "db", "dstate"), got, want, mags, (64, 256, 256, 64),
+                                     (dtype, "f32", "f32", dtype)):
+        close(name, x, w0, mg, K, t)
+
+
 def test_causal_conv_without_bias_and_state():
     c = conv_case(1, 40, 24, 4, [0, 3, 3, 40], "f32", "f32")
     y, last = gdn.causal_conv_fwd(c["x"], c["w"], cu_seqlens=c["cu"], activation=None, output_final_state=True)
