@@ -428,6 +428,60 @@ def test_selective_scan_backward(case, gate, dtype, layout):
     check_scan_grads(c, got, dtype, case[1], gate)
 
 
+# several tiles of 16 tokens per block; segments of the row x tiles on 152 SMs
+MANY_TILES = [
+    (1, 96, 16000, 16, [0, 16, 17, 48, 50, 96]),         # 2 x 3, starting at a tile's edge, inside, at the segment's
+    (1, 70, 17056, 16, [0, 3, 32, 33, 70]),              # 1 x 5
+    (1, 203, 17057, 8, [0, 100, 101, 203]),              # 1 x 13, an odd number of channels
+    (1, 150, 8000, 24, None),                            # 2 x 5
+    (1, 100, 4900, 64, [0, 40, 64, 64, 100]),            # 1 x 7
+    (2, 333, 4000, 16, None),                            # 4 x 6
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", MANY_TILES)
+def test_selective_scan_many_tiles(case, dtype):
+    """A block walks several tiles: rows on their way in three stages, steps prepared
+    and outputs finished beside the scan, states carried from tile to tile and into
+    segments of several tiles.  The oracle takes every 61st channel and the last 40."""
+    c = scan_case(*case, dtype)
+    T, D = case[1], case[2]
+    y, last = gdn.selective_scan_fwd(c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c), check=True)
+    pick = torch.tensor(sorted(set(range(0, D, 61)) | set(range(D - 40, D))), device="cuda")
+    p = dict(c, A=c["A"][pick], D=c["D"][pick], bias=c["bias"][pick], s=c["s"][:, pick],
+             **{k: c[k][..., pick] for k in ("x", "dt", "z")})
+    y0, last0 = ref.selective_scan(**scan_ref(p), z=num(p["z"]))
+    ym, lm = ref.selective_scan(**scan_ref(p, np.abs))
+    longest = max(t1 - t0 for _, t0, t1 in c["seqs"])
+    close("y", y[..., pick], y0, ym * np.abs(silu(num(p["z"]))), 8 * (longest + 8), dtype)
+    close("state", last[:, pick], last0, lm, 8 * (longest + 8))
+    assert torch.isfinite(y).all() and torch.isfinite(last).all()
+
+
+# segments x tiles of the main kernel, segments per block of the maps on 152 SMs
+MANY_TILES_BWD = [
+    ("bf16", (1, 500, 4096, 16, [0, 16, 41, 64, 128, 200, 201, 256, 300, 300, 460, 500])),   # 8 x 4, 2
+    ("f32", (1, 500, 4096, 16, [0, 16, 41, 64, 128, 200, 201, 256, 300, 300, 460, 500])),
+    ("f32", (1, 595, 4096, 16, None)),                        # 19 x 2, 3
+    ("bf16", (1, 300, 4096, 24, [0, 80, 81, 170, 300])),      # 4 x 5, 1
+    ("f32", (1, 333, 2047, 40, [0, 333])),                    # 7 x 3, 1
+    ("bf16", (2, 300, 4096, 8, None)),                        # 19 x 1, 7
+    ("f32", (1, 400, 8192, 8, [0, 48, 49, 144, 150, 400])),   # 9 x 3, 3
+]
+
+
+@pytest.mark.parametrize("dtype,case", MANY_TILES_BWD)
+def test_selective_scan_backward_many_tiles(dtype, case):
+    """Segments of several tiles and blocks of the maps of several segments: every
+    tile's kept start state, the gradient carried from tile to tile, sequences that
+    start and end at the edges of tiles, of segments and of blocks and inside."""
+    c = scan_case(*case, dtype)
+    got = gdn.selective_scan_bwd(c["dy"], c["x"], c["dt"], c["A"], c["B"], c["C"], **scan_kw(c), d_final_state=c["dl"],
+                                 check=True)
+    check_scan_grads(c, got, dtype, case[1])
+
+
 def test_selective_scan_backward_over_many_blocks():
     """More channels than a block of any kernel holds and longer than a segment,
     twice with the same bits; plain steps without a bias."""
