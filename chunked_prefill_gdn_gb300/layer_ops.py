@@ -238,10 +238,13 @@ def _apart(out, inputs, same=()):
             raise ValueError("out overlaps %s" % name)
 
 
-def _wrote(*tensors):
-    """Tells autograd that a kernel wrote into tensors of the caller's (None: not
-    given), as an in-place operation of torch's own does."""
-    _increment_version([t for t in tensors if t is not None])
+def _wrote(state, out):
+    """Tells autograd that a kernel wrote into the caller's state or `out` (None:
+    not given), as an in-place operation of torch's own does."""
+    if state is not None:
+        _increment_version(state)
+    if out is not None:
+        _increment_version(out)
 
 
 def _workspace(on, workspace, size):
@@ -324,7 +327,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats
                                        y.data_ptr(), _p(mean), _p(rstd), on.raw)
         if st != 0:
             _raise(st, "gdn_layer_norm_fwd")
-        _wrote(out)
+        _wrote(None, out)
     finally:
         on.done()
     return y, mean, rstd
@@ -428,7 +431,7 @@ def causal_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, a
                                         _p(word), on.raw)
         if rc != 0:
             _raise(rc, "gdn_causal_conv_fwd")
-        _wrote(out)
+        _wrote(None, out)
         _read_status(word, on, "gdn_causal_conv_fwd")
     finally:
         on.done()
@@ -585,7 +588,7 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
                                         ws.numel() if ws is not None else 0, on.raw)
         if rc != 0:
             _raise(rc, "gdn_selective_scan_fwd")
-        _wrote(out)
+        _wrote(None, out)
         _read_status(word, on, "gdn_selective_scan_fwd")
     finally:
         on.done()
