@@ -27,7 +27,7 @@
 // TB/s, 92% of the measured copy rate; backward 4 x 4095 x 4096 87 us, 4.6 TB/s
 // (69%): there the 116 registers of a thread leave 16 warps per SM, which issue 2.3
 // instructions per clock, 28 per element; one token of 64 sequences x 12288
-// channels 3.3 us, 3.8 TB/s.
+// channels 3.3 us, 3.8 TB/s.  fp32: 489 us (6.6 TB/s), 130 us (6.2) and 5.2 us (4.9).
 #include <algorithm>
 
 #include "elem.cuh"

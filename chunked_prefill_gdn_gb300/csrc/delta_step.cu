@@ -16,7 +16,7 @@
 // four SMs.
 //
 // Measured (bf16, 128 x 128 states): 128 sequences x 32 heads 86 us, 6.3 TB/s, 94%
-// of the measured copy rate; one sequence x 32 heads (4.2 MB) 2.3 us.
+// of the measured copy rate (fp32 88 us); one sequence x 32 heads (4.2 MB) 2.4 us.
 #include <algorithm>
 
 #include "elem.cuh"

@@ -21,12 +21,13 @@
 // Measured (bf16, 16 n): 8 x 1024 tokens x 4096 channels 171 us (11 per clock and
 // SM): 6.7 scanning warps per SM are what 32768 channels give, and without the
 // feeding warps' work they alone take 136 us.  A row of 32768 tokens x 1024
-// channels 287 us, of it 118 the maps and 7 their combination.  Tried and dropped:
-// eight n per thread and twice the warps (lanes or warps sharing a channel: 213
-// and 199 us where 16 n took 197), two channels x eight n per thread, which halves
-// the reads of B and C (201 / 298 us: the same rate per SM, but blocks of 64
-// channels fill the SMs less evenly), tiles of 8 or 32 tokens, the exponentials of
-// the next token computed ahead (181 us).
+// channels 287 us, of it 118 the maps and 7 their combination.  24 n, padded to 32,
+// 332 us on the batch, 32 n 302, 64 n 584, 8 n 118.  Tried and dropped: eight n per
+// thread and twice the warps (lanes or warps sharing a channel: 213 and 199 us
+// where 16 n took 197, before the feeding warp; not measured with it), two channels
+// x eight n per thread, which halves the reads of B and C (201 / 298 us: the same
+// rate per SM, but blocks of 64 channels fill the SMs less evenly), tiles of 8 or 32
+// tokens, the exponentials of the next token computed ahead (181 us).
 //
 // When the (sequence, channel) pairs do not fill the GPU, the token axis is cut
 // into segments: a first pass gives every segment's end state from a zero
@@ -415,7 +416,8 @@ __global__ void __launch_bounds__(64) scan_combine_kernel(ScanArgs a, int maps, 
 
 // One token of each sequence: 4 n per thread, LANES threads per channel, so that a
 // warp reads and writes 512 contiguous bytes of the states; bound by their traffic
-// (32 x 4096 x 16, 18 MB: 5 us).
+// (32 x 4096 x 16, 18 MB: 6.0 us with the states in HBM, 3.0 TB/s, 45% of the
+// measured copy rate: a thread has one 16-byte load of its state in flight).
 template <typename T, int LANES>
 __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     const int part = threadIdx.x % LANES, ch = (int)((blockIdx.x * 128ll + threadIdx.x) / LANES);
@@ -477,7 +479,11 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a, int vec) {
     }
 }
 
-// Blocks of the scanning kernels that an SM holds, by N.
+// Blocks of the scanning kernels that the plans count on per SM, by N: what
+// registers and shared memory leave for bf16 inputs.  The plans do not know the
+// type: with fp32 inputs and N <= 16 shared memory holds 5 of the 7, so a row cut
+// for 7 runs as a wave and a part of one (8 x 1024 tokens x 4096 channels 225 us,
+// bf16 171; a row of 32768 x 1024 342 us, bf16 287).
 int scan_resident(int N) { return N <= 16 ? 7 : N <= 32 ? 4 : 2; }
 
 template <typename T, int NPT, int NW, int MODE>
@@ -524,7 +530,7 @@ cudaError_t launch_step_typed(const ScanArgs &a, int vec, cudaStream_t s) {
 // Segments per row in the forward pass.  One segment takes each exponential
 // once; several take it twice but put that many times the blocks to work: they
 // are cut when whole rows leave half of the SMs' room free, as many as fill it
-// once.
+// once (at bf16's room).
 int scan_segments(int B, int T, int D, int N) {
     const int tiles = (T + kTile - 1) / kTile;
     const long long blocks = (long long)B * ((D + 31) / 32), room = (long long)scan_resident(N) * device_sm_count();
@@ -544,7 +550,9 @@ namespace {
 
 // Segments of `tiles` tiles that a block of the maps walks: what gives the
 // shortest schedule on six blocks per SM, with a tile's time for a block's own
-// start and end; that schedule's length in tiles.
+// start and end; that schedule's length in tiles.  Six is what an SM holds for bf16
+// inputs and N <= 16 (fp32: four; N up to 32 four, above two), for the others it
+// only weighs the choices.
 int maps_per_block(int B, int row_segs, int tiles, int chan_blocks, long long *cost) {
     const long long slots = 6ll * device_sm_count(), unit = (long long)B * chan_blocks;
     int per = 1;

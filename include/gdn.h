@@ -649,9 +649,11 @@ gdn_status gdn_causal_conv_step(const void *x, int64_t x_stride, void *state, co
  * fp32 [D]; initial_state fp32 [n, D, N], n = B or n_seqs.  z (no gate),
  * D_skip and dt_bias (zero), initial_state (zero) and cu_seqlens may be NULL.
  * N at most 64, B at most 65535, T at most 2^30, D at most 2^26.  s A <= 0 is
- * expected (a state that grows overflows as the formula does).  A step or x that
- * is not finite makes its channel's outputs non-finite from that token to the
- * end of its sequence, and no other channel's.
+ * expected: a row is cut into segments, and where the product of exp(s A) over one
+ * exceeds fp32's range, states and outputs are not the formula's (an infinity times
+ * a zero state is not zero).  A step or x that is not finite makes its channel's
+ * outputs non-finite from that token to the end of its sequence, and no other
+ * channel's.
  */
 typedef struct {
     const void *x, *dt, *z, *B_, *C_;
