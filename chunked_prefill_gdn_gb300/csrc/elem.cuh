@@ -191,8 +191,10 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // wanted the argument x log2(e) is rounded once, which adds |x| 2^-24 or less: 2e-7
 // at 5, 1e-6 at 20, 4e-6 at 80.  Kept, because what it scales is as small as that
 // error is large: sigmoid(-20), softplus(-20) and a decay e^-20 are 2e-9, so at
-// most 2e-15 is off beside terms of order one, and the rounding's remainder would
-// take three more operations on pairs and a guard for infinities.
+// most 2e-15 is off beside terms of order one.  Carrying the remainder along in
+// softplus and its slope (four more operations on pairs and a guard for infinities)
+// brought no output of the scan nearer its 64-bit value: the states stay at 9e-7,
+// dA at 1.5e-6, ddt and dB at 4e-7, for 173 us instead of 171 and 305 instead of 301.
 __device__ __forceinline__ float exp2_f32(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
