@@ -185,6 +185,9 @@ def test_layer_norm_refuses_forward_mode(monkeypatch):
                 args[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
                 with pytest.raises(RuntimeError):
                     gdn.layer_norm(*args)
+    # nested, with the tangent of the outer level in a captured tensor
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda u: torch.func.jvp(lambda t: t.sum() * gdn.layer_norm(u), (x,), (x,))[0], (x,), (x,))
     # without tangents: the values, and statistics only where a backward pass will ask for them
     del calls[:]
     want = kernel(x, w, b)[0]
