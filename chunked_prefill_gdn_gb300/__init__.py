@@ -27,7 +27,8 @@ from typing import Optional
 import torch
 
 from . import build as _build
-from . import layer_ops
+from . import block_ops, layer_ops
+from .block_ops import *  # noqa: F401,F403
 from .layer_ops import *  # noqa: F401,F403
 
 __all__ = [
@@ -45,7 +46,7 @@ __all__ = [
     "gdn_status_string", "gdn_version", "gdn_last_error_detail", "chunk_fwd", "chunk_fwd_host", "workspace_for", "GdnError",
     "CP_AUTO", "CP_OFF", "CP_FORCE", "KERNEL_AUTO", "KERNEL_TC", "KERNEL_SIMT", "BF16", "F32",
     "STAGE_PREP", "STAGE_INVERSE", "STAGE_CORRECTION", "STAGE_FUSED",
-] + layer_ops.__all__
+] + layer_ops.__all__ + block_ops.__all__
 
 BF16, F32 = 0, 1
 CP_AUTO, CP_OFF, CP_FORCE = 0, 1, 2
@@ -175,6 +176,7 @@ def load_library(build_if_missing: bool = False):
     lib.gdn_last_error_detail.argtypes = []
     lib.gdn_last_error_detail.restype = ctypes.c_char_p
     layer_ops.bind(lib)
+    block_ops.bind(lib)
     _lib = lib
     _apply_measured_costs(lib)
     return lib

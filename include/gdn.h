@@ -704,6 +704,53 @@ gdn_status gdn_delta_step(const void *q, int64_t q_stride, const void *k, int64_
                           const int32_t *state_indices, int n_states, float scale, int qk_l2norm, int N, int H,
                           int dk, int dv, gdn_dtype dtype, void *o, gdn_stream_t stream);
 
+/*
+ * Gated feed-forward block over M rows:
+ *
+ *     g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T,
+ *
+ * act SiLU, or GELU in its tanh form.  x: M rows of D, x_stride elements apart;
+ * w_gate, w_up: [F, D], w_down: [D_out, F], all in dtype; y: [M, D_out]; gate, up:
+ * [M, F], g and u for the backward pass, or both NULL.  bf16 (h is rounded to bf16
+ * between the two products, whose sums are fp32) or fp32 (products of three bf16
+ * terms a value, sums fp32: as exact as fp32 products).  A row that is not finite
+ * makes its own outputs non-finite (with fp32 an infinity may give NaN).
+ *
+ * The workspace is 16-byte aligned and holds gdn_gated_ffn_fwd_workspace_size()
+ * bytes, which depends on the sizes and on how x and the weights are aligned (0:
+ * arguments that the call refuses); with fp32, or rows that are not 16-byte aligned,
+ * it holds copies of x and of the weights.  Sizes at most 2^24, the largest tensor 2^38 elements.
+ *
+ * device_status: NULL, or a device int32 into which the call writes 0, or
+ * GDN_ERR_TIMEOUT where a wait inside a kernel ran out.
+ */
+typedef enum { GDN_ACT_SILU = 0, GDN_ACT_GELU_TANH = 1 } gdn_activation;
+typedef struct {
+    const void *x, *w_gate, *w_up, *w_down;
+    int64_t x_stride, M, D, F, D_out;
+    int32_t activation, dtype;
+} gdn_ffn_desc;
+
+size_t gdn_gated_ffn_fwd_workspace_size(const gdn_ffn_desc *desc);
+gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc *desc, void *y, void *gate, void *up, int32_t *device_status,
+                             void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Its backward pass, from dy (M rows of D_out, dy_stride elements apart) and the
+ * forward pass's gate and up: with dh = dy w_down,
+ *
+ *     dg = dh u act'(g),  du = dh act(g),  dx = dg w_gate + du w_up,
+ *     dw_gate = dg^T x,  dw_up = du^T x,  dw_down = dy^T h.
+ *
+ * dx [M, D] and the weights' gradients (laid out like the weights) in dtype, each
+ * may be NULL; for bf16 dg, du and h are rounded to bf16 between the products.  The
+ * same inputs give the same bits.  Workspace and device_status as above.
+ */
+size_t gdn_gated_ffn_bwd_workspace_size(const gdn_ffn_desc *desc, const void *dy, int64_t dy_stride);
+gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy, int64_t dy_stride, const void *gate,
+                             const void *up, void *dx, void *dw_gate, void *dw_up, void *dw_down,
+                             int32_t *device_status, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 /* The CUDA error (and, for tensor-map encoding, the driver result) behind the
  * most recent GDN_ERR_CUDA returned on the calling host thread, as text such
  * as "launch fused_tc: cudaErrorInvalidValue"; after gdn_chunk_fwd_static
