@@ -1,14 +1,18 @@
-"""The operators of a layer's blocks beside the recurrence: the gated feed-forward
+"""The operators of a layer beside its recurrence: what lies between two blocks
+(norm, gate, scale, residual sum, norm, in one pass) and the gated feed-forward
 block (include/gdn.h has the definitions).
 
+    x, h, rstd_post, rstd_pre = block_norm_fwd(y, residual, gate, post_weight, scale, pre_weight)
+    dy, dresidual, dgate, dpost_weight, dscale, dpre_weight = block_norm_bwd(dx, dh, y, x, rstd_post, rstd_pre, ...)
     y, gate, up = gated_ffn_fwd(x, w_gate, w_up, w_down)
     dx, dw_gate, dw_up, dw_down = gated_ffn_bwd(dy, x, w_gate, w_up, w_down, gate, up)
 
-and with autograd: gated_ffn.
+and with autograd: block_norm, gated_ffn.
 
-Types, layouts, streams, `out` and version counters are those of layer_ops.  The
-weights of the feed-forward block have the activations' type, and so have their
-gradients.
+Types, layouts, streams, `out` and version counters are those of layer_ops.
+block_norm also takes rows in two levels (heads of a token that is a slice of a
+wider projection).  The weights of the feed-forward block have the activations'
+type, and so have their gradients.
 """
 from __future__ import annotations
 
@@ -19,10 +23,21 @@ import torch
 
 from .layer_ops import _CODE, _On, _act, _apart, _like, _p, _raise, _row_stride, _workspace, _wrote
 
-__all__ = ["gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn", "GdnFfnDesc"]
+__all__ = ["block_norm_fwd", "block_norm_bwd", "block_norm", "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn",
+           "GdnBlockNormDesc", "GdnFfnDesc"]
 
-_I32 = torch.int32
+_F32, _I32 = torch.float32, torch.int32
+_GATES = {"silu": 0, "sigmoid": 1}
 _ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+class GdnBlockNormDesc(ctypes.Structure):
+    """gdn_block_norm_desc of include/gdn.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("y", "gate", "post_weight", "scale", "pre_weight")] +
+                [(n, ctypes.c_int64) for n in ("outer", "inner", "D", "y_outer_stride", "y_inner_stride",
+                                               "gate_outer_stride", "gate_inner_stride")] +
+                [("eps", ctypes.c_float)] +
+                [(n, ctypes.c_int32) for n in ("post_norm", "pre_norm", "gate_activation", "dtype", "w_dtype")])
 
 
 class GdnFfnDesc(ctypes.Structure):
@@ -35,8 +50,11 @@ class GdnFfnDesc(ctypes.Structure):
 def bind(lib):
     """Argument types of these operators' C entry points."""
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
-    ffn = ctypes.POINTER(GdnFfnDesc)
+    norm, ffn = ctypes.POINTER(GdnBlockNormDesc), ctypes.POINTER(GdnFfnDesc)
     for name, res, args in (
+            ("gdn_block_norm_fwd", i32, [norm, vp, i64, i64] + [vp] * 5),
+            ("gdn_block_norm_bwd_workspace_size", sz, [norm]),
+            ("gdn_block_norm_bwd", i32, [norm] + [vp, i64, i64] * 3 + [vp] * 9 + [sz, vp]),
             ("gdn_gated_ffn_fwd_workspace_size", sz, [ffn]),
             ("gdn_gated_ffn_fwd", i32, [ffn, vp, vp, vp, vp, vp, sz, vp]),
             ("gdn_gated_ffn_bwd_workspace_size", sz, [ffn, vp, i64]),
@@ -68,6 +86,188 @@ def _read_status(word, on, where):
     st = int(word.item())
     if st != 0:
         _raise(st, where + " (device check)")
+
+
+# -------------------------------------------------------- between two blocks
+
+def _levels(name, t):
+    """The rows of a [..., D] tensor as (size, stride) levels, neighbouring levels
+    that run on into one another merged."""
+    D = t.shape[-1]
+    at = []
+    for n, s in zip(t.shape[:-1], t.stride()[:-1]):
+        if n == 1:
+            continue
+        if at and at[-1][1] == n * s:
+            at[-1] = (at[-1][0] * n, s)
+        else:
+            at.append((n, s))
+    if len(at) > 2:
+        raise ValueError("%s: its rows are not equally spaced in two levels" % name)
+    if any(s < D for _, s in at):
+        raise ValueError("%s: rows overlap" % name)
+    return at
+
+
+def _row_levels(tensors):
+    """A common (outer, inner) for the rows of several [..., D] tensors of one shape,
+    and their (outer, inner) strides."""
+    first = next(t for _, t in tensors if t is not None)
+    D, rows = first.shape[-1], first.numel() // first.shape[-1] if first.shape[-1] else 0
+    if rows == 0 or all(t is None or t.is_contiguous() for _, t in tensors):
+        return rows, 1, [(D, D)] * len(tensors)
+    levels = [_levels(name, t) if t is not None else [] for name, t in tensors]
+    inner = 1
+    for (name, _), at in zip(tensors, levels):
+        if len(at) == 2:
+            if inner not in (1, at[1][0]):
+                raise ValueError("%s: its rows are in levels of %d, another input's of %d" % (name, at[1][0], inner))
+            inner = at[1][0]
+    strides = []
+    for at in levels:
+        if len(at) == 2:
+            strides.append((at[0][1], at[1][1]))
+        else:
+            s = at[0][1] if at else D
+            strides.append((s * inner, s))
+    return rows // inner, inner, strides
+
+
+def _vectors(D, device, dtype, named):
+    """Type code of the [D] parameters (float32 or the activations' type, all alike)."""
+    given = [(n, t) for n, t in named if t is not None]
+    if not given:
+        return 1
+    w = given[0][1].dtype
+    if w != _F32 and w != dtype:
+        raise TypeError("%s must be float32 or %s, got %s" % (given[0][0], dtype, w))
+    for n, t in given:
+        _like(n, t, (D,), w, device)
+    return _CODE[w]
+
+
+def _norm_desc(y, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps, others):
+    """Checks the operator's inputs; returns (descriptor, strides of `others`)."""
+    _act("y", y)
+    D, dev, dtype = y.shape[-1], y.device, y.dtype
+    for name, t in (("gate", gate), *others):
+        if t is not None:
+            _like(name, t, y.shape, dtype, dev, strided=True)
+    if activation not in _GATES:
+        raise ValueError("activation must be 'silu' or 'sigmoid', got %r" % (activation,))
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight needs pre_norm")
+    wcode = _vectors(D, dev, dtype, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)))
+    outer, inner, strides = _row_levels((("y", y), ("gate", gate), *others))
+    return GdnBlockNormDesc(y.data_ptr(), _p(gate), _p(post_weight), _p(scale), _p(pre_weight), outer, inner, D,
+                            *strides[0], *strides[1], eps, 1 if post_norm else 0, 1 if pre_norm else 0,
+                            _GATES[activation], _CODE[dtype], wcode), strides[2:]
+
+
+def block_norm_fwd(y, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, post_norm: bool = True,
+                   pre_norm: bool = True, activation: str = "silu", eps: float = 1e-5, out=None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """What lies between two blocks, over the last axis of y [..., D]: x = residual +
+    scale * norm(y) * act(gate) and h = norm(x), norm(t) = t * (mean t^2 + eps)^-1/2 * weight;
+    returns (x, h, rstd_post, rstd_pre), the last two float32 [...] for the backward pass.
+    Each part may be left out: post_norm=False takes y itself, pre_norm=False makes no h
+    (None); residual, gate, scale and the weights are optional.  gate and residual have
+    y's shape; weights and scale are [D] in float32 or y's type.  activation: 'silu' or
+    'sigmoid'.  `out` receives x."""
+    desc, ((ro, ri),) = _norm_desc(y, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps,
+                                   (("residual", residual),))
+    dtype, dev = y.dtype, y.device
+    if out is not None:
+        _like("out", out, y.shape, dtype, dev)
+        _apart(out, (("y", y), ("residual", residual), ("gate", gate), ("post_weight", post_weight), ("scale", scale),
+                     ("pre_weight", pre_weight)), same=("y", "residual", "gate"))
+    on = _On(dev, stream)
+    try:
+        x = out if out is not None else on.empty(y.shape, dtype)
+        h = on.empty(y.shape, dtype) if pre_norm else None
+        rp = on.empty(y.shape[:-1], _F32) if post_norm else None
+        rn = on.empty(y.shape[:-1], _F32) if pre_norm else None
+        rc = _lib().gdn_block_norm_fwd(desc, _p(residual), ro, ri, x.data_ptr(), _p(h), _p(rp), _p(rn), on.raw)
+        if rc != 0:
+            _raise(rc, "gdn_block_norm_fwd")
+        _wrote(None, out)
+    finally:
+        on.done()
+    return x, h, rp, rn
+
+
+def block_norm_bwd(dx, dh, y, x, rstd_post, rstd_pre, gate=None, post_weight=None, scale=None, pre_weight=None,
+                   activation: str = "silu", residual: bool = True, workspace=None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of block_norm_fwd from dx and dh (the gradients of x and h; dh None
+    without the second norm, dx None where x is used for h only), the forward pass's y, x
+    and rstd (None for a norm that was left out): (dy, dresidual, dgate, dpost_weight,
+    dscale, dpre_weight).  dresidual is the gradient of x as a whole (None with
+    residual=False); the parameters' gradients are float32, None for those not given."""
+    post, pre = rstd_post is not None, rstd_pre is not None
+    if pre and (dh is None or x is None):
+        raise ValueError("the second norm's backward pass needs dh and x")
+    if not pre and (dh is not None or dx is None):
+        raise ValueError("without the second norm dx is needed and there is no dh")
+    xs = x if pre else None
+    desc, strides = _norm_desc(y, gate, post_weight, scale, pre_weight, post, pre, activation, 0.0,
+                               (("dx", dx), ("dh", dh), ("x", xs)))
+    D, dtype, dev = y.shape[-1], y.dtype, y.device
+    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
+        if t is not None:
+            _like(name, t, y.shape[:-1], _F32, dev)
+    lib = _lib()
+    on = _On(dev, stream)
+    try:
+        dy = on.empty(y.shape, dtype)
+        dr = on.empty(y.shape, dtype) if residual else None
+        dz = on.empty(y.shape, dtype) if gate is not None else None
+        grads = [on.empty((D,), _F32) if t is not None else None for t in (post_weight, scale, pre_weight)]
+        ws = None
+        if any(t is not None for t in grads):
+            ws = _workspace(on, workspace, lib.gdn_block_norm_bwd_workspace_size(desc))
+        rc = lib.gdn_block_norm_bwd(desc, _p(dx), *strides[0], _p(dh), *strides[1], _p(xs), *strides[2], _p(rstd_post),
+                                    _p(rstd_pre), dy.data_ptr(), _p(dr), _p(dz), *(_p(t) for t in grads), _p(ws),
+                                    ws.numel() if ws is not None else 0, on.raw)
+        if rc != 0:
+            _raise(rc, "gdn_block_norm_bwd")
+    finally:
+        on.done()
+    return (dy, dr, dz, *grads)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, residual, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps):
+        x, h, rp, rn = block_norm_fwd(y, residual, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation,
+                                      eps)
+        ctx.save_for_backward(y, x if pre_norm else None, rp, rn, gate, post_weight, scale, pre_weight)
+        ctx.activation, ctx.residual = activation, residual is not None
+        ctx.types = [None if t is None else t.dtype for t in (post_weight, scale, pre_weight)]
+        ctx.set_materialize_grads(False)
+        return x, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dx, dh):
+        y, x, rp, rn, gate, post_weight, scale, pre_weight = ctx.saved_tensors
+        if dx is None and dh is None:
+            return (None,) * 10
+        if rn is not None and dh is None:
+            dh = torch.zeros(y.shape, dtype=y.dtype, device=y.device)
+        dy, dr, dz, *params = block_norm_bwd(
+            dx.contiguous() if dx is not None else None, dh.contiguous() if dh is not None else None, y, x, rp, rn, gate,
+            post_weight, scale, pre_weight, ctx.activation, residual=ctx.residual)
+        return (dy, dr, dz, *(None if g is None else g.to(t) for g, t in zip(params, ctx.types)), None, None, None, None)
+
+
+def block_norm(y, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, post_norm: bool = True,
+               pre_norm: bool = True, activation: str = "silu", eps: float = 1e-5):
+    """block_norm_fwd with autograd (every tensor); returns (x, h), h None without
+    pre_norm."""
+    return _BlockNorm.apply(y, residual, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps)
 
 
 # ---------------------------------------------------- the gated feed-forward block

@@ -1,0 +1,740 @@
+// What lies between two blocks of a layer, in one pass, forward and backward:
+//
+//     n = y rstd_post w_post,          rstd_post = (sum y^2 / D + eps)^-1/2,
+//     x = r + s n a(z),                a(z) = z sigmoid(z), or sigmoid(z),
+//     h = x rstd_pre w_pre,            rstd_pre = (sum x^2 / D + eps)^-1/2,
+//
+// of which the first norm, the gate z, the scale s, the residual r and the second
+// norm may each be left out; and, for upstream gradients dx and dh,
+//
+//     d  = dx + rstd_pre (g - xh sum g xh / D),       g = dh w_pre, xh = x rstd_pre,
+//     dr = d,   dz = d s n a'(z),
+//     dy = rstd_post (e - yh sum e yh / D),           e = d s a(z) w_post, yh = y rstd_post,
+//     dw_pre = sum_rows dh xh,   P = sum_rows d a(z) yh,   dw_post = s P,   ds = w_post P.
+//
+// Statistics and h are taken from x before it is rounded.  Both passes are streams
+// bound by HBM: every tensor is read once and written once (five tensors forward,
+// eight backward).  A row is held by 8 to 512 threads, 8 or 16 columns each; the
+// blocks are persistent and own their columns, so the parameters and the sums P and
+// dw_pre stay in registers over all rows of a block.  The next rows come in by
+// asynchronous copies; what is needed twice is read again from those copies instead
+// of being held.  The blocks' sums leave as partial rows that a second kernel adds in
+// a fixed order.
+#include <algorithm>
+
+#include "elem.cuh"
+
+namespace gdn {
+namespace {
+
+// Rows [outer][inner]: row i starts at (i / inner) so + (i % inner) si elements.
+struct View {
+    const void *p;
+    long long so, si;
+};
+struct BlockNormArgs {
+    View y, z, r, dx, dh;             // r: the residual, or x in the backward pass
+    void *x, *h, *dy, *dr, *dz;       // outputs, contiguous
+    const void *w_post, *w_pre, *scale;
+    float *rstd_post, *rstd_pre;
+    float *partial;                   // [grid][P, dw_pre][D] or null
+    long long rows;
+    uint32_t inner, magic, shift;     // division by inner
+    int D, w_f32, post, pre, gate, res;   // gate: 0 none, 1 silu, 2 sigmoid
+    float eps;
+};
+
+__device__ __forceinline__ long long row_at(const BlockNormArgs &a, const View &v, long long row) {
+    if (a.inner == 1) return row * v.so;
+    const uint32_t n = (uint32_t)row, q = (__umulhi(a.magic, n) + n) >> a.shift;
+    return (long long)q * v.so + (long long)(n - q * a.inner) * v.si;
+}
+__device__ __forceinline__ float param_at(const void *p, int i, int f32) {
+    return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+// Sum over the TPR threads of a row.  Each use takes the other of the two arrays: who
+// writes one again has passed the barrier of the use in between, by which all have
+// read it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (*both_red)[32], int &phase) {
+    float *red = both_red[phase];
+    phase ^= 1;
+#pragma unroll
+    for (int off = (TPR < 32 ? TPR : 32) / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) v += red[i];
+    }
+    return v;
+}
+
+constexpr int bn_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
+
+// Rows in flight per row of threads: as many as `most` bytes per block hold, at most
+// four; a single one where not even two fit.
+template <typename T, int TPR, int VEC, int NV, int ARRAYS>
+struct BnStages {
+    static constexpr bool async = VEC * sizeof(T) == 16;
+    static constexpr int bytes = bn_threads(TPR) * NV * ARRAYS * 16;
+    static constexpr int fit = 98304 / bytes;
+    static constexpr int count = !async ? 1 : fit >= 4 ? 4 : fit >= 2 ? fit : bytes <= 106496 ? 2 : 1;
+    static constexpr int smem = async ? count * bytes : 0;
+    static constexpr int by_smem = smem ? 225 * 1024 / (smem + 1024) : 8;
+    static constexpr int by_threads = (ARRAYS == 3 ? 768 : 512) / bn_threads(TPR);
+    static constexpr int blocks = by_smem < by_threads ? (by_smem > 0 ? by_smem : 1) : (by_threads > 0 ? by_threads : 1);
+};
+
+__device__ __forceinline__ void bn_copy16(uint4 *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// Column of a thread's element e (of NV vectors of VEC, TPR vectors apart).
+template <int TPR, int VEC>
+__device__ __forceinline__ int col_of(int e, int t) {
+    return (e / VEC * TPR + t) * VEC + e % VEC;
+}
+template <int TPR, int VEC, int NV>
+__device__ __forceinline__ void params(const void *p, const void *q, int f32, int D, int t, F2 (&v)[NV * VEC / 2]) {
+    float x[NV * VEC];
+#pragma unroll
+    for (int e = 0; e < NV * VEC; ++e) {
+        const int c = col_of<TPR, VEC>(e, t);
+        x[e] = 1.f;
+        if (c < D && p) x[e] = param_at(p, c, f32);
+        if (c < D && q) x[e] *= param_at(q, c, f32);
+    }
+#pragma unroll
+    for (int i = 0; i < NV * VEC / 2; ++i) v[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+
+// A thread's part of one array's row: from the copies, or element by element from
+// the row itself; zero past the row's end.
+template <typename T, int TPR, int VEC, int NV, bool ASYNC>
+struct Part {
+    const uint4 *at;     // [NV] vectors, NT apart
+    const T *row;
+    int t, D;
+    bool live;
+    template <int NT>
+    __device__ __forceinline__ void get(F2 (&v)[NV * VEC / 2]) const {
+        if constexpr (ASYNC) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool in = live && (i * TPR + t) * VEC < D;
+                F2 u[VEC / 2];
+                unpack_pairs<T, VEC>(in ? load_raw<T, VEC>(reinterpret_cast<const T *>(at + i * NT)) : zero_raw<T, VEC>(), u);
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) v[i * (VEC / 2) + j] = u[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV * VEC / 2; ++i) {
+                const int c0 = col_of<TPR, VEC>(2 * i, t), c1 = col_of<TPR, VEC>(2 * i + 1, t);
+                v[i] = pair(live && c0 < D ? to_f32(row[c0]) : 0.f, live && c1 < D ? to_f32(row[c1]) : 0.f);
+            }
+        }
+    }
+};
+
+template <typename T, int TPR, int VEC, int NV>
+__device__ __forceinline__ void put_row(T *row, int D, int t, bool live, const F2 (&v)[NV * VEC / 2]) {
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        if (c >= D) continue;
+        if constexpr (VEC > 1) {
+            F2 u[VEC / 2];
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) u[j] = v[i * (VEC / 2) + j];
+            store_raw<T, VEC>(row + c, pack_pairs<T, VEC>(u));
+        } else {
+            row[c] = from_f32<T>(i & 1 ? hi(v[i / 2]) : lo(v[i / 2]));
+        }
+    }
+}
+
+template <typename T, int TPR, int VEC, int NV>
+__global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 3>::blocks) block_norm_fwd_kernel(const BlockNormArgs a) {
+    using St = BnStages<T, TPR, VEC, NV, 3>;
+    constexpr int NT = bn_threads(TPR), RPB = NT / TPR, S = St::count, NP = NV * VEC / 2;
+    __shared__ float red[2][32];
+    extern __shared__ uint4 stages[];              // [S][y, z, r][NV][thread]
+    const int t = threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * RPB;
+    grid_dependency_wait();
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int behind = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;   // rows of a warp go together
+    auto load_row = [&](long long r, int slot) {
+        if constexpr (St::async) {
+            if (r < a.rows) {
+                const T *y = static_cast<const T *>(a.y.p) + row_at(a, a.y, r);
+                const T *z = a.gate ? static_cast<const T *>(a.z.p) + row_at(a, a.z, r) : nullptr;
+                const T *rr = a.res ? static_cast<const T *>(a.r.p) + row_at(a, a.r, r) : nullptr;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * TPR + t) * VEC;
+                    uint4 *at = stages + (slot * 3 * NV + i) * NT + threadIdx.x;
+                    if (c < a.D) {
+                        bn_copy16(at, y + c);
+                        if (a.gate) bn_copy16(at + NV * NT, z + c);
+                        if (a.res) bn_copy16(at + 2 * NV * NT, rr + c);
+                    }
+                }
+            }
+            copy_commit();
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    F2 c[NP], wn[NP];
+    params<TPR, VEC, NV>(a.w_post, a.scale, a.w_f32, a.D, t, c);
+    params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
+    const float inv_d = 1.f / (float)a.D;
+    int phase = 0;
+    for (int slot = 0; row - behind < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1) {
+        const bool live = row < a.rows;
+        Part<T, TPR, VEC, NV, St::async> y, z, r;
+        y.t = z.t = r.t = t, y.D = z.D = r.D = a.D, y.live = z.live = r.live = live;
+        if constexpr (St::async) {
+            if constexpr (S > 1) load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+            y.at = stages + slot * 3 * NV * NT + threadIdx.x;
+            z.at = y.at + NV * NT, r.at = z.at + NV * NT;
+        } else if (live) {
+            y.row = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
+            if (a.gate) z.row = static_cast<const T *>(a.z.p) + row_at(a, a.z, row);
+            if (a.res) r.row = static_cast<const T *>(a.r.p) + row_at(a, a.r, row);
+        }
+        F2 v[NP], u[NP];
+        y.template get<NT>(v);
+        float rstd = 1.f;
+        if (a.post) {
+            F2 q = mul2(v[0], v[0]);
+#pragma unroll
+            for (int p = 1; p < NP; ++p) q = fma2(v[p], v[p], q);
+            rstd = rsqrtf(row_sum<TPR>(lo(q) + hi(q), red, phase) * inv_d + a.eps);
+            if (t == 0 && live) a.rstd_post[row] = rstd;
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) v[p] = mul2(mul2(v[p], both(rstd)), c[p]);
+        if (a.gate) {
+            z.template get<NT>(u);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const F2 s = sigmoid_pair(u[p]);
+                v[p] = mul2(v[p], a.gate == 1 ? mul2(u[p], s) : s);
+            }
+        }
+        if (a.res) {
+            r.template get<NT>(u);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) v[p] = add2(v[p], u[p]);
+        }
+        if constexpr (S == 1 && St::async) load_row(row + step, 0);
+        put_row<T, TPR, VEC, NV>(static_cast<T *>(a.x) + row * a.D, a.D, t, live, v);
+        if (a.pre) {
+            F2 q = both(0.f);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) q = fma2(v[p], v[p], q);
+            const float r2 = rsqrtf(row_sum<TPR>(lo(q) + hi(q), red, phase) * inv_d + a.eps);
+            if (t == 0 && live) a.rstd_pre[row] = r2;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) v[p] = mul2(mul2(v[p], both(r2)), wn[p]);
+            put_row<T, TPR, VEC, NV>(static_cast<T *>(a.h) + row * a.D, a.D, t, live, v);
+        }
+    }
+}
+
+template <typename T, int TPR, int VEC, int NV>
+__global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 5>::blocks) block_norm_bwd_kernel(const BlockNormArgs a) {
+    using St = BnStages<T, TPR, VEC, NV, 5>;
+    constexpr int NT = bn_threads(TPR), RPB = NT / TPR, S = St::count, NP = NV * VEC / 2;
+    __shared__ float red[2][32];
+    extern __shared__ uint4 stages[];              // [S][y, z, dx, dh, x][NV][thread]
+    const int t = threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * RPB;
+    grid_dependency_wait();
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int behind = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
+    const bool has_dx = a.dx.p != nullptr;
+    auto load_row = [&](long long r, int slot) {
+        if constexpr (St::async) {
+            if (r < a.rows) {
+                const View *view[5] = {&a.y, &a.z, &a.dx, &a.dh, &a.r};
+                const bool there[5] = {true, a.gate != 0, has_dx, a.pre != 0, a.pre != 0};
+#pragma unroll
+                for (int k = 0; k < 5; ++k) {
+                    if (!there[k]) continue;
+                    const T *src = static_cast<const T *>(view[k]->p) + row_at(a, *view[k], r);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int c = (i * TPR + t) * VEC;
+                        if (c < a.D) bn_copy16(stages + ((slot * 5 + k) * NV + i) * NT + threadIdx.x, src + c);
+                    }
+                }
+            }
+            copy_commit();
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    F2 c[NP], wn[NP], P[NP], Q[NP];
+    params<TPR, VEC, NV>(a.w_post, a.scale, a.w_f32, a.D, t, c);
+    params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) P[p] = Q[p] = both(0.f);
+    const float inv_d = 1.f / (float)a.D;
+    int phase = 0;
+    for (int slot = 0; row - behind < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1) {
+        const bool live = row < a.rows;
+        const float rp = a.post && live ? a.rstd_post[row] : 1.f, rn = a.pre && live ? a.rstd_pre[row] : 1.f;
+        Part<T, TPR, VEC, NV, St::async> part[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) part[k].t = t, part[k].D = a.D, part[k].live = live;
+        if constexpr (St::async) {
+            if constexpr (S > 1) load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+            copy_wait<S - 1>();
+#pragma unroll
+            for (int k = 0; k < 5; ++k) part[k].at = stages + (slot * 5 + k) * NV * NT + threadIdx.x;
+        } else if (live) {
+            part[0].row = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
+            if (a.gate) part[1].row = static_cast<const T *>(a.z.p) + row_at(a, a.z, row);
+            if (has_dx) part[2].row = static_cast<const T *>(a.dx.p) + row_at(a, a.dx, row);
+            if (a.pre) {
+                part[3].row = static_cast<const T *>(a.dh.p) + row_at(a, a.dh, row);
+                part[4].row = static_cast<const T *>(a.r.p) + row_at(a, a.r, row);
+            }
+        }
+        F2 d[NP], u[NP], v[NP];
+        if (a.pre) {
+            part[3].template get<NT>(u);
+            part[4].template get<NT>(v);
+            F2 q = both(0.f);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                v[p] = mul2(v[p], both(rn));
+                Q[p] = fma2(u[p], v[p], Q[p]);
+                u[p] = mul2(u[p], wn[p]);
+                q = fma2(u[p], v[p], q);
+            }
+            const float m = row_sum<TPR>(lo(q) + hi(q), red, phase) * inv_d;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) d[p] = mul2(fma2(v[p], both(-m), u[p]), both(rn));
+            if (has_dx) {
+                part[2].template get<NT>(u);
+#pragma unroll
+                for (int p = 0; p < NP; ++p) d[p] = add2(d[p], u[p]);
+            }
+        } else {
+            part[2].template get<NT>(d);
+        }
+        if (a.dr) put_row<T, TPR, VEC, NV>(static_cast<T *>(a.dr) + row * a.D, a.D, t, live, d);
+        part[0].template get<NT>(v);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) v[p] = mul2(v[p], both(rp));      // yh
+        if (a.gate) {
+            part[1].template get<NT>(u);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const F2 s = sigmoid_pair(u[p]), one = fma2(s, both(-1.f), both(1.f));   // 1 - s
+                const F2 g = a.gate == 1 ? mul2(u[p], s) : s;                              // a(z)
+                const F2 slope = a.gate == 1 ? fma2(g, one, s) : mul2(s, one);             // a'(z)
+                const F2 dc = mul2(d[p], c[p]);
+                P[p] = fma2(mul2(d[p], g), v[p], P[p]);
+                u[p] = mul2(mul2(dc, v[p]), slope);
+                d[p] = mul2(dc, g);
+            }
+            put_row<T, TPR, VEC, NV>(static_cast<T *>(a.dz) + row * a.D, a.D, t, live, u);
+        } else {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                P[p] = fma2(d[p], v[p], P[p]);
+                d[p] = mul2(d[p], c[p]);
+            }
+        }
+        if constexpr (S == 1 && St::async) load_row(row + step, 0);
+        if (a.post) {
+            F2 q = both(0.f);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) q = fma2(d[p], v[p], q);
+            const float m = row_sum<TPR>(lo(q) + hi(q), red, phase) * inv_d;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) d[p] = mul2(fma2(v[p], both(-m), d[p]), both(rp));
+        }
+        put_row<T, TPR, VEC, NV>(static_cast<T *>(a.dy) + row * a.D, a.D, t, live, d);
+    }
+    if (!a.partial) return;
+    float *pp = a.partial + 2ll * blockIdx.x * a.D, *pq = pp + a.D;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int e = 0; e < NV * VEC; ++e) {
+            const int col = col_of<TPR, VEC>(e, t);
+            if (col < a.D) {
+                pp[col] = e & 1 ? hi(P[e / 2]) : lo(P[e / 2]);
+                pq[col] = e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]);
+            }
+        }
+    } else {
+        // the sums of the block's rows of threads, in order
+        constexpr int COLS = TPR * NV * VEC;
+        __shared__ float sum[2][COLS];
+        for (int r = 0; r < RPB; ++r) {
+            if ((int)threadIdx.x / TPR == r) {
+#pragma unroll
+                for (int e = 0; e < NV * VEC; ++e) {
+                    const int col = col_of<TPR, VEC>(e, t);
+                    sum[0][col] = (r ? sum[0][col] : 0.f) + (e & 1 ? hi(P[e / 2]) : lo(P[e / 2]));
+                    sum[1][col] = (r ? sum[1][col] : 0.f) + (e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]));
+                }
+            }
+            __syncthreads();
+        }
+        for (int col = threadIdx.x; col < a.D; col += blockDim.x) pp[col] = sum[0][col], pq[col] = sum[1][col];
+    }
+}
+
+// Rows wider than the register-resident kernels take: a block per row, which it
+// reads several times, element by element.
+template <typename T>
+__global__ void __launch_bounds__(1024) block_norm_wide_fwd_kernel(const BlockNormArgs a) {
+    __shared__ float red[2][32];
+    const float inv_d = 1.f / (float)a.D;
+    int phase = 0;
+    grid_dependency_wait();
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *y = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
+        const T *z = a.gate ? static_cast<const T *>(a.z.p) + row_at(a, a.z, row) : nullptr;
+        const T *r = a.res ? static_cast<const T *>(a.r.p) + row_at(a, a.r, row) : nullptr;
+        float rstd = 1.f, q = 0.f;
+        if (a.post) {
+            for (int c = threadIdx.x; c < a.D; c += 1024) q = fmaf(to_f32(y[c]), to_f32(y[c]), q);
+            rstd = rsqrtf(row_sum<1024>(q, red, phase) * inv_d + a.eps);
+            if (threadIdx.x == 0) a.rstd_post[row] = rstd;
+        }
+        auto value = [&](int c) {
+            float v = to_f32(y[c]) * rstd;
+            if (a.w_post) v *= param_at(a.w_post, c, a.w_f32);
+            if (a.scale) v *= param_at(a.scale, c, a.w_f32);
+            if (a.gate) {
+                const float s = sigmoid_f32(to_f32(z[c]));
+                v *= a.gate == 1 ? to_f32(z[c]) * s : s;
+            }
+            return a.res ? v + to_f32(r[c]) : v;
+        };
+        float r2 = 1.f;
+        if (a.pre) {
+            q = 0.f;
+            for (int c = threadIdx.x; c < a.D; c += 1024) {
+                const float v = value(c);
+                q = fmaf(v, v, q);
+            }
+            r2 = rsqrtf(row_sum<1024>(q, red, phase) * inv_d + a.eps);
+            if (threadIdx.x == 0) a.rstd_pre[row] = r2;
+        }
+        for (int c = threadIdx.x; c < a.D; c += 1024) {   // x may be the memory of y, z or r: written last
+            const float v = value(c);
+            static_cast<T *>(a.x)[row * a.D + c] = from_f32<T>(v);
+            if (a.pre) static_cast<T *>(a.h)[row * a.D + c] = from_f32<T>(v * r2 * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f));
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) block_norm_wide_bwd_kernel(const BlockNormArgs a) {
+    __shared__ float red[2][32];
+    const float inv_d = 1.f / (float)a.D;
+    int phase = 0;
+    float *pp = a.partial ? a.partial + 2ll * blockIdx.x * a.D : nullptr;
+    grid_dependency_wait();
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T *y = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
+        const T *z = a.gate ? static_cast<const T *>(a.z.p) + row_at(a, a.z, row) : nullptr;
+        const T *dx = a.dx.p ? static_cast<const T *>(a.dx.p) + row_at(a, a.dx, row) : nullptr;
+        const T *dh = a.pre ? static_cast<const T *>(a.dh.p) + row_at(a, a.dh, row) : nullptr;
+        const T *x = a.pre ? static_cast<const T *>(a.r.p) + row_at(a, a.r, row) : nullptr;
+        const float rp = a.post ? a.rstd_post[row] : 1.f, rn = a.pre ? a.rstd_pre[row] : 1.f;
+        float m = 0.f, q = 0.f;
+        if (a.pre) {
+            for (int c = threadIdx.x; c < a.D; c += 1024)
+                q = fmaf(to_f32(dh[c]) * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f), to_f32(x[c]) * rn, q);
+            m = row_sum<1024>(q, red, phase) * inv_d;
+        }
+        struct One { float d, yh, e, dz, p, q; };
+        auto value = [&](int c) {
+            One o = {};
+            o.d = dx ? to_f32(dx[c]) : 0.f;
+            if (a.pre) {
+                const float xh = to_f32(x[c]) * rn, g = to_f32(dh[c]);
+                o.q = g * xh;
+                o.d += rn * (g * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f) - xh * m);
+            }
+            o.yh = to_f32(y[c]) * rp;
+            float act = 1.f, slope = 0.f;
+            if (a.gate) {
+                const float zz = to_f32(z[c]), s = sigmoid_f32(zz);
+                act = a.gate == 1 ? zz * s : s;
+                slope = a.gate == 1 ? fmaf(act, 1.f - s, s) : s * (1.f - s);
+            }
+            float dc = o.d;
+            if (a.w_post) dc *= param_at(a.w_post, c, a.w_f32);
+            if (a.scale) dc *= param_at(a.scale, c, a.w_f32);
+            o.p = o.d * act * o.yh, o.dz = dc * o.yh * slope, o.e = dc * act;
+            return o;
+        };
+        float m2 = 0.f;
+        if (a.post) {
+            q = 0.f;
+            for (int c = threadIdx.x; c < a.D; c += 1024) {
+                const One o = value(c);
+                q = fmaf(o.e, o.yh, q);
+            }
+            m2 = row_sum<1024>(q, red, phase) * inv_d;
+        }
+        for (int c = threadIdx.x; c < a.D; c += 1024) {
+            const One o = value(c);
+            if (a.dr) static_cast<T *>(a.dr)[row * a.D + c] = from_f32<T>(o.d);
+            if (a.gate) static_cast<T *>(a.dz)[row * a.D + c] = from_f32<T>(o.dz);
+            static_cast<T *>(a.dy)[row * a.D + c] = from_f32<T>(rp * (o.e - o.yh * m2));
+            if (pp) {
+                const bool first = row == blockIdx.x;
+                pp[c] = (first ? 0.f : pp[c]) + o.p;
+                pp[a.D + c] = (first ? 0.f : pp[a.D + c]) + o.q;
+            }
+        }
+    }
+}
+
+// The blocks' partial rows added in their order (32 groups of rows of blocks, then the
+// groups), and the parameters' gradients from the sums.
+__global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const BlockNormArgs a, int blocks, float *dpost, float *dscale,
+                                                                 float *dpre) {
+    __shared__ float sum[32][33];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    grid_dependency_wait();
+    if (c < a.D) {
+        const float *p = a.partial + (long long)blockIdx.y * a.D + c;
+#pragma unroll 8
+        for (int r = grp; r < blocks; r += 32) s += p[2ll * r * a.D];
+    }
+    sum[grp][lane] = s;
+    __syncthreads();
+    if (grp != 0 || c >= a.D) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += sum[i][lane];
+    if (blockIdx.y) {
+        if (dpre) dpre[c] = s;
+    } else {
+        if (dpost) dpost[c] = a.scale ? s * param_at(a.scale, c, a.w_f32) : s;
+        if (dscale) dscale[c] = a.w_post ? s * param_at(a.w_post, c, a.w_f32) : s;
+    }
+}
+
+constexpr int kBnMaxCols = 8192;
+
+// Calls f<TPR, EPT>: the threads of a row and the columns of each by the row's length.
+template <typename F>
+auto by_columns(int D, F f) {
+    if (D <= 64) return f.template operator()<8, 8>();
+    if (D <= 128) return f.template operator()<16, 8>();
+    if (D <= 256) return f.template operator()<32, 8>();
+    if (D <= 512) return f.template operator()<32, 16>();
+    if (D <= 1024) return f.template operator()<128, 8>();
+    if (D <= 2048) return f.template operator()<256, 8>();
+    if (D <= 4096) return f.template operator()<256, 16>();
+    return f.template operator()<512, 16>();
+}
+
+template <typename T, bool BWD, bool VECTORS>
+struct Shape {
+    long long rows;
+    template <int TPR, int EPT>
+    int operator()() const {   // blocks of the persistent grid
+        constexpr int VEC = VECTORS ? 16 / (int)sizeof(T) : 1;
+        using St = BnStages<T, TPR, VEC, EPT / VEC, BWD ? 5 : 3>;
+        constexpr int rpb = bn_threads(TPR) / TPR;
+        return (int)std::min<long long>((rows + rpb - 1) / rpb, (long long)device_sm_count() * St::blocks);
+    }
+};
+template <typename T, bool BWD, bool VECTORS>
+struct Launch {
+    const BlockNormArgs &a;
+    int grid;
+    cudaStream_t s;
+    template <int TPR, int EPT>
+    cudaError_t operator()() const {
+        constexpr int VEC = VECTORS ? 16 / (int)sizeof(T) : 1;
+        constexpr int NV = EPT / VEC, smem = BnStages<T, TPR, VEC, NV, BWD ? 5 : 3>::smem;
+        void (*kernel)(const BlockNormArgs);
+        if constexpr (BWD) kernel = block_norm_bwd_kernel<T, TPR, VEC, NV>;
+        else kernel = block_norm_fwd_kernel<T, TPR, VEC, NV>;
+        if (smem > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_dependent(kernel, dim3(grid), dim3(bn_threads(TPR)), smem, s, a);
+    }
+};
+
+template <typename T, bool BWD>
+int grid_of(long long rows, int D, bool vec) {
+    if (D > kBnMaxCols) return (int)std::min<long long>(rows, device_sm_count());
+    return vec ? by_columns(D, Shape<T, BWD, true>{rows}) : by_columns(D, Shape<T, BWD, false>{rows});
+}
+int bwd_grid(long long rows, int D, int dtype, bool vec) {
+    return dtype == GDN_BF16 ? grid_of<__nv_bfloat16, true>(rows, D, vec) : grid_of<float, true>(rows, D, vec);
+}
+
+template <typename T, bool BWD>
+cudaError_t launch_rows(const BlockNormArgs &a, bool vec, cudaStream_t s) {
+    const int grid = grid_of<T, BWD>(a.rows, a.D, vec);
+    if (a.D > kBnMaxCols) {
+        void (*wide)(const BlockNormArgs);
+        if constexpr (BWD) wide = block_norm_wide_bwd_kernel<T>;
+        else wide = block_norm_wide_fwd_kernel<T>;
+        return launch_dependent(wide, dim3(grid), dim3(1024), 0, s, a);
+    }
+    return vec ? by_columns(a.D, Launch<T, BWD, true>{a, grid, s}) : by_columns(a.D, Launch<T, BWD, false>{a, grid, s});
+}
+
+bool bn_elem_aligned(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == GDN_F32 ? 3u : 1u)) == 0; }
+
+gdn_status bn_args(const gdn_block_norm_desc *d, BlockNormArgs &a) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    if (d->outer < 0 || d->inner < 1 || d->D < 1 || !(d->eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+    if ((d->dtype != GDN_BF16 && d->dtype != GDN_F32) || (d->w_dtype != GDN_BF16 && d->w_dtype != GDN_F32)) return GDN_ERR_INVALID_ARG;
+    if (d->w_dtype == GDN_BF16 && d->dtype == GDN_F32) return GDN_ERR_INVALID_ARG;
+    if (d->gate_activation != GDN_GATE_SILU && d->gate_activation != GDN_GATE_SIGMOID) return GDN_ERR_INVALID_ARG;
+    // rows are counted in 32 bits, columns too
+    if (d->D > (1 << 30) || d->inner > 0x7fffffff || (d->outer > 0 && d->inner > 0x7fffffff / d->outer)) return GDN_ERR_UNSUPPORTED;
+    if (!d->post_norm && d->post_weight) return GDN_ERR_INVALID_ARG;
+    if (!d->pre_norm && d->pre_weight) return GDN_ERR_INVALID_ARG;
+    for (const void *p : {d->post_weight, d->scale, d->pre_weight})
+        if (!bn_elem_aligned(p, d->w_dtype)) return GDN_ERR_INVALID_ARG;
+    a = {};
+    a.y = {d->y, d->y_outer_stride, d->y_inner_stride};
+    a.z = {d->gate, d->gate_outer_stride, d->gate_inner_stride};
+    a.w_post = d->post_weight, a.scale = d->scale, a.w_pre = d->pre_weight;
+    a.rows = d->outer * d->inner, a.D = (int)d->D, a.w_f32 = d->w_dtype == GDN_F32, a.eps = d->eps;
+    a.post = d->post_norm != 0, a.pre = d->pre_norm != 0;
+    a.gate = d->gate ? (d->gate_activation == GDN_GATE_SILU ? 1 : 2) : 0;
+    a.inner = (uint32_t)d->inner;
+    if (a.inner > 1) {   // n / inner = (umulhi(magic, n) + n) >> shift for n < 2^31
+        uint32_t l = 0;
+        while ((1ull << l) < a.inner) ++l;
+        a.shift = l;
+        a.magic = (uint32_t)((((1ull << l) - a.inner) << 32) / a.inner + 1);
+    }
+    return GDN_OK;
+}
+// Strides: rows may not overlap (a single row, or a single one per outer row, has none).
+bool bn_view_ok(const gdn_block_norm_desc &d, const void *p, int64_t so, int64_t si) {
+    if (!bn_elem_aligned(p, d.dtype)) return false;
+    return (d.inner <= 1 || si >= d.D) && (d.outer <= 1 || so >= d.D);
+}
+bool bn_view_vec(const gdn_block_norm_desc &d, const void *p, int64_t so, int64_t si) {
+    const int v = d.dtype == GDN_F32 ? 4 : 8;
+    return aligned16(p) && (d.inner <= 1 || si % v == 0) && (d.outer <= 1 || so % v == 0);
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" gdn_status gdn_block_norm_fwd(const gdn_block_norm_desc *desc, const void *residual, int64_t r_outer_stride,
+                                         int64_t r_inner_stride, void *x, void *h, float *rstd_post, float *rstd_pre,
+                                         gdn_stream_t stream) {
+    using namespace gdn;
+    BlockNormArgs a;
+    const gdn_status st = bn_args(desc, a);
+    if (st != GDN_OK) return st;
+    const gdn_block_norm_desc &d = *desc;
+    if (a.rows == 0) return GDN_OK;
+    if (!d.y || !x || !bn_elem_aligned(x, d.dtype) || !bn_elem_aligned(h, d.dtype) || !bn_elem_aligned(rstd_post, GDN_F32) ||
+        !bn_elem_aligned(rstd_pre, GDN_F32) || (a.pre && (!h || !rstd_pre)) || (a.post && !rstd_post))
+        return GDN_ERR_INVALID_ARG;
+    if (!bn_view_ok(d, d.y, a.y.so, a.y.si) || (a.gate && !bn_view_ok(d, d.gate, a.z.so, a.z.si)) ||
+        (residual && !bn_view_ok(d, residual, r_outer_stride, r_inner_stride)))
+        return GDN_ERR_INVALID_ARG;
+    a.r = {residual, r_outer_stride, r_inner_stride};
+    a.res = residual != nullptr;
+    a.x = x, a.h = h, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
+    const bool vec = d.D % (d.dtype == GDN_F32 ? 4 : 8) == 0 && bn_view_vec(d, d.y, a.y.so, a.y.si) &&
+                     (!a.gate || bn_view_vec(d, d.gate, a.z.so, a.z.si)) && (!a.res || bn_view_vec(d, residual, r_outer_stride, r_inner_stride)) &&
+                     aligned16(x) && (!a.pre || aligned16(h));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = d.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16, false>(a, vec, s) : launch_rows<float, false>(a, vec, s);
+    if (e != cudaSuccess) {
+        set_error_detail("launch block_norm_fwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+extern "C" size_t gdn_block_norm_bwd_workspace_size(const gdn_block_norm_desc *desc) {
+    using namespace gdn;
+    BlockNormArgs a;
+    if (bn_args(desc, a) != GDN_OK) return 0;
+    // alignment is not known here: the larger of both grids
+    const int grid = std::max(bwd_grid(a.rows, a.D, desc->dtype, true), bwd_grid(a.rows, a.D, desc->dtype, false));
+    return std::max<size_t>(16, (size_t)grid * 2 * (size_t)a.D * sizeof(float));
+}
+
+extern "C" gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const void *dx, int64_t dx_outer_stride,
+                                         int64_t dx_inner_stride, const void *dh, int64_t dh_outer_stride,
+                                         int64_t dh_inner_stride, const void *x, int64_t x_outer_stride,
+                                         int64_t x_inner_stride, const float *rstd_post, const float *rstd_pre, void *dy,
+                                         void *dresidual, void *dgate, float *dpost_weight, float *dscale,
+                                         float *dpre_weight, void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    using namespace gdn;
+    BlockNormArgs a;
+    const gdn_status st = bn_args(desc, a);
+    if (st != GDN_OK) return st;
+    const gdn_block_norm_desc &d = *desc;
+    for (const float *p : {dpost_weight, dscale, dpre_weight, (float *)rstd_post, (float *)rstd_pre})
+        if (!bn_elem_aligned(p, GDN_F32)) return GDN_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)dy, (const void *)dresidual, (const void *)dgate})
+        if (!bn_elem_aligned(p, d.dtype)) return GDN_ERR_INVALID_ARG;
+    const bool params = dpost_weight || dscale || dpre_weight;
+    bool vec = false;
+    if (a.rows > 0) {
+        if (!d.y || !dy || (a.post && !rstd_post) || (a.pre && (!rstd_pre || !dh || !x)) || (!a.pre && !dx) || (a.gate && !dgate))
+            return GDN_ERR_INVALID_ARG;
+        if (!bn_view_ok(d, d.y, a.y.so, a.y.si) || (a.gate && !bn_view_ok(d, d.gate, a.z.so, a.z.si)) ||
+            (dx && !bn_view_ok(d, dx, dx_outer_stride, dx_inner_stride)) ||
+            (a.pre && (!bn_view_ok(d, dh, dh_outer_stride, dh_inner_stride) || !bn_view_ok(d, x, x_outer_stride, x_inner_stride))))
+            return GDN_ERR_INVALID_ARG;
+        if (params) {
+            if (!workspace || !aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+            if (workspace_bytes < gdn_block_norm_bwd_workspace_size(desc)) return GDN_ERR_WORKSPACE;
+        }
+        a.dx = {dx, dx_outer_stride, dx_inner_stride};
+        a.dh = {dh, dh_outer_stride, dh_inner_stride};
+        a.r = {x, x_outer_stride, x_inner_stride};
+        a.dy = dy, a.dr = dresidual, a.dz = dgate;
+        a.rstd_post = const_cast<float *>(rstd_post), a.rstd_pre = const_cast<float *>(rstd_pre);
+        a.partial = params ? static_cast<float *>(workspace) : nullptr;
+        vec = d.D % (d.dtype == GDN_F32 ? 4 : 8) == 0 && bn_view_vec(d, d.y, a.y.so, a.y.si) &&
+              (!a.gate || (bn_view_vec(d, d.gate, a.z.so, a.z.si) && aligned16(dgate))) &&
+              (!dx || bn_view_vec(d, dx, dx_outer_stride, dx_inner_stride)) &&
+              (!a.pre || (bn_view_vec(d, dh, dh_outer_stride, dh_inner_stride) && bn_view_vec(d, x, x_outer_stride, x_inner_stride))) &&
+              aligned16(dy) && aligned16(dresidual);
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (a.rows > 0) e = d.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16, true>(a, vec, s) : launch_rows<float, true>(a, vec, s);
+    if (e == cudaSuccess && params) {   // no rows: the sums are zero
+        const int blocks = a.rows > 0 ? bwd_grid(a.rows, a.D, d.dtype, vec) : 0;
+        e = launch_dependent(block_norm_reduce_kernel, dim3((a.D + 31) / 32, 2), dim3(1024), 0, s, a, blocks, dpost_weight, dscale, dpre_weight);
+    }
+    if (e != cudaSuccess) {
+        set_error_detail("launch block_norm_bwd", e);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}

@@ -705,6 +705,56 @@ gdn_status gdn_delta_step(const void *q, int64_t q_stride, const void *k, int64_
                           int dk, int dv, gdn_dtype dtype, void *o, gdn_stream_t stream);
 
 /*
+ * Block norm: what lies between two blocks of a layer, over rows of D elements,
+ *
+ *     n = y rstd_post w_post   (post_norm; else n = y),  rstd_post = (mean y^2 + eps)^-1/2,
+ *     x = residual + scale n a(gate),                    a = SiLU or sigmoid,
+ *     h = x rstd_pre w_pre     (pre_norm),               rstd_pre = (mean x^2 + eps)^-1/2.
+ *
+ * The rows are [outer][inner] (heads of a token are inner rows; inner = 1: plain
+ * rows), outer inner < 2^31, with a stride for each level; outputs are contiguous.
+ * gate, residual (no gate, no residual), the weights and scale ([D] in w_dtype, fp32 or
+ * dtype; one) may be NULL.  x, h: [rows, D] in dtype; rstd_post, rstd_pre: fp32 [rows],
+ * needed with their norm.  h and rstd_pre are of x before it is rounded.  x or h may be
+ * the memory of y, gate or residual itself where that is contiguous.
+ */
+typedef enum { GDN_GATE_SILU = 0, GDN_GATE_SIGMOID = 1 } gdn_gate;
+typedef struct {
+    const void *y, *gate, *post_weight, *scale, *pre_weight;
+    int64_t outer, inner, D;
+    int64_t y_outer_stride, y_inner_stride, gate_outer_stride, gate_inner_stride;
+    float eps;
+    int32_t post_norm, pre_norm, gate_activation, dtype, w_dtype;
+} gdn_block_norm_desc;
+
+gdn_status gdn_block_norm_fwd(const gdn_block_norm_desc *desc, const void *residual, int64_t r_outer_stride,
+                              int64_t r_inner_stride, void *x, void *h, float *rstd_post, float *rstd_pre,
+                              gdn_stream_t stream);
+
+/*
+ * Its backward pass, from dx (the gradient of x beside h's; NULL: zero, with pre_norm
+ * only), dh and x (with pre_norm; NULL else), and the forward pass's rstd: with g = dh
+ * w_pre, xh = x rstd_pre, yh = y rstd_post,
+ *
+ *     d = dx + rstd_pre (g - xh mean(g xh)),   dresidual = d,   dgate = d scale n a'(gate),
+ *     dy = rstd_post (e - yh mean(e yh)),      e = d scale a(gate) w_post,
+ *     dpre_weight = sum dh xh,  dpost_weight = scale sum d a yh,  dscale = sum d a n.
+ *
+ * dy, dgate (with a gate), dresidual (may be NULL) in dtype, contiguous; the
+ * parameters' gradients fp32 [D], each may be NULL.  The workspace (16-byte aligned,
+ * gdn_block_norm_bwd_workspace_size() bytes) is needed for those only.  The same
+ * inputs give the same bits.  dresidual or dy may be the memory of dx, dh or x, and
+ * dgate that of gate.
+ */
+size_t gdn_block_norm_bwd_workspace_size(const gdn_block_norm_desc *desc);
+gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const void *dx, int64_t dx_outer_stride,
+                              int64_t dx_inner_stride, const void *dh, int64_t dh_outer_stride, int64_t dh_inner_stride,
+                              const void *x, int64_t x_outer_stride, int64_t x_inner_stride, const float *rstd_post,
+                              const float *rstd_pre, void *dy, void *dresidual, void *dgate, float *dpost_weight,
+                              float *dscale, float *dpre_weight, void *workspace, size_t workspace_bytes,
+                              gdn_stream_t stream);
+
+/*
  * Gated feed-forward block over M rows:
  *
  *     g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T,
