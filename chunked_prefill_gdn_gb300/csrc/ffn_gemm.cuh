@@ -1,6 +1,6 @@
 // The matrix products of the gated feed-forward block: one persistent tcgen05
 // kernel, out = sum over K of A B^T, with the block's elementwise parts in its
-// epilogue.
+// epilogue, for up to four products in one launch.
 //
 // Operands are bf16 in memory, [rows][K] (K-major) or [K][rows] (MN-major, for
 // the products that sum over rows of what is stored), read by TMA into tiles with
@@ -9,12 +9,16 @@
 // the six terms x_i y_j with i + j <= 2 (the three left out are below 2^-24),
 // smallest first.
 //
-// A tile is 128 rows x 256 columns per CTA; with CTAS = 2 two CTAs form a pair
+// A tile is 128 rows x BN columns per CTA; with CTAS = 2 two CTAs form a pair
 // (cta_group::2) of 256 x 256, each holding its own 128 rows of A and half of B,
-// which halves what B costs in L2 and shared memory.  The accumulators are in
-// tensor memory, two sets of 256 columns, so that the epilogue of one tile runs
-// under the products of the next.  Warps: 0 loads, 1 issues the products, 2 to 9
-// are the epilogue (two warps per quarter of the lanes, half of the columns each).
+// which halves what B costs in L2 and shared memory.  Single CTAs of 128 columns run
+// two to an SM, for few rows (bound by the weights' bytes) and for small products.
+// The accumulators are in tensor memory, two sets of BN columns, so that the epilogue
+// of one tile runs under the products of the next.  Warps: 0 loads, 1 issues the
+// products, the others are the epilogue, a quarter of the lanes and CW columns each.
+// Its bf16 outputs leave through two boxes per warp in shared memory by TMA stores;
+// the backward pass's gate and up come into the same boxes by TMA loads that run
+// under the products.
 //
 // With PROMOTE (fp32) the tensor cores sum only kPromote blocks of K at a time;
 // those sums are added in registers, in fp32 with rounding to nearest.
@@ -33,27 +37,34 @@ namespace ffn {
 
 enum Epi { kUp = 0, kBack = 1, kPlain = 2 };
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
-constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kTileM = 128, kBlockK = 64;
 constexpr int kPromote = 8;   // blocks of 64 along K per sum in tensor memory (fp32)
+constexpr int kMaxStages = 7, kMaxGroups = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-struct GemmArgs {
-    CUtensorMap a[2], b[2], c[3];
-    int M, N;                 // outputs of a group (kUp: N = F, half a tile's columns)
-    int mt, nt, groups;       // tiles per group, groups (a[g] and out[g], one b)
-    int kb, pairs, splits;    // K blocks of one (a[p], b[p]) pair; pairs summed up; parts of that sum
-    int terms;                // 1, or 6 for three planes
-    int a_mn, b_mn, dual;     // dual: the tile's column halves come from b[0] and b[1]
-    int tma_out, vec_out, vec_io, act;
-    void *out[2];             // kPlain: [M, N] per group
+// One product of the launch: out = sum over its pairs of A B^T.
+struct Group {
+    int M, N;                 // outputs (kUp: N = F, half a tile's columns)
+    int mt, nt;               // tiles
+    int kb, pairs, splits;    // K blocks of a pair of operands; pairs summed up; parts of that sum
+    int a, b, c;              // first of its maps
+    int a_mn, b_mn, tma_out, vec_out;
+    void *out;                // kPlain: [M, N], rows ld_out apart
     long long ld_out;
-    __nv_bfloat16 *planes[3]; // kUp: h; kBack: dgate, dup, h: three planes each (fp32)
-    long long ld_plane, plane_stride;
-    void *gate, *up;          // kUp: outputs or null; kBack: inputs
-    long long ld_io;
-    float *partial;           // splits > 1: [split][dual ? 2 : groups][M][ld_part]
+    float *partial;           // splits > 1: [split][kUp ? 2 : 1][M][ld_part]
     long long ld_part;
+};
+struct GemmArgs {
+    CUtensorMap a[kMaxGroups + 1], b[kMaxGroups + 1], c[kMaxGroups], io[2];   // one product may have two pairs
+    Group group[kMaxGroups];
+    int groups, dual;         // dual: the tile's column halves come from b[0] and b[1]
+    // the schedule: units [0, first) are group 0's, the others follow; see item_of
+    int first, rest, ratio;
+    int terms;                // 1, or 6 for three planes
+    int act, tma_io, vec_io;
+    __nv_bfloat16 *planes[3]; // kUp: h; kBack: dgate, dup, h: one plane (bf16) or three (fp32)
+    long long ld_plane, plane_stride;
+    void *gate, *up;          // kUp: outputs or null; kBack: inputs; contiguous
     int *err;
 };
 
@@ -143,63 +154,98 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
     else
         tc::tc_commit(bar);
 }
-template <int CTAS>
-__device__ __forceinline__ void tmem_alloc_all(uint32_t *dst) {
+template <int CTAS, int COLS>
+__device__ __forceinline__ void tmem_get(uint32_t *dst) {
     if constexpr (CTAS == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(dst)), "n"(COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     } else {
-        tc::tmem_alloc(dst, 512);
+        tc::tmem_alloc(dst, COLS);
         tc::tmem_relinquish();
     }
 }
-template <int CTAS>
-__device__ __forceinline__ void tmem_free_all(uint32_t addr) {
+template <int CTAS, int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t addr) {
     if constexpr (CTAS == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "n"(COLS) : "memory");
     else
-        tc::tmem_dealloc(addr, 512);
+        tc::tmem_dealloc(addr, COLS);
+}
+template <int LATER>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LATER) : "memory");
 }
 
-template <int CTAS>
+template <typename T, int CTAS, int BN>
 struct Shape {
-    static constexpr int b_rows = kTileN / CTAS;                 // of B in this CTA
-    static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128;
-    static constexpr int stage = a_bytes + b_bytes;              // 32 or 48 KB
-    static constexpr int stages = CTAS == 2 ? 6 : 4;
-    static constexpr int epi = kEpiWarps * 4096;
-    static constexpr int smem = 1024 + stages * stage + epi;     // 1024: alignment
+    static constexpr bool promote = sizeof(T) == 4;
+    // fp32 keeps its sums in registers: 64 columns per warp; else 128
+    static constexpr int CW = promote ? 64 : 128, epi_warps = BN * 4 / CW, threads = 64 + 32 * epi_warps;
+    static constexpr int b_rows = BN / CTAS;                     // of B in this CTA
+    static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128, stage = a_bytes + b_bytes;
+#ifndef FFN_STAGES
+#define FFN_STAGES 5
+#define FFN_BOXES 2
+#endif
+    static constexpr int boxes = promote || BN == 128 ? 0 : CTAS == 2 ? FFN_BOXES : 2;   // per warp
+    static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? FFN_STAGES : promote ? 4 : 3;
+    static constexpr int smem = 1024 + stages * stage + epi_warps * boxes * 4096;   // 1024: alignment
+    static constexpr int per_sm = BN == 128 ? 2 : 1;
+    static_assert(stages <= kMaxStages && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
 };
 
 struct Barriers {
-    uint64_t full[6], empty[6], tmem_full[2], tmem_empty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], tmem_full[2], tmem_empty[2], in[16];
     uint32_t tmem;
     int abort;
 };
 
 // One part of the work: a tile and a range of blocks along K.
 struct Item {
-    int m, n, group, split, q0, q1;   // tile coordinates; blocks [q0, q1) of pairs * kb
+    int group, m, n, split, q0, q1;   // tile coordinates; blocks [q0, q1) of pairs * kb
 };
-// Tiles in columns of eight rows of tiles, so that the tiles at work at one time
-// share what they read in L2.
+// The i-th unit of worker p of P, or none (false).  Group 0's units (`first`) are the
+// longest and are dealt out in turn; the workers that get one less take `ratio` units of
+// the others instead, which are then dealt out in turn too.  Within a group the tiles go
+// in bands of 16 rows of tiles of 128, so that what is at work at one time shares what it
+// reads in L2.
 template <int CTAS>
-__device__ __forceinline__ Item item_of(const GemmArgs &g, int w) {
-    Item it;
-    it.split = w % g.splits;
-    w /= g.splits;
-    const int per = g.mt * g.nt;
-    it.group = w / per;
-    w -= it.group * per;
+__device__ __forceinline__ bool item_of(const GemmArgs &g, int p, int P, int i, Item &it) {
+    const int extra = g.first % P, mine = (g.first - p + P - 1) / P, behind = extra ? P - extra : 0;
+    int w;
+    if (i < mine) {
+        w = p + i * P;
+    } else {
+        i -= mine;
+        if (extra && p >= extra) {
+            w = i < g.ratio ? i * behind + (p - extra) : g.ratio * behind + p + (i - g.ratio) * P;
+        } else {
+            w = g.ratio * behind + p + i * P;
+        }
+        if (w >= g.rest) return false;
+        w += g.first;
+    }
+    int grp = 0;
+    while (true) {
+        const Group &q = g.group[grp];
+        const int units = q.mt * q.nt * q.splits;
+        if (w < units) break;
+        w -= units;
+        ++grp;
+    }
+    const Group &q = g.group[grp];
+    it.group = grp;
+    it.split = w % q.splits;
+    w /= q.splits;
     constexpr int GM = 16 / CTAS;
-    const int band = w / (GM * g.nt), first = band * GM, rows = min(GM, g.mt - first);
-    w -= band * GM * g.nt;
+    const int band = w / (GM * q.nt), first = band * GM, rows = min(GM, q.mt - first);
+    w -= band * GM * q.nt;
     it.m = first + w % rows;
     it.n = w / rows;
-    const int q = g.kb * g.pairs;
-    it.q0 = (int)((long long)q * it.split / g.splits);
-    it.q1 = (int)((long long)q * (it.split + 1) / g.splits);
-    return it;
+    const int blocks = q.kb * q.pairs;
+    it.q0 = (int)((long long)blocks * it.split / q.splits);
+    it.q1 = (int)((long long)blocks * (it.split + 1) / q.splits);
+    return true;
 }
 // Terms of a product of three planes by three, smallest first.
 __device__ __forceinline__ void term_planes(int terms, int t, int &pa, int &pb) {
@@ -208,50 +254,71 @@ __device__ __forceinline__ void term_planes(int terms, int t, int &pa, int &pb) 
     pb = (0x010210 >> (4 * t)) & 15;   //           0 1 2 0 1 0
 }
 
-// 32 neighbouring columns of a row in type T, `live` of which exist.
-template <typename T>
-__device__ __forceinline__ void store32(T *p, const float *v, int live, bool vec) {
-    constexpr int E = 16 / (int)sizeof(T);
-    if (vec && live >= 32) {
+// E neighbouring columns of a row in type T, `live` of which exist.
+template <typename T, int E>
+__device__ __forceinline__ void store_cols(T *p, const float *v, int live, bool vec) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (vec && live >= E) {
 #pragma unroll
-        for (int i = 0; i < 32 / E; ++i) store_raw<T, E>(p + i * E, pack<T, E>(v + i * E));
+        for (int i = 0; i < E / V; ++i) store_raw<T, V>(p + i * V, pack<T, V>(v + i * V));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < E; ++i)
             if (i < live) p[i] = from_f32<T>(v[i]);
     }
 }
-template <typename T>
-__device__ __forceinline__ void load32(const T *p, float *v, int live, bool vec) {
-    constexpr int E = 16 / (int)sizeof(T);
-    if (vec && live >= 32) {
-        Raw<T, E> r[32 / E];
+template <typename T, int E>
+__device__ __forceinline__ void load_cols(const T *p, float *v, int live, bool vec) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (vec && live >= E) {
+        Raw<T, V> r[E / V];
 #pragma unroll
-        for (int i = 0; i < 32 / E; ++i) r[i] = load_raw<T, E>(p + i * E);
+        for (int i = 0; i < E / V; ++i) r[i] = load_raw<T, V>(p + i * V);
 #pragma unroll
-        for (int i = 0; i < 32 / E; ++i) unpack<T, E>(r[i], v + i * E);
+        for (int i = 0; i < E / V; ++i) unpack<T, V>(r[i], v + i * V);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < live ? to_f32(p[i]) : 0.f;
+        for (int i = 0; i < E; ++i) v[i] = i < live ? to_f32(p[i]) : 0.f;
+    }
+}
+// E columns into one plane (bf16) or three (fp32); ld is a multiple of 8, so whole
+// vectors lie in the row.
+template <typename T, int E>
+__device__ __forceinline__ void store_planes(__nv_bfloat16 *p, long long stride, const float *v, int live) {
+    if constexpr (sizeof(T) == 2) {
+        store_cols<__nv_bfloat16, E>(p, v, live, true);
+    } else {
+        float s[3][E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float t[3];
+            split3(v[e], t);
+            s[0][e] = t[0], s[1][e] = t[1], s[2][e] = t[2];
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) store_cols<__nv_bfloat16, E>(p + k * stride, s[k], live, true);
     }
 }
 
-template <int EPI, typename T, int CTAS>
-__global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_constant__ GemmArgs g) {
-    using S = Shape<CTAS>;
-    constexpr bool PROMOTE = sizeof(T) == 4;
+template <int EPI, typename T, int CTAS, int BN>
+__global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN>::per_sm)
+    ffn_gemm_kernel(const __grid_constant__ GemmArgs g) {
+    using S = Shape<T, CTAS, BN>;
+    constexpr bool PROMOTE = S::promote, BOXES = S::boxes > 0;
+    constexpr int CW = S::CW, E = PROMOTE ? 16 : 32;   // columns of a step of the epilogue
     extern __shared__ uint8_t raw[];
     __shared__ Barriers bars;
     uint8_t *smem = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::stages; ++i) tc::mbar_init(&bars.full[i], 1), tc::mbar_init(&bars.empty[i], 1);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.tmem_full[i], 1), tc::mbar_init(&bars.tmem_empty[i], kEpiWarps * CTAS);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.tmem_full[i], 1), tc::mbar_init(&bars.tmem_empty[i], S::epi_warps * CTAS);
+        for (int i = 0; i < 16; ++i) tc::mbar_init(&bars.in[i], 1);
         bars.abort = 0;
         tc::fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc_all<CTAS>(&bars.tmem);
+    if (warp == 1) tmem_get<CTAS, 2 * BN>(&bars.tmem);
     tc::tc_fence_before();
     __syncthreads();
     if constexpr (CTAS == 2) cluster_sync_all();
@@ -265,303 +332,365 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
         return false;
     };
     grid_dependency_wait();
-    const int work = g.groups * g.mt * g.nt * g.splits;
-    const int step = gridDim.x / CTAS;
+    const int P = gridDim.x / CTAS, p = blockIdx.x / CTAS;
     const int chunk = PROMOTE ? kPromote : 1 << 30;
+    Item i;
 
+    // Loads and products are issued by one lane, but the whole warp goes through their
+    // loops: what it decides on is then the warp's, and stays in uniform registers (with
+    // only one lane in the loops the copies were issued at half the rate).
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            asm volatile("fence.proxy.async;" ::: "memory");   // what earlier kernels stored is read by TMA
-            for (int w = blockIdx.x / CTAS; ok && w < work; w += step) {
-                const Item i = item_of<CTAS>(g, w);
-                const int row = (i.m * CTAS + (int)rank) * kTileM;
-                const int ncol = g.dual ? i.n * (kTileN / 2) : i.n * kTileN + (int)rank * S::b_rows;
-                for (int c0 = i.q0; ok && c0 < i.q1; c0 += chunk) {
-                    const int c1 = min(c0 + chunk, i.q1);
-                    if (c1 < c0) break;
-                    for (int t = 0; ok && t < g.terms; ++t) {
-                        int pa, pb;
-                        term_planes(g.terms, t, pa, pb);
-                        for (int q = c0; q < c1; ++q, ++it) {
-                            const uint32_t s = it % S::stages, round = it / S::stages;
-                            if (round > 0 && !wait(&bars.empty[s], (round - 1) & 1)) { ok = false; break; }
-                            const int pair = q >= g.kb ? 1 : 0, k = (q - pair * g.kb) * kBlockK;
-                            const CUtensorMap *ma = &g.a[g.groups > 1 ? i.group : pair];
-                            const uint32_t at = tc::smem_u32(smem) + s * S::stage, bt = at + S::a_bytes;
-                            uint32_t bar = tc::smem_u32(&bars.full[s]);
+        const bool leader = tc::elect_one();
+        uint32_t s = 0, turn = 0, loads = 0;   // the stage, the parity of its rounds
+        bool ok = true;
+        const uint32_t base = tc::smem_u32(smem);
+        uint32_t full0 = tc::smem_u32(&bars.full[0]);
+        if constexpr (CTAS == 2) full0 = map_to_cta(full0, 0);
+        asm volatile("fence.proxy.async;" ::: "memory");   // what earlier kernels stored is read by TMA
+        const bool dual = g.dual;
+        const int terms = g.terms;
+        for (int k = 0; ok && item_of<CTAS>(g, p, P, k, i); ++k) {
+            const Group &gr = g.group[i.group];
+            const bool a_mn = gr.a_mn, b_mn = gr.b_mn;
+            const int row = (i.m * CTAS + (int)rank) * kTileM, kb = gr.kb, a0 = gr.a, b0 = gr.b;
+            const int ncol = dual ? i.n * (BN / 2) : i.n * BN + (int)rank * S::b_rows;
+            for (int c0 = i.q0; ok && c0 < i.q1; c0 += chunk) {
+                const int c1 = min(c0 + chunk, i.q1);
+                if (c1 < c0) break;
+                for (int t = 0; ok && t < terms; ++t) {
+                    int pa, pb;
+                    term_planes(terms, t, pa, pb);
+                    for (int q = c0; q < c1; ++q) {
+                        ok = warp_wait(&bars.empty[s], turn ^ 1);
+                        if (!ok) break;
+                        const int second = q >= kb ? 1 : 0, kc = (q - second * kb) * kBlockK;
+                        const CUtensorMap *ma = &g.a[a0 + second], *mb = &g.b[b0 + (dual && CTAS == 2 ? (int)rank : second)];
+                        const uint32_t at = base + s * S::stage, bt = at + S::a_bytes, bar = full0 + s * 8;
+                        if (leader) {
                             if (CTAS == 1 || rank == 0) tc::mbar_arrive_expect_tx(&bars.full[s], S::stage * CTAS);
-                            if constexpr (CTAS == 2) bar = map_to_cta(bar, 0);
-                            if (g.a_mn) {
-                                for (int j = 0; j < kTileM / 64; ++j) load_box<CTAS>(at + j * 8192, ma, bar, row + j * 64, k, pa);
+                            if (a_mn) {
+#pragma unroll
+                                for (int j = 0; j < kTileM / 64; ++j) load_box<CTAS>(at + j * 8192, ma, bar, row + j * 64, kc, pa);
                             } else {
-                                load_box<CTAS>(at, ma, bar, k, row, pa);
+                                load_box<CTAS>(at, ma, bar, kc, row, pa);
                             }
-                            if (g.dual) {
-                                if constexpr (CTAS == 2) {
-                                    load_box<CTAS>(bt, &g.b[rank], bar, k, ncol, pb);
-                                } else {
-                                    load_box<CTAS>(bt, &g.b[0], bar, k, ncol, pb);
-                                    load_box<CTAS>(bt + 16384, &g.b[1], bar, k, ncol, pb);
-                                }
-                            } else if (g.b_mn) {
-                                for (int j = 0; j < S::b_rows / 64; ++j) load_box<CTAS>(bt + j * 8192, &g.b[pair], bar, ncol + j * 64, k, pb);
+                            // B: boxes of 64 rows where it is MN-major or where a tile has 64 of each half, else of 128
+                            if (b_mn) {
+#pragma unroll
+                                for (int j = 0; j < S::b_rows / 64; ++j) load_box<CTAS>(bt + j * 8192, mb, bar, ncol + j * 64, kc, pb);
+                            } else if (CTAS == 1 && dual) {
+                                load_box<CTAS>(bt, &g.b[0], bar, kc, ncol, pb);
+                                load_box<CTAS>(bt + S::b_bytes / 2, &g.b[1], bar, kc, ncol, pb);
                             } else {
-                                for (int j = 0; j < S::b_rows / 128; ++j) load_box<CTAS>(bt + j * 16384, &g.b[pair], bar, k, ncol + j * 128, pb);
+#pragma unroll
+                                for (int j = 0; j < S::b_rows / 128; ++j) load_box<CTAS>(bt + j * 16384, mb, bar, kc, ncol + j * 128, pb);
                             }
                         }
+                        __syncwarp();
+                        ++loads;
+                        if (++s == S::stages) s = 0, turn ^= 1;
                     }
                 }
             }
-            // the products have read every stage before the CTA may leave
-            for (uint32_t j = it > S::stages ? it - S::stages : 0; ok && j < it; ++j)
-                ok = wait(&bars.empty[j % S::stages], (j / S::stages) & 1);
+        }
+        // the products have read every stage before the CTA may leave
+        for (uint32_t j = 0; ok && j < min(loads, (uint32_t)S::stages); ++j) {
+            if (s == 0) s = S::stages, turn ^= 1;
+            ok = warp_wait(&bars.empty[--s], turn);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::idesc_bf16_f32(kTileM * CTAS, kTileN, g.a_mn, g.b_mn);
-            const uint32_t ka = g.a_mn ? 128 : 2, kbs = g.b_mn ? 128 : 2;   // 16 of K on, in 16-byte units
-            uint32_t it = 0, n = 0;
+        const bool leader = tc::elect_one();
+        if (rank == 0) {
+            uint32_t s = 0, turn = 0, n = 0;
             bool ok = true;
-            for (int w = blockIdx.x / CTAS; ok && w < work; w += step) {
-                const Item i = item_of<CTAS>(g, w);
+            const uint32_t base = tc::smem_u32(smem);
+            const int terms = g.terms;
+            for (int k = 0; ok && item_of<CTAS>(g, p, P, k, i); ++k) {
+                const int a_mn = g.group[i.group].a_mn, b_mn = g.group[i.group].b_mn;
+                const uint32_t idesc = tc::idesc_bf16_f32(kTileM * CTAS, BN, a_mn, b_mn);
+                const uint32_t ka = a_mn ? 128 : 2, kbs = b_mn ? 128 : 2;   // 16 of K on, in 16-byte units
+                const uint64_t da0 = tc::smem_desc_sw128(base, a_mn ? 8192 : 16, 1024);
+                const uint64_t db0 = tc::smem_desc_sw128(base + S::a_bytes, b_mn ? 8192 : 16, 1024);
                 for (int c0 = i.q0; ok && c0 < i.q1; c0 += chunk, ++n) {
                     const int c1 = min(c0 + chunk, i.q1);
                     if (c1 < c0) break;
                     const uint32_t buf = n & 1;
-                    if (n >= 2 && !wait(&bars.tmem_empty[buf], ((n >> 1) - 1) & 1)) { ok = false; break; }
+                    ok = n < 2 || warp_wait(&bars.tmem_empty[buf], ((n >> 1) - 1) & 1);
+                    if (!ok) break;
                     tc::tc_fence_after();
-                    const uint32_t d = tmem + buf * kTileN;
-                    const int count = (c1 - c0) * g.terms;
-                    for (int q = 0; q < count; ++q, ++it) {
-                        const uint32_t s = it % S::stages;
-                        if (!wait(&bars.full[s], (it / S::stages) & 1)) { ok = false; break; }
+                    const uint32_t d = tmem + buf * BN;
+                    const int count = (c1 - c0) * terms;
+                    for (int q = 0; q < count; ++q) {
+                        ok = warp_wait(&bars.full[s], turn);
+                        if (!ok) break;
                         tc::tc_fence_after();
-                        const uint32_t at = tc::smem_u32(smem) + s * S::stage;
-                        const uint64_t da = tc::smem_desc_sw128(at, g.a_mn ? 8192 : 16, 1024);
-                        const uint64_t db = tc::smem_desc_sw128(at + S::a_bytes, g.b_mn ? 8192 : 16, 1024);
+                        const uint64_t da = da0 + s * (S::stage / 16), db = db0 + s * (S::stage / 16);
+                        if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma_bf16<CTAS>(d, da + kk * ka, db + kk * kbs, idesc, q > 0 || kk > 0);
-                        commit<CTAS>(&bars.empty[s]);
+                            for (int kk = 0; kk < 4; ++kk) mma_bf16<CTAS>(d, da + kk * ka, db + kk * kbs, idesc, q > 0 || kk > 0);
+                            commit<CTAS>(&bars.empty[s]);
+                        }
+                        __syncwarp();
+                        if (++s == S::stages) s = 0, turn ^= 1;
                     }
-                    if (ok) commit<CTAS>(&bars.tmem_full[buf]);
+                    if (ok && leader) commit<CTAS>(&bars.tmem_full[buf]);
+                    __syncwarp();
                 }
             }
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, part_of = (warp - 2) >> 2;   // the warp's lanes, and its CW columns
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * 4096;
+        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * S::boxes * 4096;
         const uint32_t box_at = tc::smem_u32(box);
-        const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : tc::smem_u32(&bars.tmem_empty[0]);
-        uint32_t n = 0;
+        uint64_t *in_bar = &bars.in[warp - 2];
+        const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : 0u;
+        uint32_t n = 0, turn = 0, in_phase = 0;
         bool ok = true;
-        // 32 columns of a row, packed, into the swizzled box (part 0 or 1 of its 64)
-        auto put = [&](const float *v, int part) {
+        // 32 packed columns of a row into half `part` of box k (swizzled as TMA reads it)
+        auto put = [&](int k, const float *v, int part) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const Raw<__nv_bfloat16, 8> r = pack<__nv_bfloat16, 8>(v + 8 * c);
-                tc::sts_u4(box_at + tc::sw128_offset(lane, part * 4 + c), make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+                tc::sts_u4(box_at + k * 4096 + tc::sw128_offset(lane, part * 4 + c), make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
             }
         };
-        auto box_free = [&]() {
-            if (lane == 0) tc::bulk_wait_group_read_all();
+        // the next box, once the store before the last has read it
+        auto next_box = [&]() {
+            if (lane == 0) bulk_wait_read<(S::boxes > 1 ? 1 : 0)>();
             __syncwarp();
+            return S::boxes > 1 ? (int)(turn++ & 1) : 0;
         };
-        auto box_out = [&](const CUtensorMap *map, int col, int row, int ncols, int nrows) {
+        auto box_out = [&](int k, const CUtensorMap *map, int col, int row, int ncols, int nrows) {
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && col < ncols && row < nrows) {
-                tc::tma_store_3d(map, box, col, row, 0);
-                tc::bulk_commit_group();
+            if (lane == 0) {
+                if (col < ncols && row < nrows) tc::tma_store_3d(map, box + k * 4096, col, row, 0);
+                tc::bulk_commit_group();   // empty where there is nothing to store: groups are counted
             }
         };
-        for (int w = blockIdx.x / CTAS; ok && w < work; w += step) {
-            const Item i = item_of<CTAS>(g, w);
+        // kBack: gate and up of a warp's 64 columns and 32 rows into its two boxes
+        auto load_io = [&](const Item &t, int part) {
+            if (lane == 0) {
+                const int col = t.n * BN + part_of * CW + part * 64, row = (t.m * CTAS + (int)rank) * kTileM + quarter * 32;
+                tc::mbar_arrive_expect_tx(in_bar, 8192);
+                tc::tma_load_3d(box, &g.io[0], in_bar, col, row, 0);
+                tc::tma_load_3d(box + 4096, &g.io[1], in_bar, col, row, 0);
+            }
+        };
+        bool more = item_of<CTAS>(g, p, P, 0, i);
+        const bool io_boxes = S::boxes == 2 && EPI == kBack && g.tma_io && g.group[0].splits == 1;
+        if (io_boxes && more) load_io(i, 0);
+        for (int k = 1; ok && more; ++k) {
+            const Group &gr = g.group[i.group];
+            Item next;
+            more = item_of<CTAS>(g, p, P, k, next);
             const int row0 = (i.m * CTAS + (int)rank) * kTileM + quarter * 32, row = row0 + lane;
-            // the accumulator: 128 columns per warp; kUp: 64 of the gate's and 64 of the projection's
-            constexpr int CW = kTileN / 2;
-            float acc[PROMOTE ? CW : 1];
+            const bool in = row < gr.M;
             uint32_t from = 0;
             auto column = [&](int j) {   // tensor memory column of the warp's column j
-                return EPI == kUp ? (j < 64 ? half * 64 + j : 128 + half * 64 + j - 64) : half * 128 + j;
+                return EPI == kUp ? (j < CW / 2 ? part_of * (CW / 2) + j : BN / 2 + part_of * (CW / 2) + j - CW / 2) : part_of * CW + j;
             };
             auto done = [&]() {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t bar = release + (n & 1) * 8;
                     if constexpr (CTAS == 2)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(release + (n & 1) * 8) : "memory");
                     else
                         tc::mbar_arrive(&bars.tmem_empty[n & 1]);
                 }
                 ++n;
             };
+            // fp32: all sums but the last are taken out, added up in registers, and the total
+            // goes back to where the last one lies
             if constexpr (PROMOTE) {
-                for (int c0 = i.q0; c0 < i.q1; c0 += chunk) {
+                float acc[CW];
+                const int chunks = (i.q1 - i.q0 + kPromote - 1) / kPromote;
+                for (int c = 0; c < chunks; ++c) {
                     ok = __all_sync(0xffffffffu, wait(&bars.tmem_full[n & 1], (n >> 1) & 1));
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint32_t d = tmem + (n & 1) * kTileN + lanes;
+                    from = tmem + (n & 1) * BN + lanes;
+                    if (chunks == 1) break;
+                    const bool last = c + 1 == chunks;
 #pragma unroll
-                    for (int j = 0; j < CW; j += 32) {
-                        uint32_t v[32];
-                        tc::tmem_ld32(d + column(j), v);
+                    for (int j = 0; j < CW; j += 16) {
+                        uint32_t v[16];
+                        tc::tmem_ld16(from + column(j), v);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[j + e] = c0 == i.q0 ? __uint_as_float(v[e]) : acc[j + e] + __uint_as_float(v[e]);
+                        for (int e = 0; e < 16; ++e) {
+                            acc[j + e] = c == 0 ? __uint_as_float(v[e]) : acc[j + e] + __uint_as_float(v[e]);
+                            v[e] = __float_as_uint(acc[j + e]);
+                        }
+                        if (last) tc::tmem_st16(from + column(j), v);
                     }
-                    done();
+                    if (last) tc::tmem_wait_st();
+                    else done();
                 }
             } else {
                 ok = __all_sync(0xffffffffu, wait(&bars.tmem_full[n & 1], (n >> 1) & 1));
                 tc::tc_fence_after();
-                from = tmem + (n & 1) * kTileN + lanes;
+                from = tmem + (n & 1) * BN + lanes;
             }
             if (!ok) break;
-            auto get = [&](int j, float *v) {   // columns j .. j + 31 of the warp's
-                if constexpr (PROMOTE) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = acc[j + e];
-                } else {
-                    tc::tmem_ld32(from + column(j), reinterpret_cast<uint32_t *>(v));
-                    tc::tmem_wait_ld();
-                }
+            auto get = [&](int j, float *v) {   // columns j .. j + E - 1 of the warp's
+                if constexpr (E == 16) tc::tmem_ld16(from + column(j), reinterpret_cast<uint32_t *>(v));
+                else tc::tmem_ld32(from + column(j), reinterpret_cast<uint32_t *>(v));
+                tc::tmem_wait_ld();
             };
-            const bool in = row < g.M;
-            if (g.splits > 1) {
-#pragma unroll
-                for (int j = 0; j < CW; j += 32) {
-                    float v[32];
+            // first output column of the warp
+            const int col = EPI == kUp ? i.n * (BN / 2) + part_of * (CW / 2) : i.n * BN + part_of * CW;
+            constexpr int kUnroll = PROMOTE ? 1 : 4;
+            if (gr.splits > 1) {
+#pragma unroll kUnroll
+                for (int j = 0; j < CW; j += E) {
+                    float v[E];
                     get(j, v);
-                    const int which = EPI == kUp ? j / 64 : i.group;
-                    const int col = EPI == kUp ? i.n * 128 + half * 64 + j % 64 : i.n * kTileN + half * 128 + j;
-                    if (in && col < g.N)
-                        store32<float>(g.partial + (((long long)i.split * (EPI == kUp ? 2 : g.groups) + which) * g.M + row) * g.ld_part + col,
-                                       v, (int)g.ld_part - col, true);
+                    const int which = EPI == kUp ? j / (CW / 2) : 0, at = EPI == kUp ? col + j % (CW / 2) : col + j;
+                    if (in && at < gr.N)
+                        store_cols<float, E>(gr.partial + (((long long)i.split * (EPI == kUp ? 2 : 1) + which) * gr.M + row) * gr.ld_part + at,
+                                             v, (int)gr.ld_part - at, true);
                 }
             } else if constexpr (EPI == kUp) {
-                const int col = i.n * 128 + half * 64;
                 if (g.gate) {
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
                         T *dst = static_cast<T *>(o ? g.up : g.gate);
-                        if (!PROMOTE && g.tma_out) box_free();
-#pragma unroll
-                        for (int j = 0; j < 64; j += 32) {
-                            float v[32];
-                            get(64 * o + j, v);
-                            if (!PROMOTE && g.tma_out) put(v, j / 32);
-                            else if (in && col + j < g.N) store32<T>(dst + row * g.ld_io + col + j, v, g.N - col - j, g.vec_io);
+                        int b = 0;
+                        if (BOXES && g.tma_io) b = next_box();
+#pragma unroll kUnroll
+                        for (int j = 0; j < CW / 2; j += E) {
+                            float v[E];
+                            get(CW / 2 * o + j, v);
+                            if (BOXES && g.tma_io) put(b, v, j / 32);
+                            else if (in && col + j < gr.N) store_cols<T, E>(dst + (long long)row * gr.N + col + j, v, gr.N - col - j, g.vec_io);
                         }
-                        if (!PROMOTE && g.tma_out) box_out(&g.c[1 + o], col, row0, g.N, g.M);
+                        if (BOXES && g.tma_io) box_out(b, &g.io[o], col, row0, gr.N, gr.M);
                     }
                 }
-                if (!PROMOTE) box_free();
+                int b = 0;
+                if constexpr (BOXES) b = next_box();
+#pragma unroll kUnroll
+                for (int j = 0; j < CW / 2; j += E) {
+                    float x[E], u[E];
+                    get(j, x);
+                    get(CW / 2 + j, u);
 #pragma unroll
-                for (int j = 0; j < 64; j += 32) {
-                    float a[32], b[32];
-                    get(j, a);
-                    get(64 + j, b);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) a[e] = act_times(a[e], b[e], g.act);
-                    if constexpr (!PROMOTE) {
-                        put(a, j / 32);
-                    } else if (in && col + j < g.N) {
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float s[3];
-                                split3(a[e], s);
-                                b[e] = s[p];
-                            }
-                            store32<__nv_bfloat16>(g.planes[0] + p * g.plane_stride + row * g.ld_plane + col + j, b, (int)g.ld_plane - col - j, true);
-                        }
-                    }
+                    for (int e = 0; e < E; ++e) x[e] = act_times(x[e], u[e], g.act);
+                    if constexpr (BOXES) put(b, x, j / 32);
+                    else if (in && col + j < gr.N)
+                        store_planes<T, E>(g.planes[0] + row * g.ld_plane + col + j, g.plane_stride, x, (int)g.ld_plane - col - j);
                 }
-                if (!PROMOTE) box_out(&g.c[0], col, row0, g.N, g.M);
+                if constexpr (BOXES) box_out(b, &g.c[0], col, row0, gr.N, gr.M);
             } else if constexpr (EPI == kBack) {
                 const T *gate = static_cast<const T *>(g.gate), *up = static_cast<const T *>(g.up);
+                if constexpr (BOXES) {
 #pragma unroll 1
-                for (int part = 0; part < 2; ++part) {
-                    const int col = i.n * kTileN + half * 128 + part * 64;
-                    uint32_t pk[PROMOTE ? 1 : 3][32];
+                    for (int part = 0; ok && part < CW / 64; ++part) {
+                        if (io_boxes) {
+                            ok = __all_sync(0xffffffffu, wait(in_bar, in_phase & 1));
+                            ++in_phase;
+                            if (!ok) break;
+                        }
+                        uint32_t pk[3][32];
 #pragma unroll
-                    for (int j = 0; j < 64; j += 32) {
-                        float d[32], x[32], u[32];
-                        const int live = in ? g.N - col - j : 0;
-                        load32<T>(gate + (live > 0 ? row * g.ld_io + col + j : 0), x, live, g.vec_io);
-                        load32<T>(up + (live > 0 ? row * g.ld_io + col + j : 0), u, live, g.vec_io);
-                        if constexpr (PROMOTE) {
+                        for (int j = 0; j < 64; j += 32) {
+                            float d[32], x[32], u[32];
+                            if (io_boxes) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) d[e] = part ? acc[64 + j + e] : acc[j + e];
-                        } else {
+                                for (int c = 0; c < 4; ++c) {
+                                    const uint32_t off = tc::sw128_offset(lane, j / 8 + c);
+                                    const uint4 a = tc::lds_u4(box_at + off), b = tc::lds_u4(box_at + 4096 + off);
+                                    const Raw<__nv_bfloat16, 8> ra = {{a.x, a.y, a.z, a.w}}, rb = {{b.x, b.y, b.z, b.w}};
+                                    unpack<__nv_bfloat16, 8>(ra, x + 8 * c);
+                                    unpack<__nv_bfloat16, 8>(rb, u + 8 * c);
+                                }
+                            } else {
+                                const int live = in ? gr.N - col - part * 64 - j : 0;
+                                const long long at = live > 0 ? (long long)row * gr.N + col + part * 64 + j : 0;
+                                load_cols<T, 32>(gate + at, x, live, g.vec_io);
+                                load_cols<T, 32>(up + at, u, live, g.vec_io);
+                            }
                             get(part * 64 + j, d);
-                        }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float dg, du, h;
-                            act_back(d[e], x[e], u[e], g.act, dg, du, h);
-                            d[e] = dg, u[e] = du, x[e] = h;
-                        }
-                        if constexpr (!PROMOTE) {
+                            for (int e = 0; e < 32; ++e) {
+                                float dg, du, h;
+                                act_back(d[e], x[e], u[e], g.act, dg, du, h);
+                                d[e] = dg, u[e] = du, x[e] = h;
+                            }
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 pk[0][j / 2 + e] = tc::pack_bf16x2(d[2 * e], d[2 * e + 1]);
                                 pk[1][j / 2 + e] = tc::pack_bf16x2(u[2 * e], u[2 * e + 1]);
                                 pk[2][j / 2 + e] = tc::pack_bf16x2(x[2 * e], x[2 * e + 1]);
                             }
-                        } else if (live > 0) {
-#pragma unroll
-                            for (int o = 0; o < 3; ++o) {
-#pragma unroll
-                                for (int p = 0; p < 3; ++p) {
-                                    float v[32];
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) {
-                                        float s[3];
-                                        split3(o == 0 ? d[e] : o == 1 ? u[e] : x[e], s);
-                                        v[e] = s[p];
-                                    }
-                                    store32<__nv_bfloat16>(g.planes[o] + p * g.plane_stride + row * g.ld_plane + col + j, v,
-                                                           (int)g.ld_plane - col - j, true);
-                                }
-                            }
                         }
-                    }
-                    if constexpr (!PROMOTE) {
 #pragma unroll
                         for (int o = 0; o < 3; ++o) {
-                            box_free();
+                            // with the inputs in the boxes: all lanes have read them
+                            const int b = next_box();
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                tc::sts_u4(box_at + tc::sw128_offset(lane, c),
+                                tc::sts_u4(box_at + b * 4096 + tc::sw128_offset(lane, c),
                                            make_uint4(pk[o][4 * c], pk[o][4 * c + 1], pk[o][4 * c + 2], pk[o][4 * c + 3]));
-                            box_out(&g.c[o], col, row0, g.N, g.M);
+                            box_out(b, &g.c[o], col + part * 64, row0, gr.N, gr.M);
+                        }
+                        if (io_boxes) {
+                            const bool last = part + 1 == CW / 64;
+                            if (lane == 0) bulk_wait_read<0>();
+                            if (!last) load_io(i, part + 1);
+                            else if (more) load_io(next, 0);
+                            __syncwarp();
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < CW; j += E) {
+                        float d[E], x[E], u[E];
+                        const int live = in ? gr.N - col - j : 0;
+                        const long long at = live > 0 ? (long long)row * gr.N + col + j : 0;
+                        load_cols<T, E>(gate + at, x, live, g.vec_io);
+                        load_cols<T, E>(up + at, u, live, g.vec_io);
+                        get(j, d);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            float dg, du, h;
+                            act_back(d[e], x[e], u[e], g.act, dg, du, h);
+                            d[e] = dg, u[e] = du, x[e] = h;
+                        }
+                        if (live > 0) {
+                            const long long to = row * g.ld_plane + col + j;
+                            const int room = (int)g.ld_plane - col - j;
+                            store_planes<T, E>(g.planes[0] + to, g.plane_stride, d, room);
+                            store_planes<T, E>(g.planes[1] + to, g.plane_stride, u, room);
+                            store_planes<T, E>(g.planes[2] + to, g.plane_stride, x, room);
                         }
                     }
                 }
+                if (!ok) break;
             } else {
-                const int col = i.n * kTileN + half * 128;
-                T *out = static_cast<T *>(g.out[i.group]);
+                T *out = static_cast<T *>(gr.out);
+                const bool box_it = BOXES && gr.tma_out;
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    if (!PROMOTE && g.tma_out) box_free();
-#pragma unroll
-                    for (int j = 0; j < 64; j += 32) {
-                        float v[32];
+                for (int part = 0; part < CW / 64; ++part) {
+                    int b = 0;
+                    if (box_it) b = next_box();
+#pragma unroll kUnroll
+                    for (int j = 0; j < 64; j += E) {
+                        float v[E];
                         get(part * 64 + j, v);
                         const int at = col + part * 64 + j;
-                        if (!PROMOTE && g.tma_out) put(v, j / 32);
-                        else if (in && at < g.N) store32<T>(out + row * g.ld_out + at, v, g.N - at, g.vec_out);
+                        if (box_it) put(b, v, j / 32);
+                        else if (in && at < gr.N) store_cols<T, E>(out + row * gr.ld_out + at, v, gr.N - at, gr.vec_out);
                     }
-                    if (!PROMOTE && g.tma_out) box_out(&g.c[i.group], col + part * 64, row0, g.N, g.M);
+                    if (box_it) box_out(b, &g.c[gr.c], col + part * 64, row0, gr.N, gr.M);
                 }
             }
-            if constexpr (!PROMOTE) done();
+            done();
+            i = next;
         }
         if (lane == 0) tc::bulk_wait_group_all();
     }
@@ -575,17 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_gemm_kernel(const __grid_cons
     __syncthreads();
     if constexpr (CTAS == 2) cluster_sync_all();
     tc::tc_fence_after();
-    if (warp == 1) tmem_free_all<CTAS>(tmem);
+    if (warp == 1) tmem_free<CTAS, 2 * BN>(tmem);
 }
 
-template <int EPI, typename T, int CTAS>
+template <int EPI, typename T, int CTAS, int BN>
 cudaError_t launch_gemm(const GemmArgs &g, int grid, cudaStream_t s) {
-    using S = Shape<CTAS>;
-    cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+    using S = Shape<T, CTAS, BN>;
+    cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, CTAS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(S::threads);
     cfg.dynamicSmemBytes = S::smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -595,18 +724,26 @@ cudaError_t launch_gemm(const GemmArgs &g, int grid, cudaStream_t s) {
     attr[1].val.clusterDim.x = CTAS, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CTAS == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, T, CTAS>, g);
+    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, T, CTAS, BN>, g);
 }
 
-// The instantiations, one translation unit each (ffn_gemm_*.cu).
-cudaError_t launch_up(const GemmArgs &g, bool f32, int ctas, int grid, cudaStream_t s);
-cudaError_t launch_back(const GemmArgs &g, bool f32, int ctas, int grid, cudaStream_t s);
-cudaError_t launch_plain(const GemmArgs &g, bool f32, int ctas, int grid, cudaStream_t s);
+// The tile shapes: a pair of 256 x 256, a CTA of 128 x 256, two CTAs to an SM of 128 x 128.
+enum Tile { kPair = 0, kWide = 1, kSmall = 2 };
 
-#define GDN_FFN_LAUNCHER(NAME, EPI)                                                                          \
-    cudaError_t NAME(const GemmArgs &g, bool f32, int ctas, int grid, cudaStream_t s) {                      \
-        if (f32) return ctas == 2 ? launch_gemm<EPI, float, 2>(g, grid, s) : launch_gemm<EPI, float, 1>(g, grid, s); \
-        return ctas == 2 ? launch_gemm<EPI, __nv_bfloat16, 2>(g, grid, s) : launch_gemm<EPI, __nv_bfloat16, 1>(g, grid, s); \
+// The instantiations, one translation unit each (ffn_gemm_*.cu).
+cudaError_t launch_up(const GemmArgs &g, bool f32, int tile, int grid, cudaStream_t s);
+cudaError_t launch_back(const GemmArgs &g, bool f32, int tile, int grid, cudaStream_t s);
+cudaError_t launch_plain(const GemmArgs &g, bool f32, int tile, int grid, cudaStream_t s);
+
+template <int EPI, typename T>
+cudaError_t launch_tile(const GemmArgs &g, int tile, int grid, cudaStream_t s) {
+    return tile == kPair ? launch_gemm<EPI, T, 2, 256>(g, grid, s)
+           : tile == kWide ? launch_gemm<EPI, T, 1, 256>(g, grid, s)
+                           : launch_gemm<EPI, T, 1, 128>(g, grid, s);
+}
+#define GDN_FFN_LAUNCHER(NAME, EPI)                                                                                  \
+    cudaError_t NAME(const GemmArgs &g, bool f32, int tile, int grid, cudaStream_t s) {                              \
+        return f32 ? launch_tile<EPI, float>(g, tile, grid, s) : launch_tile<EPI, __nv_bfloat16>(g, tile, grid, s);  \
     }
 
 }  // namespace ffn

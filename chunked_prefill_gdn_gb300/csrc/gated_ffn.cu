@@ -104,110 +104,194 @@ __global__ void __launch_bounds__(256) ffn_stage_kernel(const StageArgs a) {
 }
 
 // ------------------------------------------------------ adding a split's parts
-struct FinishArgs {
+struct FinishGroup {
     const float *partial;
-    int splits, which, groups, act;   // which: partial matrices per split
-    long long M, N, ld_part;
-    void *out[2];
-    long long ld_out;
+    int splits;
+    long long M, N, ld_part, ld_out;
+    void *out;
+};
+struct FinishArgs {
+    FinishGroup group[kMaxGroups];
+    int act;
     __nv_bfloat16 *planes[3];
     long long ld_plane, plane_stride;
-    int n_planes;
     void *gate, *up;
-    long long ld_io;
 };
-__device__ __forceinline__ void store_planes(__nv_bfloat16 *p, long long stride, int n, const float *v, int live) {
-    float s[3][4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float t[3];
-        split3(v[e], t);
-        s[0][e] = n == 1 ? v[e] : t[0], s[1][e] = t[1], s[2][e] = t[2];
-    }
-    for (int k = 0; k < n; ++k) store_some<__nv_bfloat16, 4>(p + k * stride, s[k], live);
-}
+// Four columns a thread; blockIdx.y: the product.
 template <int EPI, typename T>
-__global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs a) {
+__global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs f) {
     grid_dependency_wait();
-    const long long per = (a.N + 3) / 4, total = a.M * per * (EPI == kPlain ? a.groups : 1);
-    const long long matrix = a.M * a.ld_part;
+    const FinishGroup &a = f.group[blockIdx.y];
+    const long long per = (a.N + 3) / 4, total = a.splits > 1 ? a.M * per : 0, matrix = a.M * a.ld_part;
     auto sum = [&](long long at, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = 0.f;
         for (int s = 0; s < a.splits; ++s) {
-            const float4 p = *reinterpret_cast<const float4 *>(a.partial + s * a.which * matrix + at);
+            const float4 p = *reinterpret_cast<const float4 *>(a.partial + s * (EPI == kUp ? 2 : 1) * matrix + at);
             v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
         }
     };
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long rr = i / per, c = (i - rr * per) * 4, grp = rr / a.M, r = rr - grp * a.M;
+        const long long r = i / per, c = (i - r * per) * 4;
         const int live = (int)(a.N - c < 4 ? a.N - c : 4);
         float v[4], w[4];
-        sum(grp * matrix + r * a.ld_part + c, v);
+        sum(r * a.ld_part + c, v);
+        auto planes = [&](int o, const float *x) {
+            __nv_bfloat16 *to = f.planes[o] + r * f.ld_plane + c;
+            if constexpr (sizeof(T) == 2) {
+                store_some<__nv_bfloat16, 4>(to, x, live);
+            } else {
+                float s[3][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float t[3];
+                    split3(x[e], t);
+                    s[0][e] = t[0], s[1][e] = t[1], s[2][e] = t[2];
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) store_some<__nv_bfloat16, 4>(to + k * f.plane_stride, s[k], live);
+            }
+        };
         if constexpr (EPI == kUp) {
             sum(matrix + r * a.ld_part + c, w);
-            if (a.gate) {
-                store_some<T, 4>(static_cast<T *>(a.gate) + r * a.ld_io + c, v, live);
-                store_some<T, 4>(static_cast<T *>(a.up) + r * a.ld_io + c, w, live);
+            if (f.gate) {
+                store_some<T, 4>(static_cast<T *>(f.gate) + r * a.N + c, v, live);
+                store_some<T, 4>(static_cast<T *>(f.up) + r * a.N + c, w, live);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = act_times(v[e], w[e], a.act);
-            store_planes(a.planes[0] + r * a.ld_plane + c, a.plane_stride, a.n_planes, v, live);
+            for (int e = 0; e < 4; ++e) v[e] = act_times(v[e], w[e], f.act);
+            planes(0, v);
         } else if constexpr (EPI == kBack) {
             float g[4], u[4];
-            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(a.gate) + r * a.ld_io + c, live), g);
-            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(a.up) + r * a.ld_io + c, live), u);
+            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(f.gate) + r * a.N + c, live), g);
+            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(f.up) + r * a.N + c, live), u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float dg, du, h;
-                act_back(v[e], g[e], u[e], a.act, dg, du, h);
+                act_back(v[e], g[e], u[e], f.act, dg, du, h);
                 v[e] = dg, w[e] = du, g[e] = h;
             }
-            store_planes(a.planes[0] + r * a.ld_plane + c, a.plane_stride, a.n_planes, v, live);
-            store_planes(a.planes[1] + r * a.ld_plane + c, a.plane_stride, a.n_planes, w, live);
-            store_planes(a.planes[2] + r * a.ld_plane + c, a.plane_stride, a.n_planes, g, live);
+            planes(0, v);
+            planes(1, w);
+            planes(2, g);
         } else {
-            store_some<T, 4>(static_cast<T *>(a.out[grp]) + r * a.ld_out + c, v, live);
+            store_some<T, 4>(static_cast<T *>(a.out) + r * a.ld_out + c, v, live);
         }
     }
 }
 
-// ------------------------------------------------------------------- planning
+// ------------------------------------------------------------------- the work
+struct Problem {
+    long long M, D, F, O;
+    bool f32;
+    int act, planes, terms;
+};
+struct Product {
+    long long M, N, k;        // k: of one pair
+    int pairs;
+    Mat a[2], b[2];
+    bool a_mn, b_mn;
+    void *out;                // contiguous
+};
 struct Plan {
-    int ctas, splits, mt, nt;
-    long long ld_part;
-    size_t partial_bytes;
+    int tile, splits[kMaxGroups], mt[kMaxGroups], nt[kMaxGroups], kb[kMaxGroups];
+    int order[kMaxGroups], ahead, first, rest, ratio;   // ahead: how many of `order` make up `first`
+    size_t part_bytes[kMaxGroups], bytes;
+};
+// One launch: products that share an epilogue (those without an output are planned
+// for, so that a result does not depend on which others are wanted, and left out).
+struct Batch {
+    int epi, n;
+    Product p[kMaxGroups];
+    Mat planes[3];            // kUp, kBack: outputs
+    void *gate, *up;
+    Plan plan;
 };
 
-// One product of M x N outputs per group (cols: a tile's columns of N) over kb
-// blocks along K.  The model, in clocks: a block of K costs a CTA or pair 512 of the
-// tensor pipe (single CTAs 640: they read twice as much of B), a tile 2500 for its
-// first loads and its last epilogue, a split the second kernel and its traffic.
-Plan plan_product(long long M, long long N, int cols, int groups, int which, long long kb, int terms) {
+int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
+long long up_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Tile shape and parts of a batch, by a model in clocks.  A block of K takes a pair 512 of
+// the tensor pipe for each term; a single CTA of 256 columns a little more (it reads twice as
+// much of B); two CTAs of 128 columns share their SM and are held by shared memory, 700 each.
+// A tile takes at least its epilogue; a launch 4000 to fill and drain; the operands come at
+// 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another launch
+// and their traffic.
+Plan plan_batch(const Batch &b, const Problem &pr) {
     Plan best = {};
     double best_cost = 1e300;
     const int sms = device_sm_count();
-    for (int ctas = 2; ctas >= 1; --ctas) {
-        const long long mt = (M + kTileM * ctas - 1) / (kTileM * ctas), nt = (N + cols - 1) / cols;
-        const long long tiles = mt * nt * groups, slots = sms / ctas;
-        for (int s = 1; s <= 32 && s <= kb; ++s) {
-            const double part = (double)M * N * which * 4 * s;
-            if (s > 1 && (tiles >= 2 * slots || part > 512e6)) break;
-            const long long waves = (tiles * s + slots - 1) / slots;
-            double cost = (double)waves * ((double)((kb + s - 1) / s) * terms * (ctas == 2 ? 512 : 640) + 2500);
-            if (s > 1) cost += 6000 + part * 2 / 4000;   // 4000 bytes per clock to and from L2
-            if (cost < best_cost * 0.97) {
+    const int which = b.epi == kUp ? 2 : 1;
+    long long kmax = 1;
+    double bytes = 0;
+    for (int i = 0; i < b.n; ++i) {
+        const Product &p = b.p[i];
+        kmax = std::max<long long>(kmax, (long long)blocks(p.k) * p.pairs);
+        bytes += 2.0 * pr.planes * p.k * p.pairs * (p.M + (double)p.N * which) + 4.0 * p.M * p.N;
+    }
+    static const int parts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    for (int tile = 0; tile < 3; ++tile) {
+        const int ctas = tile == kPair ? 2 : 1, bn = tile == kSmall ? 128 : 256, cols = b.epi == kUp ? bn / 2 : bn;
+        const int P = tile == kPair ? sms / 2 : tile == kWide ? sms : 2 * sms;
+        const double epi = (b.epi == kBack ? 14000 : b.epi == kUp ? 7000 : 4000) * (tile == kSmall ? 0.8 : 1.0) * (pr.f32 ? 1.5 : 1.0);
+        long long last = 0;
+        for (int want : parts) {
+            const long long target = up_div(kmax, want);
+            if (target == last) continue;
+            last = target;
+            Plan c = {};
+            c.tile = tile;
+            double len[kMaxGroups], longest = 0;
+            long long units[kMaxGroups], all = 0;
+            bool split = false;
+            double part = 0;
+            for (int i = 0; i < b.n; ++i) {
+                const Product &p = b.p[i];
+                const long long q = (long long)blocks(p.k) * p.pairs;
+                c.kb[i] = blocks(p.k);
+                c.mt[i] = (int)up_div(p.M, kTileM * ctas), c.nt[i] = (int)up_div(p.N, cols);
+                c.splits[i] = (int)std::min<long long>(up_div(q, target), q);
+                units[i] = (long long)c.mt[i] * c.nt[i] * c.splits[i];
+                all += units[i];
+                len[i] = (double)q / c.splits[i];
+                longest = std::max(longest, len[i]);
+                c.part_bytes[i] = c.splits[i] > 1 ? (size_t)c.splits[i] * which * p.M * ((p.N + 3) / 4 * 4) * 4 : 0;
+                split |= c.splits[i] > 1, part += c.part_bytes[i];
+            }
+            if (split && (all > 8ll * P || part > 1e9)) break;
+            // the longest first
+            int n = 0;
+            double la = 0, lb = 0;
+            for (int i = 0; i < b.n; ++i)
+                if (len[i] >= 0.75 * longest) c.order[n++] = i, c.first += (int)units[i], la = std::max(la, len[i]);
+            c.ahead = n;
+            for (int i = 0; i < b.n; ++i)
+                if (len[i] < 0.75 * longest) c.order[n++] = i, c.rest += (int)units[i], lb = std::max(lb, len[i]);
+            c.ratio = lb > 0 ? std::max(1, (int)(la / lb + 0.5)) : 1;
+            double clock = tile == kPair ? 512 : tile == kWide ? 560 : 700;
+            if (tile == kSmall && all <= sms) clock = 350;
+            auto unit = [&](double l) { return std::max(l * pr.terms * clock, epi) + 300; };
+            const int extra = c.first % P, behind = extra ? P - extra : 0;
+            double span = 0;
+            for (int p : {0, extra, P - 1}) {
+                const long long a = up_div(std::max(c.first - p, 0), P), base = (long long)c.ratio * behind;
+                long long r = up_div(std::max<long long>(c.rest - base - p, 0), P);
+                if (extra && p >= extra) r += std::min<long long>(c.ratio, up_div(std::max(c.rest - (p - extra), 0), behind));
+                span = std::max(span, a * unit(la) + r * unit(lb));
+            }
+            const double in_flight = (tile == kPair ? 5 * 16384 : tile == kWide ? 3 * 32768 : 3 * 16384) / 1800.0;
+            const double active = (double)std::min<long long>(all, P) * ctas;
+            double cost = std::max(span, bytes / std::min(3500.0, active * in_flight)) + 4000;
+            if (split) cost += 5000 + part * 2 / 4000;
+            if (cost < best_cost * 0.98) {
                 best_cost = cost;
-                best.ctas = ctas, best.splits = s, best.mt = (int)mt, best.nt = (int)nt;
+                best = c;
             }
         }
     }
-    best.ld_part = (N + 3) / 4 * 4;
-    best.partial_bytes = best.splits > 1 ? (size_t)best.splits * which * M * best.ld_part * 4 : 0;
+    for (int i = 0; i < b.n; ++i) best.bytes += (best.part_bytes[i] + 255) / 256 * 256;
     return best;
 }
-
-int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
 
 struct Carve {
     char *base;
@@ -217,14 +301,6 @@ struct Carve {
         at += (bytes + 255) / 256 * 256;
         return p;
     }
-};
-
-// What a call needs besides its arguments: operands as TMA reads them, the
-// intermediates, the parts of split sums.
-struct Problem {
-    long long M, D, F, O;
-    bool f32;
-    int act, planes, terms;
 };
 
 bool tma_ok(const void *p, long long rows, long long ld) {
@@ -256,102 +332,95 @@ cudaError_t run_stage(const Problem &pr, const StageArgs &st, int n, cudaStream_
                   : launch_dependent(ffn_stage_kernel<__nv_bfloat16>, dim3(grid, n), dim3(256), 0, s, st);
 }
 
-struct Product {
-    int epi;
-    long long M, N;
-    int groups, pairs;
-    Mat a[2], b[2];
-    bool a_mn, b_mn, dual;
-    Mat planes[3];            // kUp, kBack outputs
-    void *out[2];
-    long long ld_out;
-    void *gate, *up;
-    long long k;              // of one pair
-};
-
-Plan plan_of(const Product &p, const Problem &pr) {
-    return plan_product(p.M, p.N, p.dual ? kTileN / 2 : kTileN, p.groups, p.dual ? 2 : p.groups,
-                        (long long)blocks(p.k) * p.pairs, pr.terms);
-}
-
 template <int EPI>
-cudaError_t run_finish(const Problem &pr, const FinishArgs &f, cudaStream_t s) {
-    const long long total = f.M * ((f.N + 3) / 4) * f.groups;
-    const int grid = (int)std::min<long long>((total + 255) / 256, 8ll * device_sm_count());
-    return pr.f32 ? launch_dependent(ffn_finish_kernel<EPI, float>, dim3(grid), dim3(256), 0, s, f)
-                  : launch_dependent(ffn_finish_kernel<EPI, __nv_bfloat16>, dim3(grid), dim3(256), 0, s, f);
+cudaError_t run_finish(const Problem &pr, const FinishArgs &f, int n, cudaStream_t s) {
+    long long most = 0;
+    for (int i = 0; i < n; ++i) most = std::max(most, f.group[i].M * ((f.group[i].N + 3) / 4));
+    const int grid = (int)std::min<long long>((most + 255) / 256, 8ll * device_sm_count());
+    return pr.f32 ? launch_dependent(ffn_finish_kernel<EPI, float>, dim3(grid, n), dim3(256), 0, s, f)
+                  : launch_dependent(ffn_finish_kernel<EPI, __nv_bfloat16>, dim3(grid, n), dim3(256), 0, s, f);
 }
 
-cudaError_t run_product(const Product &p, const Problem &pr, float *partial, int *err, cudaStream_t s) {
-    const Plan pl = plan_of(p, pr);
+cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err, cudaStream_t s) {
+    const Plan &pl = b.plan;
     GemmArgs g = {};
     const int e = pr.f32 ? 4 : 2;
     auto vec = [&](const void *q, long long ld) { return aligned16(q) && ld * e % 16 == 0; };
-    const int nb = p.dual ? 2 : p.pairs, na = p.groups > 1 ? p.groups : p.pairs;
-    for (int i = 0; i < na; ++i)
-        if (!encode(&g.a[i], p.a[i], p.a_mn ? 64 : kTileM)) return cudaErrorInvalidValue;
-    for (int i = 0; i < nb; ++i)
-        if (!encode(&g.b[i], p.b[i], p.b_mn ? 64 : 128)) return cudaErrorInvalidValue;
-    g.M = (int)p.M, g.N = (int)p.N, g.mt = pl.mt, g.nt = pl.nt, g.groups = p.groups;
-    g.kb = blocks(p.k), g.pairs = p.pairs, g.splits = pl.splits, g.terms = pr.terms;
-    g.a_mn = p.a_mn, g.b_mn = p.b_mn, g.dual = p.dual, g.act = pr.act;
-    g.err = err;
-    g.partial = partial, g.ld_part = pl.ld_part;
-    g.gate = p.gate, g.up = p.up, g.ld_io = p.N;
-    g.vec_io = vec(p.gate, g.ld_io) && vec(p.up, g.ld_io);
-    for (int i = 0; i < 2; ++i) g.out[i] = p.out[i];
-    g.ld_out = p.ld_out;
-    g.vec_out = vec(p.out[0], p.ld_out) && (p.groups < 2 || vec(p.out[1], p.ld_out));
-    const int np = p.epi == kUp ? 1 : p.epi == kBack ? 3 : 0;
-    for (int i = 0; i < np; ++i) g.planes[i] = static_cast<__nv_bfloat16 *>(const_cast<void *>(p.planes[i].p));
-    g.ld_plane = p.planes[0].ld, g.plane_stride = p.planes[0].plane;
-    if (pl.splits == 1 && !pr.f32) {
-        if (p.epi == kPlain) {
-            g.tma_out = g.vec_out;
-            for (int i = 0; g.tma_out && i < p.groups; ++i)
-                if (!encode(&g.c[i], Mat{p.out[i], p.M, p.N, p.ld_out, 0, 1}, 32)) return cudaErrorInvalidValue;
-        } else {
-            for (int i = 0; i < np; ++i)
-                if (!encode(&g.c[i], p.planes[i], 32)) return cudaErrorInvalidValue;
-            if (p.epi == kUp && p.gate) {
-                g.tma_out = g.vec_io;
-                if (g.tma_out && (!encode(&g.c[1], Mat{p.gate, p.M, p.N, p.N, 0, 1}, 32) || !encode(&g.c[2], Mat{p.up, p.M, p.N, p.N, 0, 1}, 32)))
-                    return cudaErrorInvalidValue;
-            }
+    g.dual = b.epi == kUp, g.ratio = pl.ratio;
+    g.terms = pr.terms, g.act = pr.act, g.err = err;
+    FinishArgs f = {};
+    int na = 0, nb = 0, nc = 0;
+    bool split = false;
+    for (int k = 0; k < b.n; ++k) {
+        const int i = pl.order[k];
+        const Product &p = b.p[i];
+        if (b.epi == kPlain && !p.out) continue;
+        Group &q = g.group[g.groups];
+        q.M = (int)p.M, q.N = (int)p.N, q.mt = pl.mt[i], q.nt = pl.nt[i], q.kb = pl.kb[i], q.pairs = p.pairs, q.splits = pl.splits[i];
+        q.a = na, q.b = nb, q.c = nc, q.a_mn = p.a_mn, q.b_mn = p.b_mn;
+        q.out = p.out, q.ld_out = p.N, q.vec_out = vec(p.out, p.N);
+        q.partial = reinterpret_cast<float *>(partial), q.ld_part = (p.N + 3) / 4 * 4;
+        partial += (pl.part_bytes[i] + 255) / 256 * 256;
+        (k < pl.ahead ? g.first : g.rest) += q.mt * q.nt * q.splits;
+        const int b_maps = g.dual ? 2 : p.pairs;
+        if (na + p.pairs > kMaxGroups + 1 || nb + b_maps > kMaxGroups + 1) return cudaErrorInvalidValue;
+        for (int j = 0; j < p.pairs; ++j)
+            if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : kTileM)) return cudaErrorInvalidValue;
+        for (int j = 0; j < b_maps; ++j)
+            if (!encode(&g.b[nb++], p.b[j], p.b_mn || (g.dual && pl.tile == kSmall) ? 64 : 128)) return cudaErrorInvalidValue;
+        if (b.epi == kPlain && !pr.f32 && q.splits == 1 && q.vec_out) {
+            q.tma_out = 1;
+            if (!encode(&g.c[nc++], Mat{p.out, p.M, p.N, p.N, 0, 1}, 32)) return cudaErrorInvalidValue;
+        }
+        split |= q.splits > 1;
+        f.group[g.groups++] = {q.partial, q.splits, p.M, p.N, q.ld_part, q.ld_out, p.out};
+    }
+    if (g.groups == 0) return cudaSuccess;
+    if (b.epi != kPlain) {
+        const int n = b.epi == kUp ? 1 : 3;
+        for (int i = 0; i < n; ++i) {
+            g.planes[i] = static_cast<__nv_bfloat16 *>(const_cast<void *>(b.planes[i].p));
+            if (!pr.f32 && !encode(&g.c[i], b.planes[i], 32)) return cudaErrorInvalidValue;
+        }
+        g.ld_plane = b.planes[0].ld, g.plane_stride = b.planes[0].plane;
+        g.gate = b.gate, g.up = b.up;
+        const Product &p = b.p[0];
+        g.vec_io = vec(b.gate, p.N) && vec(b.up, p.N);
+        if (b.gate && !pr.f32 && g.vec_io) {
+            g.tma_io = 1;
+            if (!encode(&g.io[0], Mat{b.gate, p.M, p.N, p.N, 0, 1}, 32) || !encode(&g.io[1], Mat{b.up, p.M, p.N, p.N, 0, 1}, 32))
+                return cudaErrorInvalidValue;
         }
     }
-    const long long work = (long long)g.groups * g.mt * g.nt * g.splits;
-    const int grid = (int)std::min<long long>(work, device_sm_count() / pl.ctas) * pl.ctas;
-    cudaError_t rc = p.epi == kUp ? launch_up(g, pr.f32, pl.ctas, grid, s)
-                     : p.epi == kBack ? launch_back(g, pr.f32, pl.ctas, grid, s)
-                                      : launch_plain(g, pr.f32, pl.ctas, grid, s);
-    if (rc != cudaSuccess || pl.splits == 1) return rc;
-    FinishArgs f = {};
-    f.partial = partial, f.splits = pl.splits, f.which = p.dual ? 2 : p.groups, f.groups = p.groups, f.act = pr.act;
-    f.M = p.M, f.N = p.N, f.ld_part = pl.ld_part;
-    for (int i = 0; i < 2; ++i) f.out[i] = p.out[i];
-    f.ld_out = p.ld_out;
+    const int sms = device_sm_count(), workers = pl.tile == kPair ? sms / 2 : pl.tile == kWide ? sms : 2 * sms;
+    const int grid = std::min(workers, g.first + g.rest) * (pl.tile == kPair ? 2 : 1);
+    const cudaError_t rc = b.epi == kUp ? launch_up(g, pr.f32, pl.tile, grid, s)
+                           : b.epi == kBack ? launch_back(g, pr.f32, pl.tile, grid, s)
+                                            : launch_plain(g, pr.f32, pl.tile, grid, s);
+    if (rc != cudaSuccess || !split) return rc;
+    f.act = pr.act;
     for (int i = 0; i < 3; ++i) f.planes[i] = g.planes[i];
-    f.ld_plane = g.ld_plane, f.plane_stride = g.plane_stride, f.n_planes = pr.planes;
-    f.gate = p.gate, f.up = p.up, f.ld_io = g.ld_io;
-    return p.epi == kUp ? run_finish<kUp>(pr, f, s) : p.epi == kBack ? run_finish<kBack>(pr, f, s) : run_finish<kPlain>(pr, f, s);
+    f.ld_plane = g.ld_plane, f.plane_stride = g.plane_stride, f.gate = b.gate, f.up = b.up;
+    return b.epi == kUp ? run_finish<kUp>(pr, f, g.groups, s) : b.epi == kBack ? run_finish<kBack>(pr, f, g.groups, s) : run_finish<kPlain>(pr, f, g.groups, s);
 }
 
 // ------------------------------------------------------------------ the passes
 struct Pass {
     Problem pr;
     StageArgs stage;
-    int n_stage;
-    Product product[4];
-    int n;
-    float *partial;
+    int n_stage, n;
+    Batch batch[2];
+    char *partial;
     size_t bytes;
 };
 
 void finish_plan(Pass &p, Carve &c) {
     size_t most = 0;
-    for (int i = 0; i < p.n; ++i) most = std::max(most, plan_of(p.product[i], p.pr).partial_bytes);
-    p.partial = static_cast<float *>(c.take(most));
+    for (int i = 0; i < p.n; ++i) {
+        p.batch[i].plan = plan_batch(p.batch[i], p.pr);
+        most = std::max(most, p.batch[i].plan.bytes);
+    }
+    p.partial = static_cast<char *>(c.take(most));
     p.bytes = std::max<size_t>(c.at, 16);
 }
 
@@ -372,12 +441,12 @@ Pass plan_fwd(const gdn_ffn_desc &d, void *y, void *gate, void *up, void *worksp
     const Mat wu = operand(c, p.stage, p.n_stage, pr, d.w_up, pr.F, pr.D, pr.D);
     const Mat wd = operand(c, p.stage, p.n_stage, pr, d.w_down, pr.O, pr.F, pr.F);
     const Mat h = intermediate(c, pr, pr.M, pr.F);
-    Product &a = p.product[0], &b = p.product[1];
-    a.epi = kUp, a.M = pr.M, a.N = pr.F, a.groups = a.pairs = 1, a.a[0] = x, a.b[0] = wg, a.b[1] = wu, a.dual = true;
-    a.planes[0] = h, a.gate = gate, a.up = up, a.k = pr.D;
-    b.epi = kPlain, b.M = pr.M, b.N = pr.O, b.groups = b.pairs = 1, b.a[0] = h, b.b[0] = wd;
-    b.out[0] = y, b.ld_out = pr.O, b.k = pr.F;
+    Batch &a = p.batch[0], &b = p.batch[1];
     p.n = 2;
+    a.epi = kUp, a.n = 1, a.planes[0] = h, a.gate = gate, a.up = up;
+    a.p[0].M = pr.M, a.p[0].N = pr.F, a.p[0].k = pr.D, a.p[0].pairs = 1, a.p[0].a[0] = x, a.p[0].b[0] = wg, a.p[0].b[1] = wu;
+    b.epi = kPlain, b.n = 1;
+    b.p[0].M = pr.M, b.p[0].N = pr.O, b.p[0].k = pr.F, b.p[0].pairs = 1, b.p[0].a[0] = h, b.p[0].b[0] = wd, b.p[0].out = y;
     finish_plan(p, c);
     return p;
 }
@@ -393,31 +462,22 @@ Pass plan_bwd(const gdn_ffn_desc &d, const void *dy, int64_t dy_stride, const vo
     const Mat wg = operand(c, p.stage, p.n_stage, pr, d.w_gate, pr.F, pr.D, pr.D);
     const Mat wu = operand(c, p.stage, p.n_stage, pr, d.w_up, pr.F, pr.D, pr.D);
     const Mat dg = intermediate(c, pr, pr.M, pr.F), du = intermediate(c, pr, pr.M, pr.F), h = intermediate(c, pr, pr.M, pr.F);
-    auto add = [&]() -> Product & {
-        Product &q = p.product[p.n++];
-        q.groups = q.pairs = 1;
+    Batch &a = p.batch[0], &b = p.batch[1];
+    a.epi = kBack, a.n = 1, a.planes[0] = dg, a.planes[1] = du, a.planes[2] = h;
+    a.gate = const_cast<void *>(gate), a.up = const_cast<void *>(up);
+    a.p[0].M = pr.M, a.p[0].N = pr.F, a.p[0].k = pr.O, a.p[0].pairs = 1, a.p[0].a[0] = gy, a.p[0].b[0] = wd, a.p[0].b_mn = true;
+    b.epi = kPlain;
+    auto add = [&](long long M, long long N, long long k, const Mat &A, const Mat &B, bool a_mn, void *out) -> Product & {
+        Product &q = b.p[b.n++];
+        q.M = M, q.N = N, q.k = k, q.pairs = 1, q.a[0] = A, q.b[0] = B, q.a_mn = a_mn, q.b_mn = true, q.out = out;
         return q;
     };
-    Product &a = add();
-    a.epi = kBack, a.M = pr.M, a.N = pr.F, a.a[0] = gy, a.b[0] = wd, a.b_mn = true, a.k = pr.O;
-    a.planes[0] = dg, a.planes[1] = du, a.planes[2] = h, a.gate = const_cast<void *>(gate), a.up = const_cast<void *>(up);
-    if (dx) {
-        Product &q = add();
-        q.epi = kPlain, q.M = pr.M, q.N = pr.D, q.pairs = 2, q.a[0] = dg, q.a[1] = du, q.b[0] = wg, q.b[1] = wu, q.b_mn = true;
-        q.k = pr.F, q.out[0] = dx, q.ld_out = pr.D;
-    }
-    if (dwg || dwu) {
-        Product &q = add();
-        q.epi = kPlain, q.M = pr.F, q.N = pr.D, q.a_mn = q.b_mn = true, q.b[0] = x, q.k = pr.M, q.ld_out = pr.D;
-        q.groups = 0;
-        if (dwg) q.a[q.groups] = dg, q.out[q.groups++] = dwg;
-        if (dwu) q.a[q.groups] = du, q.out[q.groups++] = dwu;
-    }
-    if (dwd) {
-        Product &q = add();
-        q.epi = kPlain, q.M = pr.O, q.N = pr.F, q.a[0] = gy, q.b[0] = h, q.a_mn = q.b_mn = true, q.k = pr.M;
-        q.out[0] = dwd, q.ld_out = pr.F;
-    }
+    Product &q = add(pr.M, pr.D, pr.F, dg, wg, false, dx);
+    q.pairs = 2, q.a[1] = du, q.b[1] = wu;
+    add(pr.F, pr.D, pr.M, dg, x, true, dwg);
+    add(pr.F, pr.D, pr.M, du, x, true, dwu);
+    add(pr.O, pr.F, pr.M, gy, h, true, dwd);
+    p.n = 2;
     finish_plan(p, c);
     return p;
 }
@@ -425,8 +485,8 @@ Pass plan_bwd(const gdn_ffn_desc &d, const void *dy, int64_t dy_stride, const vo
 gdn_status run_pass(const Pass &p, int32_t *status, cudaStream_t s, const char *where) {
     cudaError_t e = cudaSuccess;
     if (status) e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
-    if (e == cudaSuccess) e = run_stage(p.pr, p.stage, p.n_stage, s);
-    for (int i = 0; e == cudaSuccess && i < p.n; ++i) e = run_product(p.product[i], p.pr, p.partial, status, s);
+    if (e == cudaSuccess && p.n) e = run_stage(p.pr, p.stage, p.n_stage, s);
+    for (int i = 0; e == cudaSuccess && i < p.n; ++i) e = run_batch(p.batch[i], p.pr, p.partial, status, s);
     if (e != cudaSuccess) {
         set_error_detail(where, e);
         return GDN_ERR_CUDA;
@@ -484,10 +544,7 @@ extern "C" gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc *desc, void *y, void 
 extern "C" size_t gdn_gated_ffn_bwd_workspace_size(const gdn_ffn_desc *desc, const void *dy, int64_t dy_stride) {
     if (gdn::ffn::desc_ok(desc) != GDN_OK || (desc->M > 1 && dy_stride < desc->D_out)) return 0;
     if (desc->M == 0) return 16;
-    // enough for any choice of gradients (the pair of dw_gate and dw_up is split otherwise than one alone)
-    void *some = reinterpret_cast<void *>((uintptr_t)16);   // never dereferenced
-    return std::max(gdn::ffn::plan_bwd(*desc, dy, dy_stride, nullptr, nullptr, some, some, some, some, nullptr).bytes,
-                    gdn::ffn::plan_bwd(*desc, dy, dy_stride, nullptr, nullptr, some, some, nullptr, some, nullptr).bytes);
+    return gdn::ffn::plan_bwd(*desc, dy, dy_stride, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr).bytes;
 }
 
 extern "C" gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy, int64_t dy_stride, const void *gate,
@@ -505,8 +562,9 @@ extern "C" gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy
     gdn::ffn::Pass p = {};
     if (desc->M > 0) {
         if (!dy || !gate || !up || !workspace || !gdn::aligned16(workspace)) return GDN_ERR_INVALID_ARG;
-        if (workspace_bytes < gdn_gated_ffn_bwd_workspace_size(desc, dy, dy_stride)) return GDN_ERR_WORKSPACE;
         p = gdn::ffn::plan_bwd(*desc, dy, dy_stride, gate, up, dx, dw_gate, dw_up, dw_down, workspace);
+        if (workspace_bytes < p.bytes) return GDN_ERR_WORKSPACE;
+        if (!dx && !dw_gate && !dw_up && !dw_down) p.n = 0;
         return gdn::ffn::run_pass(p, device_status, s, "launch gated_ffn_bwd");
     }
     // no tokens: the weights' gradients are zero
