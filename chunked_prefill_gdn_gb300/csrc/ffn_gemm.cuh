@@ -16,9 +16,10 @@
 // The accumulators are in tensor memory, two sets of BN columns, so that the epilogue
 // of one tile runs under the products of the next.  Warps: 0 loads, 1 issues the
 // products, the others are the epilogue, a quarter of the lanes and CW columns each.
-// Its bf16 outputs leave through two boxes per warp in shared memory by TMA stores;
-// the backward pass's gate and up come into the same boxes by TMA loads that run
-// under the products.
+// bf16 outputs leave through a box per warp in shared memory by TMA stores.  A sixth
+// stage of operands is worth more than a second box per warp, or than boxes into which
+// the backward pass's gate and up are loaded ahead (8191 x 4096 x 12288: first backward
+// product 514 us, with those 555).
 //
 // With PROMOTE (fp32) the tensor cores sum only kPromote blocks of K at a time;
 // those sums are added in registers, in fp32 with rounding to nearest.
@@ -39,7 +40,7 @@ enum Epi { kUp = 0, kBack = 1, kPlain = 2 };
 
 constexpr int kTileM = 128, kBlockK = 64;
 constexpr int kPromote = 8;   // blocks of 64 along K per sum in tensor memory (fp32)
-constexpr int kMaxStages = 7, kMaxGroups = 4;
+constexpr int kMaxStages = 6, kMaxGroups = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // One product of the launch: out = sum over its pairs of A B^T.
@@ -61,7 +62,7 @@ struct GemmArgs {
     // the schedule: units [0, first) are group 0's, the others follow; see item_of
     int first, rest, ratio;
     int terms;                // 1, or 6 for three planes
-    int act, tma_io, vec_io;
+    int act, tma_io, vec_io;  // kUp: gate and up leave through boxes; rows of both in 16-byte vectors
     __nv_bfloat16 *planes[3]; // kUp: h; kBack: dgate, dup, h: one plane (bf16) or three (fp32)
     long long ld_plane, plane_stride;
     void *gate, *up;          // kUp: outputs or null; kBack: inputs; contiguous
@@ -183,19 +184,15 @@ struct Shape {
     static constexpr int CW = promote ? 64 : 128, epi_warps = BN * 4 / CW, threads = 64 + 32 * epi_warps;
     static constexpr int b_rows = BN / CTAS;                     // of B in this CTA
     static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128, stage = a_bytes + b_bytes;
-#ifndef FFN_STAGES
-#define FFN_STAGES 5
-#define FFN_BOXES 2
-#endif
-    static constexpr int boxes = promote || BN == 128 ? 0 : CTAS == 2 ? FFN_BOXES : 2;   // per warp
-    static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? FFN_STAGES : promote ? 4 : 3;
-    static constexpr int smem = 1024 + stages * stage + epi_warps * boxes * 4096;   // 1024: alignment
+    static constexpr bool boxes = !promote && BN == 256;
+    static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? 6 : 4;
+    static constexpr int smem = 1024 + stages * stage + (boxes ? epi_warps * 4096 : 0);   // 1024: alignment
     static constexpr int per_sm = BN == 128 ? 2 : 1;
     static_assert(stages <= kMaxStages && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
 };
 
 struct Barriers {
-    uint64_t full[kMaxStages], empty[kMaxStages], tmem_full[2], tmem_empty[2], in[16];
+    uint64_t full[kMaxStages], empty[kMaxStages], tmem_full[2], tmem_empty[2];
     uint32_t tmem;
     int abort;
 };
@@ -304,7 +301,7 @@ template <int EPI, typename T, int CTAS, int BN>
 __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN>::per_sm)
     ffn_gemm_kernel(const __grid_constant__ GemmArgs g) {
     using S = Shape<T, CTAS, BN>;
-    constexpr bool PROMOTE = S::promote, BOXES = S::boxes > 0;
+    constexpr bool PROMOTE = S::promote, BOXES = S::boxes;
     constexpr int CW = S::CW, E = PROMOTE ? 16 : 32;   // columns of a step of the epilogue
     extern __shared__ uint8_t raw[];
     __shared__ Barriers bars;
@@ -314,7 +311,6 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::stages; ++i) tc::mbar_init(&bars.full[i], 1), tc::mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.tmem_full[i], 1), tc::mbar_init(&bars.tmem_empty[i], S::epi_warps * CTAS);
-        for (int i = 0; i < 16; ++i) tc::mbar_init(&bars.in[i], 1);
         bars.abort = 0;
         tc::fence_barrier_init();
     }
@@ -442,50 +438,33 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
     } else {
         const int quarter = warp & 3, part_of = (warp - 2) >> 2;   // the warp's lanes, and its CW columns
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * S::boxes * 4096;
+        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * 4096;
         const uint32_t box_at = tc::smem_u32(box);
-        uint64_t *in_bar = &bars.in[warp - 2];
         const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : 0u;
-        uint32_t n = 0, turn = 0, in_phase = 0;
+        uint32_t n = 0;
         bool ok = true;
-        // 32 packed columns of a row into half `part` of box k (swizzled as TMA reads it)
-        auto put = [&](int k, const float *v, int part) {
+        // 32 packed columns of a row into half `part` of the box (swizzled as TMA reads it)
+        auto put = [&](const float *v, int part) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const Raw<__nv_bfloat16, 8> r = pack<__nv_bfloat16, 8>(v + 8 * c);
-                tc::sts_u4(box_at + k * 4096 + tc::sw128_offset(lane, part * 4 + c), make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+                tc::sts_u4(box_at + tc::sw128_offset(lane, part * 4 + c), make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
             }
         };
-        // the next box, once the store before the last has read it
-        auto next_box = [&]() {
-            if (lane == 0) bulk_wait_read<(S::boxes > 1 ? 1 : 0)>();
+        auto box_free = [&]() {   // the last store has read it
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
-            return S::boxes > 1 ? (int)(turn++ & 1) : 0;
         };
-        auto box_out = [&](int k, const CUtensorMap *map, int col, int row, int ncols, int nrows) {
+        auto box_out = [&](const CUtensorMap *map, int col, int row, int ncols, int nrows) {
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                if (col < ncols && row < nrows) tc::tma_store_3d(map, box + k * 4096, col, row, 0);
-                tc::bulk_commit_group();   // empty where there is nothing to store: groups are counted
+            if (lane == 0 && col < ncols && row < nrows) {
+                tc::tma_store_3d(map, box, col, row, 0);
+                tc::bulk_commit_group();
             }
         };
-        // kBack: gate and up of a warp's 64 columns and 32 rows into its two boxes
-        auto load_io = [&](const Item &t, int part) {
-            if (lane == 0) {
-                const int col = t.n * BN + part_of * CW + part * 64, row = (t.m * CTAS + (int)rank) * kTileM + quarter * 32;
-                tc::mbar_arrive_expect_tx(in_bar, 8192);
-                tc::tma_load_3d(box, &g.io[0], in_bar, col, row, 0);
-                tc::tma_load_3d(box + 4096, &g.io[1], in_bar, col, row, 0);
-            }
-        };
-        bool more = item_of<CTAS>(g, p, P, 0, i);
-        const bool io_boxes = S::boxes == 2 && EPI == kBack && g.tma_io && g.group[0].splits == 1;
-        if (io_boxes && more) load_io(i, 0);
-        for (int k = 1; ok && more; ++k) {
+        for (int k = 0; item_of<CTAS>(g, p, P, k, i); ++k) {
             const Group &gr = g.group[i.group];
-            Item next;
-            more = item_of<CTAS>(g, p, P, k, next);
             const int row0 = (i.m * CTAS + (int)rank) * kTileM + quarter * 32, row = row0 + lane;
             const bool in = row < gr.M;
             uint32_t from = 0;
@@ -559,20 +538,18 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
                         T *dst = static_cast<T *>(o ? g.up : g.gate);
-                        int b = 0;
-                        if (BOXES && g.tma_io) b = next_box();
+                        if (BOXES && g.tma_io) box_free();
 #pragma unroll kUnroll
                         for (int j = 0; j < CW / 2; j += E) {
                             float v[E];
                             get(CW / 2 * o + j, v);
-                            if (BOXES && g.tma_io) put(b, v, j / 32);
+                            if (BOXES && g.tma_io) put(v, j / 32);
                             else if (in && col + j < gr.N) store_cols<T, E>(dst + (long long)row * gr.N + col + j, v, gr.N - col - j, g.vec_io);
                         }
-                        if (BOXES && g.tma_io) box_out(b, &g.io[o], col, row0, gr.N, gr.M);
+                        if (BOXES && g.tma_io) box_out(&g.io[o], col, row0, gr.N, gr.M);
                     }
                 }
-                int b = 0;
-                if constexpr (BOXES) b = next_box();
+                if constexpr (BOXES) box_free();
 #pragma unroll kUnroll
                 for (int j = 0; j < CW / 2; j += E) {
                     float x[E], u[E];
@@ -580,40 +557,24 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                     get(CW / 2 + j, u);
 #pragma unroll
                     for (int e = 0; e < E; ++e) x[e] = act_times(x[e], u[e], g.act);
-                    if constexpr (BOXES) put(b, x, j / 32);
+                    if constexpr (BOXES) put(x, j / 32);
                     else if (in && col + j < gr.N)
                         store_planes<T, E>(g.planes[0] + row * g.ld_plane + col + j, g.plane_stride, x, (int)g.ld_plane - col - j);
                 }
-                if constexpr (BOXES) box_out(b, &g.c[0], col, row0, gr.N, gr.M);
+                if constexpr (BOXES) box_out(&g.c[0], col, row0, gr.N, gr.M);
             } else if constexpr (EPI == kBack) {
                 const T *gate = static_cast<const T *>(g.gate), *up = static_cast<const T *>(g.up);
                 if constexpr (BOXES) {
 #pragma unroll 1
-                    for (int part = 0; ok && part < CW / 64; ++part) {
-                        if (io_boxes) {
-                            ok = __all_sync(0xffffffffu, wait(in_bar, in_phase & 1));
-                            ++in_phase;
-                            if (!ok) break;
-                        }
+                    for (int part = 0; part < CW / 64; ++part) {
                         uint32_t pk[3][32];
 #pragma unroll
                         for (int j = 0; j < 64; j += 32) {
                             float d[32], x[32], u[32];
-                            if (io_boxes) {
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    const uint32_t off = tc::sw128_offset(lane, j / 8 + c);
-                                    const uint4 a = tc::lds_u4(box_at + off), b = tc::lds_u4(box_at + 4096 + off);
-                                    const Raw<__nv_bfloat16, 8> ra = {{a.x, a.y, a.z, a.w}}, rb = {{b.x, b.y, b.z, b.w}};
-                                    unpack<__nv_bfloat16, 8>(ra, x + 8 * c);
-                                    unpack<__nv_bfloat16, 8>(rb, u + 8 * c);
-                                }
-                            } else {
-                                const int live = in ? gr.N - col - part * 64 - j : 0;
-                                const long long at = live > 0 ? (long long)row * gr.N + col + part * 64 + j : 0;
-                                load_cols<T, 32>(gate + at, x, live, g.vec_io);
-                                load_cols<T, 32>(up + at, u, live, g.vec_io);
-                            }
+                            const int live = in ? gr.N - col - part * 64 - j : 0;
+                            const long long at = live > 0 ? (long long)row * gr.N + col + part * 64 + j : 0;
+                            load_cols<T, 32>(gate + at, x, live, g.vec_io);
+                            load_cols<T, 32>(up + at, u, live, g.vec_io);
                             get(part * 64 + j, d);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
@@ -630,20 +591,12 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                         }
 #pragma unroll
                         for (int o = 0; o < 3; ++o) {
-                            // with the inputs in the boxes: all lanes have read them
-                            const int b = next_box();
+                            box_free();
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                tc::sts_u4(box_at + b * 4096 + tc::sw128_offset(lane, c),
+                                tc::sts_u4(box_at + tc::sw128_offset(lane, c),
                                            make_uint4(pk[o][4 * c], pk[o][4 * c + 1], pk[o][4 * c + 2], pk[o][4 * c + 3]));
-                            box_out(b, &g.c[o], col + part * 64, row0, gr.N, gr.M);
-                        }
-                        if (io_boxes) {
-                            const bool last = part + 1 == CW / 64;
-                            if (lane == 0) bulk_wait_read<0>();
-                            if (!last) load_io(i, part + 1);
-                            else if (more) load_io(next, 0);
-                            __syncwarp();
+                            box_out(&g.c[o], col + part * 64, row0, gr.N, gr.M);
                         }
                     }
                 } else {
@@ -670,27 +623,24 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                         }
                     }
                 }
-                if (!ok) break;
             } else {
                 T *out = static_cast<T *>(gr.out);
                 const bool box_it = BOXES && gr.tma_out;
 #pragma unroll
                 for (int part = 0; part < CW / 64; ++part) {
-                    int b = 0;
-                    if (box_it) b = next_box();
+                    if (box_it) box_free();
 #pragma unroll kUnroll
                     for (int j = 0; j < 64; j += E) {
                         float v[E];
                         get(part * 64 + j, v);
                         const int at = col + part * 64 + j;
-                        if (box_it) put(b, v, j / 32);
+                        if (box_it) put(v, j / 32);
                         else if (in && at < gr.N) store_cols<T, E>(out + row * gr.ld_out + at, v, gr.N - at, gr.vec_out);
                     }
-                    if (box_it) box_out(b, &g.c[gr.c], col + part * 64, row0, gr.N, gr.M);
+                    if (box_it) box_out(&g.c[gr.c], col + part * 64, row0, gr.N, gr.M);
                 }
             }
             done();
-            i = next;
         }
         if (lane == 0) tc::bulk_wait_group_all();
     }

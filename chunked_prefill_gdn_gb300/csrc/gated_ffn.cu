@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "ffn_few.cuh"
 #include "ffn_gemm.cuh"
 
 namespace gdn {
@@ -214,7 +215,7 @@ long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 // Tile shape and parts of a batch, by a model in clocks.  A block of K takes a pair 512 of
 // the tensor pipe for each term; a single CTA of 256 columns a little more (it reads twice as
 // much of B); two CTAs of 128 columns share their SM and are held by shared memory, 700 each.
-// A tile takes at least its epilogue; a launch 4000 to fill and drain; the operands come at
+// A tile takes at least its epilogue; a launch 4000 to 7000 to fill and drain; the operands come at
 // 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another launch
 // and their traffic.
 Plan plan_batch(const Batch &b, const Problem &pr) {
@@ -268,7 +269,7 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
             for (int i = 0; i < b.n; ++i)
                 if (len[i] < 0.75 * longest) c.order[n++] = i, c.rest += (int)units[i], lb = std::max(lb, len[i]);
             c.ratio = lb > 0 ? std::max(1, (int)(la / lb + 0.5)) : 1;
-            double clock = tile == kPair ? 512 : tile == kWide ? 560 : 700;
+            double clock = tile == kPair ? 512 : tile == kWide ? 610 : 700;
             if (tile == kSmall && all <= sms) clock = 350;
             auto unit = [&](double l) { return std::max(l * pr.terms * clock, epi) + 300; };
             const int extra = c.first % P, behind = extra ? P - extra : 0;
@@ -279,10 +280,10 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
                 if (extra && p >= extra) r += std::min<long long>(c.ratio, up_div(std::max(c.rest - (p - extra), 0), behind));
                 span = std::max(span, a * unit(la) + r * unit(lb));
             }
-            const double in_flight = (tile == kPair ? 5 * 16384 : tile == kWide ? 3 * 32768 : 3 * 16384) / 1800.0;
+            const double in_flight = (tile == kPair ? 6 * 16384 : tile == kWide ? 4 * 32768 : 3 * 16384) / 1800.0;
             const double active = (double)std::min<long long>(all, P) * ctas;
-            double cost = std::max(span, bytes / std::min(3500.0, active * in_flight)) + 4000;
-            if (split) cost += 5000 + part * 2 / 4000;
+            double cost = std::max(span, bytes / std::min(3500.0, active * in_flight)) + (tile == kPair ? 7000 : tile == kWide ? 5500 : 4000);
+            if (split) cost += 6000 + part * 2 / 4000;
             if (cost < best_cost * 0.98) {
                 best_cost = cost;
                 best = c;
@@ -386,7 +387,7 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         g.gate = b.gate, g.up = b.up;
         const Product &p = b.p[0];
         g.vec_io = vec(b.gate, p.N) && vec(b.up, p.N);
-        if (b.gate && !pr.f32 && g.vec_io) {
+        if (b.epi == kUp && b.gate && !pr.f32 && g.vec_io) {
             g.tma_io = 1;
             if (!encode(&g.io[0], Mat{b.gate, p.M, p.N, p.N, 0, 1}, 32) || !encode(&g.io[1], Mat{b.up, p.M, p.N, p.N, 0, 1}, 32))
                 return cudaErrorInvalidValue;
@@ -430,6 +431,30 @@ Problem problem_of(const gdn_ffn_desc &d) {
     pr.f32 = d.dtype == GDN_F32, pr.act = d.activation;
     pr.planes = pr.f32 ? 3 : 1, pr.terms = pr.f32 ? 6 : 1;
     return pr;
+}
+
+// Whether the forward products are those of ffn_few.cu.
+bool few(const Problem &pr) { return pr.M <= (pr.f32 ? kFewF32 : kFewBf16); }
+
+gdn_status run_few(const gdn_ffn_desc &d, const Problem &pr, void *y, void *gate, void *up, int32_t *status, void *workspace,
+                   cudaStream_t s) {
+    const int e = pr.f32 ? 4 : 2;
+    auto vec = [&](const void *p, long long rows, long long ld) { return aligned16(p) && (rows <= 1 || ld * e % 16 == 0); };
+    FewArgs a = {};
+    a.x = d.x, a.x_stride = d.x_stride, a.w0 = d.w_gate, a.w1 = d.w_up, a.K = pr.D, a.M = (int)pr.M, a.rows = (int)pr.F, a.act = pr.act;
+    a.out = workspace, a.out_ld = pad8(pr.F), a.gate = gate, a.up = up;
+    FewArgs b = {};
+    b.x = workspace, b.x_stride = pad8(pr.F), b.w0 = d.w_down, b.K = pr.F, b.M = a.M, b.rows = (int)pr.O, b.out = y, b.out_ld = pr.O;
+    cudaError_t rc = status ? cudaMemsetAsync(status, 0, sizeof(int32_t), s) : cudaSuccess;
+    const bool va = pr.D * e % 16 == 0 && vec(d.x, pr.M, d.x_stride) && aligned16(d.w_gate) && aligned16(d.w_up);
+    const bool vb = pr.F * e % 16 == 0 && aligned16(d.w_down);
+    if (rc == cudaSuccess) rc = launch_few(a, true, pr.f32, va, s);
+    if (rc == cudaSuccess) rc = launch_few(b, false, pr.f32, vb, s);
+    if (rc != cudaSuccess) {
+        set_error_detail("launch gated_ffn_fwd", rc);
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
 }
 
 Pass plan_fwd(const gdn_ffn_desc &d, void *y, void *gate, void *up, void *workspace) {
@@ -521,6 +546,8 @@ bool pointers_ok(const gdn_ffn_desc &d) {
 extern "C" size_t gdn_gated_ffn_fwd_workspace_size(const gdn_ffn_desc *desc) {
     if (gdn::ffn::desc_ok(desc) != GDN_OK) return 0;
     if (desc->M == 0) return 16;
+    const gdn::ffn::Problem pr = gdn::ffn::problem_of(*desc);
+    if (gdn::ffn::few(pr)) return (size_t)pr.M * gdn::ffn::pad8(pr.F) * (pr.f32 ? 4 : 2);
     return gdn::ffn::plan_fwd(*desc, nullptr, nullptr, nullptr, nullptr).bytes;
 }
 
@@ -535,6 +562,11 @@ extern "C" gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc *desc, void *y, void 
     gdn::ffn::Pass p = {};
     if (desc->M > 0) {
         if (!y || !workspace || !gdn::aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+        const gdn::ffn::Problem pr = gdn::ffn::problem_of(*desc);
+        if (gdn::ffn::few(pr)) {
+            if (workspace_bytes < gdn_gated_ffn_fwd_workspace_size(desc)) return GDN_ERR_WORKSPACE;
+            return gdn::ffn::run_few(*desc, pr, y, gate, up, device_status, workspace, s);
+        }
         p = gdn::ffn::plan_fwd(*desc, y, gate, up, workspace);
         if (workspace_bytes < p.bytes) return GDN_ERR_WORKSPACE;
     }
