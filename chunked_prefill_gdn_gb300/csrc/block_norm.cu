@@ -21,16 +21,20 @@
 // of being held.  The blocks' sums leave as partial rows that a second kernel adds in
 // a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 
 namespace gdn {
 namespace {
 
-// Rows [outer][inner]: row i starts at (i / inner) so + (i % inner) si elements.
+// Rows [outer][inner]: row i starts at (i / inner) so + (i % inner) si elements.  From
+// a row to the one `step` rows on it is `ahead` elements, and `wrap` more where the inner
+// index passes its end.
 struct View {
     const void *p;
-    long long so, si;
+    long long so, si, ahead, wrap;
+    const void *end;          // past the last row
 };
 struct BlockNormArgs {
     View y, z, r, dx, dh;             // r: the residual, or x in the backward pass
@@ -40,6 +44,7 @@ struct BlockNormArgs {
     float *partial;                   // [grid][P, dw_pre][D] or null
     long long rows;
     uint32_t inner, magic, shift;     // division by inner
+    uint32_t inner_step;              // of a block's step from row to row
     int D, w_f32, post, pre, gate, res;   // gate: 0 none, 1 silu, 2 sigmoid
     float eps;
 };
@@ -48,6 +53,11 @@ __device__ __forceinline__ long long row_at(const BlockNormArgs &a, const View &
     if (a.inner == 1) return row * v.so;
     const uint32_t n = (uint32_t)row, q = (__umulhi(a.magic, n) + n) >> a.shift;
     return (long long)q * v.so + (long long)(n - q * a.inner) * v.si;
+}
+__device__ __forceinline__ uint32_t inner_of(const BlockNormArgs &a, long long row) {
+    if (a.inner == 1) return 0u;
+    const uint32_t n = (uint32_t)row;
+    return n - ((__umulhi(a.magic, n) + n) >> a.shift) * a.inner;
 }
 __device__ __forceinline__ float param_at(const void *p, int i, int f32) {
     return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
@@ -76,20 +86,55 @@ constexpr int bn_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
 
 // Rows in flight per row of threads: as many as `most` bytes per block hold, at most
 // four; a single one where not even two fit.
-template <typename T, int TPR, int VEC, int NV, int ARRAYS>
+// Blocks per SM that the registers are budgeted for: THREADS threads.
+template <typename T, int TPR, int VEC, int NV, int ARRAYS, int THREADS>
 struct BnStages {
+    // Vectors: each thread reads back what it copied.  Else a row comes as the 16-byte
+    // chunks that it touches, and its threads read from all of them.
     static constexpr bool async = VEC * sizeof(T) == 16;
-    static constexpr int bytes = bn_threads(TPR) * NV * ARRAYS * 16;
-    static constexpr int fit = 98304 / bytes;
-    static constexpr int count = !async ? 1 : fit >= 4 ? 4 : fit >= 2 ? fit : bytes <= 106496 ? 2 : 1;
-    static constexpr int smem = async ? count * bytes : 0;
-    static constexpr int by_smem = smem ? 225 * 1024 / (smem + 1024) : 8;
-    static constexpr int by_threads = (ARRAYS == 3 ? 768 : 512) / bn_threads(TPR);
+    static constexpr int row_bytes = TPR * NV * VEC * (int)sizeof(T) + 16;
+    static constexpr int bytes = async ? bn_threads(TPR) * NV * ARRAYS * 16 : bn_threads(TPR) / TPR * ARRAYS * row_bytes;
+    static constexpr int fit = (THREADS >= 1024 ? 65536 : 98304) / bytes;
+    static constexpr int count = fit >= 4 ? 4 : fit >= 2 ? fit : bytes <= 106496 ? 2 : 1;
+    static constexpr int smem = count * bytes;
+    static constexpr int by_smem = 225 * 1024 / (smem + 1024);
+    static constexpr int by_threads = THREADS / bn_threads(TPR);
     static constexpr int blocks = by_smem < by_threads ? (by_smem > 0 ? by_smem : 1) : (by_threads > 0 ? by_threads : 1);
 };
 
 __device__ __forceinline__ void bn_copy16(uint4 *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+template <typename T, int TPR, int VEC, int NV>
+using FwdStages = BnStages<T, TPR, VEC, NV, 3, TPR >= 512 ? 1536 : 768>;
+template <typename T, int TPR, int VEC, int NV, bool PRE>
+using BwdStages = BnStages<T, TPR, VEC, NV, PRE ? 5 : 3, !PRE && NV * VEC <= 8 ? 768 : 512>;
+
+// The threads of a row, which read what any of them copied.
+template <int TPR>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (TPR > 32) __syncthreads();
+    else __syncwarp();
+}
+// Copies the 16-byte chunks that a row of D elements at src touches; of chunks that reach
+// past the tensor's ends its elements only.
+template <typename T, int TPR>
+__device__ __forceinline__ void window_copy(uint8_t *dst, const T *src, const View &v, int D, int t) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15, lo = reinterpret_cast<uintptr_t>(v.p),
+                    hi = reinterpret_cast<uintptr_t>(v.end);
+    const int n = (int)((reinterpret_cast<uintptr_t>(src + D) - first + 15) >> 4);
+    for (int j = t; j < n; j += TPR) {
+        const uintptr_t at = first + 16ull * j;
+        if (at >= lo && at + 16 <= hi) {
+            bn_copy16(reinterpret_cast<uint4 *>(dst + 16 * j), reinterpret_cast<const void *>(at));
+        } else {
+            for (int b = 0; b < 16; b += (int)sizeof(T)) {
+                const T *el = reinterpret_cast<const T *>(at + b);
+                if (el >= src && el < src + D) *reinterpret_cast<T *>(dst + 16 * j + b) = *el;
+            }
+        }
+    }
 }
 
 // Column of a thread's element e (of NV vectors of VEC, TPR vectors apart).
@@ -111,8 +156,8 @@ __device__ __forceinline__ void params(const void *p, const void *q, int f32, in
     for (int i = 0; i < NV * VEC / 2; ++i) v[i] = pair(x[2 * i], x[2 * i + 1]);
 }
 
-// A thread's part of one array's row: from the copies, or element by element from
-// the row itself; zero past the row's end.
+// A thread's part of one array's row, from the copies: its vectors, or its elements of
+// the row; zero past the row's end.
 template <typename T, int TPR, int VEC, int NV, bool ASYNC>
 struct Part {
     const uint4 *at;     // [NV] vectors, NT apart
@@ -159,38 +204,54 @@ __device__ __forceinline__ void put_row(T *row, int D, int t, bool live, const F
 }
 
 template <typename T, int TPR, int VEC, int NV>
-__global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 3>::blocks) block_norm_fwd_kernel(const BlockNormArgs a) {
-    using St = BnStages<T, TPR, VEC, NV, 3>;
+__global__ void __launch_bounds__(bn_threads(TPR), FwdStages<T, TPR, VEC, NV>::blocks) block_norm_fwd_kernel(const BlockNormArgs a) {
+    using St = FwdStages<T, TPR, VEC, NV>;
     constexpr int NT = bn_threads(TPR), RPB = NT / TPR, S = St::count, NP = NV * VEC / 2;
     __shared__ float red[2][32];
-    extern __shared__ uint4 stages[];              // [S][y, z, r][NV][thread]
+    extern __shared__ uint4 stages[];              // [S][y, z, r][NV][thread], or [S][y, z, r][row][chunk]
+    uint8_t *const windows = reinterpret_cast<uint8_t *>(stages) + threadIdx.x / TPR * St::row_bytes;
+    constexpr int kArray = RPB * St::row_bytes;
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
     grid_dependency_wait();
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const int behind = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;   // rows of a warp go together
+    // the rows are loaded in turn: pointers walk instead of being computed
+    const T *src[3] = {static_cast<const T *>(a.y.p) + row_at(a, a.y, row), a.gate ? static_cast<const T *>(a.z.p) + row_at(a, a.z, row) : nullptr,
+                       a.res ? static_cast<const T *>(a.r.p) + row_at(a, a.r, row) : nullptr};
+    uint32_t rem = inner_of(a, row);
     auto load_row = [&](long long r, int slot) {
-        if constexpr (St::async) {
-            if (r < a.rows) {
-                const T *y = static_cast<const T *>(a.y.p) + row_at(a, a.y, r);
-                const T *z = a.gate ? static_cast<const T *>(a.z.p) + row_at(a, a.z, r) : nullptr;
-                const T *rr = a.res ? static_cast<const T *>(a.r.p) + row_at(a, a.r, r) : nullptr;
+        if (r < a.rows) {
+            if constexpr (St::async) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = (i * TPR + t) * VEC;
                     uint4 *at = stages + (slot * 3 * NV + i) * NT + threadIdx.x;
                     if (c < a.D) {
-                        bn_copy16(at, y + c);
-                        if (a.gate) bn_copy16(at + NV * NT, z + c);
-                        if (a.res) bn_copy16(at + 2 * NV * NT, rr + c);
+                        bn_copy16(at, src[0] + c);
+                        if (a.gate) bn_copy16(at + NV * NT, src[1] + c);
+                        if (a.res) bn_copy16(at + 2 * NV * NT, src[2] + c);
                     }
                 }
+            } else {
+                uint8_t *at = windows + slot * 3 * kArray;
+                window_copy<T, TPR>(at, src[0], a.y, a.D, t);
+                if (a.gate) window_copy<T, TPR>(at + kArray, src[1], a.z, a.D, t);
+                if (a.res) window_copy<T, TPR>(at + 2 * kArray, src[2], a.r, a.D, t);
             }
-            copy_commit();
         }
+        copy_commit();
+        rem += a.inner_step;
+        const bool wrap = rem >= a.inner;
+        if (wrap) rem -= a.inner;
+        src[0] += a.y.ahead + (wrap ? a.y.wrap : 0);
+        src[1] += a.z.ahead + (wrap ? a.z.wrap : 0);
+        src[2] += a.r.ahead + (wrap ? a.r.wrap : 0);
     };
+    if constexpr (S > 1 || St::async) {
 #pragma unroll
-    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+        for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    }
     F2 c[NP], wn[NP];
     params<TPR, VEC, NV>(a.w_post, a.scale, a.w_f32, a.D, t, c);
     params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
@@ -205,10 +266,16 @@ __global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 3>:
             copy_wait<S - 1>();
             y.at = stages + slot * 3 * NV * NT + threadIdx.x;
             z.at = y.at + NV * NT, r.at = z.at + NV * NT;
-        } else if (live) {
-            y.row = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
-            if (a.gate) z.row = static_cast<const T *>(a.z.p) + row_at(a, a.z, row);
-            if (a.res) r.row = static_cast<const T *>(a.r.p) + row_at(a, a.r, row);
+        } else {
+            if constexpr (S == 1) row_sync<TPR>(), load_row(row, 0);
+            copy_wait<(S > 1 ? S - 2 : 0)>();
+            row_sync<TPR>();   // all have this row, and none reads the last one any more
+            if constexpr (S > 1) load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+            const uint8_t *at = windows + slot * 3 * kArray;
+            auto place = [&](const View &w, int k) {
+                return reinterpret_cast<const T *>(at + k * kArray + ((reinterpret_cast<uintptr_t>(w.p) + row_at(a, w, row) * sizeof(T)) & 15));
+            };
+            y.row = place(a.y, 0), z.row = place(a.z, 1), r.row = place(a.r, 2);
         }
         F2 v[NP], u[NP];
         y.template get<NT>(v);
@@ -250,68 +317,85 @@ __global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 3>:
     }
 }
 
-template <typename T, int TPR, int VEC, int NV>
-__global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 5>::blocks) block_norm_bwd_kernel(const BlockNormArgs a) {
-    using St = BnStages<T, TPR, VEC, NV, 5>;
+// PRE: with the second norm (kept apart: without it a third of the registers go).
+template <typename T, int TPR, int VEC, int NV, bool PRE>
+__global__ void __launch_bounds__(bn_threads(TPR), BwdStages<T, TPR, VEC, NV, PRE>::blocks) block_norm_bwd_kernel(const BlockNormArgs a) {
+    using St = BwdStages<T, TPR, VEC, NV, PRE>;
+    constexpr int ARR = PRE ? 5 : 3;
     constexpr int NT = bn_threads(TPR), RPB = NT / TPR, S = St::count, NP = NV * VEC / 2;
     __shared__ float red[2][32];
-    extern __shared__ uint4 stages[];              // [S][y, z, dx, dh, x][NV][thread]
+    extern __shared__ uint4 stages[];              // [S][y, z, dx(, dh, x)][NV][thread], or [..][row][chunk]
+    uint8_t *const windows = reinterpret_cast<uint8_t *>(stages) + threadIdx.x / TPR * St::row_bytes;
+    constexpr int kArray = RPB * St::row_bytes;
     const int t = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * RPB;
     grid_dependency_wait();
     long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const int behind = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
     const bool has_dx = a.dx.p != nullptr;
-    auto load_row = [&](long long r, int slot) {
-        if constexpr (St::async) {
-            if (r < a.rows) {
-                const View *view[5] = {&a.y, &a.z, &a.dx, &a.dh, &a.r};
-                const bool there[5] = {true, a.gate != 0, has_dx, a.pre != 0, a.pre != 0};
+    const View *view[5] = {&a.y, &a.z, &a.dx, &a.dh, &a.r};
+    const bool there[5] = {true, a.gate != 0, has_dx, true, true};
+    const T *src[ARR];
 #pragma unroll
-                for (int k = 0; k < 5; ++k) {
-                    if (!there[k]) continue;
-                    const T *src = static_cast<const T *>(view[k]->p) + row_at(a, *view[k], r);
+    for (int k = 0; k < ARR; ++k) src[k] = static_cast<const T *>(view[k]->p) + (there[k] ? row_at(a, *view[k], row) : 0);
+    uint32_t rem = inner_of(a, row);
+    auto load_row = [&](long long r, int slot) {
+        if (r < a.rows) {
+#pragma unroll
+            for (int k = 0; k < ARR; ++k) {
+                if (!there[k]) continue;
+                if constexpr (St::async) {
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         const int c = (i * TPR + t) * VEC;
-                        if (c < a.D) bn_copy16(stages + ((slot * 5 + k) * NV + i) * NT + threadIdx.x, src + c);
+                        if (c < a.D) bn_copy16(stages + ((slot * ARR + k) * NV + i) * NT + threadIdx.x, src[k] + c);
                     }
+                } else {
+                    window_copy<T, TPR>(windows + (slot * ARR + k) * kArray, src[k], *view[k], a.D, t);
                 }
             }
-            copy_commit();
         }
+        copy_commit();
+        rem += a.inner_step;
+        const bool wrap = rem >= a.inner;
+        if (wrap) rem -= a.inner;
+#pragma unroll
+        for (int k = 0; k < ARR; ++k) src[k] += view[k]->ahead + (wrap ? view[k]->wrap : 0);
     };
+    if constexpr (S > 1 || St::async) {
 #pragma unroll
-    for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
-    F2 c[NP], wn[NP], P[NP], Q[NP];
+        for (int k = 0; k < (S > 1 ? S - 1 : 1); ++k) load_row(row + k * step, k);
+    }
+    F2 c[NP], P[NP], wn[PRE ? NP : 1], Q[PRE ? NP : 1];
     params<TPR, VEC, NV>(a.w_post, a.scale, a.w_f32, a.D, t, c);
-    params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
+    if constexpr (PRE) params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) P[p] = Q[p] = both(0.f);
+    for (int p = 0; p < NP; ++p) P[p] = Q[PRE ? p : 0] = both(0.f);
     const float inv_d = 1.f / (float)a.D;
     int phase = 0;
     for (int slot = 0; row - behind < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1) {
         const bool live = row < a.rows;
-        const float rp = a.post && live ? a.rstd_post[row] : 1.f, rn = a.pre && live ? a.rstd_pre[row] : 1.f;
-        Part<T, TPR, VEC, NV, St::async> part[5];
+        const float rp = a.post && live ? a.rstd_post[row] : 1.f, rn = PRE && live ? a.rstd_pre[row] : 1.f;
+        Part<T, TPR, VEC, NV, St::async> part[ARR];
 #pragma unroll
-        for (int k = 0; k < 5; ++k) part[k].t = t, part[k].D = a.D, part[k].live = live;
+        for (int k = 0; k < ARR; ++k) part[k].t = t, part[k].D = a.D, part[k].live = live;
         if constexpr (St::async) {
             if constexpr (S > 1) load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
             copy_wait<S - 1>();
 #pragma unroll
-            for (int k = 0; k < 5; ++k) part[k].at = stages + (slot * 5 + k) * NV * NT + threadIdx.x;
-        } else if (live) {
-            part[0].row = static_cast<const T *>(a.y.p) + row_at(a, a.y, row);
-            if (a.gate) part[1].row = static_cast<const T *>(a.z.p) + row_at(a, a.z, row);
-            if (has_dx) part[2].row = static_cast<const T *>(a.dx.p) + row_at(a, a.dx, row);
-            if (a.pre) {
-                part[3].row = static_cast<const T *>(a.dh.p) + row_at(a, a.dh, row);
-                part[4].row = static_cast<const T *>(a.r.p) + row_at(a, a.r, row);
-            }
+            for (int k = 0; k < ARR; ++k) part[k].at = stages + (slot * ARR + k) * NV * NT + threadIdx.x;
+        } else {
+            if constexpr (S == 1) row_sync<TPR>(), load_row(row, 0);
+            copy_wait<(S > 1 ? S - 2 : 0)>();
+            row_sync<TPR>();   // all have this row, and none reads the last one any more
+            if constexpr (S > 1) load_row(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+#pragma unroll
+            for (int k = 0; k < ARR; ++k)
+                part[k].row = reinterpret_cast<const T *>(windows + (slot * ARR + k) * kArray +
+                                                          ((reinterpret_cast<uintptr_t>(view[k]->p) + row_at(a, *view[k], row) * sizeof(T)) & 15));
         }
         F2 d[NP], u[NP], v[NP];
-        if (a.pre) {
+        if constexpr (PRE) {
             part[3].template get<NT>(u);
             part[4].template get<NT>(v);
             F2 q = both(0.f);
@@ -376,25 +460,28 @@ __global__ void __launch_bounds__(bn_threads(TPR), BnStages<T, TPR, VEC, NV, 5>:
             const int col = col_of<TPR, VEC>(e, t);
             if (col < a.D) {
                 pp[col] = e & 1 ? hi(P[e / 2]) : lo(P[e / 2]);
-                pq[col] = e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]);
+                if constexpr (PRE) pq[col] = e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]);
             }
         }
     } else {
         // the sums of the block's rows of threads, in order
         constexpr int COLS = TPR * NV * VEC;
-        __shared__ float sum[2][COLS];
+        __shared__ float sum[PRE ? 2 : 1][COLS];
         for (int r = 0; r < RPB; ++r) {
             if ((int)threadIdx.x / TPR == r) {
 #pragma unroll
                 for (int e = 0; e < NV * VEC; ++e) {
                     const int col = col_of<TPR, VEC>(e, t);
                     sum[0][col] = (r ? sum[0][col] : 0.f) + (e & 1 ? hi(P[e / 2]) : lo(P[e / 2]));
-                    sum[1][col] = (r ? sum[1][col] : 0.f) + (e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]));
+                    if constexpr (PRE) sum[1][col] = (r ? sum[1][col] : 0.f) + (e & 1 ? hi(Q[e / 2]) : lo(Q[e / 2]));
                 }
             }
             __syncthreads();
         }
-        for (int col = threadIdx.x; col < a.D; col += blockDim.x) pp[col] = sum[0][col], pq[col] = sum[1][col];
+        for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
+            pp[col] = sum[0][col];
+            if constexpr (PRE) pq[col] = sum[1][col];
+        }
     }
 }
 
@@ -539,7 +626,11 @@ __global__ void __launch_bounds__(1024) block_norm_reduce_kernel(const BlockNorm
 constexpr int kBnMaxCols = 8192;
 
 // Calls f<TPR, EPT>: the threads of a row and the columns of each by the row's length.
-template <typename F>
+// The forward pass is held up by its two sums over a block: more threads of fewer
+// registers (32768 x 4096 bf16: 512 x 8 columns at three blocks an SM 212 us, 256 x 16 at
+// two 235).  The backward pass has more bytes to a sum and is not (324 us, 99% of the
+// measured copy rate, with 256 x 16).
+template <bool FWD, typename F>
 auto by_columns(int D, F f) {
     if (D <= 64) return f.template operator()<8, 8>();
     if (D <= 128) return f.template operator()<16, 8>();
@@ -547,60 +638,79 @@ auto by_columns(int D, F f) {
     if (D <= 512) return f.template operator()<32, 16>();
     if (D <= 1024) return f.template operator()<128, 8>();
     if (D <= 2048) return f.template operator()<256, 8>();
-    if (D <= 4096) return f.template operator()<256, 16>();
-    return f.template operator()<512, 16>();
+    if (D <= 4096) return f.template operator()<FWD ? 512 : 256, FWD ? 8 : 16>();
+    return f.template operator()<FWD ? 1024 : 512, FWD ? 8 : 16>();
 }
 
-template <typename T, bool BWD, bool VECTORS>
-struct Shape {
+// What a launch is: forward, backward without and with the second norm.
+enum BnPass { kBnFwd = 0, kBnBwd = 1, kBnBwdPre = 2 };
+template <typename T, int TPR, int EPT, int PASS, bool VECTORS>
+struct BnKernel {
+    static constexpr int VEC = VECTORS ? 16 / (int)sizeof(T) : 1, NV = EPT / VEC;
+    using St = std::conditional_t<PASS == kBnFwd, FwdStages<T, TPR, VEC, NV>, BwdStages<T, TPR, VEC, NV, PASS == kBnBwdPre>>;
+    static auto get() {
+        if constexpr (PASS == kBnFwd) return block_norm_fwd_kernel<T, TPR, VEC, NV>;
+        else return block_norm_bwd_kernel<T, TPR, VEC, NV, PASS == kBnBwdPre>;
+    }
+};
+template <typename T, int PASS, bool VECTORS>
+struct GridOf {
     long long rows;
     template <int TPR, int EPT>
     int operator()() const {   // blocks of the persistent grid
-        constexpr int VEC = VECTORS ? 16 / (int)sizeof(T) : 1;
-        using St = BnStages<T, TPR, VEC, EPT / VEC, BWD ? 5 : 3>;
         constexpr int rpb = bn_threads(TPR) / TPR;
-        return (int)std::min<long long>((rows + rpb - 1) / rpb, (long long)device_sm_count() * St::blocks);
+        return (int)std::min<long long>((rows + rpb - 1) / rpb, (long long)device_sm_count() * BnKernel<T, TPR, EPT, PASS, VECTORS>::St::blocks);
     }
 };
-template <typename T, bool BWD, bool VECTORS>
+template <typename T, int PASS, bool VECTORS>
 struct Launch {
     const BlockNormArgs &a;
     int grid;
     cudaStream_t s;
     template <int TPR, int EPT>
     cudaError_t operator()() const {
-        constexpr int VEC = VECTORS ? 16 / (int)sizeof(T) : 1;
-        constexpr int NV = EPT / VEC, smem = BnStages<T, TPR, VEC, NV, BWD ? 5 : 3>::smem;
-        void (*kernel)(const BlockNormArgs);
-        if constexpr (BWD) kernel = block_norm_bwd_kernel<T, TPR, VEC, NV>;
-        else kernel = block_norm_fwd_kernel<T, TPR, VEC, NV>;
+        using K = BnKernel<T, TPR, EPT, PASS, VECTORS>;
+        constexpr int smem = K::St::smem;
+        void (*kernel)(const BlockNormArgs) = K::get();
         if (smem > 40 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
-        return launch_dependent(kernel, dim3(grid), dim3(bn_threads(TPR)), smem, s, a);
+        BlockNormArgs b = a;
+        const long long step = (long long)grid * (bn_threads(TPR) / TPR), q = step / b.inner, r = step % b.inner;
+        b.inner_step = (uint32_t)r;
+        for (View *v : {&b.y, &b.z, &b.r, &b.dx, &b.dh}) {
+            v->ahead = q * v->so + r * v->si, v->wrap = v->so - (long long)b.inner * v->si;
+            if (v->p) v->end = static_cast<const T *>(v->p) + (b.rows / b.inner - 1) * v->so + (b.inner - 1ll) * v->si + b.D;
+        }
+        return launch_dependent(kernel, dim3(grid), dim3(bn_threads(TPR)), smem, s, b);
     }
 };
 
-template <typename T, bool BWD>
+template <typename T, int PASS>
 int grid_of(long long rows, int D, bool vec) {
     if (D > kBnMaxCols) return (int)std::min<long long>(rows, device_sm_count());
-    return vec ? by_columns(D, Shape<T, BWD, true>{rows}) : by_columns(D, Shape<T, BWD, false>{rows});
+    return vec ? by_columns<PASS == kBnFwd>(D, GridOf<T, PASS, true>{rows}) : by_columns<PASS == kBnFwd>(D, GridOf<T, PASS, false>{rows});
 }
-int bwd_grid(long long rows, int D, int dtype, bool vec) {
-    return dtype == GDN_BF16 ? grid_of<__nv_bfloat16, true>(rows, D, vec) : grid_of<float, true>(rows, D, vec);
+int bwd_grid(long long rows, int D, int dtype, bool vec, bool pre) {
+    if (dtype == GDN_BF16) return pre ? grid_of<__nv_bfloat16, kBnBwdPre>(rows, D, vec) : grid_of<__nv_bfloat16, kBnBwd>(rows, D, vec);
+    return pre ? grid_of<float, kBnBwdPre>(rows, D, vec) : grid_of<float, kBnBwd>(rows, D, vec);
 }
 
-template <typename T, bool BWD>
+template <typename T, int PASS>
 cudaError_t launch_rows(const BlockNormArgs &a, bool vec, cudaStream_t s) {
-    const int grid = grid_of<T, BWD>(a.rows, a.D, vec);
+    const int grid = grid_of<T, PASS>(a.rows, a.D, vec);
     if (a.D > kBnMaxCols) {
         void (*wide)(const BlockNormArgs);
-        if constexpr (BWD) wide = block_norm_wide_bwd_kernel<T>;
+        if constexpr (PASS != kBnFwd) wide = block_norm_wide_bwd_kernel<T>;
         else wide = block_norm_wide_fwd_kernel<T>;
         return launch_dependent(wide, dim3(grid), dim3(1024), 0, s, a);
     }
-    return vec ? by_columns(a.D, Launch<T, BWD, true>{a, grid, s}) : by_columns(a.D, Launch<T, BWD, false>{a, grid, s});
+    return vec ? by_columns<PASS == kBnFwd>(a.D, Launch<T, PASS, true>{a, grid, s}) : by_columns<PASS == kBnFwd>(a.D, Launch<T, PASS, false>{a, grid, s});
+}
+cudaError_t launch_bwd(const BlockNormArgs &a, int dtype, bool vec, cudaStream_t s) {
+    if (dtype == GDN_BF16) return a.pre ? launch_rows<__nv_bfloat16, kBnBwdPre>(a, vec, s) : launch_rows<__nv_bfloat16, kBnBwd>(a, vec, s);
+    return a.pre ? launch_rows<float, kBnBwdPre>(a, vec, s) : launch_rows<float, kBnBwd>(a, vec, s);
 }
 
 bool bn_elem_aligned(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == GDN_F32 ? 3u : 1u)) == 0; }
@@ -668,7 +778,7 @@ extern "C" gdn_status gdn_block_norm_fwd(const gdn_block_norm_desc *desc, const 
                      (!a.gate || bn_view_vec(d, d.gate, a.z.so, a.z.si)) && (!a.res || bn_view_vec(d, residual, r_outer_stride, r_inner_stride)) &&
                      aligned16(x) && (!a.pre || aligned16(h));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = d.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16, false>(a, vec, s) : launch_rows<float, false>(a, vec, s);
+    const cudaError_t e = d.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16, kBnFwd>(a, vec, s) : launch_rows<float, kBnFwd>(a, vec, s);
     if (e != cudaSuccess) {
         set_error_detail("launch block_norm_fwd", e);
         return GDN_ERR_CUDA;
@@ -681,7 +791,7 @@ extern "C" size_t gdn_block_norm_bwd_workspace_size(const gdn_block_norm_desc *d
     BlockNormArgs a;
     if (bn_args(desc, a) != GDN_OK) return 0;
     // alignment is not known here: the larger of both grids
-    const int grid = std::max(bwd_grid(a.rows, a.D, desc->dtype, true), bwd_grid(a.rows, a.D, desc->dtype, false));
+    const int grid = std::max(bwd_grid(a.rows, a.D, desc->dtype, true, a.pre), bwd_grid(a.rows, a.D, desc->dtype, false, a.pre));
     return std::max<size_t>(16, (size_t)grid * 2 * (size_t)a.D * sizeof(float));
 }
 
@@ -700,6 +810,7 @@ extern "C" gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const 
         if (!bn_elem_aligned(p, GDN_F32)) return GDN_ERR_INVALID_ARG;
     for (const void *p : {(const void *)dy, (const void *)dresidual, (const void *)dgate})
         if (!bn_elem_aligned(p, d.dtype)) return GDN_ERR_INVALID_ARG;
+    if ((dpost_weight && !a.post) || (dpre_weight && !a.pre)) return GDN_ERR_INVALID_ARG;
     const bool params = dpost_weight || dscale || dpre_weight;
     bool vec = false;
     if (a.rows > 0) {
@@ -727,10 +838,10 @@ extern "C" gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const 
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (a.rows > 0) e = d.dtype == GDN_BF16 ? launch_rows<__nv_bfloat16, true>(a, vec, s) : launch_rows<float, true>(a, vec, s);
+    if (a.rows > 0) e = launch_bwd(a, d.dtype, vec, s);
     if (e == cudaSuccess && params) {   // no rows: the sums are zero
-        const int blocks = a.rows > 0 ? bwd_grid(a.rows, a.D, d.dtype, vec) : 0;
-        e = launch_dependent(block_norm_reduce_kernel, dim3((a.D + 31) / 32, 2), dim3(1024), 0, s, a, blocks, dpost_weight, dscale, dpre_weight);
+        const int blocks = a.rows > 0 ? bwd_grid(a.rows, a.D, d.dtype, vec, a.pre) : 0;
+        e = launch_dependent(block_norm_reduce_kernel, dim3((a.D + 31) / 32, a.pre ? 2 : 1), dim3(1024), 0, s, a, blocks, dpost_weight, dscale, dpre_weight);
     }
     if (e != cudaSuccess) {
         set_error_detail("launch block_norm_bwd", e);
