@@ -112,8 +112,17 @@ def _levels(name, t):
 def _row_levels(tensors):
     """A common (outer, inner) for the rows of several [..., D] tensors of one shape,
     and their (outer, inner) strides."""
-    first = next(t for _, t in tensors if t is not None)
-    D, rows = first.shape[-1], first.numel() // first.shape[-1] if first.shape[-1] else 0
+    first = tensors[0][1]
+    D = first.shape[-1]
+    if first.dim() == 2:            # plain rows: a single-token call's path
+        rows, strides = first.shape[0], []
+        for name, t in tensors:
+            s = t.stride(0) if t is not None and rows > 1 else D
+            if s < D and rows:
+                raise ValueError("%s: rows overlap" % name)
+            strides.append((s, s))
+        return rows, 1, strides
+    rows = first.numel() // D if D else 0
     if rows == 0 or all(t is None or t.is_contiguous() for _, t in tensors):
         return rows, 1, [(D, D)] * len(tensors)
     levels = [_levels(name, t) if t is not None else [] for name, t in tensors]
@@ -224,9 +233,11 @@ def block_norm_bwd(dx, dh, y, x, rstd_post, rstd_pre, gate=None, post_weight=Non
         dy = on.empty(y.shape, dtype)
         dr = on.empty(y.shape, dtype) if residual else None
         dz = on.empty(y.shape, dtype) if gate is not None else None
-        grads = [on.empty((D,), _F32) if t is not None else None for t in (post_weight, scale, pre_weight)]
-        ws = None
-        if any(t is not None for t in grads):
+        given = [t is not None for t in (post_weight, scale, pre_weight)]
+        grads, ws = [None] * 3, None
+        if any(given):
+            rows = iter(on.empty((sum(given), D), _F32).unbind(0))
+            grads = [next(rows) if g else None for g in given]
             ws = _workspace(on, workspace, lib.gdn_block_norm_bwd_workspace_size(desc))
         rc = lib.gdn_block_norm_bwd(desc, _p(dx), *strides[0], _p(dh), *strides[1], _p(xs), *strides[2], _p(rstd_post),
                                     _p(rstd_pre), dy.data_ptr(), _p(dr), _p(dz), *(_p(t) for t in grads), _p(ws),

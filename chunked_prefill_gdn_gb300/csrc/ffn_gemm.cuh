@@ -186,7 +186,8 @@ struct Shape {
     static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128, stage = a_bytes + b_bytes;
     static constexpr bool boxes = !promote && BN == 256;
     static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? 6 : 4;
-    static constexpr int smem = 1024 + stages * stage + (boxes ? epi_warps * 4096 : 0);   // 1024: alignment
+    static constexpr int box_bytes = boxes ? 4096 : 1024;         // per warp: box, or room to turn 32 x 8 values
+    static constexpr int smem = 1024 + stages * stage + epi_warps * box_bytes;   // 1024: alignment
     static constexpr int per_sm = BN == 128 ? 2 : 1;
     static_assert(stages <= kMaxStages && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
 };
@@ -251,7 +252,8 @@ __device__ __forceinline__ void term_planes(int terms, int t, int &pa, int &pb) 
     pb = (0x010210 >> (4 * t)) & 15;   //           0 1 2 0 1 0
 }
 
-// E neighbouring columns of a row in type T, `live` of which exist.
+// E neighbouring columns of a row in type T, in 16-byte vectors where the row has them
+// all, else one by one.
 template <typename T, int E>
 __device__ __forceinline__ void store_cols(T *p, const float *v, int live, bool vec) {
     constexpr int V = 16 / (int)sizeof(T);
@@ -265,17 +267,56 @@ __device__ __forceinline__ void store_cols(T *p, const float *v, int live, bool 
     }
 }
 template <typename T, int E>
-__device__ __forceinline__ void load_cols(const T *p, float *v, int live, bool vec) {
+__device__ __forceinline__ void load_cols(const T *p, float *v) {
     constexpr int V = 16 / (int)sizeof(T);
-    if (vec && live >= E) {
-        Raw<T, V> r[E / V];
+    Raw<T, V> r[E / V];
 #pragma unroll
-        for (int i = 0; i < E / V; ++i) r[i] = load_raw<T, V>(p + i * V);
+    for (int i = 0; i < E / V; ++i) r[i] = load_raw<T, V>(p + i * V);
 #pragma unroll
-        for (int i = 0; i < E / V; ++i) unpack<T, V>(r[i], v + i * V);
-    } else {
+    for (int i = 0; i < E / V; ++i) unpack<T, V>(r[i], v + i * V);
+}
+// The same for the warp's 32 rows together, where rows are not 16-byte aligned or end
+// within the E columns: eight columns at a time are turned in shared memory, so that
+// neighbouring lanes access neighbouring columns (a lane per row alone touches 32 lines
+// with every access).  The tile's first row and column are given.
+template <typename T, int E>
+__device__ __forceinline__ void store_turned(T *base, long long ld, int row0, int col, int M, int N, const float *v, float *room, int lane) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = i < live ? to_f32(p[i]) : 0.f;
+    for (int j = 0; j < E; j += 8) {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) room[lane * 8 + (e ^ (lane & 7))] = v[j + e];
+        __syncwarp();
+        const int c = lane & 7;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3);
+            if (row0 + r < M && col + j + c < N) base[(long long)(row0 + r) * ld + col + j + c] = from_f32<T>(room[r * 8 + (c ^ (r & 7))]);
+        }
+    }
+}
+template <typename T, int E>
+__device__ __forceinline__ void load_turned(const T *base, long long ld, int row0, int col, int M, int N, float *v, float *room, int lane) {
+    const int c = lane & 7;
+    float t[E];
+#pragma unroll
+    for (int j = 0; j < E; j += 8)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3);
+            t[j + k] = row0 + r < M && col + j + c < N ? to_f32(base[(long long)(row0 + r) * ld + col + j + c]) : 0.f;
+        }
+#pragma unroll
+    for (int j = 0; j < E; j += 8) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3);
+            room[r * 8 + (c ^ (r & 7))] = t[j + k];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j + e] = room[lane * 8 + (e ^ (lane & 7))];
     }
 }
 // E columns into one plane (bf16) or three (fp32); ld is a multiple of 8, so whole
@@ -438,7 +479,7 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
     } else {
         const int quarter = warp & 3, part_of = (warp - 2) >> 2;   // the warp's lanes, and its CW columns
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * 4096;
+        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * S::box_bytes;
         const uint32_t box_at = tc::smem_u32(box);
         const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : 0u;
         uint32_t n = 0;
@@ -523,6 +564,19 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
             // first output column of the warp
             const int col = EPI == kUp ? i.n * (BN / 2) + part_of * (CW / 2) : i.n * BN + part_of * CW;
             constexpr int kUnroll = PROMOTE ? 1 : 4;
+            float *room = reinterpret_cast<float *>(box);
+            // E columns of a [M, N] tensor of rows ld apart, from column `at` on
+            auto store = [&](T *base, long long ld, int at, const float *v, bool vec) {
+                if (vec && at + E <= gr.N) {
+                    if (in) store_cols<T, E>(base + row * ld + at, v, E, true);
+                } else if (at < gr.N) {
+                    store_turned<T, E>(base, ld, row0, at, gr.M, gr.N, v, room, lane);
+                }
+            };
+            auto load = [&](const T *base, int at, float *v) {
+                if (g.vec_io && at + E <= gr.N) load_cols<T, E>(base + (long long)(in ? row : 0) * gr.N + at, v);
+                else load_turned<T, E>(base, gr.N, row0, at, gr.M, gr.N, v, room, lane);
+            };
             if (gr.splits > 1) {
 #pragma unroll kUnroll
                 for (int j = 0; j < CW; j += E) {
@@ -538,13 +592,13 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
                         T *dst = static_cast<T *>(o ? g.up : g.gate);
-                        if (BOXES && g.tma_io) box_free();
+                        if constexpr (BOXES) box_free();
 #pragma unroll kUnroll
                         for (int j = 0; j < CW / 2; j += E) {
                             float v[E];
                             get(CW / 2 * o + j, v);
                             if (BOXES && g.tma_io) put(v, j / 32);
-                            else if (in && col + j < gr.N) store_cols<T, E>(dst + (long long)row * gr.N + col + j, v, gr.N - col - j, g.vec_io);
+                            else store(dst, gr.N, col + j, v, g.vec_io);
                         }
                         if (BOXES && g.tma_io) box_out(&g.io[o], col, row0, gr.N, gr.M);
                     }
@@ -568,13 +622,12 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
 #pragma unroll 1
                     for (int part = 0; part < CW / 64; ++part) {
                         uint32_t pk[3][32];
+                        if (!g.vec_io || col + part * 64 + 64 > gr.N) box_free();   // load turns the values there
 #pragma unroll
                         for (int j = 0; j < 64; j += 32) {
                             float d[32], x[32], u[32];
-                            const int live = in ? gr.N - col - part * 64 - j : 0;
-                            const long long at = live > 0 ? (long long)row * gr.N + col + part * 64 + j : 0;
-                            load_cols<T, 32>(gate + at, x, live, g.vec_io);
-                            load_cols<T, 32>(up + at, u, live, g.vec_io);
+                            load(gate, col + part * 64 + j, x);
+                            load(up, col + part * 64 + j, u);
                             get(part * 64 + j, d);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
@@ -603,10 +656,8 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
 #pragma unroll 1
                     for (int j = 0; j < CW; j += E) {
                         float d[E], x[E], u[E];
-                        const int live = in ? gr.N - col - j : 0;
-                        const long long at = live > 0 ? (long long)row * gr.N + col + j : 0;
-                        load_cols<T, E>(gate + at, x, live, g.vec_io);
-                        load_cols<T, E>(up + at, u, live, g.vec_io);
+                        load(gate, col + j, x);
+                        load(up, col + j, u);
                         get(j, d);
 #pragma unroll
                         for (int e = 0; e < E; ++e) {
@@ -614,7 +665,7 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                             act_back(d[e], x[e], u[e], g.act, dg, du, h);
                             d[e] = dg, u[e] = du, x[e] = h;
                         }
-                        if (live > 0) {
+                        if (in && col + j < gr.N) {
                             const long long to = row * g.ld_plane + col + j;
                             const int room = (int)g.ld_plane - col - j;
                             store_planes<T, E>(g.planes[0] + to, g.plane_stride, d, room);
@@ -628,14 +679,14 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                 const bool box_it = BOXES && gr.tma_out;
 #pragma unroll
                 for (int part = 0; part < CW / 64; ++part) {
-                    if (box_it) box_free();
+                    if constexpr (BOXES) box_free();
 #pragma unroll kUnroll
                     for (int j = 0; j < 64; j += E) {
                         float v[E];
                         get(part * 64 + j, v);
                         const int at = col + part * 64 + j;
                         if (box_it) put(v, j / 32);
-                        else if (in && at < gr.N) store_cols<T, E>(out + row * gr.ld_out + at, v, gr.N - at, gr.vec_out);
+                        else store(out, gr.ld_out, at, v, gr.vec_out);
                     }
                     if (box_it) box_out(&g.c[gr.c], col + part * 64, row0, gr.N, gr.M);
                 }
