@@ -15,8 +15,9 @@ initial_state [N,H,dk,dv] fp32, cu_seqlens int32 [N+1] (then B = 1), all on
 the same CUDA device.
 
 The operators of the layer around the recurrence (layer norm, the short causal
-convolution, the selective scan, single-token steps) are in layer_ops and
-re-exported here.
+convolution, the selective scan, single-token steps) are in layer_ops, those of
+the layer's blocks (the norm between two blocks with its gate, scale and residual,
+the gated feed-forward block) in block_ops; both are re-exported here.
 """
 from __future__ import annotations
 

@@ -20,6 +20,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from .layer_ops import _CODE, _On, _act, _apart, _like, _p, _raise, _row_stride, _workspace, _wrote
 
@@ -88,6 +89,13 @@ def _read_status(word, on, where):
         _raise(st, where + " (device check)")
 
 
+def _plain(tensors):
+    """Whether a call needs no autograd function: no gradients, and outside of dual
+    levels, where there may be tangents (which those functions refuse)."""
+    return getattr(forward_ad, "_current_level", 0) < 0 and not (
+        torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors))
+
+
 # -------------------------------------------------------- between two blocks
 
 def _levels(name, t):
@@ -110,21 +118,21 @@ def _levels(name, t):
 
 
 def _row_levels(tensors):
-    """A common (outer, inner) for the rows of several [..., D] tensors of one shape,
-    and their (outer, inner) strides."""
+    """A common (outer, inner) for the rows of several [..., D] tensors of one shape
+    (the first is given), and their outer and inner strides one after the other."""
     first = tensors[0][1]
-    D = first.shape[-1]
-    if first.dim() == 2:            # plain rows: a single-token call's path
-        rows, strides = first.shape[0], []
+    D, strides = first.shape[-1], []
+    if first.dim() == 2:            # plain rows: the path of a few tokens, bound by the host
+        rows = first.shape[0]
         for name, t in tensors:
             s = t.stride(0) if t is not None and rows > 1 else D
             if s < D and rows:
                 raise ValueError("%s: rows overlap" % name)
-            strides.append((s, s))
+            strides += (s, s)
         return rows, 1, strides
     rows = first.numel() // D if D else 0
     if rows == 0 or all(t is None or t.is_contiguous() for _, t in tensors):
-        return rows, 1, [(D, D)] * len(tensors)
+        return rows, 1, [D] * (2 * len(tensors))
     levels = [_levels(name, t) if t is not None else [] for name, t in tensors]
     inner = 1
     for (name, _), at in zip(tensors, levels):
@@ -132,47 +140,43 @@ def _row_levels(tensors):
             if inner not in (1, at[1][0]):
                 raise ValueError("%s: its rows are in levels of %d, another input's of %d" % (name, at[1][0], inner))
             inner = at[1][0]
-    strides = []
     for at in levels:
         if len(at) == 2:
-            strides.append((at[0][1], at[1][1]))
+            strides += (at[0][1], at[1][1])
         else:
             s = at[0][1] if at else D
-            strides.append((s * inner, s))
+            strides += (s * inner, s)
     return rows // inner, inner, strides
-
-
-def _vectors(D, device, dtype, named):
-    """Type code of the [D] parameters (float32 or the activations' type, all alike)."""
-    given = [(n, t) for n, t in named if t is not None]
-    if not given:
-        return 1
-    w = given[0][1].dtype
-    if w != _F32 and w != dtype:
-        raise TypeError("%s must be float32 or %s, got %s" % (given[0][0], dtype, w))
-    for n, t in given:
-        _like(n, t, (D,), w, device)
-    return _CODE[w]
 
 
 def _norm_desc(y, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps, others):
     """Checks the operator's inputs; returns (descriptor, strides of `others`)."""
     _act("y", y)
-    D, dev, dtype = y.shape[-1], y.device, y.dtype
-    for name, t in (("gate", gate), *others):
-        if t is not None:
-            _like(name, t, y.shape, dtype, dev, strided=True)
+    shape, dev, dtype = y.shape, y.device, y.dtype
+    D = shape[-1]
+    tensors = (("y", y), ("gate", gate), *others)
+    for name, t in tensors:
+        if t is not None and not (t.shape == shape and t.dtype == dtype and t.device == dev and t.stride(-1) == 1):
+            _like(name, t, shape, dtype, dev, strided=True)
     if activation not in _GATES:
         raise ValueError("activation must be 'silu' or 'sigmoid', got %r" % (activation,))
     if post_weight is not None and not post_norm:
         raise ValueError("post_weight needs post_norm")
     if pre_weight is not None and not pre_norm:
         raise ValueError("pre_weight needs pre_norm")
-    wcode = _vectors(D, dev, dtype, (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)))
-    outer, inner, strides = _row_levels((("y", y), ("gate", gate), *others))
+    wtype = None    # of the [D] parameters: float32 or the activations' type, all alike
+    for name, t in (("post_weight", post_weight), ("scale", scale), ("pre_weight", pre_weight)):
+        if t is None:
+            continue
+        if wtype is None:
+            wtype = t.dtype
+            if wtype != _F32 and wtype != dtype:
+                raise TypeError("%s must be float32 or %s, got %s" % (name, dtype, wtype))
+        _like(name, t, shape[-1:], wtype, dev)
+    outer, inner, strides = _row_levels(tensors)
     return GdnBlockNormDesc(y.data_ptr(), _p(gate), _p(post_weight), _p(scale), _p(pre_weight), outer, inner, D,
-                            *strides[0], *strides[1], eps, 1 if post_norm else 0, 1 if pre_norm else 0,
-                            _GATES[activation], _CODE[dtype], wcode), strides[2:]
+                            *strides[:4], eps, 1 if post_norm else 0, 1 if pre_norm else 0,
+                            _GATES[activation], _CODE[dtype], 1 if wtype is None else _CODE[wtype]), strides[4:]
 
 
 def block_norm_fwd(y, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, post_norm: bool = True,
@@ -185,7 +189,7 @@ def block_norm_fwd(y, residual=None, gate=None, post_weight=None, scale=None, pr
     (None); residual, gate, scale and the weights are optional.  gate and residual have
     y's shape; weights and scale are [D] in float32 or y's type.  activation: 'silu' or
     'sigmoid'.  `out` receives x."""
-    desc, ((ro, ri),) = _norm_desc(y, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps,
+    desc, (ro, ri) = _norm_desc(y, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps,
                                    (("residual", residual),))
     dtype, dev = y.dtype, y.device
     if out is not None:
@@ -239,7 +243,7 @@ def block_norm_bwd(dx, dh, y, x, rstd_post, rstd_pre, gate=None, post_weight=Non
             rows = iter(on.empty((sum(given), D), _F32).unbind(0))
             grads = [next(rows) if g else None for g in given]
             ws = _workspace(on, workspace, lib.gdn_block_norm_bwd_workspace_size(desc))
-        rc = lib.gdn_block_norm_bwd(desc, _p(dx), *strides[0], _p(dh), *strides[1], _p(xs), *strides[2], _p(rstd_post),
+        rc = lib.gdn_block_norm_bwd(desc, _p(dx), *strides[:2], _p(dh), *strides[2:4], _p(xs), *strides[4:], _p(rstd_post),
                                     _p(rstd_pre), dy.data_ptr(), _p(dr), _p(dz), *(_p(t) for t in grads), _p(ws),
                                     ws.numel() if ws is not None else 0, on.raw)
         if rc != 0:
@@ -278,6 +282,8 @@ def block_norm(y, residual=None, gate=None, post_weight=None, scale=None, pre_we
                pre_norm: bool = True, activation: str = "silu", eps: float = 1e-5):
     """block_norm_fwd with autograd (every tensor); returns (x, h), h None without
     pre_norm."""
+    if _plain((y, residual, gate, post_weight, scale, pre_weight)):
+        return block_norm_fwd(y, residual, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps)[:2]
     return _BlockNorm.apply(y, residual, gate, post_weight, scale, pre_weight, post_norm, pre_norm, activation, eps)
 
 
@@ -370,5 +376,8 @@ class _GatedFfn(torch.autograd.Function):
 
 def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu"):
     """gated_ffn_fwd with autograd (x and the weights); returns y."""
-    save = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up, w_down))
-    return _GatedFfn.apply(x, w_gate, w_up, w_down, activation, save)
+    tensors = x, w_gate, w_up, w_down
+    if _plain(tensors):
+        return gated_ffn_fwd(*tensors, activation)[0]
+    save = torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+    return _GatedFfn.apply(*tensors, activation, save)

@@ -90,11 +90,11 @@ __device__ __forceinline__ float act_times(float g, float u, int act) {
     return g * act_sigmoid(g, act, slope) * u;
 }
 // dg = dh u act'(g), du = dh act(g), h = act(g) u.  Where the sigmoid has reached
-// 0 or 1 the slope's term is zero (p' may be large, not infinite, there).
+// 0 or 1 the slope's term is zero, whatever p' (infinite where g^2 is).
 __device__ __forceinline__ void act_back(float dh, float g, float u, int act, float &dg, float &du, float &h) {
     float slope;
-    const float s = act_sigmoid(g, act, slope), a = g * s;
-    dg = dh * u * fmaf(a * (1.f - s), slope, s);
+    const float s = act_sigmoid(g, act, slope), a = g * s, t = a * (1.f - s);
+    dg = dh * u * (t == 0.f ? s : fmaf(t, slope, s));
     du = dh * a;
     h = a * u;
 }

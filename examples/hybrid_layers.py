@@ -8,6 +8,10 @@ Each layer is norm -> projection -> short causal convolution -> recurrence ->
 projection, added to its input.  The weights are random; what is checked is that
 the single tokens continue the prompts as one longer prompt would, and that a
 training step lowers its loss.
+
+Block makes a layer a whole block of a model: the recurrence's heads normed and
+gated, the layer's output normed, scaled and added in the same pass that norms the
+feed-forward block's input, and that block's output added in turn.
 """
 from __future__ import annotations
 
@@ -63,21 +67,43 @@ class DeltaLayer(Layer):
 
     def prompt(self, x, cu):
         """x [1, T, model]; returns the output and the states of the sequences."""
-        h = self.norm(x)
+        y, state = self.mix_prompt(self.norm(x), cu)
+        return x + y, state
+
+    def mix_prompt(self, h, cu):
         u, conv = gdn.causal_conv(h @ self.p["w_qkv"], self.p["conv_w"], self.p["conv_b"], cu_seqlens=cu,
                                   output_final_state=True)
         o, s = gdn.chunk_gated_delta_rule(*self.split(u), *self.gates(h), output_final_state=True, cu_seqlens=cu,
                                           use_qk_l2norm_in_kernel=True)
-        return x + o.flatten(-2) @ self.p["w_out"], dict(conv=conv, s=s)
+        return self.heads_norm(o, h).flatten(-2) @ self.p["w_out"], dict(conv=conv, s=s)
+
+    def heads_norm(self, o, h):
+        return o
 
     def token(self, x, state, slots):
         """x [N, model], one token of the sequences whose states are in `slots`."""
-        h = self.norm(x)
+        return x + self.mix_token(self.norm(x), state, slots)
+
+    def mix_token(self, h, state, slots):
         u = gdn.causal_conv_step(h @ self.p["w_qkv"], state["conv"], self.p["conv_w"], self.p["conv_b"],
                                  state_indices=slots)
         o = gdn.gated_delta_step(*self.split(u), *self.gates(h), state["s"], use_qk_l2norm_in_kernel=True,
                                  state_indices=slots)
-        return x + o.flatten(-2) @ self.p["w_out"]
+        return self.heads_norm(o, h).flatten(-2) @ self.p["w_out"]
+
+
+class GatedDeltaLayer(DeltaLayer):
+    """With the heads of the recurrence's output normed and gated, as a delta-rule
+    layer has them: the gate is half of a projection and used as it lies."""
+
+    def __init__(self, model, heads, d, gen):
+        super().__init__(model, heads, d, gen)
+        self.p["w_z"] = self.matrix(model, heads * d, gen)
+        self.p["heads_w"] = torch.ones(d, device="cuda")
+
+    def heads_norm(self, o, h):
+        z = (h @ self.p["w_z"]).view(o.shape)
+        return gdn.block_norm(o, gate=z, post_weight=self.p["heads_w"], pre_norm=False)[0]
 
 
 class ScanLayer(Layer):
@@ -104,20 +130,68 @@ class ScanLayer(Layer):
                 dbc[..., self.rank:self.rank + self.n], dbc[..., self.rank + self.n:])
 
     def prompt(self, x, cu):
-        xz = self.norm(x) @ self.p["w_in"]
+        y, state = self.mix_prompt(self.norm(x), cu)
+        return x + y, state
+
+    def mix_prompt(self, h, cu):
+        xz = h @ self.p["w_in"]
         u, conv = gdn.causal_conv(xz[..., :self.channels], self.p["conv_w"], self.p["conv_b"], cu_seqlens=cu,
                                   output_final_state=True)
         y, s = gdn.selective_scan(u, *self.inputs(u), self.p["skip"], xz[..., self.channels:], self.p["dt_bias"],
                                   output_final_state=True, cu_seqlens=cu)
-        return x + y @ self.p["w_out"], dict(conv=conv, s=s)
+        return y @ self.p["w_out"], dict(conv=conv, s=s)
 
     def token(self, x, state, slots):
-        xz = self.norm(x) @ self.p["w_in"]
+        return x + self.mix_token(self.norm(x), state, slots)
+
+    def mix_token(self, h, state, slots):
+        xz = h @ self.p["w_in"]
         u = gdn.causal_conv_step(xz[..., :self.channels], state["conv"], self.p["conv_w"], self.p["conv_b"],
                                  state_indices=slots)
         y = gdn.selective_scan_step(u, *self.inputs(u), state["s"], self.p["skip"], xz[..., self.channels:],
                                     self.p["dt_bias"], state_indices=slots)
-        return x + y @ self.p["w_out"]
+        return y @ self.p["w_out"]
+
+
+class Block:
+    """A layer, and the feed-forward block after it."""
+
+    def __init__(self, layer, hidden, gen):
+        self.layer, self.model = layer, layer.model
+        ones = lambda: torch.ones(self.model, device="cuda")   # noqa: E731
+        self.p = dict(in_w=ones(), mix_w=ones(), mix_scale=0.5 * ones(), ffn_in_w=ones(), ffn_w=ones(), ffn_scale=0.5 * ones(),
+                      w_gate=layer.matrix(hidden, self.model, gen), w_up=layer.matrix(hidden, self.model, gen),
+                      w_down=layer.matrix(self.model, hidden, gen))
+        for name, rows in (("w_gate", hidden), ("w_up", hidden), ("w_down", self.model)):   # rows are outputs here
+            self.p[name] = self.p[name] * (rows / self.p[name].shape[1]) ** 0.5
+
+    def parameters(self):
+        own = [t for name, t in self.layer.p.items() if name not in ("norm_w", "norm_b")]
+        return own + list(self.p.values())
+
+    def new_state(self, slots):
+        return self.layer.new_state(slots)
+
+    def norm(self, x):
+        return gdn.block_norm(x, post_weight=self.p["in_w"], pre_norm=False)[0]
+
+    def after(self, x, y):
+        """From the layer's output on: x and y [..., model]."""
+        x, h = gdn.block_norm(y, x, None, self.p["mix_w"], self.p["mix_scale"], self.p["ffn_in_w"])
+        f = gdn.gated_ffn(h, self.p["w_gate"], self.p["w_up"], self.p["w_down"])
+        return gdn.block_norm(f, x, None, self.p["ffn_w"], self.p["ffn_scale"], pre_norm=False)[0]
+
+    def prompt(self, x, cu):
+        y, state = self.layer.mix_prompt(self.norm(x), cu)
+        return self.after(x, y), state
+
+    def token(self, x, state, slots):
+        return self.after(x, self.layer.mix_token(self.norm(x), state, slots))
+
+
+def make_blocks(model=256, heads=2, d=128, channels=512, n=16, hidden=640, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    return [Block(GatedDeltaLayer(model, heads, d, gen), hidden, gen), Block(ScanLayer(model, channels, n, gen), hidden, gen)]
 
 
 def make_model(model=256, heads=2, d=128, channels=512, n=16, seed=0):
@@ -199,5 +273,17 @@ def main():
     return err, losses
 
 
+def main_blocks():
+    """The same with whole blocks."""
+    blocks = make_blocks()
+    got, want = serve(blocks)
+    err = float((got.float() - want.float()).norm() / want.float().norm())
+    print("blocks: single tokens against one longer prompt: relative difference %.2e" % err)
+    losses = train(blocks)
+    print("blocks: training: loss " + " -> ".join("%.4f" % v for v in losses))
+    return err, losses
+
+
 if __name__ == "__main__":
     main()
+    main_blocks()

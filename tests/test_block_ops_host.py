@@ -120,6 +120,8 @@ def test_levels_of_rows():
         block_ops._levels("t", t.view(-1).as_strided((5, 16), (8, 1)))
     heads = t[:, :, :4]
     outer, inner, strides = block_ops._row_levels((("a", heads), ("b", heads.contiguous()), ("c", None)))
-    assert (outer, inner) == (24, 4) and strides == [(160, 16), (64, 16), (64, 16)]
+    assert (outer, inner) == (24, 4) and strides == [160, 16, 64, 16, 64, 16]
+    assert block_ops._row_levels((("a", t[0, 0]), ("b", None))) == (10, 1, [16, 16, 16, 16])
+    assert block_ops._row_levels((("a", torch.zeros(8, 32)[:, :16]), ("b", torch.zeros(8, 16)))) == (8, 1, [32, 32, 16, 16])
     with pytest.raises(ValueError, match="levels of"):
         block_ops._row_levels((("a", heads), ("b", torch.zeros(4, 12, 4, 16)[:, :6])))

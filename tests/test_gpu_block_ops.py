@@ -391,6 +391,11 @@ def test_gated_ffn_far_values(act):
     assert torch.allclose(y, want, rtol=1e-6, atol=1e-25)
     dx = gdn.gated_ffn_bwd(torch.ones_like(y), x, *w, gate, up, activation=act)[0]
     assert torch.allclose(dx, torch.where(x > 0, 2 * x, torch.zeros_like(x)), rtol=1e-6, atol=1e-25)
+    # where g^2 overflows too: act'(g) is 1 or 0
+    far = torch.tensor([[3e25], [-3e25]], device="cuda")
+    one = torch.ones_like(far)
+    dx, _, _, _ = gdn.gated_ffn_bwd(one, one, *w, far, one, activation=act)
+    assert torch.allclose(dx, torch.tensor([[1.0 + 3e25], [0.0]], device="cuda"), rtol=1e-6, atol=0.0)
 
 
 def test_gated_ffn_autograd_matches_torch():
@@ -408,7 +413,114 @@ def test_gated_ffn_autograd_matches_torch():
     assert not gdn.gated_ffn(*frozen).requires_grad
 
 
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: the first, a middle and the last rows."""
+    g = rng(3)
+    rows, D = 525000, 4096
+    base = normal(g, 1000, D, to="bf16")
+    y = base.repeat(rows // 1000, 1)
+    w = 1 + normal(g, D, std=0.2)
+    x, h, rp, rn = gdn.block_norm_fwd(y, y, y, w, w, w)
+    want = gdn.block_norm_fwd(base, base, base, w, w, w)
+    grads = gdn.block_norm_bwd(x, h, y, x, rp, rn, y, w, w, w)
+    small = gdn.block_norm_bwd(want[0], want[1], base, *(want[0], want[2], want[3]), base, w, w, w)
+    for at in (0, 1000 * 262, rows - 1000):
+        for a, b in zip((x, h, rp, rn), want):
+            assert torch.equal(a[at:at + 1000], b)
+        for a, b in zip(grads[:3], small[:3]):
+            assert torch.equal(a[at:at + 1000], b)
+    for a, b in zip(grads[3:], small[3:]):
+        assert (a / (rows // 1000) - b).norm() <= 1e-5 * b.norm()
+    del y, x, h, grads
+    M, D, F = 70000, 64, 32768
+    base = normal(g, 1000, D, to="bf16")
+    ws = [normal(g, F, D, std=D ** -0.5, to="bf16"), normal(g, F, D, std=D ** -0.5, to="bf16"), normal(g, D, F, std=F ** -0.5, to="bf16")]
+    X = base.repeat(M // 1000, 1)
+    y, gate, up = gdn.gated_ffn_fwd(X, *ws, save=True)
+    dx = gdn.gated_ffn_bwd(X, X, *ws, gate, up, needs=(True, False, False, False))[0]
+    c = Ffn.__new__(Ffn)
+    c.dtype, c.x, c.dy, c.w = "bf16", base[:40], base[:40], ws
+    for at in (0, 35000, M - 1000):
+        c.check_forward(y[at:at + 40], gate[at:at + 40], up[at:at + 40], "silu")
+        want = ref.gated_ffn_backward(num(base[:40]), num(base[:40]), *(num(t) for t in ws), num(gate[at:at + 40]), num(up[at:at + 40]))[0][0]
+        c.rel("dx", dx[at:at + 40], want)
+
+
+@pytest.mark.parametrize("M", [2, 8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_ffn_every_count_of_tokens_beside_a_limit(M, dtype):
+    """Around the counts at which the products change their kernel, rows of an odd pitch among them."""
+    for D, F, O in ((520, 1032, 264), (131, 257, 45)):
+        c = Ffn(M, D, F, O, dtype)
+        y, gate, up = gdn.gated_ffn_fwd(c.x, *c.w, save=True, check=True)
+        c.check_forward(y, gate, up, "silu")
+
+
+def test_single_row_without_a_leading_axis():
+    c = Ffn(1, 64, 128, 72, "bf16")
+    y, gate, up = gdn.gated_ffn_fwd(c.x[0], *c.w, save=True)
+    assert y.shape == (72,) and gate.shape == up.shape == (128,)
+    assert torch.equal(y, gdn.gated_ffn_fwd(c.x, *c.w)[0][0])
+    n = Norm(1, 64, "f32", "f32", "pgrsn")
+    want = n.forward()
+    n.y, n.r, n.z = n.y[0], n.r[0], n.z[0]
+    for a, b in zip(n.forward(), want):
+        assert torch.equal(a, b[0])
+
+
 # ----------------------------------------------------------------- both together
+
+def test_two_calls_at_once():
+    """Calls on two streams at the same time give what they give alone."""
+    cs = [Ffn(900, 256, 1000, 256, "bf16", seed=1), Ffn(700, 300, 800, 200, "f32", seed=2)]
+    ns = [Norm(4000, 512, "bf16", "f32", "pgrsn", seed=1), Norm(3000, 130, "f32", "f32", "pg", seed=2)]
+
+    def run(c, n, stream=None):
+        y, gate, up = gdn.gated_ffn_fwd(c.x, *c.w, save=True, stream=stream)
+        x, h, rp, rn = n.forward(stream=stream)
+        return (y, *gdn.gated_ffn_bwd(c.dy, c.x, *c.w, gate, up, stream=stream), x, *n.backward(x, rp, rn, stream=stream))
+
+    want = [run(c, n) for c, n in zip(cs, ns)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(3):
+        for i, (c, n) in enumerate(zip(cs, ns)):
+            got[i].append(run(c, n, streams[i]))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for i in range(2):
+        for again in got[i]:
+            for a, b in zip(again, want[i]):
+                assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_training_step_in_a_graph():
+    """Forward and backward through autograd, captured and replayed on new inputs."""
+    g = rng(21)
+    M, D, F = 150, 128, 320
+    w = [normal(g, F, D, std=D ** -0.5), normal(g, F, D, std=D ** -0.5), normal(g, D, F, std=F ** -0.5), 1 + normal(g, D, std=0.1)]
+    w = [t.requires_grad_() for t in w]
+    x = normal(g, M, D)
+
+    def step():
+        r, h = gdn.block_norm(x, x, x, w[3], w[3], w[3])
+        y, _ = gdn.block_norm(gdn.gated_ffn(h, *w[:3]), r, None, w[3], pre_norm=False)
+        return torch.autograd.grad(y.square().sum(), w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    x.copy_(normal(g, M, D))
+    graph.replay()
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
 
 def test_layer_on_another_stream_and_in_a_graph():
     """norm -> feed-forward -> norm, on a stream of its own and replayed from a captured
