@@ -15,7 +15,9 @@
 // two to an SM, for few rows (bound by the weights' bytes) and for small products.
 // The accumulators are in tensor memory, two sets of BN columns, so that the epilogue
 // of one tile runs under the products of the next.  Warps: 0 loads, 1 issues the
-// products, the others are the epilogue, a quarter of the lanes and CW columns each.
+// products, the others are the epilogue, a quarter of the lanes and CW columns each: eight warps, and 16 where the
+// epilogue is the longer part (backward pass's first product of 8192 x 256 x 8192: 190 us,
+// with eight 229; the forward one with gate and up kept is 4% faster with eight).
 // bf16 outputs leave through a box per warp in shared memory by TMA stores.  A sixth
 // stage of operands is worth more than a second box per warp, or than boxes into which
 // the backward pass's gate and up are loaded ahead (8191 x 4096 x 12288: first backward
@@ -55,7 +57,7 @@ struct Group {
     int a_mn, b_mn, tma_out, vec_out;
     void *out;                // kPlain: [M, N], rows ld_out apart
     long long ld_out;
-    float *partial;           // splits > 1: [split][kUp ? 2 : 1][M][ld_part]
+    float *partial;           // or null: parts of sums, [split][kUp ? 2 : 1][M][ld_part]
     long long ld_part;
 };
 struct GemmArgs {
@@ -97,6 +99,40 @@ __device__ __forceinline__ void act_back(float dh, float g, float u, int act, fl
     dg = dh * u * (t == 0.f ? s : fmaf(t, slope, s));
     du = dh * a;
     h = a * u;
+}
+
+// The same on pairs, for an activation that is known (ACT).
+template <int ACT>
+__device__ __forceinline__ F2 act_sigmoid2(F2 g, F2 &slope) {
+    if constexpr (ACT == 0) return sigmoid_pair(g);
+    const F2 q = mul2(g, g);
+    slope = mul2(both(kGelu1), fma2(both(3.f * kGelu3), q, both(1.f)));
+    return sigmoid_pair(mul2(mul2(both(kGelu1), g), fma2(both(kGelu3), q, both(1.f))));
+}
+// x = act(x) u
+template <int ACT, int E>
+__device__ __forceinline__ void act_times_cols(float (&x)[E], const float (&u)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        F2 slope;
+        const F2 g = pair(x[e], x[e + 1]), h = mul2(mul2(g, act_sigmoid2<ACT>(g, slope)), pair(u[e], u[e + 1]));
+        x[e] = lo(h), x[e + 1] = hi(h);
+    }
+}
+// (dh, g, u) = (dg, h, du)
+template <int ACT, int E>
+__device__ __forceinline__ void act_back_cols(float (&d)[E], float (&x)[E], float (&u)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        F2 slope;
+        const F2 g = pair(x[e], x[e + 1]), uu = pair(u[e], u[e + 1]), dh = pair(d[e], d[e + 1]);
+        const F2 s = act_sigmoid2<ACT>(g, slope), a = mul2(g, s), t = mul2(a, fma2(s, both(-1.f), both(1.f)));
+        F2 f;
+        if constexpr (ACT == 0) f = add2(t, s);
+        else f = pair(lo(t) == 0.f ? lo(s) : fmaf(lo(t), lo(slope), lo(s)), hi(t) == 0.f ? hi(s) : fmaf(hi(t), hi(slope), hi(s)));
+        const F2 dg = mul2(mul2(dh, uu), f), du = mul2(dh, a), h = mul2(a, uu);
+        d[e] = lo(dg), d[e + 1] = hi(dg), u[e] = lo(du), u[e + 1] = hi(du), x[e] = lo(h), x[e + 1] = hi(h);
+    }
 }
 
 // x = p0 + p1 + p2 (three roundings to nearest); what is not finite stays in p0.
@@ -180,16 +216,17 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LATER) : "memory");
 }
 
-template <typename T, int CTAS, int BN>
+template <int EPI, typename T, int CTAS, int BN>
 struct Shape {
     static constexpr bool promote = sizeof(T) == 4;
-    // fp32 keeps its sums in registers: 64 columns per warp; else 128
-    static constexpr int CW = promote ? 64 : 128, epi_warps = BN * 4 / CW, threads = 64 + 32 * epi_warps;
+    // columns per warp of the epilogue: 64 where it holds sums (fp32) or is long (kBack)
+    static constexpr int CW = promote || EPI == kBack ? 64 : 128, epi_warps = BN * 4 / CW, threads = 64 + 32 * epi_warps;
+    static constexpr int box_cols = CW / 2;                      // of a box of 32 rows
     static constexpr int b_rows = BN / CTAS;                     // of B in this CTA
     static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128, stage = a_bytes + b_bytes;
     static constexpr bool boxes = !promote && BN == 256;
     static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? 6 : 4;
-    static constexpr int box_bytes = boxes ? 4096 : 1024;         // per warp: box, or room to turn 32 x 8 values
+    static constexpr int box_bytes = boxes ? 64 * box_cols : 1024;   // per warp: the box, or room to turn 32 x 8 values
     static constexpr int smem = 1024 + stages * stage + epi_warps * box_bytes;   // 1024: alignment
     static constexpr int per_sm = BN == 128 ? 2 : 1;
     static_assert(stages <= kMaxStages && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
@@ -342,9 +379,9 @@ __device__ __forceinline__ void store_planes(__nv_bfloat16 *p, long long stride,
 }
 
 template <int EPI, typename T, int CTAS, int BN>
-__global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN>::per_sm)
+__global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T, CTAS, BN>::per_sm)
     ffn_gemm_kernel(const __grid_constant__ GemmArgs g) {
-    using S = Shape<T, CTAS, BN>;
+    using S = Shape<EPI, T, CTAS, BN>;
     constexpr bool PROMOTE = S::promote, BOXES = S::boxes;
     constexpr int CW = S::CW, E = PROMOTE ? 16 : 32;   // columns of a step of the epilogue
     extern __shared__ uint8_t raw[];
@@ -487,12 +524,15 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
         const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : 0u;
         uint32_t n = 0;
         bool ok = true;
-        // 32 packed columns of a row into half `part` of the box (swizzled as TMA reads it)
+        // chunk c of a row of the box, swizzled as TMA reads it; 32 packed columns from chunk 4 part on
+        auto put16 = [&](int c, uint4 v) {
+            tc::sts_u4(box_at + (S::box_cols == 64 ? tc::sw128_offset(lane, c) : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)), v);
+        };
         auto put = [&](const float *v, int part) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const Raw<__nv_bfloat16, 8> r = pack<__nv_bfloat16, 8>(v + 8 * c);
-                tc::sts_u4(box_at + tc::sw128_offset(lane, part * 4 + c), make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+                put16(4 * part + c, make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
             }
         };
         auto box_free = [&]() {   // the last store has read it
@@ -559,14 +599,15 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                 from = tmem + (n & 1) * BN + lanes;
             }
             if (!ok) break;
-            auto get = [&](int j, float *v) {   // columns j .. j + E - 1 of the warp's
-                if constexpr (E == 16) tc::tmem_ld16(from + column(j), reinterpret_cast<uint32_t *>(v));
+            auto get = [&](int j, auto &v) {   // the warp's columns from j on, as many as v holds
+                constexpr int W = sizeof(v) / 4;
+                if constexpr (W == 16) tc::tmem_ld16(from + column(j), reinterpret_cast<uint32_t *>(v));
                 else tc::tmem_ld32(from + column(j), reinterpret_cast<uint32_t *>(v));
                 tc::tmem_wait_ld();
             };
             // first output column of the warp
             const int col = EPI == kUp ? i.n * (BN / 2) + part_of * (CW / 2) : i.n * BN + part_of * CW;
-            constexpr int kUnroll = PROMOTE ? 1 : 4;
+            constexpr int kUnroll = PROMOTE ? 1 : 2;
             float *room = reinterpret_cast<float *>(box);
             // E columns of a [M, N] tensor of rows ld apart, from column `at` on
             auto store = [&](T *base, long long ld, int at, const float *v, bool vec) {
@@ -576,12 +617,13 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                     store_turned<T, E>(base, ld, row0, at, gr.M, gr.N, v, room, lane);
                 }
             };
-            auto load = [&](const T *base, int at, float *v) {
-                if (g.vec_io && at + E <= gr.N) load_cols<T, E>(base + (long long)(in ? row : 0) * gr.N + at, v);
-                else load_turned<T, E>(base, gr.N, row0, at, gr.M, gr.N, v, room, lane);
+            auto load = [&](const T *base, int at, auto &v) {
+                constexpr int W = sizeof(v) / 4;
+                if (g.vec_io && at + W <= gr.N) load_cols<T, W>(base + (long long)(in ? row : 0) * gr.N + at, v);
+                else load_turned<T, W>(base, gr.N, row0, at, gr.M, gr.N, v, room, lane);
             };
-            if (gr.splits > 1) {
-#pragma unroll kUnroll
+            if (gr.partial) {
+#pragma unroll 1
                 for (int j = 0; j < CW; j += E) {
                     float v[E];
                     get(j, v);
@@ -612,8 +654,8 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                     float x[E], u[E];
                     get(j, x);
                     get(CW / 2 + j, u);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] = act_times(x[e], u[e], g.act);
+                    if (g.act) act_times_cols<1, E>(x, u);
+                    else act_times_cols<0, E>(x, u);
                     if constexpr (BOXES) put(x, j / 32);
                     else if (in && col + j < gr.N)
                         store_planes<T, E>(g.planes[0] + row * g.ld_plane + col + j, g.plane_stride, x, (int)g.ld_plane - col - j);
@@ -621,77 +663,63 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
                 if constexpr (BOXES) box_out(&g.c[0], col, row0, gr.N, gr.M);
             } else if constexpr (EPI == kBack) {
                 const T *gate = static_cast<const T *>(g.gate), *up = static_cast<const T *>(g.up);
-                if constexpr (BOXES) {
+                constexpr int W = 16;   // columns at a time: three values of each in registers
+                auto step = [&](int j, float (&d)[W], float (&x)[W], float (&u)[W]) {
+                    load(gate, col + j, x);
+                    load(up, col + j, u);
+                    get(j, d);
+                    if (g.act) act_back_cols<1, W>(d, x, u);
+                    else act_back_cols<0, W>(d, x, u);
+                };
 #pragma unroll 1
-                    for (int part = 0; part < CW / 64; ++part) {
-                        uint32_t pk[3][32];
-                        if (!g.vec_io || col + part * 64 + 64 > gr.N) box_free();   // load turns the values there
+                for (int j = 0; j < CW; j += BOXES ? 32 : W) {
+                    float d[W], x[W], u[W];
+                    if constexpr (BOXES) {
+                        if (!g.vec_io || col + j + 32 > gr.N) box_free();   // load turns the values there
+                        uint32_t pk[3][16];
 #pragma unroll
-                        for (int j = 0; j < 64; j += 32) {
-                            float d[32], x[32], u[32];
-                            load(gate, col + part * 64 + j, x);
-                            load(up, col + part * 64 + j, u);
-                            get(part * 64 + j, d);
+                        for (int half = 0; half < 2; ++half) {
+                            step(j + 16 * half, d, x, u);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float dg, du, h;
-                                act_back(d[e], x[e], u[e], g.act, dg, du, h);
-                                d[e] = dg, u[e] = du, x[e] = h;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                pk[0][j / 2 + e] = tc::pack_bf16x2(d[2 * e], d[2 * e + 1]);
-                                pk[1][j / 2 + e] = tc::pack_bf16x2(u[2 * e], u[2 * e + 1]);
-                                pk[2][j / 2 + e] = tc::pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                            for (int e = 0; e < 8; ++e) {
+                                pk[0][8 * half + e] = tc::pack_bf16x2(d[2 * e], d[2 * e + 1]);
+                                pk[1][8 * half + e] = tc::pack_bf16x2(u[2 * e], u[2 * e + 1]);
+                                pk[2][8 * half + e] = tc::pack_bf16x2(x[2 * e], x[2 * e + 1]);
                             }
                         }
 #pragma unroll
                         for (int o = 0; o < 3; ++o) {
                             box_free();
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                tc::sts_u4(box_at + tc::sw128_offset(lane, c),
-                                           make_uint4(pk[o][4 * c], pk[o][4 * c + 1], pk[o][4 * c + 2], pk[o][4 * c + 3]));
-                            box_out(&g.c[o], col + part * 64, row0, gr.N, gr.M);
+                            for (int c = 0; c < 4; ++c) put16(c, make_uint4(pk[o][4 * c], pk[o][4 * c + 1], pk[o][4 * c + 2], pk[o][4 * c + 3]));
+                            box_out(&g.c[o], col + j, row0, gr.N, gr.M);
                         }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int j = 0; j < CW; j += E) {
-                        float d[E], x[E], u[E];
-                        load(gate, col + j, x);
-                        load(up, col + j, u);
-                        get(j, d);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            float dg, du, h;
-                            act_back(d[e], x[e], u[e], g.act, dg, du, h);
-                            d[e] = dg, u[e] = du, x[e] = h;
-                        }
+                    } else {
+                        step(j, d, x, u);
                         if (in && col + j < gr.N) {
                             const long long to = row * g.ld_plane + col + j;
-                            const int room = (int)g.ld_plane - col - j;
-                            store_planes<T, E>(g.planes[0] + to, g.plane_stride, d, room);
-                            store_planes<T, E>(g.planes[1] + to, g.plane_stride, u, room);
-                            store_planes<T, E>(g.planes[2] + to, g.plane_stride, x, room);
+                            const int room_left = (int)g.ld_plane - col - j;
+                            store_planes<T, W>(g.planes[0] + to, g.plane_stride, d, room_left);
+                            store_planes<T, W>(g.planes[1] + to, g.plane_stride, u, room_left);
+                            store_planes<T, W>(g.planes[2] + to, g.plane_stride, x, room_left);
                         }
                     }
                 }
             } else {
                 T *out = static_cast<T *>(gr.out);
                 const bool box_it = BOXES && gr.tma_out;
+                constexpr int STEP = BOXES ? S::box_cols : CW;
 #pragma unroll
-                for (int part = 0; part < CW / 64; ++part) {
+                for (int part = 0; part < CW; part += STEP) {
                     if constexpr (BOXES) box_free();
 #pragma unroll kUnroll
-                    for (int j = 0; j < 64; j += E) {
+                    for (int j = 0; j < STEP; j += E) {
                         float v[E];
-                        get(part * 64 + j, v);
-                        const int at = col + part * 64 + j;
+                        get(part + j, v);
                         if (box_it) put(v, j / 32);
-                        else store(out, gr.ld_out, at, v, gr.vec_out);
+                        else store(out, gr.ld_out, col + part + j, v, gr.vec_out);
                     }
-                    if (box_it) box_out(&g.c[gr.c], col + part * 64, row0, gr.N, gr.M);
+                    if (box_it) box_out(&g.c[gr.c], col + part, row0, gr.N, gr.M);
                 }
             }
             done();
@@ -713,7 +741,7 @@ __global__ void __launch_bounds__(Shape<T, CTAS, BN>::threads, Shape<T, CTAS, BN
 
 template <int EPI, typename T, int CTAS, int BN>
 cudaError_t launch_gemm(const GemmArgs &g, int grid, cudaStream_t s) {
-    using S = Shape<T, CTAS, BN>;
+    using S = Shape<EPI, T, CTAS, BN>;
     cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, CTAS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

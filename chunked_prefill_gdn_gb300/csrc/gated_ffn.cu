@@ -45,7 +45,8 @@ struct Mat {
     int planes;
 };
 
-bool encode(CUtensorMap *map, const Mat &m, int box_rows) {
+// box_cols: 64, or 32 for the outputs of kBack (128 or 64 bytes a row, swizzled as wide).
+bool encode(CUtensorMap *map, const Mat &m, int box_rows, int box_cols = 64) {
     const EncodeFn fn = encode_fn();
     if (!fn) {
         set_error_detail("driver entry point cuTensorMapEncodeTiled", cudaErrorNotSupported);
@@ -54,9 +55,10 @@ bool encode(CUtensorMap *map, const Mat &m, int box_rows) {
     const long long ld = m.rows > 1 ? m.ld : (m.cols + 7) / 8 * 8;
     const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.planes};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(m.planes > 1 ? m.plane : ld * m.rows) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(m.p), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) set_error_detail("encode tensor map", cudaErrorInvalidValue, (int)r);
     return r == CUDA_SUCCESS;
@@ -123,7 +125,7 @@ template <int EPI, typename T>
 __global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs f) {
     grid_dependency_wait();
     const FinishGroup &a = f.group[blockIdx.y];
-    const long long per = (a.N + 3) / 4, total = a.splits > 1 ? a.M * per : 0, matrix = a.M * a.ld_part;
+    const long long per = (a.N + 3) / 4, total = a.partial ? a.M * per : 0, matrix = a.M * a.ld_part;
     auto sum = [&](long long at, float (&v)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = 0.f;
@@ -212,12 +214,14 @@ struct Batch {
 int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
 long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Tile shape and parts of a batch, by a model in clocks.  A block of K takes a pair 512 of
-// the tensor pipe for each term; a single CTA of 256 columns a little more (it reads twice as
+// Tile shape and parts of a batch, by a model in clocks (1.9 a ns).  A block of K takes a pair
+// 512 of the tensor pipe for each term; a single CTA of 256 columns more (it reads twice as
 // much of B); two CTAs of 128 columns share their SM and are held by shared memory, 700 each.
-// A tile takes at least its epilogue; a launch 4000 to 7000 to fill and drain; the operands come at
-// 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another launch
-// and their traffic.
+// A tile takes at least its epilogue; a launch 4000 to 7000 to fill and drain; the operands
+// come at 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another
+// launch and its traffic.  For fp32 the backward pass's first product may leave as one part:
+// its epilogue with three outputs of three planes takes 57 us a tile (8192 x 256 x 2048: 230 us
+// in all), which the second kernel with its rows in order does in less where K is short.
 Plan plan_batch(const Batch &b, const Problem &pr) {
     Plan best = {};
     double best_cost = 1e300;
@@ -225,6 +229,7 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
     const int which = b.epi == kUp ? 2 : 1;
     long long kmax = 1;
     double bytes = 0;
+    const double beside = (double)b.p[0].M * b.p[0].N * (pr.f32 ? 26 : 10);   // kBack: gate and up in, three outputs
     for (int i = 0; i < b.n; ++i) {
         const Product &p = b.p[i];
         kmax = std::max<long long>(kmax, (long long)blocks(p.k) * p.pairs);
@@ -234,59 +239,63 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
     for (int tile = 0; tile < 3; ++tile) {
         const int ctas = tile == kPair ? 2 : 1, bn = tile == kSmall ? 128 : 256, cols = b.epi == kUp ? bn / 2 : bn;
         const int P = tile == kPair ? sms / 2 : tile == kWide ? sms : 2 * sms;
-        const double epi = (b.epi == kBack ? 14000 : b.epi == kUp ? 7000 : 4000) * (tile == kSmall ? 0.8 : 1.0) * (pr.f32 ? 1.5 : 1.0);
+        const double direct = (pr.f32 ? (b.epi == kBack ? 108000 : b.epi == kUp ? 32000 : 12000)
+                                      : (b.epi == kBack ? 25000 : b.epi == kUp ? 7000 : 5000) * (tile == kSmall ? 1.6 : 1.0));
         long long last = 0;
         for (int want : parts) {
             const long long target = up_div(kmax, want);
             if (target == last) continue;
             last = target;
-            Plan c = {};
-            c.tile = tile;
-            double len[kMaxGroups], longest = 0;
-            long long units[kMaxGroups], all = 0;
-            bool split = false;
-            double part = 0;
-            for (int i = 0; i < b.n; ++i) {
-                const Product &p = b.p[i];
-                const long long q = (long long)blocks(p.k) * p.pairs;
-                c.kb[i] = blocks(p.k);
-                c.mt[i] = (int)up_div(p.M, kTileM * ctas), c.nt[i] = (int)up_div(p.N, cols);
-                c.splits[i] = (int)std::min<long long>(up_div(q, target), q);
-                units[i] = (long long)c.mt[i] * c.nt[i] * c.splits[i];
-                all += units[i];
-                len[i] = (double)q / c.splits[i];
-                longest = std::max(longest, len[i]);
-                c.part_bytes[i] = c.splits[i] > 1 ? (size_t)c.splits[i] * which * p.M * ((p.N + 3) / 4 * 4) * 4 : 0;
-                split |= c.splits[i] > 1, part += c.part_bytes[i];
-            }
-            if (split && (all > 8ll * P || part > 1e9)) break;
-            // the longest first
-            int n = 0;
-            double la = 0, lb = 0;
-            for (int i = 0; i < b.n; ++i)
-                if (len[i] >= 0.75 * longest) c.order[n++] = i, c.first += (int)units[i], la = std::max(la, len[i]);
-            c.ahead = n;
-            for (int i = 0; i < b.n; ++i)
-                if (len[i] < 0.75 * longest) c.order[n++] = i, c.rest += (int)units[i], lb = std::max(lb, len[i]);
-            c.ratio = lb > 0 ? std::max(1, (int)(la / lb + 0.5)) : 1;
-            double clock = tile == kPair ? 512 : tile == kWide ? 610 : 700;
-            if (tile == kSmall && all <= sms) clock = 350;
-            auto unit = [&](double l) { return std::max(l * pr.terms * clock, epi) + 300; };
-            const int extra = c.first % P, behind = extra ? P - extra : 0;
-            double span = 0;
-            for (int p : {0, extra, P - 1}) {
-                const long long a = up_div(std::max(c.first - p, 0), P), base = (long long)c.ratio * behind;
-                long long r = up_div(std::max<long long>(c.rest - base - p, 0), P);
-                if (extra && p >= extra) r += std::min<long long>(c.ratio, up_div(std::max(c.rest - (p - extra), 0), behind));
-                span = std::max(span, a * unit(la) + r * unit(lb));
-            }
-            const double in_flight = (tile == kPair ? 6 * 16384 : tile == kWide ? 4 * 32768 : 3 * 16384) / 1800.0;
-            const double active = (double)std::min<long long>(all, P) * ctas;
-            double cost = std::max(span, bytes / std::min(3500.0, active * in_flight)) + (tile == kPair ? 7000 : tile == kWide ? 5500 : 4000);
-            if (split) cost += 6000 + part * 2 / 4000;
-            if (cost < best_cost * 0.98) {
-                best_cost = cost;
-                best = c;
+            for (int via = 0; via < (pr.f32 && b.epi == kBack ? 2 : 1); ++via) {
+                Plan c = {};
+                c.tile = tile;
+                double len[kMaxGroups], longest = 0;
+                long long units[kMaxGroups], all = 0;
+                bool split = false;
+                double part = 0;
+                for (int i = 0; i < b.n; ++i) {
+                    const Product &p = b.p[i];
+                    const long long q = (long long)blocks(p.k) * p.pairs;
+                    c.kb[i] = blocks(p.k);
+                    c.mt[i] = (int)up_div(p.M, kTileM * ctas), c.nt[i] = (int)up_div(p.N, cols);
+                    c.splits[i] = (int)std::min<long long>(up_div(q, target), q);
+                    units[i] = (long long)c.mt[i] * c.nt[i] * c.splits[i];
+                    all += units[i];
+                    len[i] = (double)q / c.splits[i];
+                    longest = std::max(longest, len[i]);
+                    c.part_bytes[i] = c.splits[i] > 1 || via ? (size_t)c.splits[i] * which * p.M * ((p.N + 3) / 4 * 4) * 4 : 0;
+                    split |= c.splits[i] > 1 || via, part += c.part_bytes[i];
+                }
+                if (split && (part > 1e9 || (want > 1 && all > 8ll * P))) break;
+                // the longest first
+                int n = 0;
+                double la = 0, lb = 0;
+                for (int i = 0; i < b.n; ++i)
+                    if (len[i] >= 0.75 * longest) c.order[n++] = i, c.first += (int)units[i], la = std::max(la, len[i]);
+                c.ahead = n;
+                for (int i = 0; i < b.n; ++i)
+                    if (len[i] < 0.75 * longest) c.order[n++] = i, c.rest += (int)units[i], lb = std::max(lb, len[i]);
+                c.ratio = lb > 0 ? std::max(1, (int)(la / lb + 0.5)) : 1;
+                double clock = tile == kPair ? 512 : tile == kWide ? 610 : 700;
+                if (tile == kSmall && all <= sms) clock = 350;
+                const double epi = split ? 12000 : direct;
+                auto unit = [&](double l) { return std::max(l * pr.terms * clock, epi) + 300; };
+                const int extra = c.first % P, behind = extra ? P - extra : 0;
+                double span = 0;
+                for (int p : {0, extra, P - 1}) {
+                    const long long a = up_div(std::max(c.first - p, 0), P), base = (long long)c.ratio * behind;
+                    long long r = up_div(std::max<long long>(c.rest - base - p, 0), P);
+                    if (extra && p >= extra) r += std::min<long long>(c.ratio, up_div(std::max(c.rest - (p - extra), 0), behind));
+                    span = std::max(span, a * unit(la) + r * unit(lb));
+                }
+                const double in_flight = (tile == kPair ? 6 * 16384 : tile == kWide ? 4 * 32768 : 3 * 16384) / 1800.0;
+                const double active = (double)std::min<long long>(all, P) * ctas;
+                double cost = std::max(span, bytes / std::min(3500.0, active * in_flight)) + (tile == kPair ? 7000 : tile == kWide ? 5500 : 4000);
+                if (split) cost += 6000 + (part * 2 + (b.epi == kBack ? beside : 0)) / 3500;
+                if (cost < best_cost * 0.98) {
+                    best_cost = cost;
+                    best = c;
+                }
             }
         }
     }
@@ -360,7 +369,7 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         q.M = (int)p.M, q.N = (int)p.N, q.mt = pl.mt[i], q.nt = pl.nt[i], q.kb = pl.kb[i], q.pairs = p.pairs, q.splits = pl.splits[i];
         q.a = na, q.b = nb, q.c = nc, q.a_mn = p.a_mn, q.b_mn = p.b_mn;
         q.out = p.out, q.ld_out = p.N, q.vec_out = vec(p.out, p.N);
-        q.partial = reinterpret_cast<float *>(partial), q.ld_part = (p.N + 3) / 4 * 4;
+        q.partial = pl.part_bytes[i] ? reinterpret_cast<float *>(partial) : nullptr, q.ld_part = (p.N + 3) / 4 * 4;
         partial += (pl.part_bytes[i] + 255) / 256 * 256;
         (k < pl.ahead ? g.first : g.rest) += q.mt * q.nt * q.splits;
         const int b_maps = g.dual ? 2 : p.pairs;
@@ -369,11 +378,11 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
             if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : kTileM)) return cudaErrorInvalidValue;
         for (int j = 0; j < b_maps; ++j)
             if (!encode(&g.b[nb++], p.b[j], p.b_mn || (g.dual && pl.tile == kSmall) ? 64 : 128)) return cudaErrorInvalidValue;
-        if (b.epi == kPlain && !pr.f32 && q.splits == 1 && q.vec_out) {
+        if (b.epi == kPlain && !pr.f32 && !q.partial && q.vec_out) {
             q.tma_out = 1;
             if (!encode(&g.c[nc++], Mat{p.out, p.M, p.N, p.N, 0, 1}, 32)) return cudaErrorInvalidValue;
         }
-        split |= q.splits > 1;
+        split |= q.partial != nullptr;
         f.group[g.groups++] = {q.partial, q.splits, p.M, p.N, q.ld_part, q.ld_out, p.out};
     }
     if (g.groups == 0) return cudaSuccess;
@@ -381,7 +390,7 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         const int n = b.epi == kUp ? 1 : 3;
         for (int i = 0; i < n; ++i) {
             g.planes[i] = static_cast<__nv_bfloat16 *>(const_cast<void *>(b.planes[i].p));
-            if (!pr.f32 && !encode(&g.c[i], b.planes[i], 32)) return cudaErrorInvalidValue;
+            if (!pr.f32 && !encode(&g.c[i], b.planes[i], 32, b.epi == kBack ? 32 : 64)) return cudaErrorInvalidValue;
         }
         g.ld_plane = b.planes[0].ld, g.plane_stride = b.planes[0].plane;
         g.gate = b.gate, g.up = b.up;
