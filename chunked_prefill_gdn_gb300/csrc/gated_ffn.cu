@@ -5,8 +5,9 @@
 //     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h.
 //
 // Forward two products, the first with both projections, the activation and the
-// product h in one kernel; backward four, the first with dg, du and h in its
-// epilogue (ffn_gemm.cuh).  Operands that TMA cannot read in place (fp32, or rows
+// product h in one kernel; backward one with dg, du and h in its epilogue, and the
+// four gradients' in one launch (ffn_gemm.cuh); few tokens forward by ffn_few.cu.
+// Operands that TMA cannot read in place (fp32, or rows
 // that are not 16-byte aligned) are first laid out as bf16 planes in the workspace.
 // Where a product has too few tiles to fill the GPU its sum over K is split: the
 // parts leave as fp32 and a second kernel adds them in order and applies the
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(256) ffn_stage_kernel(const StageArgs a) {
 // ------------------------------------------------------ adding a split's parts
 struct FinishGroup {
     const float *partial;
-    int splits;
+    int splits, vec;          // vec: rows of what is read and written beside it in vectors of four
     long long M, N, ld_part, ld_out;
     void *out;
 };
@@ -139,10 +140,11 @@ __global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs f) {
         const int live = (int)(a.N - c < 4 ? a.N - c : 4);
         float v[4], w[4];
         sum(r * a.ld_part + c, v);
+        // planes have rows of a multiple of eight, so four columns are always there
         auto planes = [&](int o, const float *x) {
             __nv_bfloat16 *to = f.planes[o] + r * f.ld_plane + c;
             if constexpr (sizeof(T) == 2) {
-                store_some<__nv_bfloat16, 4>(to, x, live);
+                store_raw<__nv_bfloat16, 4>(to, pack<__nv_bfloat16, 4>(x));
             } else {
                 float s[3][4];
 #pragma unroll
@@ -152,22 +154,31 @@ __global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs f) {
                     s[0][e] = t[0], s[1][e] = t[1], s[2][e] = t[2];
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k) store_some<__nv_bfloat16, 4>(to + k * f.plane_stride, s[k], live);
+                for (int k = 0; k < 3; ++k) store_raw<__nv_bfloat16, 4>(to + k * f.plane_stride, pack<__nv_bfloat16, 4>(s[k]));
             }
+        };
+        auto load4 = [&](const void *p, float (&x)[4]) {
+            const T *at = static_cast<const T *>(p) + r * a.N + c;
+            unpack<T, 4>(a.vec ? load_raw<T, 4>(at) : load_some<T, 4>(at, live), x);
+        };
+        auto store4 = [&](void *p, long long ld, const float *x) {
+            T *at = static_cast<T *>(p) + r * ld + c;
+            if (a.vec) store_raw<T, 4>(at, pack<T, 4>(x));
+            else store_some<T, 4>(at, x, live);
         };
         if constexpr (EPI == kUp) {
             sum(matrix + r * a.ld_part + c, w);
             if (f.gate) {
-                store_some<T, 4>(static_cast<T *>(f.gate) + r * a.N + c, v, live);
-                store_some<T, 4>(static_cast<T *>(f.up) + r * a.N + c, w, live);
+                store4(f.gate, a.N, v);
+                store4(f.up, a.N, w);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = act_times(v[e], w[e], f.act);
             planes(0, v);
         } else if constexpr (EPI == kBack) {
             float g[4], u[4];
-            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(f.gate) + r * a.N + c, live), g);
-            unpack<T, 4>(load_some<T, 4>(static_cast<const T *>(f.up) + r * a.N + c, live), u);
+            load4(f.gate, g);
+            load4(f.up, u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float dg, du, h;
@@ -178,7 +189,7 @@ __global__ void __launch_bounds__(256) ffn_finish_kernel(const FinishArgs f) {
             planes(1, w);
             planes(2, g);
         } else {
-            store_some<T, 4>(static_cast<T *>(a.out) + r * a.ld_out + c, v, live);
+            store4(a.out, a.ld_out, v);
         }
     }
 }
@@ -215,8 +226,9 @@ int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
 long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Tile shape and parts of a batch, by a model in clocks (1.9 a ns).  A block of K takes a pair
-// 512 of the tensor pipe for each term; a single CTA of 256 columns more (it reads twice as
-// much of B); two CTAs of 128 columns share their SM and are held by shared memory, 700 each.
+// or a CTA of 256 columns 512 of the tensor pipe for each term, one of 128 columns 256, or its
+// operands' way to the SM longer (a pair 546, a CTA of 256 columns 820, one of 128 columns 546,
+// two of them on an SM 1092).
 // A tile takes at least its epilogue; a launch 4000 to 7000 to fill and drain; the operands
 // come at 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another
 // launch and its traffic.  For fp32 the backward pass's first product may leave as one part:
@@ -276,8 +288,10 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
                 for (int i = 0; i < b.n; ++i)
                     if (len[i] < 0.75 * longest) c.order[n++] = i, c.rest += (int)units[i], lb = std::max(lb, len[i]);
                 c.ratio = lb > 0 ? std::max(1, (int)(la / lb + 0.5)) : 1;
-                double clock = tile == kPair ? 512 : tile == kWide ? 610 : 700;
-                if (tile == kSmall && all <= sms) clock = 350;
+                // of a block of K: the tensor pipe's, or its bytes at 60 a clock and SM (rows that
+                // do not exist are not read)
+                const double share = tile == kSmall && all > sms ? 2 : 1, rows = std::min(1.0, (double)b.p[0].M / kTileM);
+                const double clock = std::max(tile == kSmall ? 256 * share : 512, (16384 * (b.p[0].a_mn ? 1 : rows) + 128.0 * bn / ctas) / 60 * share);
                 const double epi = split ? 12000 : direct;
                 auto unit = [&](double l) { return std::max(l * pr.terms * clock, epi) + 300; };
                 const int extra = c.first % P, behind = extra ? P - extra : 0;
@@ -383,7 +397,8 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
             if (!encode(&g.c[nc++], Mat{p.out, p.M, p.N, p.N, 0, 1}, 32)) return cudaErrorInvalidValue;
         }
         split |= q.partial != nullptr;
-        f.group[g.groups++] = {q.partial, q.splits, p.M, p.N, q.ld_part, q.ld_out, p.out};
+        const bool four = p.N % 4 == 0 && (b.epi == kPlain ? aligned16(p.out) : aligned16(b.gate) && aligned16(b.up));
+        f.group[g.groups++] = {q.partial, q.splits, four, p.M, p.N, q.ld_part, q.ld_out, p.out};
     }
     if (g.groups == 0) return cudaSuccess;
     if (b.epi != kPlain) {
@@ -530,6 +545,8 @@ gdn_status run_pass(const Pass &p, int32_t *status, cudaStream_t s, const char *
 
 bool elem_ok(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == GDN_F32 ? 3u : 1u)) == 0; }
 
+// Rows and the distance between them: TMA strides have 40 bits of bytes.
+bool span_ok(int64_t rows, int64_t stride) { return rows <= 1 || stride <= (1ll << 38) / rows; }
 // Sizes: TMA coordinates and the work list count in 32 bits.
 gdn_status desc_ok(const gdn_ffn_desc *d) {
     if (!d) return GDN_ERR_INVALID_ARG;
@@ -537,7 +554,8 @@ gdn_status desc_ok(const gdn_ffn_desc *d) {
     if (d->activation != GDN_ACT_SILU && d->activation != GDN_ACT_GELU_TANH) return GDN_ERR_INVALID_ARG;
     if (d->M < 0 || d->D < 1 || d->F < 1 || d->D_out < 1 || (d->M > 1 && d->x_stride < d->D)) return GDN_ERR_INVALID_ARG;
     constexpr int64_t most = 1 << 24;
-    if (d->M > most || d->D > most || d->F > most || d->D_out > most || d->x_stride > (1ll << 36)) return GDN_ERR_UNSUPPORTED;
+    if (d->M > most || d->D > most || d->F > most || d->D_out > most) return GDN_ERR_UNSUPPORTED;
+    if (!span_ok(d->M, d->x_stride)) return GDN_ERR_UNSUPPORTED;
     const int64_t big = std::max({d->D, d->F, d->D_out});
     if (std::max(d->M, big) * std::max(big, (int64_t)64) > (1ll << 38)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
@@ -583,7 +601,7 @@ extern "C" gdn_status gdn_gated_ffn_fwd(const gdn_ffn_desc *desc, void *y, void 
 }
 
 extern "C" size_t gdn_gated_ffn_bwd_workspace_size(const gdn_ffn_desc *desc, const void *dy, int64_t dy_stride) {
-    if (gdn::ffn::desc_ok(desc) != GDN_OK || (desc->M > 1 && dy_stride < desc->D_out)) return 0;
+    if (gdn::ffn::desc_ok(desc) != GDN_OK || (desc->M > 1 && dy_stride < desc->D_out) || !gdn::ffn::span_ok(desc->M, dy_stride)) return 0;
     if (desc->M == 0) return 16;
     return gdn::ffn::plan_bwd(*desc, dy, dy_stride, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr).bytes;
 }
@@ -597,7 +615,7 @@ extern "C" gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int dt = desc->dtype;
     if (!gdn::ffn::pointers_ok(*desc) || (desc->M > 1 && dy_stride < desc->D_out)) return GDN_ERR_INVALID_ARG;
-    if (dy_stride > (1ll << 36)) return GDN_ERR_UNSUPPORTED;
+    if (!gdn::ffn::span_ok(desc->M, dy_stride)) return GDN_ERR_UNSUPPORTED;
     for (const void *q : {(const void *)dx, (const void *)dw_gate, (const void *)dw_up, (const void *)dw_down, dy, gate, up})
         if (!gdn::ffn::elem_ok(q, dt)) return GDN_ERR_INVALID_ARG;
     gdn::ffn::Pass p = {};

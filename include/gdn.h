@@ -769,7 +769,8 @@ gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const void *dx, i
  * The workspace is 16-byte aligned and holds gdn_gated_ffn_fwd_workspace_size()
  * bytes, which depends on the sizes and on how x and the weights are aligned (0:
  * arguments that the call refuses); with fp32, or rows that are not 16-byte aligned,
- * it holds copies of x and of the weights.  Sizes at most 2^24, the largest tensor 2^38 elements.
+ * it holds copies of x and of the weights.  M, D, F and D_out at most 2^24, the largest
+ * tensor (x with its stride too) 2^38 elements.
  *
  * device_status: NULL, or a device int32 into which the call writes 0, or
  * GDN_ERR_TIMEOUT where a wait inside a kernel ran out.

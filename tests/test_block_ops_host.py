@@ -73,7 +73,8 @@ def test_gated_ffn_arguments(lib):
                dict(ws=ctypes.c_void_p(8))):
         assert f(**kw) == INVALID, kw
     assert f(n=size - 1) == WORKSPACE
-    for kw in (dict(M=(1 << 24) + 1), dict(F=(1 << 24) + 1), dict(M=1 << 20, F=1 << 20), dict(x_stride=1 << 37)):
+    for kw in (dict(M=(1 << 24) + 1), dict(F=(1 << 24) + 1), dict(M=1 << 20, F=1 << 20), dict(x_stride=1 << 37),
+               dict(M=1 << 20, x_stride=1 << 20)):
         assert f(**kw) == UNSUPPORTED and lib.gdn_gated_ffn_fwd_workspace_size(ffn_desc(**kw)) == 0, kw
     assert f(M=0, x=None, y=None, ws=None, n=0) == 0
     size = lib.gdn_gated_ffn_bwd_workspace_size(ffn_desc(), P, 64)
@@ -84,6 +85,9 @@ def test_gated_ffn_arguments(lib):
     for kw in (dict(dy=None), dict(st=63), dict(gate=None), dict(up=None), dict(dx=ODD), dict(ws=None), dict(w_up=None)):
         assert b(**kw) == INVALID, kw
     assert b(n=size - 1) == WORKSPACE and lib.gdn_gated_ffn_bwd_workspace_size(ffn_desc(), P, 63) == 0
+    assert b(st=1 << 37) == UNSUPPORTED and lib.gdn_gated_ffn_bwd_workspace_size(ffn_desc(), P, 1 << 37) == 0
+    one = ffn_desc(M=1, x_stride=0)
+    assert lib.gdn_gated_ffn_fwd(one, P, None, None, None, P, 0, None) == WORKSPACE          # a row's stride does not matter
 
 
 def test_gated_ffn_workspace_follows_what_has_to_be_laid_out(lib):
