@@ -14,12 +14,21 @@
 //
 // Statistics and h are taken from x before it is rounded.  Both passes are streams
 // bound by HBM: every tensor is read once and written once (five tensors forward,
-// eight backward).  A row is held by 8 to 512 threads, 8 or 16 columns each; the
+// eight backward).  A row is held by 8 to 1024 threads, 8 or 16 columns each; the
 // blocks are persistent and own their columns, so the parameters and the sums P and
 // dw_pre stay in registers over all rows of a block.  The next rows come in by
 // asynchronous copies; what is needed twice is read again from those copies instead
 // of being held.  The blocks' sums leave as partial rows that a second kernel adds in
 // a fixed order.
+//
+// Measured (all parts, fp32 parameters; of the measured copy rate): 32768 x 4096 bf16
+// forward 210 us (95%), backward 321 (100%); 8192 columns 237 and 366, 1024 columns (131072
+// rows) 248 and 373, 256 columns 246 and 466; fp32 4096 columns (16384 rows) 228 and 356.  The
+// gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 63 (80%,
+// 4 of it the sum over the blocks).  Rows that are not 16-byte aligned come in the 16-byte
+// chunks they touch and leave element by element: 32776 x 4095 bf16 379 and 650 us, fp32
+// (16388) 233 and 459.  Rows wider than 8192 columns are read two or three times: 8192 x
+// 16384 bf16 489 and 905 us.  16 rows 5.4 us (the host's call takes 25).
 #include <algorithm>
 #include <type_traits>
 
@@ -485,9 +494,25 @@ __global__ void __launch_bounds__(bn_threads(TPR), BwdStages<T, TPR, VEC, NV, PR
     }
 }
 
-// Rows wider than the register-resident kernels take: a block per row, which it
-// reads several times, element by element.
-template <typename T>
+// Rows wider than the register-resident kernels take: a block per row, which it reads
+// twice or three times (the later ones mostly from L2), V columns a thread at a time.
+template <typename T, int V>
+__device__ __forceinline__ void wide_load(const T *row, int c, float (&v)[V]) {
+    unpack<T, V>(load_raw<T, V>(row + c), v);
+}
+template <int V>
+__device__ __forceinline__ void wide_param(const void *p, int f32, int c, float (&v)[V], bool times) {
+    float w[V];
+    if (p && f32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {   // V columns: V > 1 in rows of a multiple of V
+        wide_load<float, V>(static_cast<const float *>(p), c, w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e] = p ? param_at(p, c + e, f32) : 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = times ? v[e] * w[e] : w[e];
+}
+template <typename T, int V>
 __global__ void __launch_bounds__(1024) block_norm_wide_fwd_kernel(const BlockNormArgs a) {
     __shared__ float red[2][32];
     const float inv_d = 1.f / (float)a.D;
@@ -499,39 +524,63 @@ __global__ void __launch_bounds__(1024) block_norm_wide_fwd_kernel(const BlockNo
         const T *r = a.res ? static_cast<const T *>(a.r.p) + row_at(a, a.r, row) : nullptr;
         float rstd = 1.f, q = 0.f;
         if (a.post) {
-            for (int c = threadIdx.x; c < a.D; c += 1024) q = fmaf(to_f32(y[c]), to_f32(y[c]), q);
+            for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {
+                float v[V];
+                wide_load<T, V>(y, c, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) q = fmaf(v[e], v[e], q);
+            }
             rstd = rsqrtf(row_sum<1024>(q, red, phase) * inv_d + a.eps);
             if (threadIdx.x == 0) a.rstd_post[row] = rstd;
         }
-        auto value = [&](int c) {
-            float v = to_f32(y[c]) * rstd;
-            if (a.w_post) v *= param_at(a.w_post, c, a.w_f32);
-            if (a.scale) v *= param_at(a.scale, c, a.w_f32);
+        auto value = [&](int c, float (&v)[V]) {
+            float t[V];
+            wide_load<T, V>(y, c, v);
+            wide_param<V>(a.w_post, a.w_f32, c, v, true);
+            wide_param<V>(a.scale, a.w_f32, c, v, true);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= rstd;
             if (a.gate) {
-                const float s = sigmoid_f32(to_f32(z[c]));
-                v *= a.gate == 1 ? to_f32(z[c]) * s : s;
+                wide_load<T, V>(z, c, t);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float s = sigmoid_f32(t[e]);
+                    v[e] *= a.gate == 1 ? t[e] * s : s;
+                }
             }
-            return a.res ? v + to_f32(r[c]) : v;
+            if (a.res) {
+                wide_load<T, V>(r, c, t);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += t[e];
+            }
         };
         float r2 = 1.f;
         if (a.pre) {
             q = 0.f;
-            for (int c = threadIdx.x; c < a.D; c += 1024) {
-                const float v = value(c);
-                q = fmaf(v, v, q);
+            for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {
+                float v[V];
+                value(c, v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) q = fmaf(v[e], v[e], q);
             }
             r2 = rsqrtf(row_sum<1024>(q, red, phase) * inv_d + a.eps);
             if (threadIdx.x == 0) a.rstd_pre[row] = r2;
         }
-        for (int c = threadIdx.x; c < a.D; c += 1024) {   // x may be the memory of y, z or r: written last
-            const float v = value(c);
-            static_cast<T *>(a.x)[row * a.D + c] = from_f32<T>(v);
-            if (a.pre) static_cast<T *>(a.h)[row * a.D + c] = from_f32<T>(v * r2 * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f));
+        for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {   // x may be the memory of y, z or r: written last
+            float v[V];
+            value(c, v);
+            store_raw<T, V>(static_cast<T *>(a.x) + row * a.D + c, pack<T, V>(v));
+            if (a.pre) {
+                wide_param<V>(a.w_pre, a.w_f32, c, v, true);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] *= r2;
+                store_raw<T, V>(static_cast<T *>(a.h) + row * a.D + c, pack<T, V>(v));
+            }
         }
     }
 }
 
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(1024) block_norm_wide_bwd_kernel(const BlockNormArgs a) {
     __shared__ float red[2][32];
     const float inv_d = 1.f / (float)a.D;
@@ -547,50 +596,82 @@ __global__ void __launch_bounds__(1024) block_norm_wide_bwd_kernel(const BlockNo
         const float rp = a.post ? a.rstd_post[row] : 1.f, rn = a.pre ? a.rstd_pre[row] : 1.f;
         float m = 0.f, q = 0.f;
         if (a.pre) {
-            for (int c = threadIdx.x; c < a.D; c += 1024)
-                q = fmaf(to_f32(dh[c]) * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f), to_f32(x[c]) * rn, q);
+            for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {
+                float g[V], t[V];
+                wide_load<T, V>(dh, c, g);
+                wide_load<T, V>(x, c, t);
+                wide_param<V>(a.w_pre, a.w_f32, c, g, true);
+#pragma unroll
+                for (int e = 0; e < V; ++e) q = fmaf(g[e], t[e] * rn, q);
+            }
             m = row_sum<1024>(q, red, phase) * inv_d;
         }
-        struct One { float d, yh, e, dz, p, q; };
-        auto value = [&](int c) {
-            One o = {};
-            o.d = dx ? to_f32(dx[c]) : 0.f;
+        // d, d's part of P (d a yh), dh xh; e = d s a w_post, dz
+        auto value = [&](int c, float (&d)[V], float (&yh)[V], float (&e)[V], float (&dz)[V], float (&p)[V], float (&qq)[V]) {
+            float t[V], w[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[i] = 0.f, qq[i] = 0.f;
+            if (dx) wide_load<T, V>(dx, c, d);
             if (a.pre) {
-                const float xh = to_f32(x[c]) * rn, g = to_f32(dh[c]);
-                o.q = g * xh;
-                o.d += rn * (g * (a.w_pre ? param_at(a.w_pre, c, a.w_f32) : 1.f) - xh * m);
+                float g[V];
+                wide_load<T, V>(dh, c, g);
+                wide_load<T, V>(x, c, t);
+                wide_param<V>(a.w_pre, a.w_f32, c, w, false);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float xh = t[i] * rn;
+                    qq[i] = g[i] * xh;
+                    d[i] += rn * (g[i] * w[i] - xh * m);
+                }
             }
-            o.yh = to_f32(y[c]) * rp;
-            float act = 1.f, slope = 0.f;
-            if (a.gate) {
-                const float zz = to_f32(z[c]), s = sigmoid_f32(zz);
-                act = a.gate == 1 ? zz * s : s;
-                slope = a.gate == 1 ? fmaf(act, 1.f - s, s) : s * (1.f - s);
+            wide_load<T, V>(y, c, yh);
+            wide_param<V>(a.w_post, a.w_f32, c, w, false);
+            wide_param<V>(a.scale, a.w_f32, c, w, true);
+            if (a.gate) wide_load<T, V>(z, c, t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                yh[i] *= rp;
+                float act = 1.f, slope = 0.f;
+                if (a.gate) {
+                    const float s = sigmoid_f32(t[i]);
+                    act = a.gate == 1 ? t[i] * s : s;
+                    slope = a.gate == 1 ? fmaf(act, 1.f - s, s) : s * (1.f - s);
+                }
+                const float dc = d[i] * w[i];
+                p[i] = d[i] * act * yh[i], dz[i] = dc * yh[i] * slope, e[i] = dc * act;
             }
-            float dc = o.d;
-            if (a.w_post) dc *= param_at(a.w_post, c, a.w_f32);
-            if (a.scale) dc *= param_at(a.scale, c, a.w_f32);
-            o.p = o.d * act * o.yh, o.dz = dc * o.yh * slope, o.e = dc * act;
-            return o;
         };
         float m2 = 0.f;
         if (a.post) {
             q = 0.f;
-            for (int c = threadIdx.x; c < a.D; c += 1024) {
-                const One o = value(c);
-                q = fmaf(o.e, o.yh, q);
+            for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {
+                float d[V], yh[V], e[V], dz[V], p[V], qq[V];
+                value(c, d, yh, e, dz, p, qq);
+#pragma unroll
+                for (int i = 0; i < V; ++i) q = fmaf(e[i], yh[i], q);
             }
             m2 = row_sum<1024>(q, red, phase) * inv_d;
         }
-        for (int c = threadIdx.x; c < a.D; c += 1024) {
-            const One o = value(c);
-            if (a.dr) static_cast<T *>(a.dr)[row * a.D + c] = from_f32<T>(o.d);
-            if (a.gate) static_cast<T *>(a.dz)[row * a.D + c] = from_f32<T>(o.dz);
-            static_cast<T *>(a.dy)[row * a.D + c] = from_f32<T>(rp * (o.e - o.yh * m2));
-            if (pp) {
-                const bool first = row == blockIdx.x;
-                pp[c] = (first ? 0.f : pp[c]) + o.p;
-                pp[a.D + c] = (first ? 0.f : pp[a.D + c]) + o.q;
+        for (int c = threadIdx.x * V; c < a.D; c += 1024 * V) {
+            float d[V], yh[V], e[V], dz[V], p[V], qq[V];
+            value(c, d, yh, e, dz, p, qq);
+            if (a.dr) store_raw<T, V>(static_cast<T *>(a.dr) + row * a.D + c, pack<T, V>(d));
+            if (a.gate) store_raw<T, V>(static_cast<T *>(a.dz) + row * a.D + c, pack<T, V>(dz));
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = rp * (e[i] - yh[i] * m2);
+            store_raw<T, V>(static_cast<T *>(a.dy) + row * a.D + c, pack<T, V>(e));
+            if (pp) {   // the block's sums, in its partial row (L2)
+                if (row != blockIdx.x) {
+                    float t[V];
+                    wide_load<float, V>(pp, c, t);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) p[i] += t[i];
+                    wide_load<float, V>(pp + a.D, c, t);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) qq[i] += t[i];
+                }
+                store_raw<float, V>(pp + c, pack<float, V>(p));
+                store_raw<float, V>(pp + a.D + c, pack<float, V>(qq));
             }
         }
     }
@@ -702,8 +783,9 @@ cudaError_t launch_rows(const BlockNormArgs &a, bool vec, cudaStream_t s) {
     const int grid = grid_of<T, PASS>(a.rows, a.D, vec);
     if (a.D > kBnMaxCols) {
         void (*wide)(const BlockNormArgs);
-        if constexpr (PASS != kBnFwd) wide = block_norm_wide_bwd_kernel<T>;
-        else wide = block_norm_wide_fwd_kernel<T>;
+        constexpr int V = 16 / (int)sizeof(T);
+        if constexpr (PASS != kBnFwd) wide = vec ? block_norm_wide_bwd_kernel<T, V> : block_norm_wide_bwd_kernel<T, 1>;
+        else wide = vec ? block_norm_wide_fwd_kernel<T, V> : block_norm_wide_fwd_kernel<T, 1>;
         return launch_dependent(wide, dim3(grid), dim3(1024), 0, s, a);
     }
     return vec ? by_columns<PASS == kBnFwd>(a.D, Launch<T, PASS, true>{a, grid, s}) : by_columns<PASS == kBnFwd>(a.D, Launch<T, PASS, false>{a, grid, s});

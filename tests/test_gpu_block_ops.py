@@ -89,7 +89,7 @@ def close(name, got, want, mag, K, dtype="f32", extra=0.0):
 # ------------------------------------------------------------------ block norm
 
 NORM = [(1, 1), (3, 7), (37, 33), (9, 64), (33, 128), (5, 130), (5, 256), (9, 264), (17, 512), (4, 513), (3, 1000),
-        (5, 1024), (3, 2049), (700, 96), (2, 4096), (3, 4100), (2, 8192), (2, 8193), (3, 9001)]
+        (5, 1024), (3, 2049), (700, 96), (2, 4096), (3, 4100), (2, 8192), (2, 8193), (3, 9001), (5, 9008), (2, 20000)]
 
 
 class Norm:
