@@ -15,8 +15,9 @@
 // a row is its part of two instructions' fragments: no shuffles, no shared memory, tokens
 // come from L1.  2 to 8 tokens 50 us, 16 tokens 66 (4096 x 1024: 9.5 of 3.8); beyond, the
 // tokens no longer fit L1 (32: 159 us) and the tiles of ffn_gemm.cuh take over (62 us, small
-// blocks 18).  fp32 is split into three bf16 terms a value, six products: 122 us for 2, 231
-// for 16, 369 for 32 tokens, where laying the weights out for tiles takes 490.
+// blocks 18).  fp32 is split into three bf16 terms a value, six products: 122 us for 2, 173
+// for 16, 305 for 32 tokens, where laying the weights out for tiles takes 490; (errors
+// against 64 bits 7e-7 and less, as of products in fp32).
 //
 // The second product's blocks start while the first one's last are at work.
 #include <algorithm>
@@ -124,7 +125,7 @@ __device__ __forceinline__ void split_pairs(const uint32_t (&x)[4], uint32_t (&p
 
 // Up to 8 NT tokens; SETS of 16 rows: w_gate's and w_up's, or w_down's.
 template <typename T, int NT, bool VEC, bool UP>
-__global__ void __launch_bounds__(kFewThreads, 3) ffn_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, sizeof(T) == 4 && NT == 4 ? 2 : 3) ffn_few_kernel(const FewArgs a) {
     constexpr int V = 16 / (int)sizeof(T), KC = 4 * V, SETS = UP ? 2 : 1, U = UP ? 2 : 4, WARPS = kFewThreads / 32;
     constexpr bool F32 = sizeof(T) == 4;
     __shared__ float red[WARPS][SETS][16][9];
@@ -161,11 +162,13 @@ __global__ void __launch_bounds__(kFewThreads, 3) ffn_few_kernel(const FewArgs a
     if (!UP) load(k);
     grid_dependency_wait();
     if (UP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float d[SETS][NT][4];
+    float d[SETS][NT][4], total[F32 ? SETS : 1][F32 ? NT : 1][4];
 #pragma unroll
     for (int i = 0; i < SETS; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) d[i][j][0] = d[i][j][1] = d[i][j][2] = d[i][j][3] = 0.f;
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[i][j][e] = total[F32 ? i : 0][F32 ? j : 0][e] = 0.f;
     for (bool loaded = !UP; k - ti * V < K; k += U * WARPS * KC, loaded = false) {
         if (!loaded) load(k);
 #pragma unroll
@@ -201,6 +204,23 @@ __global__ void __launch_bounds__(kFewThreads, 3) ffn_few_kernel(const FewArgs a
                 }
             }
         }
+        // the tensor instructions cut what an addition leaves over, so their sums are short
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < SETS; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) total[i][j][e] += d[i][j][e], d[i][j][e] = 0.f;
+        }
+    }
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < SETS; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[i][j][e] = total[i][j][e];
     }
     // the warps' sums, in order, eight tokens at a time
 #pragma unroll
