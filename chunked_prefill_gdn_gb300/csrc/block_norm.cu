@@ -24,7 +24,7 @@
 // Measured (all parts, fp32 parameters; of the measured copy rate): 32768 x 4096 bf16
 // forward 210 us (95%), backward 321 (100%); 8192 columns 237 and 366, 1024 columns (131072
 // rows) 248 and 373, 256 columns 246 and 466; fp32 4096 columns (16384 rows) 228 and 356.  The
-// gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 63 (80%,
+// gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 60 (84%,
 // 4 of it the sum over the blocks).  Rows that are not 16-byte aligned come in the 16-byte
 // chunks they touch and leave element by element: 32776 x 4095 bf16 379 and 650 us, fp32
 // (16388) 233 and 459.  Rows wider than 8192 columns are read two or three times: 8192 x
@@ -380,11 +380,15 @@ __global__ void __launch_bounds__(bn_threads(TPR), BwdStages<T, TPR, VEC, NV, PR
     if constexpr (PRE) params<TPR, VEC, NV>(a.w_pre, nullptr, a.w_f32, a.D, t, wn);
 #pragma unroll
     for (int p = 0; p < NP; ++p) P[p] = Q[PRE ? p : 0] = both(0.f);
+    // a row's rstd is loaded a row ahead (heads 65.5 -> 60.2 us); with the second norm its
+    // loads are hidden, and the register is not (324 us, 328 ahead)
+    float next_rp = !PRE && a.post && row < a.rows ? a.rstd_post[row] : 1.f;
     const float inv_d = 1.f / (float)a.D;
     int phase = 0;
     for (int slot = 0; row - behind < a.rows; row += step, slot = slot + 1 == S ? 0 : slot + 1) {
         const bool live = row < a.rows;
-        const float rp = a.post && live ? a.rstd_post[row] : 1.f, rn = PRE && live ? a.rstd_pre[row] : 1.f;
+        const float rp = !PRE ? next_rp : a.post && live ? a.rstd_post[row] : 1.f, rn = PRE && live ? a.rstd_pre[row] : 1.f;
+        if (!PRE && a.post && row + step < a.rows) next_rp = a.rstd_post[row + step];
         Part<T, TPR, VEC, NV, St::async> part[ARR];
 #pragma unroll
         for (int k = 0; k < ARR; ++k) part[k].t = t, part[k].D = a.D, part[k].live = live;

@@ -64,7 +64,7 @@ struct GemmArgs {
     CUtensorMap a[kMaxGroups + 1], b[kMaxGroups + 1], c[kMaxGroups], io[2];   // one product may have two pairs
     Group group[kMaxGroups];
     int groups, dual;         // dual: the tile's column halves come from b[0] and b[1]
-    // the schedule: units [0, first) are group 0's, the others follow; see item_of
+    // the schedule: the longest units come first, `rest` others follow; see item_of
     int first, rest, ratio;
     int terms;                // 1, or 6 for three planes
     int act, tma_io, vec_io;  // kUp: gate and up leave through boxes; rows of both in 16-byte vectors
@@ -242,8 +242,8 @@ struct Barriers {
 struct Item {
     int group, m, n, split, q0, q1;   // tile coordinates; blocks [q0, q1) of pairs * kb
 };
-// The i-th unit of worker p of P, or none (false).  Group 0's units (`first`) are the
-// longest and are dealt out in turn; the workers that get one less take `ratio` units of
+// The i-th unit of worker p of P, or none (false).  The longest units (the first groups',
+// `first` of them) are dealt out in turn; the workers that get one less take `ratio` units of
 // the others instead, which are then dealt out in turn too.  Within a group the tiles go
 // in bands of 16 rows of tiles of 128, so that what is at work at one time shares what it
 // reads in L2.
