@@ -273,7 +273,8 @@ def test_block_norm_autograd_matches_torch():
 
 FFN = [(1, 1, 1, 1), (1, 8, 8, 8), (1, 256, 520, 256), (2, 64, 64, 200), (5, 77, 135, 51), (16, 512, 1024, 512), (64, 128, 256, 64),
        (127, 72, 136, 72), (128, 64, 128, 128), (129, 64, 129, 65), (256, 256, 256, 256), (257, 320, 200, 264), (300, 33, 517, 30),
-       (700, 130, 70, 257), (1100, 512, 300, 512)]
+       (700, 130, 70, 257), (1100, 512, 300, 512),
+       (300, 1, 1, 1), (300, 8, 8, 8), (40, 3, 5, 7), (33, 4097, 9, 2), (35, 2, 4099, 16)]
 
 
 class Ffn:
@@ -607,6 +608,36 @@ def test_block_norm_refuses():
     # only the backward pass in reverse mode is there
     with pytest.raises(Exception):
         torch.func.jvp(lambda t: gdn.block_norm(t)[0], (c.y.float(),), (c.y.float(),))
+
+
+def test_two_host_threads():
+    """Calls from two threads, each on a stream of its own, give what they give alone."""
+    import threading
+    cs = [Ffn(400, 256, 520, 264, "bf16", seed=5), Ffn(90, 130, 300, 70, "f32", seed=6)]
+    want = [gdn.gated_ffn_fwd(c.x, *c.w, save=True) for c in cs]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                got[i].append(gdn.gated_ffn_fwd(cs[i].x, *cs[i].w, save=True, stream=stream))
+            stream.synchronize()
+        except Exception as e:   # pragma: no cover
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(2):
+        for again in got[i]:
+            for a, b in zip(again, want[i]):
+                assert torch.equal(a, b)
 
 
 def test_gated_ffn_refuses():
