@@ -22,12 +22,12 @@
 // a fixed order.
 //
 // Measured (all parts, fp32 parameters; of the measured copy rate): 32768 x 4096 bf16
-// forward 210 us (95%), backward 321 (100%); 8192 columns 237 and 366, 1024 columns (131072
-// rows) 248 and 373, 256 columns 246 and 466; fp32 4096 columns (16384 rows) 228 and 356.  The
-// gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 60 (84%,
+// forward 201 us, backward 321 (both 100%); 2^27 elements of 8192 columns 236 and 365, of
+// 1024 209 and 326, of 256 244 and 371; fp32 4096 columns (16384 rows) 227 and 361.  The
+// gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 58 (86%,
 // 4 of it the sum over the blocks).  Rows that are not 16-byte aligned come in the 16-byte
-// chunks they touch and leave element by element: 32776 x 4095 bf16 379 and 650 us, fp32
-// (16388) 233 and 459.  Rows wider than 8192 columns are read two or three times: 8192 x
+// chunks they touch and leave element by element: 32776 x 4095 bf16 363 and 648 us, fp32
+// (16388) 230 and 459.  Rows wider than 8192 columns are read two or three times: 8192 x
 // 16384 bf16 489 and 905 us.  16 rows 5.4 us (the host's call takes 25).
 #include <algorithm>
 #include <type_traits>
@@ -93,32 +93,38 @@ __device__ __forceinline__ float row_sum(float v, float (*both_red)[32], int &ph
 
 constexpr int bn_threads(int tpr) { return tpr <= 32 ? 256 : tpr; }
 
-// Rows in flight per row of threads: as many as `most` bytes per block hold, at most
-// four; a single one where not even two fit.
-// Blocks per SM that the registers are budgeted for: THREADS threads.
-template <typename T, int TPR, int VEC, int NV, int ARRAYS, int THREADS>
+// Rows in flight per row of threads: as many as a block's share of shared memory holds,
+// at most MOST; a single one where not even two fit.  Blocks per SM that the registers are
+// budgeted for: THREADS threads.
+template <typename T, int TPR, int VEC, int NV, int ARRAYS, int THREADS, int MOST>
 struct BnStages {
     // Vectors: each thread reads back what it copied.  Else a row comes as the 16-byte
     // chunks that it touches, and its threads read from all of them.
     static constexpr bool async = VEC * sizeof(T) == 16;
     static constexpr int row_bytes = TPR * NV * VEC * (int)sizeof(T) + 16;
     static constexpr int bytes = async ? bn_threads(TPR) * NV * ARRAYS * 16 : bn_threads(TPR) / TPR * ARRAYS * row_bytes;
-    static constexpr int fit = (THREADS >= 1024 ? 65536 : 98304) / bytes;
-    static constexpr int count = fit >= 4 ? 4 : fit >= 2 ? fit : bytes <= 106496 ? 2 : 1;
+    static constexpr int by_threads = THREADS >= bn_threads(TPR) ? THREADS / bn_threads(TPR) : 1;
+    static constexpr int fit = (225 * 1024 / by_threads - 1024) / bytes;
+    static constexpr int count = fit >= MOST ? MOST : fit >= 2 ? fit : 2 * bytes <= 224 * 1024 ? 2 : 1;
     static constexpr int smem = count * bytes;
     static constexpr int by_smem = 225 * 1024 / (smem + 1024);
-    static constexpr int by_threads = THREADS / bn_threads(TPR);
-    static constexpr int blocks = by_smem < by_threads ? (by_smem > 0 ? by_smem : 1) : (by_threads > 0 ? by_threads : 1);
+    static constexpr int blocks = by_smem < by_threads ? by_smem : by_threads;
+    static_assert(smem <= 226 * 1024 && blocks >= 1, "shared memory");
 };
 
 __device__ __forceinline__ void bn_copy16(uint4 *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
+// More rows in flight than these are slower, not only useless (forward, 2^27 elements in
+// bf16, all parts: 2048 columns 208 us with two rows, 225 with three or four, 1024 columns 213
+// and 243; the gated norm of heads 127 with three, 132 with four, 137 with two; backward, 256
+// columns 371 with two, 390 with four, 2048 columns 362 and 374), and so are more threads of
+// fewer registers (backward, 1024 columns 326 us at 640 threads, 365 at 768).
 template <typename T, int TPR, int VEC, int NV>
-using FwdStages = BnStages<T, TPR, VEC, NV, 3, TPR >= 512 ? 1536 : 768>;
+using FwdStages = BnStages<T, TPR, VEC, NV, 3, (TPR >= 512 ? 1024 : 768), (TPR >= 128 ? 2 : 3)>;
 template <typename T, int TPR, int VEC, int NV, bool PRE>
-using BwdStages = BnStages<T, TPR, VEC, NV, PRE ? 5 : 3, !PRE && NV * VEC <= 8 ? 768 : 512>;
+using BwdStages = BnStages<T, TPR, VEC, NV, PRE ? 5 : 3, (NV * VEC > 8 ? 512 : PRE && TPR >= 128 ? 640 : 768), (PRE ? 2 : 4)>;
 
 // The threads of a row, which read what any of them copied.
 template <int TPR>
@@ -712,9 +718,8 @@ constexpr int kBnMaxCols = 8192;
 
 // Calls f<TPR, EPT>: the threads of a row and the columns of each by the row's length.
 // The forward pass is held up by its two sums over a block: more threads of fewer
-// registers (32768 x 4096 bf16: 512 x 8 columns at three blocks an SM 212 us, 256 x 16 at
-// two 235).  The backward pass has more bytes to a sum and is not (324 us, 99% of the
-// measured copy rate, with 256 x 16).
+// columns (32768 x 4096 bf16: 512 x 8 columns at two blocks an SM 201 us, 256 x 16 at two
+// 235).  The backward pass has more bytes to a sum and is not (321 us with 256 x 16).
 template <bool FWD, typename F>
 auto by_columns(int D, F f) {
     if (D <= 64) return f.template operator()<8, 8>();

@@ -233,7 +233,7 @@ long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 // come at 3500 bytes a clock, or what the CTAs at work can have in flight; parts cost another
 // launch and its traffic.  For fp32 the backward pass's first product may leave as one part:
 // its epilogue with three outputs of three planes takes 57 us a tile (8192 x 256 x 2048: 230 us
-// in all), which the second kernel with its rows in order does in less where K is short.
+// in all, 134 with the second kernel, which takes its rows in order), so where K is short.
 Plan plan_batch(const Batch &b, const Problem &pr) {
     Plan best = {};
     double best_cost = 1e300;

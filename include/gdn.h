@@ -764,7 +764,8 @@ gdn_status gdn_block_norm_bwd(const gdn_block_norm_desc *desc, const void *dx, i
  * [M, F], g and u for the backward pass, or both NULL.  bf16 (h is rounded to bf16
  * between the two products, whose sums are fp32) or fp32 (products of three bf16
  * terms a value, sums fp32: as exact as fp32 products).  A row that is not finite
- * makes its own outputs non-finite (with fp32 an infinity may give NaN).
+ * makes its own outputs non-finite (with fp32 an infinity may give NaN, and a value
+ * from 3.39e38 on counts as one).
  *
  * The workspace is 16-byte aligned and holds gdn_gated_ffn_fwd_workspace_size()
  * bytes, which depends on the sizes and on how x and the weights are aligned (0:
