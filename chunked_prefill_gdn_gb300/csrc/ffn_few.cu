@@ -14,7 +14,7 @@
 // within a product is free as long as both operands share it, so a lane's 16-byte vector of
 // a row is its part of two instructions' fragments: no shuffles, no shared memory, tokens
 // come from L1.  2 to 8 tokens 50 us, 16 tokens 66 (4096 x 1024: 9.5 of 3.8); beyond, the
-// tokens no longer fit L1 (32: 159 us) and the tiles of ffn_gemm.cuh take over (62 us, small
+// tokens no longer fit L1 (32: 159 us) and the tiles of ffn_gemm.cuh take over (58 us, small
 // blocks 18).  fp32 is split into three bf16 terms a value, six products: 122 us for 2, 173
 // for 16, 305 for 32 tokens, where laying the weights out for tiles takes 490; (errors
 // against 64 bits 7e-7 and less, as of products in fp32).

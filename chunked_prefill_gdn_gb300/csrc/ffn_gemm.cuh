@@ -67,6 +67,7 @@ struct GemmArgs {
     // the schedule: the longest units come first, `rest` others follow; see item_of
     int first, rest, ratio;
     int terms;                // 1, or 6 for three planes
+    int a_rows, stages;       // few_rows: rows of A's boxes (32, 64, 128) and stages (5, 4, 3)
     int act, tma_io, vec_io;  // kUp: gate and up leave through boxes; rows of both in 16-byte vectors
     __nv_bfloat16 *planes[3]; // kUp: h; kBack: dgate, dup, h: one plane (bf16) or three (fp32)
     long long ld_plane, plane_stride;
@@ -225,11 +226,15 @@ struct Shape {
     static constexpr int b_rows = BN / CTAS;                     // of B in this CTA
     static constexpr int a_bytes = kTileM * 128, b_bytes = b_rows * 128, stage = a_bytes + b_bytes;
     static constexpr bool boxes = !promote && BN == 256;
-    static constexpr int stages = BN == 128 ? 3 : CTAS == 2 ? 6 : 4;
+    // Tiles of 128 columns take A in boxes of 32 or 64 rows where there are no more rows, and
+    // as many stages as then fit (the products read 128 rows from there on, B's first ones
+    // among them; what comes of those is not stored).
+    static constexpr bool few_rows = BN == 128;
+    static constexpr int stages = few_rows ? 3 : CTAS == 2 ? 6 : 4, area = few_rows ? 102400 : stages * stage;
     static constexpr int box_bytes = boxes ? 64 * box_cols : 1024;   // per warp: the box, or room to turn 32 x 8 values
-    static constexpr int smem = 1024 + stages * stage + epi_warps * box_bytes;   // 1024: alignment
+    static constexpr int smem = 1024 + area + epi_warps * box_bytes;   // 1024: alignment
     static constexpr int per_sm = BN == 128 ? 2 : 1;
-    static_assert(stages <= kMaxStages && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
+    static_assert(stages <= kMaxStages && stages * stage <= area && smem + 512 <= 227 * 1024 / per_sm - (per_sm - 1) * 1024, "shared memory");
 };
 
 struct Barriers {
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::stages; ++i) tc::mbar_init(&bars.full[i], 1), tc::mbar_init(&bars.empty[i], 1);
+        for (int i = 0; i < kMaxStages; ++i) tc::mbar_init(&bars.full[i], 1), tc::mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i) tc::mbar_init(&bars.tmem_full[i], 1), tc::mbar_init(&bars.tmem_empty[i], S::epi_warps * CTAS);
         bars.abort = 0;
         tc::fence_barrier_init();
@@ -410,6 +415,8 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
     };
     grid_dependency_wait();
     const int P = gridDim.x / CTAS, p = blockIdx.x / CTAS;
+    const uint32_t n_stages = S::few_rows ? g.stages : S::stages, a_bytes = S::few_rows ? g.a_rows * 128 : S::a_bytes;
+    const uint32_t stage = a_bytes + S::b_bytes;
     const int chunk = PROMOTE ? kPromote : 1 << 30;
     Item i;
 
@@ -443,9 +450,9 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
                         if (!ok) break;
                         const int second = q >= kb ? 1 : 0, kc = (q - second * kb) * kBlockK;
                         const CUtensorMap *ma = &g.a[a0 + second], *mb = &g.b[b0 + (dual && CTAS == 2 ? (int)rank : second)];
-                        const uint32_t at = base + s * S::stage, bt = at + S::a_bytes, bar = full0 + s * 8;
+                        const uint32_t at = base + s * stage, bt = at + a_bytes, bar = full0 + s * 8;
                         if (leader) {
-                            if (CTAS == 1 || rank == 0) tc::mbar_arrive_expect_tx(&bars.full[s], S::stage * CTAS);
+                            if (CTAS == 1 || rank == 0) tc::mbar_arrive_expect_tx(&bars.full[s], stage * CTAS);
                             if (a_mn) {
 #pragma unroll
                                 for (int j = 0; j < kTileM / 64; ++j) load_box<CTAS>(at + j * 8192, ma, bar, row + j * 64, kc, pa);
@@ -466,14 +473,14 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
                         }
                         __syncwarp();
                         ++loads;
-                        if (++s == S::stages) s = 0, turn ^= 1;
+                        if (++s == n_stages) s = 0, turn ^= 1;
                     }
                 }
             }
         }
         // the products have read every stage before the CTA may leave
-        for (uint32_t j = 0; ok && j < min(loads, (uint32_t)S::stages); ++j) {
-            if (s == 0) s = S::stages, turn ^= 1;
+        for (uint32_t j = 0; ok && j < min(loads, n_stages); ++j) {
+            if (s == 0) s = n_stages, turn ^= 1;
             ok = warp_wait(&bars.empty[--s], turn);
         }
     } else if (warp == 1) {
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
                 const uint32_t idesc = tc::idesc_bf16_f32(kTileM * CTAS, BN, a_mn, b_mn);
                 const uint32_t ka = a_mn ? 128 : 2, kbs = b_mn ? 128 : 2;   // 16 of K on, in 16-byte units
                 const uint64_t da0 = tc::smem_desc_sw128(base, a_mn ? 8192 : 16, 1024);
-                const uint64_t db0 = tc::smem_desc_sw128(base + S::a_bytes, b_mn ? 8192 : 16, 1024);
+                const uint64_t db0 = tc::smem_desc_sw128(base + a_bytes, b_mn ? 8192 : 16, 1024);
                 for (int c0 = i.q0; ok && c0 < i.q1; c0 += chunk, ++n) {
                     const int c1 = min(c0 + chunk, i.q1);
                     if (c1 < c0) break;
@@ -502,14 +509,14 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
                         ok = warp_wait(&bars.full[s], turn);
                         if (!ok) break;
                         tc::tc_fence_after();
-                        const uint64_t da = da0 + s * (S::stage / 16), db = db0 + s * (S::stage / 16);
+                        const uint64_t da = da0 + s * (stage / 16), db = db0 + s * (stage / 16);
                         if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) mma_bf16<CTAS>(d, da + kk * ka, db + kk * kbs, idesc, q > 0 || kk > 0);
                             commit<CTAS>(&bars.empty[s]);
                         }
                         __syncwarp();
-                        if (++s == S::stages) s = 0, turn ^= 1;
+                        if (++s == n_stages) s = 0, turn ^= 1;
                     }
                     if (ok && leader) commit<CTAS>(&bars.tmem_full[buf]);
                     __syncwarp();
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
     } else {
         const int quarter = warp & 3, part_of = (warp - 2) >> 2;   // the warp's lanes, and its CW columns
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        uint8_t *box = smem + S::stages * S::stage + (warp - 2) * S::box_bytes;
+        uint8_t *box = smem + S::area + (warp - 2) * S::box_bytes;
         const uint32_t box_at = tc::smem_u32(box);
         const uint32_t release = CTAS == 2 ? map_to_cta(tc::smem_u32(&bars.tmem_empty[0]), 0) : 0u;
         uint32_t n = 0;

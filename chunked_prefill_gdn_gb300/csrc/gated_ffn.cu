@@ -222,6 +222,13 @@ struct Batch {
     Plan plan;
 };
 
+// Tiles of 128 columns: the rows of A that a stage holds, and the stages that then fit.
+int rows_of_a(const Batch &b) {
+    const bool few = b.n == 1 && !b.p[0].a_mn;
+    return few && b.p[0].M <= 32 ? 32 : few && b.p[0].M <= 64 ? 64 : kTileM;
+}
+int small_stages(int a_rows) { return a_rows == 32 ? 5 : a_rows == 64 ? 4 : 3; }
+
 int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
 long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -372,6 +379,8 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
     auto vec = [&](const void *q, long long ld) { return aligned16(q) && ld * e % 16 == 0; };
     g.dual = b.epi == kUp, g.ratio = pl.ratio;
     g.terms = pr.terms, g.act = pr.act, g.err = err;
+    const int a_rows = rows_of_a(b);
+    g.a_rows = a_rows, g.stages = small_stages(a_rows);
     FinishArgs f = {};
     int na = 0, nb = 0, nc = 0;
     bool split = false;
@@ -389,7 +398,7 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         const int b_maps = g.dual ? 2 : p.pairs;
         if (na + p.pairs > kMaxGroups + 1 || nb + b_maps > kMaxGroups + 1) return cudaErrorInvalidValue;
         for (int j = 0; j < p.pairs; ++j)
-            if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : kTileM)) return cudaErrorInvalidValue;
+            if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : pl.tile == kSmall ? a_rows : kTileM)) return cudaErrorInvalidValue;
         for (int j = 0; j < b_maps; ++j)
             if (!encode(&g.b[nb++], p.b[j], p.b_mn || (g.dual && pl.tile == kSmall) ? 64 : 128)) return cudaErrorInvalidValue;
         if (b.epi == kPlain && !pr.f32 && !q.partial && q.vec_out) {
@@ -457,8 +466,13 @@ Problem problem_of(const gdn_ffn_desc &d) {
     return pr;
 }
 
-// Whether the forward products are those of ffn_few.cu.
-bool few(const Problem &pr) { return pr.M <= (pr.f32 ? kFewF32 : kFewBf16); }
+// Whether the forward products are those of ffn_few.cu.  From nine tokens in bf16 on they
+// slow down with the weights' bytes, the tiles by their launches alone: 16 tokens, 4096 x 12288
+// (302 MB) 66 us, tiles 57; 2048 x 6144 (75 MB) 23 and 27; 1024 x 4096 9.5 and 16.
+bool few(const Problem &pr) {
+    const double weights = 2.0 * (2.0 * pr.F * pr.D + (double)pr.O * pr.F);
+    return pr.M <= (pr.f32 ? kFewF32 : weights <= 134e6 ? kFewBf16 : kFewBf16 / 2);
+}
 
 gdn_status run_few(const gdn_ffn_desc &d, const Problem &pr, void *y, void *gate, void *up, int32_t *status, void *workspace,
                    cudaStream_t s) {

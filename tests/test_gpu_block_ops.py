@@ -338,7 +338,8 @@ def test_gated_ffn(M, D, F, O, dtype, layout, act):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M,D,F,O", [(2500, 512, 4000, 520), (40, 4096, 1000, 256), (4096, 64, 160, 64), (600, 2048, 640, 1030)])
+@pytest.mark.parametrize("M,D,F,O", [(2500, 512, 4000, 520), (40, 4096, 1000, 256), (4096, 64, 160, 64), (600, 2048, 640, 1030),
+                                     (12, 4096, 6000, 4096)])
 def test_gated_ffn_many_tiles(M, D, F, O, dtype):
     """More tiles than the GPU holds at once, long sums, sums in parts."""
     c = Ffn(M, D, F, O, dtype)
