@@ -232,6 +232,13 @@ int small_stages(int a_rows) { return a_rows == 32 ? 5 : a_rows == 64 ? 4 : 3; }
 int blocks(long long k) { return (int)((k + kBlockK - 1) / kBlockK); }
 long long up_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// Blocks of K that one sum may have.  Whatever an addition in tensor memory leaves over is
+// cut, not rounded: bf16 sums of terms of one sign come out 1.1e-7 of themselves too small
+// for each addition of 16 products, and so 7e-3 at 2^20 of K in one sum and 0.11 at 2^24.
+// Longer sums are cut into parts (added in fp32, rounded to nearest): at most 8192
+// additions, 9e-4, a quarter of what rounding to bf16 may be off.
+constexpr long long kLongest = 2048;
+
 // Tile shape and parts of a batch, by a model in clocks (1.9 a ns).  A block of K takes a pair
 // or a CTA of 256 columns 512 of the tensor pipe for each term, one of 128 columns 256, or its
 // operands' way to the SM longer (a pair 546, a CTA of 256 columns 820, one of 128 columns 546,
@@ -270,14 +277,15 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
                 c.tile = tile;
                 double len[kMaxGroups], longest = 0;
                 long long units[kMaxGroups], all = 0;
-                bool split = false;
+                bool split = false, chosen = false;   // chosen: not for the sums' length alone
                 double part = 0;
                 for (int i = 0; i < b.n; ++i) {
                     const Product &p = b.p[i];
-                    const long long q = (long long)blocks(p.k) * p.pairs;
+                    const long long q = (long long)blocks(p.k) * p.pairs, least = up_div(q, kLongest);
                     c.kb[i] = blocks(p.k);
                     c.mt[i] = (int)up_div(p.M, kTileM * ctas), c.nt[i] = (int)up_div(p.N, cols);
-                    c.splits[i] = (int)std::min<long long>(up_div(q, target), q);
+                    c.splits[i] = (int)std::max(up_div(q, target), least);
+                    chosen |= c.splits[i] > least || via;
                     units[i] = (long long)c.mt[i] * c.nt[i] * c.splits[i];
                     all += units[i];
                     len[i] = (double)q / c.splits[i];
@@ -285,7 +293,7 @@ Plan plan_batch(const Batch &b, const Problem &pr) {
                     c.part_bytes[i] = c.splits[i] > 1 || via ? (size_t)c.splits[i] * which * p.M * ((p.N + 3) / 4 * 4) * 4 : 0;
                     split |= c.splits[i] > 1 || via, part += c.part_bytes[i];
                 }
-                if (split && (part > 1e9 || (want > 1 && all > 8ll * P))) break;
+                if (chosen && (part > 1e9 || (want > 1 && all > 8ll * P))) break;
                 // the longest first
                 int n = 0;
                 double la = 0, lb = 0;
