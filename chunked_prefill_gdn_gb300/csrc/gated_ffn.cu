@@ -476,8 +476,10 @@ Problem problem_of(const gdn_ffn_desc &d) {
 
 // Whether the forward products are those of ffn_few.cu.  From nine tokens in bf16 on they
 // slow down with the weights' bytes, the tiles by their launches alone: 16 tokens, 4096 x 12288
-// (302 MB) 66 us, tiles 57; 2048 x 6144 (75 MB) 23 and 27; 1024 x 4096 9.5 and 16.
+// (302 MB) 66 us, tiles 57; 2048 x 6144 (75 MB) 23 and 27; 1024 x 4096 9.5 and 16.  A warp adds up
+// an eighth of K there, in one sum (kLongest).
 bool few(const Problem &pr) {
+    if (std::max(pr.D, pr.F) > 8 * kLongest * kBlockK) return false;
     const double weights = 2.0 * (2.0 * pr.F * pr.D + (double)pr.O * pr.F);
     return pr.M <= (pr.f32 ? kFewF32 : weights <= 134e6 ? kFewBf16 : kFewBf16 / 2);
 }
@@ -578,8 +580,9 @@ gdn_status desc_ok(const gdn_ffn_desc *d) {
     constexpr int64_t most = 1 << 24;
     if (d->M > most || d->D > most || d->F > most || d->D_out > most) return GDN_ERR_UNSUPPORTED;
     if (!span_ok(d->M, d->x_stride)) return GDN_ERR_UNSUPPORTED;
-    const int64_t big = std::max({d->D, d->F, d->D_out});
-    if (std::max(d->M, big) * std::max(big, (int64_t)64) > (1ll << 38)) return GDN_ERR_UNSUPPORTED;
+    const int64_t tensors[][2] = {{d->M, d->D}, {d->M, d->F}, {d->M, d->D_out}, {d->F, d->D}, {d->D_out, d->F}};
+    for (const auto &t : tensors)
+        if (t[0] * t[1] > (1ll << 38)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 bool pointers_ok(const gdn_ffn_desc &d) {
