@@ -76,6 +76,15 @@ def _lib():
     return _bound
 
 
+def _scratch(on, workspace, size):
+    """The workspace; None where size is 0: arguments that the call refuses, and says why."""
+    return _workspace(on, workspace, size) if size else None
+
+
+def _bytes(ws):
+    return ws.numel() if ws is not None else 0
+
+
 def _status(on, check):
     return on.empty(1, _I32) if check else None
 
@@ -242,10 +251,10 @@ def block_norm_bwd(dx, dh, y, x, rstd_post, rstd_pre, gate=None, post_weight=Non
         if any(given):
             rows = iter(on.empty((sum(given), D), _F32).unbind(0))
             grads = [next(rows) if g else None for g in given]
-            ws = _workspace(on, workspace, lib.gdn_block_norm_bwd_workspace_size(desc))
+            ws = _scratch(on, workspace, lib.gdn_block_norm_bwd_workspace_size(desc))
         rc = lib.gdn_block_norm_bwd(desc, _p(dx), *strides[:2], _p(dh), *strides[2:4], _p(xs), *strides[4:], _p(rstd_post),
                                     _p(rstd_pre), dy.data_ptr(), _p(dr), _p(dz), *(_p(t) for t in grads), _p(ws),
-                                    ws.numel() if ws is not None else 0, on.raw)
+                                    _bytes(ws), on.raw)
         if rc != 0:
             _raise(rc, "gdn_block_norm_bwd")
     finally:
@@ -320,9 +329,9 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", save: bool 
     try:
         y = out if out is not None else on.empty((*lead, n_out), dtype)
         gate, up = (on.empty((*lead, F), dtype), on.empty((*lead, F), dtype)) if save else (None, None)
-        ws = _workspace(on, workspace, lib.gdn_gated_ffn_fwd_workspace_size(desc))
+        ws = _scratch(on, workspace, lib.gdn_gated_ffn_fwd_workspace_size(desc))
         word = _status(on, check)
-        rc = lib.gdn_gated_ffn_fwd(desc, y.data_ptr(), _p(gate), _p(up), _p(word), ws.data_ptr(), ws.numel(), on.raw)
+        rc = lib.gdn_gated_ffn_fwd(desc, y.data_ptr(), _p(gate), _p(up), _p(word), _p(ws), _bytes(ws), on.raw)
         if rc != 0:
             _raise(rc, "gdn_gated_ffn_fwd")
         _wrote(None, out)
@@ -346,10 +355,10 @@ def gated_ffn_bwd(dy, x, w_gate, w_up, w_down, gate, up, activation: str = "silu
     on = _On(dev, stream)
     try:
         grads = [on.empty(t.shape, dtype) if need else None for t, need in zip((x, w_gate, w_up, w_down), needs)]
-        ws = _workspace(on, workspace, lib.gdn_gated_ffn_bwd_workspace_size(desc, dy.data_ptr(), stride))
+        ws = _scratch(on, workspace, lib.gdn_gated_ffn_bwd_workspace_size(desc, dy.data_ptr(), stride))
         word = _status(on, check)
         rc = lib.gdn_gated_ffn_bwd(desc, dy.data_ptr(), stride, gate.data_ptr(), up.data_ptr(), *(_p(t) for t in grads),
-                                   _p(word), ws.data_ptr(), ws.numel(), on.raw)
+                                   _p(word), _p(ws), _bytes(ws), on.raw)
         if rc != 0:
             _raise(rc, "gdn_gated_ffn_bwd")
         _read_status(word, on, "gdn_gated_ffn_bwd")
