@@ -46,7 +46,13 @@ struct Mat {
     int planes;
 };
 
+gdn_status failed(const char *where, cudaError_t e) {
+    set_error_detail(where, e);
+    return GDN_ERR_CUDA;
+}
+
 // box_cols: 64, or 32 for the outputs of kBack (128 or 64 bytes a row, swizzled as wide).
+// Records why when it fails.
 bool encode(CUtensorMap *map, const Mat &m, int box_rows, int box_cols = 64) {
     const EncodeFn fn = encode_fn();
     if (!fn) {
@@ -380,7 +386,7 @@ cudaError_t run_finish(const Problem &pr, const FinishArgs &f, int n, cudaStream
                   : launch_dependent(ffn_finish_kernel<EPI, __nv_bfloat16>, dim3(grid, n), dim3(256), 0, s, f);
 }
 
-cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err, cudaStream_t s) {
+gdn_status run_batch(const Batch &b, const Problem &pr, char *partial, int *err, cudaStream_t s, const char *where) {
     const Plan &pl = b.plan;
     GemmArgs g = {};
     const int e = pr.f32 ? 4 : 2;
@@ -404,25 +410,25 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         partial += (pl.part_bytes[i] + 255) / 256 * 256;
         (k < pl.ahead ? g.first : g.rest) += q.mt * q.nt * q.splits;
         const int b_maps = g.dual ? 2 : p.pairs;
-        if (na + p.pairs > kMaxGroups + 1 || nb + b_maps > kMaxGroups + 1) return cudaErrorInvalidValue;
+        if (na + p.pairs > kMaxGroups + 1 || nb + b_maps > kMaxGroups + 1) return failed(where, cudaErrorInvalidValue);
         for (int j = 0; j < p.pairs; ++j)
-            if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : pl.tile == kSmall ? a_rows : kTileM)) return cudaErrorInvalidValue;
+            if (!encode(&g.a[na++], p.a[j], p.a_mn ? 64 : pl.tile == kSmall ? a_rows : kTileM)) return GDN_ERR_CUDA;
         for (int j = 0; j < b_maps; ++j)
-            if (!encode(&g.b[nb++], p.b[j], p.b_mn || (g.dual && pl.tile == kSmall) ? 64 : 128)) return cudaErrorInvalidValue;
+            if (!encode(&g.b[nb++], p.b[j], p.b_mn || (g.dual && pl.tile == kSmall) ? 64 : 128)) return GDN_ERR_CUDA;
         if (b.epi == kPlain && !pr.f32 && !q.partial && q.vec_out) {
             q.tma_out = 1;
-            if (!encode(&g.c[nc++], Mat{p.out, p.M, p.N, p.N, 0, 1}, 32)) return cudaErrorInvalidValue;
+            if (!encode(&g.c[nc++], Mat{p.out, p.M, p.N, p.N, 0, 1}, 32)) return GDN_ERR_CUDA;
         }
         split |= q.partial != nullptr;
         const bool four = p.N % 4 == 0 && (b.epi == kPlain ? aligned16(p.out) : aligned16(b.gate) && aligned16(b.up));
         f.group[g.groups++] = {q.partial, q.splits, four, p.M, p.N, q.ld_part, q.ld_out, p.out};
     }
-    if (g.groups == 0) return cudaSuccess;
+    if (g.groups == 0) return GDN_OK;
     if (b.epi != kPlain) {
         const int n = b.epi == kUp ? 1 : 3;
         for (int i = 0; i < n; ++i) {
             g.planes[i] = static_cast<__nv_bfloat16 *>(const_cast<void *>(b.planes[i].p));
-            if (!pr.f32 && !encode(&g.c[i], b.planes[i], 32, b.epi == kBack ? 32 : 64)) return cudaErrorInvalidValue;
+            if (!pr.f32 && !encode(&g.c[i], b.planes[i], 32, b.epi == kBack ? 32 : 64)) return GDN_ERR_CUDA;
         }
         g.ld_plane = b.planes[0].ld, g.plane_stride = b.planes[0].plane;
         g.gate = b.gate, g.up = b.up;
@@ -431,19 +437,21 @@ cudaError_t run_batch(const Batch &b, const Problem &pr, char *partial, int *err
         if (b.epi == kUp && b.gate && !pr.f32 && g.vec_io) {
             g.tma_io = 1;
             if (!encode(&g.io[0], Mat{b.gate, p.M, p.N, p.N, 0, 1}, 32) || !encode(&g.io[1], Mat{b.up, p.M, p.N, p.N, 0, 1}, 32))
-                return cudaErrorInvalidValue;
+                return GDN_ERR_CUDA;
         }
     }
     const int sms = device_sm_count(), workers = pl.tile == kPair ? sms / 2 : pl.tile == kWide ? sms : 2 * sms;
     const int grid = std::min(workers, g.first + g.rest) * (pl.tile == kPair ? 2 : 1);
-    const cudaError_t rc = b.epi == kUp ? launch_up(g, pr.f32, pl.tile, grid, s)
-                           : b.epi == kBack ? launch_back(g, pr.f32, pl.tile, grid, s)
-                                            : launch_plain(g, pr.f32, pl.tile, grid, s);
-    if (rc != cudaSuccess || !split) return rc;
+    cudaError_t rc = b.epi == kUp ? launch_up(g, pr.f32, pl.tile, grid, s)
+                     : b.epi == kBack ? launch_back(g, pr.f32, pl.tile, grid, s)
+                                      : launch_plain(g, pr.f32, pl.tile, grid, s);
+    if (rc != cudaSuccess) return failed(where, rc);
+    if (!split) return GDN_OK;
     f.act = pr.act;
     for (int i = 0; i < 3; ++i) f.planes[i] = g.planes[i];
     f.ld_plane = g.ld_plane, f.plane_stride = g.plane_stride, f.gate = b.gate, f.up = b.up;
-    return b.epi == kUp ? run_finish<kUp>(pr, f, g.groups, s) : b.epi == kBack ? run_finish<kBack>(pr, f, g.groups, s) : run_finish<kPlain>(pr, f, g.groups, s);
+    rc = b.epi == kUp ? run_finish<kUp>(pr, f, g.groups, s) : b.epi == kBack ? run_finish<kBack>(pr, f, g.groups, s) : run_finish<kPlain>(pr, f, g.groups, s);
+    return rc == cudaSuccess ? GDN_OK : failed(where, rc);
 }
 
 // ------------------------------------------------------------------ the passes
@@ -498,11 +506,7 @@ gdn_status run_few(const gdn_ffn_desc &d, const Problem &pr, void *y, void *gate
     const bool vb = pr.F * e % 16 == 0 && aligned16(d.w_down);
     if (rc == cudaSuccess) rc = launch_few(a, true, pr.f32, va, s);
     if (rc == cudaSuccess) rc = launch_few(b, false, pr.f32, vb, s);
-    if (rc != cudaSuccess) {
-        set_error_detail("launch gated_ffn_fwd", rc);
-        return GDN_ERR_CUDA;
-    }
-    return GDN_OK;
+    return rc == cudaSuccess ? GDN_OK : failed("launch gated_ffn_fwd", rc);
 }
 
 Pass plan_fwd(const gdn_ffn_desc &d, void *y, void *gate, void *up, void *workspace) {
@@ -559,12 +563,10 @@ gdn_status run_pass(const Pass &p, int32_t *status, cudaStream_t s, const char *
     cudaError_t e = cudaSuccess;
     if (status) e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
     if (e == cudaSuccess && p.n) e = run_stage(p.pr, p.stage, p.n_stage, s);
-    for (int i = 0; e == cudaSuccess && i < p.n; ++i) e = run_batch(p.batch[i], p.pr, p.partial, status, s);
-    if (e != cudaSuccess) {
-        set_error_detail(where, e);
-        return GDN_ERR_CUDA;
-    }
-    return GDN_OK;
+    if (e != cudaSuccess) return failed(where, e);
+    gdn_status st = GDN_OK;
+    for (int i = 0; st == GDN_OK && i < p.n; ++i) st = run_batch(p.batch[i], p.pr, p.partial, status, s, where);
+    return st;
 }
 
 bool elem_ok(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == GDN_F32 ? 3u : 1u)) == 0; }
