@@ -25,7 +25,7 @@ from torch.autograd import forward_ad
 from .layer_ops import _CODE, _On, _act, _apart, _like, _p, _raise, _row_stride, _workspace, _wrote
 
 __all__ = ["block_norm_fwd", "block_norm_bwd", "block_norm", "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn",
-           "GdnBlockNormDesc", "GdnFfnDesc"]
+           "GdnBlockNormDesc", "GdnFfnDesc", "GdnFfnPlanInfo"]
 
 _F32, _I32 = torch.float32, torch.int32
 _GATES = {"silu": 0, "sigmoid": 1}
@@ -48,6 +48,12 @@ class GdnFfnDesc(ctypes.Structure):
                 [(n, ctypes.c_int32) for n in ("activation", "dtype")])
 
 
+class GdnFfnPlanInfo(ctypes.Structure):
+    """gdn_ffn_plan_info of include/gdn.h."""
+    _fields_ = [("path", ctypes.c_int32), ("tile", ctypes.c_int32 * 2), ("a_rows", ctypes.c_int32 * 2),
+                ("products", ctypes.c_int32 * 2), ("parts", ctypes.c_int32 * 4 * 2)]
+
+
 def bind(lib):
     """Argument types of these operators' C entry points."""
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
@@ -59,7 +65,8 @@ def bind(lib):
             ("gdn_gated_ffn_fwd_workspace_size", sz, [ffn]),
             ("gdn_gated_ffn_fwd", i32, [ffn, vp, vp, vp, vp, vp, sz, vp]),
             ("gdn_gated_ffn_bwd_workspace_size", sz, [ffn, vp, i64]),
-            ("gdn_gated_ffn_bwd", i32, [ffn, vp, i64] + [vp] * 8 + [sz, vp])):
+            ("gdn_gated_ffn_bwd", i32, [ffn, vp, i64] + [vp] * 8 + [sz, vp]),
+            ("gdn_gated_ffn_plan_query", i32, [ffn, i32, vp, i64, ctypes.POINTER(GdnFfnPlanInfo)])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     global _bound

@@ -665,3 +665,25 @@ extern "C" gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy
     }
     return gdn::ffn::run_pass(p, device_status, s, "launch gated_ffn_bwd");
 }
+
+extern "C" gdn_status gdn_gated_ffn_plan_query(const gdn_ffn_desc *desc, int backward, const void *dy, int64_t dy_stride,
+                                               gdn_ffn_plan_info *info) {
+    using namespace gdn::ffn;
+    const gdn_status st = desc_ok(desc);
+    if (st != GDN_OK) return st;
+    if (!info || (backward && desc->M > 1 && dy_stride < desc->D_out)) return GDN_ERR_INVALID_ARG;
+    if (backward && !span_ok(desc->M, dy_stride)) return GDN_ERR_UNSUPPORTED;
+    *info = {};
+    if (desc->M == 0) return GDN_OK;
+    info->path = !backward && few(problem_of(*desc)) ? GDN_FFN_FEW : GDN_FFN_TILES;
+    if (info->path == GDN_FFN_FEW) return GDN_OK;
+    const Pass p = backward ? plan_bwd(*desc, dy, dy_stride, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr)
+                            : plan_fwd(*desc, nullptr, nullptr, nullptr, nullptr);
+    for (int i = 0; i < p.n; ++i) {
+        const Batch &b = p.batch[i];
+        info->tile[i] = b.plan.tile, info->products[i] = b.n;
+        info->a_rows[i] = b.plan.tile == kSmall ? rows_of_a(b) : kTileM;
+        for (int k = 0; k < b.n; ++k) info->parts[i][k] = b.plan.part_bytes[k] ? b.plan.splits[k] : 0;
+    }
+    return GDN_OK;
+}

@@ -803,6 +803,24 @@ gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy, int64_t d
                              const void *up, void *dx, void *dw_gate, void *dw_up, void *dw_down,
                              int32_t *device_status, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/*
+ * How the block's products run (host only, no GPU needed), for tests and tools: few
+ * tokens forward by kernels of their own, else each pass as two launches on tiles,
+ * first = 0 (both projections; backward dh) and 1 (y; backward the gradients of x, w_gate,
+ * w_up, w_down).  backward = 0 ignores dy.
+ */
+enum { GDN_FFN_NOTHING = 0, GDN_FFN_FEW = 1, GDN_FFN_TILES = 2 };
+typedef struct {
+    int32_t path;             /* GDN_FFN_*: no tokens, a few, or tiles (then the rest) */
+    int32_t tile[2];          /* 0: pairs of CTAs of 256 x 256, 1: 128 x 256, 2: 128 x 128 */
+    int32_t a_rows[2];        /* tiles of 128 x 128: rows of the first operand's boxes */
+    int32_t products[2];
+    int32_t parts[2][4];      /* of each product: 0: leaves at once, n > 0: as n parts of
+                                 its sum, which another kernel adds */
+} gdn_ffn_plan_info;
+gdn_status gdn_gated_ffn_plan_query(const gdn_ffn_desc *desc, int backward, const void *dy, int64_t dy_stride,
+                                    gdn_ffn_plan_info *info);
+
 /* The CUDA error (and, for tensor-map encoding, the driver result) behind the
  * most recent GDN_ERR_CUDA returned on the calling host thread, as text such
  * as "launch fused_tc: cudaErrorInvalidValue"; after gdn_chunk_fwd_static

@@ -14,11 +14,9 @@ import torch
 import chunked_prefill_gdn_gb300 as gdn
 from chunked_prefill_gdn_gb300 import build as gdn_build
 
+from ffn_check import TORCH, U, check_ffn
+
 pytestmark = pytest.mark.gpu
-
-U = 2.0 ** -24
-TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
-
 
 @pytest.fixture(scope="module", autouse=True)
 def lib():
@@ -64,46 +62,4 @@ LONG = [(4, 64, 600000, 64), (16, 8, 600008, 9), (40, 24, 600000, 16), (200, 8, 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,D,F,O", LONG)
 def test_long_sides_of_weights(M, D, F, O, dtype):
-    """Bars on the sum of the absolute values of a result's terms: a sum in tensor memory 2^-9
-    (8192 additions of 2^-22), and fp32 as above with K / 256 additions of U for a few tokens;
-    what lies between the products is off by as much in its terms, and rounded (bf16)."""
-    bf16 = dtype == "bf16"
-    g = torch.Generator(device="cuda").manual_seed(F + D + O)
-    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(TORCH[dtype])   # noqa: E731
-    x, dy = n(M, D), n(M, O)
-    w = [n(F, D, std=D ** -0.5), n(F, D, std=D ** -0.5), n(O, F, std=F ** -0.5)]
-    y, gate, up = gdn.gated_ffn_fwd(x, *w, save=True, check=True)
-    assert torch.equal(y, gdn.gated_ffn_fwd(x, *w)[0])
-    half = 2.0 ** -8 if bf16 else 0.0
-    part = lambda K: 2.0 ** -9 if bf16 else (1024 + K / 256) * U   # noqa: E731
-
-    def check(name, got, want, mag, K, before=0.0):
-        tol = half * want.abs() + part(K) * mag + before
-        assert ((got.double() - want).abs() <= tol + 1e-37).all(), name
-        assert (got.double() - want).norm() <= (5e-3 if bf16 else 1e-5) * want.norm(), name
-
-    X, DY, (WG, WU, WD) = x.double(), dy.double(), (t.double() for t in w)
-    G, V = X @ WG.t(), X @ WU.t()
-    mg, mu = X.abs() @ WG.abs().t(), X.abs() @ WU.abs().t()
-    check("gate", gate, G, mg, D)
-    check("up", up, V, mu, D)
-    h = G * torch.sigmoid(G) * V
-    dh = part(D) * (1.13 * mg * V.abs() + G.abs() * mu) + 16 * U * h.abs() + half * h.abs()
-    check("y", y, h @ WD.t(), h.abs() @ WD.abs().t(), F, 1.01 * dh @ WD.abs().t())
-    del G, V, mg, mu, h, dh
-    got = gdn.gated_ffn_bwd(dy, x, *w, gate, up, check=True)
-    G, V = gate.double(), up.double()
-    s = torch.sigmoid(G)
-    a, slope = G * s, s + G * s * (1 - s)
-    dh, mdh = DY @ WD, DY.abs() @ WD.abs()
-    dg, du, h = dh * V * slope, dh * a, a * V
-    edg = part(O) * mdh * V.abs() * (slope.abs() + 0.01) + half * dg.abs() + 16 * U * dg.abs()
-    edu = part(O) * mdh * (a.abs() + 0.01) + half * du.abs() + 16 * U * du.abs()
-    eh = (half + 16 * U) * h.abs()
-    adg, adu, ah = dg.abs() + edg, du.abs() + edu, h.abs() + eh
-    check("dx", got[0], dg @ WG + du @ WU, adg @ WG.abs() + adu @ WU.abs(), 2 * F, edg @ WG.abs() + edu @ WU.abs())
-    check("dw_gate", got[1], dg.t() @ X, adg.t() @ X.abs(), M, edg.t() @ X.abs())
-    check("dw_up", got[2], du.t() @ X, adu.t() @ X.abs(), M, edu.t() @ X.abs())
-    check("dw_down", got[3], DY.t() @ h, DY.abs().t() @ ah, M, DY.abs().t() @ eh)
-    for p, q in zip(got, gdn.gated_ffn_bwd(dy, x, *w, gate, up)):
-        assert torch.equal(p, q)
+    check_ffn(M, D, F, O, dtype)
