@@ -66,6 +66,7 @@ def bind(lib):
             ("gdn_gated_ffn_fwd", i32, [ffn, vp, vp, vp, vp, vp, sz, vp]),
             ("gdn_gated_ffn_bwd_workspace_size", sz, [ffn, vp, i64]),
             ("gdn_gated_ffn_bwd", i32, [ffn, vp, i64] + [vp] * 8 + [sz, vp]),
+            ("gdn_gated_ffn_debug", i32, [i32]),
             ("gdn_gated_ffn_plan_query", i32, [ffn, i32, vp, i64, ctypes.POINTER(GdnFfnPlanInfo)])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
@@ -325,7 +326,9 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", save: bool 
     """The gated feed-forward block of x [..., D]: y = (act(x w_gate^T) * (x w_up^T)) w_down^T
     with w_gate, w_up [F, D] and w_down [D_out, F] in x's type; returns (y [..., D_out],
     gate, up), gate and up the two projections [..., F] for the backward pass (None without
-    save).  activation: 'silu' or 'gelu_tanh'."""
+    save).  activation: 'silu' or 'gelu_tanh'.  check=True waits for the call and raises
+    GdnError where a bounded wait inside a kernel ran out (the outputs are then not those of
+    the inputs); without it nothing is said."""
     desc, M, F, n_out = _ffn_desc(x, w_gate, w_up, w_down, activation)
     lead, dtype, dev = x.shape[:-1], x.dtype, x.device
     if out is not None:
@@ -351,7 +354,8 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", save: bool 
 def gated_ffn_bwd(dy, x, w_gate, w_up, w_down, gate, up, activation: str = "silu", needs=(True, True, True, True),
                   workspace=None, stream: Optional[torch.cuda.Stream] = None, check: bool = False):
     """Gradients of gated_ffn_fwd: (dx, dw_gate, dw_up, dw_down) in x's type from dy and the
-    forward pass's gate and up; `needs` says which are wanted (None for the others)."""
+    forward pass's gate and up; `needs` says which are wanted (None for the others).  check as
+    in gated_ffn_fwd."""
     desc, M, F, n_out = _ffn_desc(x, w_gate, w_up, w_down, activation)
     lead, dtype, dev = x.shape[:-1], x.dtype, x.device
     _like("dy", dy, (*lead, n_out), dtype, dev, strided=True)
@@ -376,10 +380,10 @@ def gated_ffn_bwd(dy, x, w_gate, w_up, w_down, gate, up, activation: str = "silu
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, w_down, activation, save):
-        y, gate, up = gated_ffn_fwd(x, w_gate, w_up, w_down, activation, save=save)
+    def forward(ctx, x, w_gate, w_up, w_down, activation, save, check):
+        y, gate, up = gated_ffn_fwd(x, w_gate, w_up, w_down, activation, save=save, check=check)
         ctx.save_for_backward(x, w_gate, w_up, w_down, gate, up)
-        ctx.activation = activation
+        ctx.activation, ctx.check = activation, check
         return y
 
     @staticmethod
@@ -387,13 +391,14 @@ class _GatedFfn(torch.autograd.Function):
     def backward(ctx, dy):
         x, w_gate, w_up, w_down, gate, up = ctx.saved_tensors
         return (*gated_ffn_bwd(dy.contiguous(), x, w_gate, w_up, w_down, gate, up, ctx.activation,
-                               needs=ctx.needs_input_grad[:4]), None, None)
+                               needs=ctx.needs_input_grad[:4], check=ctx.check), None, None, None)
 
 
-def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu"):
-    """gated_ffn_fwd with autograd (x and the weights); returns y."""
+def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", check: bool = False):
+    """gated_ffn_fwd with autograd (x and the weights); returns y.  check as in gated_ffn_fwd,
+    in the backward pass too."""
     tensors = x, w_gate, w_up, w_down
     if _plain(tensors):
-        return gated_ffn_fwd(*tensors, activation)[0]
+        return gated_ffn_fwd(*tensors, activation, check=check)[0]
     save = torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
-    return _GatedFfn.apply(*tensors, activation, save)
+    return _GatedFfn.apply(*tensors, activation, save, check)

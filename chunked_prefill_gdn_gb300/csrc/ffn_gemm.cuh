@@ -68,6 +68,7 @@ struct GemmArgs {
     int first, rest, ratio;
     int terms;                // 1, or 6 for three planes
     int a_rows, stages;       // few_rows: rows of A's boxes (32, 64, 128) and stages (5, 4, 3)
+    int probe;                // GDN_DEBUG_TIMEOUT_PROBE: nothing is loaded, every wait runs out
     int act, tma_io, vec_io;  // kUp: gate and up leave through boxes; rows of both in 16-byte vectors
     __nv_bfloat16 *planes[3]; // kUp: h; kBack: dgate, dup, h: one plane (bf16) or three (fp32)
     long long ld_plane, plane_stride;
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(Shape<EPI, T, CTAS, BN>::threads, Shape<EPI, T
     if (warp == 0) {
         const bool leader = tc::elect_one();
         uint32_t s = 0, turn = 0, loads = 0;   // the stage, the parity of its rounds
-        bool ok = true;
+        bool ok = !g.probe;
         const uint32_t base = tc::smem_u32(smem);
         uint32_t full0 = tc::smem_u32(&bars.full[0]);
         if constexpr (CTAS == 2) full0 = map_to_cta(full0, 0);

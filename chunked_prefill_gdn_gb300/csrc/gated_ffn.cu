@@ -46,6 +46,8 @@ struct Mat {
     int planes;
 };
 
+thread_local int debug_checks = 0;   // gdn_gated_ffn_debug
+
 gdn_status failed(const char *where, cudaError_t e) {
     set_error_detail(where, e);
     return GDN_ERR_CUDA;
@@ -395,6 +397,7 @@ gdn_status run_batch(const Batch &b, const Problem &pr, char *partial, int *err,
     g.terms = pr.terms, g.act = pr.act, g.err = err;
     const int a_rows = rows_of_a(b);
     g.a_rows = a_rows, g.stages = small_stages(a_rows);
+    g.probe = (debug_checks & GDN_DEBUG_TIMEOUT_PROBE) != 0;
     FinishArgs f = {};
     int na = 0, nb = 0, nc = 0;
     bool split = false;
@@ -685,5 +688,11 @@ extern "C" gdn_status gdn_gated_ffn_plan_query(const gdn_ffn_desc *desc, int bac
         info->a_rows[i] = b.plan.tile == kSmall ? rows_of_a(b) : kTileM;
         for (int k = 0; k < b.n; ++k) info->parts[i][k] = b.plan.part_bytes[k] ? b.plan.splits[k] : 0;
     }
+    return GDN_OK;
+}
+
+extern "C" gdn_status gdn_gated_ffn_debug(int checks) {
+    if (checks & ~GDN_DEBUG_TIMEOUT_PROBE) return GDN_ERR_INVALID_ARG;
+    gdn::ffn::debug_checks = checks;
     return GDN_OK;
 }

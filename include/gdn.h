@@ -803,6 +803,11 @@ gdn_status gdn_gated_ffn_bwd(const gdn_ffn_desc *desc, const void *dy, int64_t d
                              const void *up, void *dx, void *dw_gate, void *dw_up, void *dw_down,
                              int32_t *device_status, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/* Tests of the error path: 0, or GDN_DEBUG_TIMEOUT_PROBE (the products on tiles load
+ * nothing, so that their bounded waits run out, about 2 s a launch, and the call reports
+ * GDN_ERR_TIMEOUT), for the later calls of this host thread. */
+gdn_status gdn_gated_ffn_debug(int debug_checks);
+
 /*
  * How the block's products run (host only, no GPU needed), for tests and tools: few
  * tokens forward by kernels of their own, else each pass as two launches on tiles,
