@@ -23,12 +23,12 @@
 //
 // Measured (all parts, fp32 parameters; of the measured copy rate): 32768 x 4096 bf16
 // forward 201 us, backward 321 (both 100%); 2^27 elements of 8192 columns 236 and 365, of
-// 1024 209 and 326, of 256 244 and 371; fp32 4096 columns (16384 rows) 227 and 361.  The
+// 1024 210 and 326, of 256 245 and 372; fp32 4096 columns (16384 rows) 227 and 361.  The
 // gated norm of 16384 x 32 heads of 128 62 us (97%), its backward pass on 8191 x 32 58 (86%,
 // 4 of it the sum over the blocks).  Rows that are not 16-byte aligned come in the 16-byte
 // chunks they touch and leave element by element: 32776 x 4095 bf16 363 and 648 us, fp32
 // (16388) 230 and 459.  Rows wider than 8192 columns are read two or three times: 8192 x
-// 16384 bf16 489 and 905 us.  16 rows 5.4 us (the host's call takes 25).
+// 16384 bf16 489 and 905 us.  16 rows 5.4 us (a call takes 28 to 32, on the host).
 #include <algorithm>
 #include <type_traits>
 
@@ -117,7 +117,7 @@ __device__ __forceinline__ void bn_copy16(uint4 *dst, const void *src) {
 }
 
 // More rows in flight than these are slower, not only useless (forward, 2^27 elements in
-// bf16, all parts: 2048 columns 208 us with two rows, 225 with three or four, 1024 columns 213
+// bf16, all parts: 2048 columns 208 us with two rows, 225 with three or four, 1024 columns 210
 // and 243; the gated norm of heads 127 with three, 132 with four, 137 with two; backward, 256
 // columns 371 with two, 390 with four, 2048 columns 362 and 374), and so are more threads of
 // fewer registers (backward, 1024 columns 326 us at 640 threads, 365 at 768).

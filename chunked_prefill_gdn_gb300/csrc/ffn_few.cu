@@ -1,5 +1,5 @@
 // Few tokens through the feed-forward block: every row of the weights times up to 16
-// tokens (fp32: 32), bound by the weights' bytes (4096 x 12288 bf16: 45 us at the measured
+// tokens (8 where the weights are large; fp32: 32), bound by the weights' bytes (4096 x 12288 bf16: 45 us at the measured
 // copy rate, fp32 90).
 //
 // One token: a group of one to eight warps owns two rows of weights, the gate's and the
@@ -13,9 +13,9 @@
 // w_gate and of w_up, or of w_down, its eight warps take turns along K.  The order of K
 // within a product is free as long as both operands share it, so a lane's 16-byte vector of
 // a row is its part of two instructions' fragments: no shuffles, no shared memory, tokens
-// come from L1.  2 to 8 tokens 50 us, 16 tokens 66 (4096 x 1024: 9.5 of 3.8); beyond, the
-// tokens no longer fit L1 (32: 159 us) and the tiles of ffn_gemm.cuh take over (58 us, small
-// blocks 18).  fp32 is split into three bf16 terms a value, six products: 122 us for 2, 173
+// come from L1.  2 to 8 tokens 50 us; 16 would take 66, so from nine on the tiles of ffn_gemm.cuh
+// take over (57 us), but for weights of up to 134 MB (4096 x 1024: 16 tokens 9.4 of 3.8).  Beyond
+// 16 the tokens no longer fit L1 (32: 159 us, on tiles 58; small blocks 18).  fp32 is split into three bf16 terms a value, six products: 122 us for 2, 173
 // for 16, 305 for 32 tokens, where laying the weights out for tiles takes 490; (errors
 // against 64 bits 7e-7 and less, as of products in fp32).
 //

@@ -42,8 +42,9 @@ enum Epi { kUp = 0, kBack = 1, kPlain = 2 };
 
 constexpr int kTileM = 128, kBlockK = 64;
 // Blocks of 64 along K per sum in tensor memory (fp32).  The tensor cores cut what an
-// addition leaves over; errors against 64 bits at 2048 x 2048 x 6144: 1.5e-6 with eight blocks
-// (629 us), 7e-7 with four (664), 4e-7 with two (682); products in fp32 throughout 1.9e-6.
+// addition leaves over; errors against 64 bits at 2048 x 2048 x 6144: 1.5e-6 with eight blocks,
+// 7e-7 with four (5% slower: 645 us), 4e-7 with two (another 3%); products in fp32 throughout
+// 1.9e-6.
 constexpr int kPromote = 4;
 constexpr int kMaxStages = 6, kMaxGroups = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;

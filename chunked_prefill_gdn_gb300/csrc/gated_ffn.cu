@@ -487,8 +487,13 @@ Problem problem_of(const gdn_ffn_desc &d) {
 
 // Whether the forward products are those of ffn_few.cu.  From nine tokens in bf16 on they
 // slow down with the weights' bytes, the tiles by their launches alone: 16 tokens, 4096 x 12288
-// (302 MB) 66 us, tiles 57; 2048 x 6144 (75 MB) 23 and 27; 1024 x 4096 9.5 and 16.  A warp adds up
-// an eighth of K there, in one sum (kLongest).
+// (302 MB) 66 us, tiles 57; 2048 x 6144 (75 MB) 23 and 27; 1024 x 4096 9.4 and 16.
+// Rows that are not 16-byte aligned follow the same rule, although tiles lay them out in every
+// call (9 and 16 tokens there, and on tiles): 4095 x 12287 191 and 227, 173; 4096 x 12287
+// (w_down's rows alone) 138 and 170, 101; 2500 x 9001 (135 MB) 108 and 120, 87; only with
+// w_down's alone aligned is it the other way round, 4095 x 12288 117 and 124, 135.  Of smaller
+// weights no copies are made: 2047 x 6143 (75 MB) 73 and 91 (17 tokens, on tiles, 56).
+// A warp adds up an eighth of K there, in one sum (kLongest).
 bool few(const Problem &pr) {
     if (std::max(pr.D, pr.F) > 8 * kLongest * kBlockK) return false;
     const double weights = 2.0 * (2.0 * pr.F * pr.D + (double)pr.O * pr.F);
