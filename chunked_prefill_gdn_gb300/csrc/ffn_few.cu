@@ -19,6 +19,9 @@
 // for 16, 305 for 32 tokens, where laying the weights out for tiles takes 490; (errors
 // against 64 bits 7e-7 and less, as of products in fp32).
 //
+// h is rounded to the activations' type here too, so that a token's h does not depend on how
+// many come with it.
+//
 // The second product's blocks start while the first one's last are at work.
 #include <algorithm>
 

@@ -12,6 +12,10 @@
 // Where a product has too few tiles to fill the GPU its sum over K is split: the
 // parts leave as fp32 and a second kernel adds them in order and applies the
 // epilogue, so the result does not depend on the launch.
+//
+// In bf16 what lies between the products (h; backward dg, du and h) is rounded to bf16, the
+// type in which the tensor cores read it: as fp32 planes the second product would be six.
+// Outputs are 2.35e-3 from 64 bits (rms, relative), 1.66e-3 of which are their own rounding.
 #include <algorithm>
 #include <mutex>
 

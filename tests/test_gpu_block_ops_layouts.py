@@ -108,3 +108,42 @@ def test_graphs_that_share_a_workspace():
             graph.replay()
     for got, alone in zip(out, want):
         equal(got, alone)
+
+
+def test_beside_the_recurrence_on_another_stream():
+    """The feed-forward block's and the recurrence's tensor-core kernels at the same time: the
+    bits of each alone."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
+    q, k, v = (torch.nn.functional.normalize(n(2, 2000, 16, 128), dim=-1).bfloat16() for _ in range(3))
+    decay, beta = -0.1 * torch.rand(2, 2000, 16, generator=g, device="cuda"), torch.rand(2, 2000, 16, generator=g, device="cuda")
+    cases = []
+    for M, D, F in ((1500, 512, 2048), (100, 1024, 4096), (40, 512, 512)):
+        x, w = n(M, D).bfloat16(), [(n(*s) / s[1] ** 0.5).bfloat16() for s in ((F, D), (F, D), (D, F))]
+        cases.append((x, w))
+
+    def recurrence(stream=None):
+        return gdn.chunk_fwd(q, k, v, decay, beta, stream=stream)
+
+    def block(stream=None):
+        out = []
+        for x, w in cases:
+            y, gate, up = gdn.gated_ffn_fwd(x, *w, save=True, stream=stream)
+            out += [y, *gdn.gated_ffn_bwd(y, x, *w, gate, up, stream=stream)]
+        return out
+
+    want = recurrence(), block()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, (call, s) in enumerate(zip((recurrence, block), streams)):
+            with torch.cuda.stream(s):
+                got[i].append(call())
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for again in got[i]:
+            equal(again, want[i])
